@@ -474,6 +474,113 @@ MAMBA_API int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const floa
                             const float* weight, float eps, int64_t M, int64_t D, void* stream);
 
 /*
+ * The gated delta rule: a recurrent layer whose state S [dv][dk] per value head
+ * is decayed by a gate and corrected towards v_t along the key k_t:
+ *
+ *     alpha_t = exp(-exp(A_log) softplus(a_t + dt_bias)),  beta_t = sigmoid(b_t)
+ *     S_t = alpha_t S_{t-1} + beta_t (v_t - alpha_t S_{t-1} k_t) k_t^T
+ *     y_t = scale S_t q_t
+ *
+ * (No counterpart in the mamba-rs pages: an addition of this library, in the
+ *  manner of its scan and step.)  Value head h reads key head h / (Hv / Hk).
+ * Keys are taken as given: the rule contracts for |k_t| <= 1, which
+ * mamba_qk_norm_rotary with MAMBA_NORM_L2 gives.
+ *
+ * mamba_gated_delta_prefill runs T tokens from a state and returns the state
+ * after the last one; prefill(T1) then prefill(T2) equals prefill(T1 + T2) up
+ * to rounding.
+ *
+ *   y          [B][T][Hv][dv], row (b T + t) at ld_y, dtype y_dtype     (out)
+ *   q, k       [B][T][Hk][dk] at ld_q, ld_k, dtype in_dtype             (in)
+ *   v          [B][T][Hv][dv] at ld_v, dtype in_dtype                   (in)
+ *   a, b       [B][T][Hv] at ld_a, ld_b, dtype in_dtype                 (in)
+ *   A_log      [Hv] f32;  dt_bias [Hv] f32 or NULL                      (in)
+ *   scale      of the output, finite (usually 1 / sqrt(dk))
+ *   state_in   [B][Hv][dv][dk] f32, or NULL for a zero state            (in)
+ *   state_out  the same, or NULL; may equal state_in                    (out)
+ *   workspace  mamba_gated_delta_workspace_bytes of scratch, or NULL
+ * Heads are dense inside a row (columns of a packed projection can be passed in
+ * place).  T == 0 copies state_in to state_out (zeros if state_in is NULL).
+ * Sizes: 1 <= dk <= MAMBA_GDR_MAX_DK, 1 <= dv <= MAMBA_GDR_MAX_DV, Hv a multiple
+ * of Hk.
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL tensors, strides smaller than a row, a
+ * scale that is not finite, misaligned elements, outputs overlapping anything;
+ * MAMBA_ERR_UNSUPPORTED for dk or dv out of range.
+ */
+#define MAMBA_GDR_MAX_DK 256
+#define MAMBA_GDR_MAX_DV 1024
+MAMBA_API int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, const void* q, int64_t ld_q,
+                                        const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* a,
+                                        int64_t ld_a, const void* b, int64_t ld_b, int in_dtype, const float* A_log,
+                                        const float* dt_bias, float scale, const float* state_in, float* state_out,
+                                        int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Scratch bytes with which mamba_gated_delta_prefill spreads a long prefill of
+ * few heads over every SM of the current device (0: it needs none); negative on
+ * an error. */
+MAMBA_API int64_t mamba_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk,
+                                                    int64_t dv, int in_dtype);
+
+/*
+ * One T = 1 step of the rule in place on the `layer` slab of a persistent state
+ * [n_layers][B][Hv][dv][dk] f32.  q, k [B][Hk][dk], v, y [B][Hv][dv], a, b
+ * [B][Hv], each with its row stride; the rest and the errors as above, and
+ * MAMBA_ERR_INVALID_ARG for a layer outside [0, n_layers).
+ */
+MAMBA_API int mamba_gated_delta_step_batched(void* y, int64_t ld_y, int y_dtype, const void* q, int64_t ld_q,
+                                             const void* k, int64_t ld_k, const void* v, int64_t ld_v, const void* a,
+                                             int64_t ld_a, const void* b, int64_t ld_b, int in_dtype,
+                                             const float* A_log, const float* dt_bias, float scale, float* state,
+                                             int64_t layer, int64_t n_layers, int64_t B, int64_t Hk, int64_t Hv,
+                                             int64_t dk, int64_t dv, void* stream);
+
+/*
+ * Norms of queries and keys per head, with the position rotation in the same
+ * pass (the inputs of the rule above).  Every head x of d components becomes
+ *     x / sqrt(mean_j x_j^2 + eps) * w        (w: q_weight for q, k_weight for k)
+ *     x / sqrt(sum_j x_j^2 + eps) * w         with MAMBA_NORM_L2
+ * and then the pairs of its first rot_dim components are turned by
+ * theta_i = position * inv_freq[i], i < rot_dim / 2:
+ *     (x, y) -> (x cos - y sin, y cos + x sin)
+ * where pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * MAMBA_ROTARY_INTERLEAVED.  Angles are reduced exactly before they reach 32
+ * bits, so far positions cost no accuracy.
+ *
+ *   q_out, k_out  [B][T][Hq][d], [B][T][Hk][d] at ld_qo, ld_ko, out_dtype (out);
+ *                 may be q and k themselves (same pointer, stride and dtype)
+ *   q, k          at ld_q, ld_k, in_dtype; Hq or Hk may be 0 (then NULL)
+ *   q_weight, k_weight  [d] f32 or NULL
+ *   inv_freq      [rot_dim / 2] f32 radians per position (NULL if rot_dim == 0)
+ *   positions     [B][T] int64, or NULL: a token's index in its row
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL tensors, strides smaller than a row, an
+ * odd rot_dim or one over d, unknown flags, eps outside [0, 1], overlap;
+ * MAMBA_ERR_UNSUPPORTED for d over MAMBA_HEAD_NORM_MAX_D.
+ */
+#define MAMBA_NORM_L2 1
+#define MAMBA_ROTARY_INTERLEAVED 2
+#define MAMBA_HEAD_NORM_MAX_D 256
+MAMBA_API int mamba_qk_norm_rotary(void* q_out, int64_t ld_qo, void* k_out, int64_t ld_ko, int out_dtype,
+                                   const void* q, int64_t ld_q, const void* k, int64_t ld_k, int in_dtype,
+                                   const float* q_weight, const float* k_weight, const float* inv_freq,
+                                   int64_t rot_dim, const int64_t* positions, float eps, int flags, int64_t B,
+                                   int64_t T, int64_t Hq, int64_t Hk, int64_t d, void* stream);
+
+/*
+ * The gated norm of a recurrent layer's output, per head of d components:
+ *     out = y / sqrt(mean_j y_j^2 + eps) * weight * SiLU(z)
+ *
+ *   out     [rows][H][d] at ld_out, out_dtype; may be y itself             (out)
+ *   y, z    [rows][H][d] at ld_y, ld_z, in_dtype; z may be NULL (no gate)  (in)
+ *   weight  [d] f32 or NULL                                               (in)
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL out or y, strides smaller than a row,
+ * eps outside [0, 1], overlap, extent overflow.
+ */
+MAMBA_API int mamba_head_norm_gated(void* out, int64_t ld_out, int out_dtype, const void* y, int64_t ld_y,
+                                    const void* z, int64_t ld_z, int in_dtype, const float* weight, float eps,
+                                    int64_t rows, int64_t H, int64_t d, void* stream);
+
+/*
  * One whole Mamba-1 block (residual block around the mixer), as the mamba-rs
  * engine runs a layer (inference.rs step chain F1-F12; prefill.rs
  * `prefill_body`, mixed-precision path with the residual stream in f32):

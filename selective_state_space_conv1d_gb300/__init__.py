@@ -14,6 +14,10 @@ C-ABI entry points (include/mamba_ssm.h), each backed by hand-written CUDA kerne
   mamba3_decode_graph_create    n_steps x n_layers such tokens recorded once as a CUDA graph
   mamba_linear_bf16             a projection of the layer on the tensor cores (tcgen05)
   mamba_rmsnorm                 RMSNorm of the f32 residual stream
+  mamba_gated_delta_prefill     the gated delta rule over T tokens, state in/out
+  mamba_gated_delta_step_batched  its T=1 step on a [n_layers][B][Hv][dv][dk] state
+  mamba_qk_norm_rotary          per-head norms of queries and keys with the position rotation
+  mamba_head_norm_gated         per-head RMSNorm of a layer's output with its SiLU(z) gate
   mamba_layer_prefill / _step   the whole Mamba-1 block (norm, projections, mixer, residual)
   mamba_layer_decode_graph_create  one decode token through n_layers blocks as one CUDA graph
   mamba_selective_scan_prefill_noalloc  the scan prefill with a static scratch
@@ -37,6 +41,8 @@ from ._binding import (  # noqa: F401
     MAMBA_FAULT_GEMM_WAIT,
     MAMBA_MAX_FUSED_D_CONV,
     MAMBA_NOALLOC_SCRATCH_BYTES,
+    MAMBA_NORM_L2,
+    MAMBA_ROTARY_INTERLEAVED,
     MAMBA_OK,
     MambaError,
     load,
@@ -46,6 +52,10 @@ from ._binding import (  # noqa: F401
     mamba_conv1d_silu_prefill,
     mamba_conv1d_silu_step,
     mamba_device_faults,
+    mamba_gated_delta_prefill,
+    mamba_gated_delta_step_batched,
+    mamba_gated_delta_workspace_bytes,
+    mamba_head_norm_gated,
     mamba_last_error,
     mamba_layer_prefill,
     mamba_layer_step,
@@ -56,6 +66,7 @@ from ._binding import (  # noqa: F401
     LAYER_WEIGHTS,
     mamba_mixer_prefill,
     mamba_mixer_step_batched,
+    mamba_qk_norm_rotary,
     mamba_selective_scan_prefill,
     mamba_selective_scan_prefill_noalloc,
     mamba_selective_scan_workspace_bytes,

@@ -43,6 +43,11 @@ ABI_SYMBOLS = (
     "mamba3_decode_graph_create",
     "mamba_linear_bf16",
     "mamba_rmsnorm",
+    "mamba_gated_delta_prefill",
+    "mamba_gated_delta_workspace_bytes",
+    "mamba_gated_delta_step_batched",
+    "mamba_qk_norm_rotary",
+    "mamba_head_norm_gated",
     "mamba_layer_workspace_bytes",
     "mamba_layer_prefill",
     "mamba_layer_step",
@@ -120,6 +125,20 @@ def load(path: str | None = None):
         lib.mamba_linear_bf16.restype = ctypes.c_int
         lib.mamba_rmsnorm.argtypes = [vp, i64, i32, vp, i64, vp, ctypes.c_float, i64, i64, vp]
         lib.mamba_rmsnorm.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.mamba_gated_delta_prefill.argtypes = ([vp, i64, i32] + [vp, i64] * 5 + [i32, vp, vp, f32, vp, vp]
+                                                  + [i64] * 6 + [vp, i64, vp])
+        lib.mamba_gated_delta_prefill.restype = ctypes.c_int
+        lib.mamba_gated_delta_workspace_bytes.argtypes = [i64] * 6 + [i32]
+        lib.mamba_gated_delta_workspace_bytes.restype = i64
+        lib.mamba_gated_delta_step_batched.argtypes = ([vp, i64, i32] + [vp, i64] * 5 + [i32, vp, vp, f32, vp]
+                                                       + [i64] * 7 + [vp])
+        lib.mamba_gated_delta_step_batched.restype = ctypes.c_int
+        lib.mamba_qk_norm_rotary.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp, i64, vp, f32,
+                                             i32] + [i64] * 5 + [vp]
+        lib.mamba_qk_norm_rotary.restype = ctypes.c_int
+        lib.mamba_head_norm_gated.argtypes = [vp, i64, i32, vp, i64, vp, i64, i32, vp, f32, i64, i64, i64, vp]
+        lib.mamba_head_norm_gated.restype = ctypes.c_int
         lp = ctypes.POINTER(_MambaLayer)
         lib.mamba_layer_workspace_bytes.argtypes = [lp, i64, i64]
         lib.mamba_layer_workspace_bytes.restype = i64
@@ -592,6 +611,154 @@ def mamba_rmsnorm(out, x, weight, eps=1e-5, *, stream=None):
         raise ValueError(f"out must be [M, D] = {(M, Dm)}, got {tuple(out.shape)}")
     _check(load().mamba_rmsnorm(_ptr(out), _rows2d(out, "out"), _dtype_code(out), _ptr(x), _rows2d(x, "x"),
                                 _ptr(weight), float(eps), M, Dm, _stream(stream, x)))
+
+
+MAMBA_NORM_L2 = 1
+MAMBA_ROTARY_INTERLEAVED = 2
+
+
+def _heads_ld(t, name, lead, H, d, dtype=None):
+    """Row stride of a [*lead, H, d] tensor (H * d dense columns per row, rows
+    (b*T + t)*ld apart); d is None for a [*lead, H] tensor."""
+    shape = (*lead, H) if d is None else (*lead, H, d)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    st, cols = t.stride(), H if d is None else H * d
+    n = len(lead)
+    if d is not None and ((d > 1 and st[-1] != 1) or (H > 1 and st[n] != d)) or d is None and H > 1 and st[n] != 1:
+        raise ValueError(f"{name}: heads must be dense inside a row, got strides {st}")
+    if n == 1:
+        return st[0] if lead[0] > 1 else cols
+    Bsz, T = lead
+    if T > 1:
+        if Bsz > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name}: batch stride {st[0]} != T * row stride {T * st[1]}")
+        return st[1]
+    return st[0] if Bsz > 1 else cols
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead):
+    """Shapes, dtypes and strides of a gated-delta call, checked before any
+    launch.  Returns (Hk, Hv, dk, dv, the activations' C arguments, the rest)."""
+    n = len(lead)
+    if q.dim() != n + 2 or v.dim() != n + 2:
+        raise ValueError(f"q and v must have {n + 2} dimensions, got {tuple(q.shape)} and {tuple(v.shape)}")
+    (Hk, dk), (Hv, dv) = q.shape[n:], v.shape[n:]
+    dt = v.dtype
+    acts = []
+    for name, t, H, d in (("q", q, Hk, dk), ("k", k, Hk, dk), ("v", v, Hv, dv), ("a", a, Hv, None),
+                          ("b", b, Hv, None)):
+        acts += [_ptr(t), _heads_ld(t, name, lead, H, d, dt)]
+    ld_y = _heads_ld(y, "y", lead, Hv, dv)
+    _f32_param(A_log, "A_log", (Hv,))
+    _f32_param(dt_bias, "dt_bias", (Hv,))
+    _same_device(v, y=y, q=q, k=k, a=a, b=b, A_log=A_log, dt_bias=dt_bias)
+    s = float(dk) ** -0.5 if scale is None else float(scale)
+    return Hk, Hv, dk, dv, [_ptr(y), ld_y, _dtype_code(y), *acts, _dtype_code(v), _ptr(A_log), _ptr(dt_bias), s]
+
+
+def mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, dtype_code=MAMBA_BF16) -> int:
+    """Workspace bytes of a gated-delta prefill on the current device (0: none)."""
+    n = load().mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, dtype_code)
+    if n < 0:
+        raise MambaError(int(n), mamba_last_error())
+    return int(n)
+
+
+def mamba_gated_delta_prefill(y, q, k, v, a, b, A_log, dt_bias=None, state_in=None, state_out=None, *,
+                              scale=None, workspace=None, stream=None):
+    """The gated delta rule over T tokens, from state_in (None: zeros) to state_out.
+
+    q, k: [B, T, Hk, dk]; v, y: [B, T, Hv, dv]; a, b: [B, T, Hv] (the decay's
+    and beta's pre-activations); A_log, dt_bias: [Hv] f32; states
+    [B, Hv, dv, dk] f32 (state_out may be state_in).  scale: dk ** -0.5 if None.
+    workspace: a uint8 scratch tensor (default: one kept per stream)."""
+    lead = tuple(v.shape[:2])
+    Hk, Hv, dk, dv, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead)
+    Bsz, T = lead
+    for name, s in (("state_in", state_in), ("state_out", state_out)):
+        _f32_param(s, name, (Bsz, Hv, dv, dk))
+    _same_device(v, state_in=state_in, state_out=state_out, workspace=workspace)
+    st = _stream(stream, v)
+    if workspace is None:
+        need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, _dtype_code(v)) if Hk and Hv else 0
+        workspace = _workspace(v.device, need, st) if need else None
+    ws, nbytes = (_ptr(workspace), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
+    _check(load().mamba_gated_delta_prefill(*args, _ptr(state_in), _ptr(state_out), Bsz, T, Hk, Hv, dk, dv, ws,
+                                            nbytes, st))
+
+
+def mamba_gated_delta_step_batched(y, q, k, v, a, b, A_log, dt_bias, state, layer, *, scale=None, stream=None):
+    """One T=1 step of the gated delta rule in place on slab `layer` of state
+    [n_layers, B, Hv, dv, dk]; q, k: [B, Hk, dk]; v, y: [B, Hv, dv]; a, b: [B, Hv]
+    (row-strided views allowed)."""
+    lead = tuple(v.shape[:1])
+    Hk, Hv, dk, dv, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead)
+    if state.dim() != 5:
+        raise ValueError("state must be a [n_layers, B, Hv, dv, dk] tensor")
+    _f32_param(state, "state", (state.shape[0], lead[0], Hv, dv, dk))
+    _same_device(v, state=state)
+    _check(load().mamba_gated_delta_step_batched(*args, _ptr(state), int(layer), state.shape[0], lead[0], Hk, Hv, dk,
+                                                 dv, _stream(stream, v)))
+
+
+def mamba_qk_norm_rotary(q_out, k_out, q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, *,
+                         eps=1e-6, l2=False, interleaved=False, stream=None):
+    """Per-head norms of q [B, T, Hq, d] and k [B, T, Hk, d] (k and k_out may be
+    None) with the position rotation of the first 2 len(inv_freq) components.
+
+    RMS norms with weights [d] f32 (None: ones), or L2 norms; positions: int64
+    [B, T] (None: 0..T-1 in every row).  q_out, k_out may be q and k."""
+    import torch
+
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out must be given together")
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be 4-D [B, T, heads, d] tensors")
+    Bsz, T, Hq, d = q.shape
+    Hk = k.shape[2] if k is not None else 0
+    lead = (Bsz, T)
+    args = [_ptr(q_out), _heads_ld(q_out, "q_out", lead, Hq, d)]
+    args += [_ptr(k_out), _heads_ld(k_out, "k_out", lead, Hk, d, q_out.dtype)] if k is not None else [None, 0]
+    args += [_dtype_code(q_out), _ptr(q), _heads_ld(q, "q", lead, Hq, d)]
+    args += [_ptr(k), _heads_ld(k, "k", lead, Hk, d, q.dtype)] if k is not None else [None, 0]
+    _f32_param(q_weight, "q_weight", (d,))
+    _f32_param(k_weight, "k_weight", (d,))
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D tensor [rot / 2]")
+    _f32_param(inv_freq, "inv_freq")
+    rot = 2 * inv_freq.shape[0] if inv_freq is not None else 0
+    if positions is not None and (positions.dtype != torch.int64 or tuple(positions.shape) != lead
+                                  or not positions.is_contiguous()):
+        raise ValueError(f"positions must be a contiguous int64 {lead} tensor")
+    _same_device(q, q_out=q_out, k_out=k_out, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
+                 positions=positions)
+    flags = (MAMBA_NORM_L2 if l2 else 0) | (MAMBA_ROTARY_INTERLEAVED if interleaved else 0)
+    _check(load().mamba_qk_norm_rotary(*args, _dtype_code(q), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), rot,
+                                       _ptr(positions), float(eps), flags, Bsz, T, Hq, Hk, d, _stream(stream, q)))
+
+
+def mamba_head_norm_gated(out, y, z=None, weight=None, *, eps=1e-5, stream=None):
+    """out = y / sqrt(mean(y^2) + eps) * weight * SiLU(z) per head of d; out, y, z:
+    [B, T, H, d] (z may be None, out may be y), weight [d] f32 or None."""
+    if y.dim() != 4:
+        raise ValueError(f"y must be a 4-D [B, T, H, d] tensor, got {tuple(y.shape)}")
+    Bsz, T, H, d = y.shape
+    lead = (Bsz, T)
+    ld_z = _heads_ld(z, "z", lead, H, d, y.dtype) if z is not None else 0
+    _f32_param(weight, "weight", (d,))
+    _same_device(y, out=out, z=z, weight=weight)
+    _check(load().mamba_head_norm_gated(_ptr(out), _heads_ld(out, "out", lead, H, d), _dtype_code(out), _ptr(y),
+                                        _heads_ld(y, "y", lead, H, d), _ptr(z), ld_z, _dtype_code(y), _ptr(weight),
+                                        float(eps), Bsz * T, H, d, _stream(stream, y)))
 
 
 LAYER_WEIGHTS = ("norm_w", "in_proj_w", "conv_w", "conv_b", "x_proj_w", "dt_proj_w", "dt_bias", "A_log", "D",

@@ -112,6 +112,65 @@ int check_overlaps(const Range* outs, int n_out, const Range* ins, int n_in) {
   return MAMBA_OK;
 }
 
+// Row-strided views: rows of `cols` elements, `ld` apart.  Two views whose rows
+// interleave in one buffer (columns of a packed projection) span the same bytes
+// without sharing any.
+struct View {
+  const char* name;
+  const void* p;
+  int64_t rows, cols, ld;
+  int es;
+  int64_t bytes;  // set by view_of
+};
+
+int view_of(View* v) {
+  if (!v->p || v->rows <= 0 || v->cols <= 0) {
+    v->bytes = 0;
+    return MAMBA_OK;
+  }
+  if (v->ld < v->cols)
+    return fail(MAMBA_ERR_INVALID_ARG, "%s: row stride %lld is smaller than its row of %lld", v->name,
+                (long long)v->ld, (long long)v->cols);
+  if (!span_bytes(v->rows, v->cols, v->ld, v->es, &v->bytes))
+    return fail(MAMBA_ERR_INVALID_ARG, "%s: extent overflow", v->name);
+  if (reinterpret_cast<uintptr_t>(v->p) % v->es)
+    return fail(MAMBA_ERR_INVALID_ARG, "%s is not aligned to its elements", v->name);
+  return MAMBA_OK;
+}
+
+bool views_overlap(const View& a, const View& b) {
+  if (!overlaps(range_of(a.name, a.p, a.bytes), range_of(b.name, b.p, b.bytes))) return false;
+  const int64_t pa = a.ld * a.es, pb = b.ld * b.es;
+  if (pa != pb || a.rows < 2 || b.rows < 2) return true;
+  // rows repeat every pa bytes in both: they are disjoint if their columns are
+  const uintptr_t ua = reinterpret_cast<uintptr_t>(a.p), ub = reinterpret_cast<uintptr_t>(b.p);
+  const int64_t d = ub >= ua ? (int64_t)((ub - ua) % (uintptr_t)pa) : pa - (int64_t)((ua - ub) % (uintptr_t)pa);
+  const int64_t off = d % pa;  // b's first column after a's, in [0, pa)
+  return off < a.cols * a.es || off + b.cols * b.es > pa;
+}
+
+// outs must not share bytes with each other or with ins; ins[i] that is the
+// very view outs[i] (same pointer, stride and type) is an update in place
+int check_views(View* outs, int n_out, View* ins, int n_in, bool in_place) {
+  int rc;
+  for (int i = 0; i < n_out; ++i)
+    if ((rc = view_of(&outs[i]))) return rc;
+  for (int i = 0; i < n_in; ++i)
+    if ((rc = view_of(&ins[i]))) return rc;
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j) {
+      const bool same = in_place && i == j && outs[i].p == ins[j].p && outs[i].es == ins[j].es &&
+                        (outs[i].ld == ins[j].ld || outs[i].rows == 1);
+      if (!same && views_overlap(outs[i], ins[j]))
+        return fail(MAMBA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, ins[j].name);
+    }
+    for (int j = i + 1; j < n_out; ++j)
+      if (views_overlap(outs[i], outs[j]))
+        return fail(MAMBA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+  }
+  return MAMBA_OK;
+}
+
 // the kernels dereference these: they must be memory this device can reach
 int check_pointer(const char* name, const void* p, int dev) {
   if (!p) return MAMBA_OK;
@@ -137,6 +196,15 @@ int check_pointers(const Range* rs, int n, int dev) {
   return MAMBA_OK;
 }
 
+int check_view_pointers(const View* vs, int n, int dev) {
+  for (int i = 0; i < n; ++i) {
+    if (vs[i].bytes == 0) continue;
+    int rc = check_pointer(vs[i].name, vs[i].p, dev);
+    if (rc) return rc;
+  }
+  return MAMBA_OK;
+}
+
 int check_dtype(const char* name, int dt) {
   if (dt != MAMBA_F32 && dt != MAMBA_BF16)
     return fail(MAMBA_ERR_INVALID_ARG, "%s: unknown dtype %d (expected MAMBA_F32=0 or MAMBA_BF16=1)", name, dt);
@@ -149,6 +217,55 @@ int es_of(int dt) { return dt == MAMBA_BF16 ? 2 : 4; }
 bool sizes_ok(int64_t a, int64_t b, int64_t c = 1) {
   if (a > kMaxExtent || b > kMaxExtent || c > kMaxExtent) return false;
   return (__int128)a * b * c <= (__int128)kMaxExtent;
+}
+
+// ---- the gated delta rule ------------------------------------------------------
+// Checks what the prefill and the step share (everything but the states) and
+// fills the launch arguments.  n_rows = B T.
+int gated_delta_args(mamba::GatedDeltaArgs* g, int in_dtype, int y_dtype, View* extra_out, int n_extra_out,
+                     View* extra_in, int n_extra_in) {
+  int rc;
+  if ((rc = check_dtype("in_dtype", in_dtype)) || (rc = check_dtype("y_dtype", y_dtype))) return rc;
+  const int64_t rows = g->B * g->T;
+  if (rows > 0 && (!g->y || !g->q || !g->k || !g->v || !g->a || !g->b || !g->A_log))
+    return fail(MAMBA_ERR_INVALID_ARG, "y, q, k, v, a, b and A_log must not be NULL");
+  if (!(g->scale == g->scale) || g->scale - g->scale != 0.0f)
+    return fail(MAMBA_ERR_INVALID_ARG, "scale must be finite");
+  const int es = es_of(in_dtype);
+  const int64_t kc = (int64_t)g->Hk * g->dk, vc = (int64_t)g->Hv * g->dv;
+  View ins[12] = {{"q", g->q, rows, kc, g->ld_q, es, 0},
+                  {"k", g->k, rows, kc, g->ld_k, es, 0},
+                  {"v", g->v, rows, vc, g->ld_v, es, 0},
+                  {"a", g->a, rows, g->Hv, g->ld_a, es, 0},
+                  {"b", g->b, rows, g->Hv, g->ld_b, es, 0},
+                  {"A_log", g->A_log, 1, g->Hv, g->Hv, 4, 0},
+                  {"dt_bias", g->dt_bias, 1, g->Hv, g->Hv, 4, 0}};
+  View outs[4] = {{"y", g->y, rows, vc, g->ld_y, es_of(y_dtype), 0}};
+  int n_in = 7, n_out = 1;
+  for (int i = 0; i < n_extra_in; ++i) ins[n_in++] = extra_in[i];
+  for (int i = 0; i < n_extra_out; ++i) outs[n_out++] = extra_out[i];
+  if ((rc = check_views(outs, n_out, ins, n_in, false))) return rc;
+  int dev_id = 0;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, n_in, dev_id)) || (rc = check_view_pointers(outs, n_out, dev_id))) return rc;
+  g->in_bf16 = in_dtype == MAMBA_BF16;
+  g->y_bf16 = y_dtype == MAMBA_BF16;
+  return MAMBA_OK;
+}
+
+int gated_delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv) {
+  if (B < 0 || T < 0) return fail(MAMBA_ERR_INVALID_ARG, "negative size (B=%lld T=%lld)", (long long)B, (long long)T);
+  if (Hk < 1 || Hv < 1 || Hv % Hk)
+    return fail(MAMBA_ERR_INVALID_ARG, "Hv=%lld must be a positive multiple of Hk=%lld", (long long)Hv, (long long)Hk);
+  if (dk < 1 || dk > MAMBA_GDR_MAX_DK || dv < 1 || dv > MAMBA_GDR_MAX_DV)
+    return fail(MAMBA_ERR_UNSUPPORTED, "dk=%lld not in 1..%d or dv=%lld not in 1..%d", (long long)dk,
+                MAMBA_GDR_MAX_DK, (long long)dv, MAMBA_GDR_MAX_DV);
+  if (Hv > 65536 || !sizes_ok(B, T) || !sizes_ok(B * T, Hv * dv) || !sizes_ok(B * T, Hk * dk) ||
+      !sizes_ok(B, Hv * dv, dk) || !sizes_ok(B, Hv, (dv + 15) / 16) || B * Hv * ((dv + 15) / 16) > INT32_MAX)
+    return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  return MAMBA_OK;
 }
 
 bool valid_n(int64_t n) {
@@ -792,6 +909,141 @@ int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const float* x, int6
   mamba::RmsNormArgs a{out, ld_out, out_dtype == MAMBA_BF16, x, ld_x, weight, eps, M, D};
   cudaError_t e = mamba::launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("rmsnorm launch", e);
+  return ok();
+}
+
+int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, const void* q, int64_t ld_q, const void* k,
+                              int64_t ld_k, const void* v, int64_t ld_v, const void* a, int64_t ld_a, const void* b,
+                              int64_t ld_b, int in_dtype, const float* A_log, const float* dt_bias, float scale,
+                              const float* state_in, float* state_out, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
+                              int64_t dk, int64_t dv, void* workspace, int64_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = gated_delta_sizes(B, T, Hk, Hv, dk, dv))) return rc;
+  if (workspace_bytes < 0) return fail(MAMBA_ERR_INVALID_ARG, "negative workspace_bytes");
+  if (B == 0) return ok();
+  const int64_t ns = Hv * dv * dk;
+  mamba::GatedDeltaArgs g{y,  ld_y, 0,       q,     ld_q,     k,         ld_k, v, ld_v,    a,       ld_a,    b,      ld_b,
+                          0,  A_log, dt_bias, scale, state_in, state_out, B,    T, (int)Hk, (int)Hv, (int)dk, (int)dv};
+  // the state may be updated in place
+  View so{"state_out", state_out, B, ns, ns, 4, 0}, si{"state_in", state_in, B, ns, ns, 4, 0};
+  View ws{"workspace", workspace, 1, workspace_bytes, workspace_bytes, 1, 0};
+  View outs[2] = {so, ws};
+  if ((rc = gated_delta_args(&g, in_dtype, y_dtype, outs, 2, &si, state_in == state_out ? 0 : 1))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return copy_state(state_out, state_in, B * ns, s);
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  const cudaError_t e = mamba::launch_gated_delta_recurrent(g, dev, s);
+  if (e != cudaSuccess) return cuda_fail("gated_delta_prefill launch", e);
+  return ok();
+}
+
+int64_t mamba_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                          int in_dtype) {
+  int rc;
+  if ((rc = gated_delta_sizes(B, T, Hk, Hv, dk, dv)) || (rc = check_dtype("in_dtype", in_dtype))) return rc;
+  ok();
+  return 0;
+}
+
+int mamba_gated_delta_step_batched(void* y, int64_t ld_y, int y_dtype, const void* q, int64_t ld_q, const void* k,
+                                   int64_t ld_k, const void* v, int64_t ld_v, const void* a, int64_t ld_a,
+                                   const void* b, int64_t ld_b, int in_dtype, const float* A_log,
+                                   const float* dt_bias, float scale, float* state, int64_t layer, int64_t n_layers,
+                                   int64_t B, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, void* stream) {
+  int rc;
+  if ((rc = gated_delta_sizes(B, 1, Hk, Hv, dk, dv))) return rc;
+  if (layer < 0 || layer >= n_layers)
+    return fail(MAMBA_ERR_INVALID_ARG, "layer=%lld outside [0, %lld)", (long long)layer, (long long)n_layers);
+  if (B == 0) return ok();
+  const int64_t ns = Hv * dv * dk;
+  if (!sizes_ok(n_layers, B * ns)) return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if (!state) return fail(MAMBA_ERR_INVALID_ARG, "state must not be NULL");
+  float* slab = state + layer * B * ns;
+  mamba::GatedDeltaArgs g{y, ld_y,  0,       q,     ld_q, k,    ld_k, v, ld_v,    a,       ld_a,    b,      ld_b,
+                          0, A_log, dt_bias, scale, slab, slab, B,    1, (int)Hk, (int)Hv, (int)dk, (int)dv};
+  View so{"state", slab, B, ns, ns, 4, 0};
+  if ((rc = gated_delta_args(&g, in_dtype, y_dtype, &so, 1, nullptr, 0))) return rc;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  const cudaError_t e = mamba::launch_gated_delta_recurrent(g, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("gated_delta_step_batched launch", e);
+  return ok();
+}
+
+int mamba_qk_norm_rotary(void* q_out, int64_t ld_qo, void* k_out, int64_t ld_ko, int out_dtype, const void* q,
+                         int64_t ld_q, const void* k, int64_t ld_k, int in_dtype, const float* q_weight,
+                         const float* k_weight, const float* inv_freq, int64_t rot_dim, const int64_t* positions,
+                         float eps, int flags, int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t d,
+                         void* stream) {
+  int rc;
+  if ((rc = check_dtype("in_dtype", in_dtype)) || (rc = check_dtype("out_dtype", out_dtype))) return rc;
+  if (B < 0 || T < 0 || Hq < 0 || Hk < 0)
+    return fail(MAMBA_ERR_INVALID_ARG, "negative size (B=%lld T=%lld Hq=%lld Hk=%lld)", (long long)B, (long long)T,
+                (long long)Hq, (long long)Hk);
+  if (d < 1 || d > MAMBA_HEAD_NORM_MAX_D)
+    return fail(MAMBA_ERR_UNSUPPORTED, "d=%lld not in 1..%d", (long long)d, MAMBA_HEAD_NORM_MAX_D);
+  if (rot_dim < 0 || rot_dim > d || rot_dim % 2)
+    return fail(MAMBA_ERR_INVALID_ARG, "rot_dim=%lld must be even and in 0..d", (long long)rot_dim);
+  if (flags & ~(MAMBA_NORM_L2 | MAMBA_ROTARY_INTERLEAVED))
+    return fail(MAMBA_ERR_INVALID_ARG, "unknown flags %d", flags);
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(MAMBA_ERR_INVALID_ARG, "eps must be in [0, 1]");
+  if (B == 0 || T == 0 || Hq + Hk == 0) return ok();
+  if (Hq > 65536 || Hk > 65536 || !sizes_ok(B, T) || !sizes_ok(B * T, (Hq + Hk) * d) ||
+      B * T * (Hq + Hk) > (int64_t)INT32_MAX * 4)
+    return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if ((Hq && (!q || !q_out)) || (Hk && (!k || !k_out)) || (rot_dim && !inv_freq))
+    return fail(MAMBA_ERR_INVALID_ARG, "q, q_out (Hq > 0), k, k_out (Hk > 0) and inv_freq (rot_dim > 0) must not be NULL");
+  const int64_t rows = B * T;
+  const int ei = es_of(in_dtype), eo = es_of(out_dtype);
+  View outs[2] = {{"q_out", Hq ? q_out : nullptr, rows, Hq * d, ld_qo, eo, 0},
+                  {"k_out", Hk ? k_out : nullptr, rows, Hk * d, ld_ko, eo, 0}};
+  View ins[6] = {{"q", Hq ? q : nullptr, rows, Hq * d, ld_q, ei, 0},
+                 {"k", Hk ? k : nullptr, rows, Hk * d, ld_k, ei, 0},
+                 {"q_weight", q_weight, 1, d, d, 4, 0},
+                 {"k_weight", k_weight, 1, d, d, 4, 0},
+                 {"inv_freq", rot_dim ? inv_freq : nullptr, 1, rot_dim / 2, rot_dim / 2, 4, 0},
+                 {"positions", rot_dim ? positions : nullptr, 1, rows, rows, 8, 0}};
+  if ((rc = check_views(outs, 2, ins, 6, true))) return rc;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, 6, dev_id)) || (rc = check_view_pointers(outs, 2, dev_id))) return rc;
+  mamba::QkNormArgs g{q_out, ld_qo, k_out, ld_ko, out_dtype == MAMBA_BF16, q, ld_q, k, ld_k, in_dtype == MAMBA_BF16,
+                      q_weight, k_weight, inv_freq, positions, (int)rot_dim, eps, (flags & MAMBA_NORM_L2) != 0,
+                      (flags & MAMBA_ROTARY_INTERLEAVED) != 0, B, T, (int)Hq, (int)Hk, (int)d};
+  const cudaError_t e = mamba::launch_qk_norm_rotary(g, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("qk_norm_rotary launch", e);
+  return ok();
+}
+
+int mamba_head_norm_gated(void* out, int64_t ld_out, int out_dtype, const void* y, int64_t ld_y, const void* z,
+                          int64_t ld_z, int in_dtype, const float* weight, float eps, int64_t rows, int64_t H,
+                          int64_t d, void* stream) {
+  int rc;
+  if ((rc = check_dtype("in_dtype", in_dtype)) || (rc = check_dtype("out_dtype", out_dtype))) return rc;
+  if (rows < 0 || H < 0 || d < 0)
+    return fail(MAMBA_ERR_INVALID_ARG, "negative size (rows=%lld H=%lld d=%lld)", (long long)rows, (long long)H,
+                (long long)d);
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(MAMBA_ERR_INVALID_ARG, "eps must be in [0, 1]");
+  if (rows == 0 || H == 0 || d == 0) return ok();
+  if (H > INT32_MAX || d > INT32_MAX || !sizes_ok(rows, H, d) || rows * H > (int64_t)INT32_MAX * 4)
+    return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if (!out || !y) return fail(MAMBA_ERR_INVALID_ARG, "out and y must not be NULL");
+  const int ei = es_of(in_dtype), eo = es_of(out_dtype);
+  View outs[1] = {{"out", out, rows, H * d, ld_out, eo, 0}};
+  View ins[3] = {{"y", y, rows, H * d, ld_y, ei, 0}, {"z", z, rows, H * d, ld_z, ei, 0}, {"weight", weight, 1, d, d, 4, 0}};
+  if ((rc = check_views(outs, 1, ins, 3, true))) return rc;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, 3, dev_id)) || (rc = check_view_pointers(outs, 1, dev_id))) return rc;
+  mamba::HeadNormArgs g{out, ld_out, out_dtype == MAMBA_BF16, y, ld_y, z, ld_z, in_dtype == MAMBA_BF16, weight, eps,
+                        rows, (int)H, (int)d};
+  const cudaError_t e = mamba::launch_head_norm_gated(g, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("head_norm_gated launch", e);
   return ok();
 }
 

@@ -1,0 +1,416 @@
+// head_norm.cu - per-head norms around a recurrent layer's state update:
+//
+//   qk_norm_rotary   x / sqrt(mean x^2 + eps) w  (or x / sqrt(sum x^2 + eps) w)
+//                    for every head of q and k, then the pairs of its first
+//                    rot components turned by theta_i = position inv_freq_i
+//   head_norm_gated  y / sqrt(mean y^2 + eps) w SiLU(z) for every head of y
+//
+// Bound: HBM (each value read once and written once).  A group of G = d / 8
+// lanes (8, 16 or 32) holds a head, 8 values per lane (16-byte accesses), so
+// the sum is a butterfly and the rotation's partner sits in the same lane
+// (interleaved pairs) or in one other lane (halves).  A group keeps its
+// token's cosines and sines in registers and goes over heads with them.
+//
+// Angles: position inv_freq loses its low bits in f32 (at position 10^6 the
+// product's rounding is 0.03 rad), so the lane holds inv_freq as a 64-bit
+// fraction of a turn and multiplies in integers: whole turns overflow out of
+// the word exactly, for either sign, and its high half is the angle to 2^-32
+// turns.  The table entry's own error is 2^-53 turns times the position.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "device_math.cuh"
+#include "launch.h"
+
+namespace mamba {
+namespace {
+
+constexpr int kThreads = 256;
+
+// inv_freq (radians per position) as a 2^-64 fraction of a turn; whole turns
+// per position do not matter, positions being integers
+__device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
+  double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+  t -= rint(t);                                          // in [-1/2, 1/2]
+  return (uint64_t)__double2ll_rn(t * 9223372036854775808.0) << 1;
+}
+
+__device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turns) {
+  const int32_t hi = (int32_t)(((uint64_t)position * turns) >> 32);  // signed: [-1/2, 1/2) turn
+  float s, c;
+  sincospif((float)hi * 4.656612873077393e-10f, &s, &c);  // 2^-31: half-turns
+  return make_float2(c, s);
+}
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 raw;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// One group of G lanes: one token, heads [h0, h0 + per_group) of the Hq + Hk.
+// kHeads heads' loads are in flight together.  The weights of the lane's 8
+// components are re-read per head (L1) rather than held for both q and k.
+template <typename IN, typename OUT, int G, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs g, int per_group, int slices) {
+  grid_dependency_begin();
+  constexpr int kHeads = 4;
+  constexpr int kGroups = kThreads / G;
+  const int lane = threadIdx.x % G;
+  const int64_t unit = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+  const int64_t rows = g.B * g.T;
+  const int64_t row_raw = unit / slices;
+  const bool live = row_raw < rows;
+  const int64_t row = live ? row_raw : rows - 1;  // idle groups stay for the shuffles
+  const int heads = g.Hq + g.Hk;
+  const int h0 = (int)(unit % slices) * per_group;
+  const int h1 = h0 + per_group < heads ? h0 + per_group : heads;
+  const int c = 8 * lane;
+  const bool in = c < g.d;  // d % 8 == 0
+
+  // this token's turns for the lane's components
+  const bool turned = c < g.rot;
+  const int half = g.rot / 2;
+  float cs[8], sn[8];
+  int partner = threadIdx.x % 32;
+  if (g.rot > 0) {
+    if (INTERLEAVED) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 a = make_float2(1.0f, 0.0f);
+        if (turned) a = cos_sin(g.positions ? g.positions[row] : row % g.T, turns_per_position(g.inv_freq[c / 2 + i]));
+        cs[i] = a.x, sn[i] = a.y;
+      }
+    } else {
+      const bool low = c < half;
+      if (turned) partner += low ? half / 8 : -(half / 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 a = make_float2(1.0f, 0.0f);
+        if (turned)
+          a = cos_sin(g.positions ? g.positions[row] : row % g.T,
+                      turns_per_position(g.inv_freq[(low ? c : c - half) + i]));
+        cs[i] = a.x, sn[i] = low ? -a.y : a.y;  // x cos - y sin below, y cos + x sin above
+      }
+    }
+  }
+
+  for (int h = h0; h < h1; h += kHeads) {
+    Vec8<IN> raw[kHeads];
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int hh = h + j < h1 ? h + j : h1 - 1;
+      const IN* p = hh < g.Hq ? reinterpret_cast<const IN*>(g.q) + row * g.ld_q + (int64_t)hh * g.d
+                              : reinterpret_cast<const IN*>(g.k) + row * g.ld_k + (int64_t)(hh - g.Hq) * g.d;
+      if (in) raw[j].load(p + c);
+    }
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      if (h + j >= h1) break;  // uniform in the group; the shuffles below stay inside it
+      float f[8];
+      if (in) {
+        raw[j].unpack(f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+      }
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+      const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << ((threadIdx.x % 32) / G * G);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+      const float inv = rsqrtf((g.l2 ? ss : ss / (float)g.d) + g.eps);
+      const bool is_q = h + j < g.Hq;
+      const float* w = is_q ? g.q_weight : g.k_weight;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= inv;
+      if (w && in) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= __ldg(w + c + i);
+      }
+      if (g.rot > 0) {
+        if (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = f[2 * i], y = f[2 * i + 1];
+            f[2 * i] = fmaf(-y, sn[i], x * cs[i]);
+            f[2 * i + 1] = fmaf(x, sn[i], y * cs[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float o = __shfl_sync(mask, f[i], partner);
+            f[i] = turned ? fmaf(o, sn[i], f[i] * cs[i]) : f[i];
+          }
+        }
+      }
+      if (in && live) {
+        OUT* p = is_q ? reinterpret_cast<OUT*>(g.q_out) + row * g.ld_qo + (int64_t)(h + j) * g.d
+                      : reinterpret_cast<OUT*>(g.k_out) + row * g.ld_ko + (int64_t)(h + j - g.Hq) * g.d;
+        store8(p + c, f);
+      }
+    }
+  }
+}
+
+constexpr int kMaxD = 256;
+constexpr int kAnyWarps = 4;
+
+// Any d <= 256, any alignment, any even rot: one warp per (token, head), the
+// head staged in shared memory for the rotation's partners.
+template <typename IN, typename OUT>
+__global__ void __launch_bounds__(32 * kAnyWarps) qk_norm_any_kernel(const QkNormArgs g) {
+  grid_dependency_begin();
+  __shared__ float stage[kAnyWarps][kMaxD];
+  const int lane = threadIdx.x % 32;
+  float* x = stage[threadIdx.x / 32];
+  const int heads = g.Hq + g.Hk;
+  const int64_t unit = (int64_t)blockIdx.x * kAnyWarps + threadIdx.x / 32;
+  if (unit >= g.B * g.T * heads) return;
+  const int64_t row = unit / heads;
+  const int h = (int)(unit % heads);
+  const bool is_q = h < g.Hq;
+  const IN* p = is_q ? reinterpret_cast<const IN*>(g.q) + row * g.ld_q + (int64_t)h * g.d
+                     : reinterpret_cast<const IN*>(g.k) + row * g.ld_k + (int64_t)(h - g.Hq) * g.d;
+  OUT* o = is_q ? reinterpret_cast<OUT*>(g.q_out) + row * g.ld_qo + (int64_t)h * g.d
+                : reinterpret_cast<OUT*>(g.k_out) + row * g.ld_ko + (int64_t)(h - g.Hq) * g.d;
+  const float* w = is_q ? g.q_weight : g.k_weight;
+  float ss = 0.0f;
+  for (int c = lane; c < g.d; c += 32) {
+    x[c] = to_f32(p[c]);
+    ss = fmaf(x[c], x[c], ss);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+  const float inv = rsqrtf((g.l2 ? ss : ss / (float)g.d) + g.eps);
+  for (int c = lane; c < g.d; c += 32) x[c] = x[c] * inv * (w ? w[c] : 1.0f);
+  __syncwarp();
+  const int64_t pos = g.positions ? g.positions[row] : row % g.T;
+  const int half = g.rot / 2;
+  for (int c = lane; c < g.d; c += 32) {
+    float v = x[c];
+    if (c < g.rot) {
+      const int pair = g.interleaved ? c / 2 : c % half;
+      const bool low = g.interleaved ? c % 2 == 0 : c < half;
+      const float other = x[g.interleaved ? c ^ 1 : low ? c + half : c - half];
+      const float2 a = cos_sin(pos, turns_per_position(g.inv_freq[pair]));
+      v = fmaf(other, low ? -a.y : a.y, v * a.x);
+    }
+    o[c] = from_f32<OUT>(v);
+  }
+}
+
+template <typename IN, typename OUT, int G>
+__global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadNormArgs g, int64_t units, int per_group) {
+  grid_dependency_begin();
+  constexpr int kHeads = 4;
+  constexpr int kGroups = kThreads / G;
+  const int lane = threadIdx.x % G;
+  const int c = 8 * lane;
+  const bool in = c < g.d;
+  const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << ((threadIdx.x % 32) / G * G);
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = g.weight && in ? __ldg(g.weight + c + i) : 1.0f;
+  // unit u is head u % H of token u / H; a CTA takes per_group strides of kGroups
+  const int64_t base = (int64_t)blockIdx.x * kGroups * per_group + threadIdx.x / G;
+  for (int s = 0; s < per_group; s += kHeads) {
+    Vec8<IN> ry[kHeads], rz[kHeads];
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int64_t u = base + (int64_t)(s + j) * kGroups;
+      if (s + j < per_group && u < units && in) {
+        const int64_t row = u / g.H, h = u % g.H;
+        ry[j].load(reinterpret_cast<const IN*>(g.y) + row * g.ld_y + h * g.d + c);
+        if (g.z) rz[j].load(reinterpret_cast<const IN*>(g.z) + row * g.ld_z + h * g.d + c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int64_t u = base + (int64_t)(s + j) * kGroups;
+      if (s + j >= per_group || u >= units) break;  // uniform in the group
+      float f[8];
+      if (in) {
+        ry[j].unpack(f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+      }
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+      const float inv = rsqrtf(ss / (float)g.d + g.eps);
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= inv * w[i];
+        if (g.z) {
+          float z[8];
+          rz[j].unpack(z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= silu_f(z[i]);
+        }
+        const int64_t row = u / g.H, h = u % g.H;
+        store8(reinterpret_cast<OUT*>(g.out) + row * g.ld_out + h * g.d + c, f);
+      }
+    }
+  }
+}
+
+// any d, any alignment: one warp per head, read twice (the second time from L1)
+template <typename IN, typename OUT>
+__global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const HeadNormArgs g, int64_t units) {
+  grid_dependency_begin();
+  const int lane = threadIdx.x % 32;
+  const int64_t u = (int64_t)blockIdx.x * kAnyWarps + threadIdx.x / 32;
+  if (u >= units) return;
+  const int64_t row = u / g.H, h = u % g.H;
+  const IN* y = reinterpret_cast<const IN*>(g.y) + row * g.ld_y + h * g.d;
+  const IN* z = g.z ? reinterpret_cast<const IN*>(g.z) + row * g.ld_z + h * g.d : nullptr;
+  OUT* o = reinterpret_cast<OUT*>(g.out) + row * g.ld_out + h * g.d;
+  float ss = 0.0f;
+  for (int c = lane; c < g.d; c += 32) {
+    const float v = to_f32(y[c]);
+    ss = fmaf(v, v, ss);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+  const float inv = rsqrtf(ss / (float)g.d + g.eps);
+  for (int c = lane; c < g.d; c += 32) {
+    float v = to_f32(y[c]) * (inv * (g.weight ? g.weight[c] : 1.0f));
+    if (z) v *= silu_f(to_f32(z[c]));
+    o[c] = from_f32<OUT>(v);
+  }
+}
+
+// 8-value accesses: base, row stride and head size keep every head's groups aligned
+bool vec8(const void* p, int64_t ld, int d, int es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (es == 2 ? 16 : 16) == 0 && (ld * es) % 16 == 0 && d % 8 == 0);
+}
+
+template <typename IN, typename OUT, int G>
+cudaError_t launch_qk_g(const QkNormArgs& a, int sms, cudaStream_t stream) {
+  const int heads = a.Hq + a.Hk;
+  const int64_t rows = a.B * a.T;
+  // heads per group: all of a token's heads once there are enough tokens to
+  // give every SM its threads, else fewer, so that a decode step's few tokens
+  // still spread over the SMs
+  const int64_t groups = (int64_t)sms * 1024 / G;
+  int64_t slices = rows > 0 ? (groups + rows - 1) / rows : 1;
+  if (slices > (heads + 3) / 4) slices = rows * ((heads + 3) / 4) * 2 > groups ? (heads + 3) / 4 : heads;
+  if (slices < 1) slices = 1;
+  const int per_group = (int)((heads + slices - 1) / slices);
+  slices = (heads + per_group - 1) / per_group;
+  const int64_t ctas = (rows * slices + kThreads / G - 1) / (kThreads / G);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)ctas), block(kThreads);
+  if (a.interleaved)
+    return launch_pdl(true, qk_norm_kernel<IN, OUT, G, true>, grid, block, 0, stream, a, per_group, (int)slices);
+  return launch_pdl(true, qk_norm_kernel<IN, OUT, G, false>, grid, block, 0, stream, a, per_group, (int)slices);
+}
+
+template <typename IN, typename OUT>
+cudaError_t launch_qk_t(const QkNormArgs& a, int sms, cudaStream_t stream) {
+  const int ei = sizeof(IN), eo = sizeof(OUT);
+  const bool vec = vec8(a.Hq ? a.q : nullptr, a.ld_q, a.d, ei) && vec8(a.Hk ? a.k : nullptr, a.ld_k, a.d, ei) &&
+                   vec8(a.Hq ? a.q_out : nullptr, a.ld_qo, a.d, eo) &&
+                   vec8(a.Hk ? a.k_out : nullptr, a.ld_ko, a.d, eo) && a.d % 8 == 0 &&
+                   (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0);
+  if (!vec) {
+    const int64_t ctas = (a.B * a.T * (a.Hq + a.Hk) + kAnyWarps - 1) / kAnyWarps;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(true, qk_norm_any_kernel<IN, OUT>, dim3((unsigned)ctas), dim3(32 * kAnyWarps), 0, stream, a);
+  }
+  if (a.d <= 64) return launch_qk_g<IN, OUT, 8>(a, sms, stream);
+  if (a.d <= 128) return launch_qk_g<IN, OUT, 16>(a, sms, stream);
+  return launch_qk_g<IN, OUT, 32>(a, sms, stream);
+}
+
+template <typename IN, typename OUT, int G>
+cudaError_t launch_hn_g(const HeadNormArgs& a, int sms, cudaStream_t stream) {
+  const int64_t units = a.rows * a.H;
+  constexpr int kGroups = kThreads / G;
+  // four heads per group once that still fills every SM
+  const int per_group = units >= (int64_t)sms * 4 * kGroups * 4 ? 4 : 1;
+  const int64_t ctas = (units + kGroups * per_group - 1) / (kGroups * per_group);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_pdl(true, head_norm_kernel<IN, OUT, G>, dim3((unsigned)ctas), dim3(kThreads), 0, stream, a, units,
+                    per_group);
+}
+
+template <typename IN, typename OUT>
+cudaError_t launch_hn_t(const HeadNormArgs& a, int sms, cudaStream_t stream) {
+  const int ei = sizeof(IN), eo = sizeof(OUT);
+  const bool vec = vec8(a.y, a.ld_y, a.d, ei) && vec8(a.z, a.ld_z, a.d, ei) && vec8(a.out, a.ld_out, a.d, eo) &&
+                   a.d <= kMaxD;
+  const int64_t units = a.rows * a.H;
+  if (!vec) {
+    const int64_t ctas = (units + kAnyWarps - 1) / kAnyWarps;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(true, head_norm_any_kernel<IN, OUT>, dim3((unsigned)ctas), dim3(32 * kAnyWarps), 0, stream, a,
+                      units);
+  }
+  if (a.d <= 64) return launch_hn_g<IN, OUT, 8>(a, sms, stream);
+  if (a.d <= 128) return launch_hn_g<IN, OUT, 16>(a, sms, stream);
+  return launch_hn_g<IN, OUT, 32>(a, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rotary(const QkNormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (a.B <= 0 || a.T <= 0 || a.Hq + a.Hk <= 0 || a.d <= 0) return cudaSuccess;
+  if (a.in_bf16)
+    return a.out_bf16 ? launch_qk_t<__nv_bfloat16, __nv_bfloat16>(a, dev.sm_count, stream)
+                      : launch_qk_t<__nv_bfloat16, float>(a, dev.sm_count, stream);
+  return a.out_bf16 ? launch_qk_t<float, __nv_bfloat16>(a, dev.sm_count, stream)
+                    : launch_qk_t<float, float>(a, dev.sm_count, stream);
+}
+
+cudaError_t launch_head_norm_gated(const HeadNormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (a.rows <= 0 || a.H <= 0 || a.d <= 0) return cudaSuccess;
+  if (a.in_bf16)
+    return a.out_bf16 ? launch_hn_t<__nv_bfloat16, __nv_bfloat16>(a, dev.sm_count, stream)
+                      : launch_hn_t<__nv_bfloat16, float>(a, dev.sm_count, stream);
+  return a.out_bf16 ? launch_hn_t<float, __nv_bfloat16>(a, dev.sm_count, stream)
+                    : launch_hn_t<float, float>(a, dev.sm_count, stream);
+}
+
+}  // namespace mamba

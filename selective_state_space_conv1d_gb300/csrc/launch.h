@@ -270,4 +270,76 @@ struct MixerStepArgs {
 cudaError_t launch_mixer_step_batched(const MixerStepArgs& a, const DeviceInfo& dev,
                                       cudaStream_t stream);
 
+// ---------------------------------------------------------- gated delta ----
+// The gated delta rule over B x T tokens (T = 1 in place is the decode step).
+// Row (b T + t) of each activation starts at (b T + t) ld; heads are dense
+// inside a row.  state_in / state_out: [B][Hv][dv][dk] f32.
+struct GatedDeltaArgs {
+  void* y;
+  int64_t ld_y;
+  int y_bf16;
+  const void* q;
+  int64_t ld_q;
+  const void* k;
+  int64_t ld_k;
+  const void* v;
+  int64_t ld_v;
+  const void* a;
+  int64_t ld_a;
+  const void* b;
+  int64_t ld_b;
+  int in_bf16;
+  const float* A_log;
+  const float* dt_bias;   // may be null
+  float scale;
+  const float* state_in;  // may be null
+  float* state_out;       // may be null, may equal state_in
+  int64_t B, T;
+  int Hk, Hv, dk, dv;
+};
+cudaError_t launch_gated_delta_recurrent(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// ------------------------------------------------------------ head norms ----
+// Per-head norms of q [B T][Hq][d] and k [B T][Hk][d], with the first rot
+// components turned by positions x inv_freq.
+struct QkNormArgs {
+  void* q_out;
+  int64_t ld_qo;
+  void* k_out;
+  int64_t ld_ko;
+  int out_bf16;
+  const void* q;
+  int64_t ld_q;
+  const void* k;
+  int64_t ld_k;
+  int in_bf16;
+  const float* q_weight;     // may be null
+  const float* k_weight;     // may be null
+  const float* inv_freq;     // [rot / 2]; null if rot == 0
+  const int64_t* positions;  // [B T]; null: the token's index in its sequence
+  int rot;
+  float eps;
+  int l2, interleaved;
+  int64_t B, T;
+  int Hq, Hk, d;
+};
+cudaError_t launch_qk_norm_rotary(const QkNormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// out = y / sqrt(mean(y^2) + eps) * weight * SiLU(z) per head of d
+struct HeadNormArgs {
+  void* out;
+  int64_t ld_out;
+  int out_bf16;
+  const void* y;
+  int64_t ld_y;
+  const void* z;        // may be null
+  int64_t ld_z;
+  int in_bf16;
+  const float* weight;  // may be null
+  float eps;
+  int64_t rows;
+  int H, d;
+};
+cudaError_t launch_head_norm_gated(const HeadNormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace mamba
