@@ -724,6 +724,7 @@ MAMBA_API int mamba_selective_scan_prefill_noalloc(
 #define MAMBA_FAULT_RING_WAIT 1
 #define MAMBA_FAULT_SCAN_WAIT 2 /* a prefill unit waited too long for the state it continues */
 #define MAMBA_FAULT_GEMM_WAIT 4 /* a projection GEMM waited too long for a tile or its MMAs */
+#define MAMBA_FAULT_DELTA_WAIT 8 /* a chunked gated-delta prefill waited too long for a chunk or its MMAs */
 MAMBA_API int mamba_device_faults(int clear);
 
 /*

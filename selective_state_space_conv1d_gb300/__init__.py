@@ -38,6 +38,7 @@ from ._binding import (  # noqa: F401
     MAMBA_F32,
     MAMBA_FAULT_RING_WAIT,
     MAMBA_FAULT_SCAN_WAIT,
+    MAMBA_FAULT_DELTA_WAIT,
     MAMBA_FAULT_GEMM_WAIT,
     MAMBA_MAX_FUSED_D_CONV,
     MAMBA_NOALLOC_SCRATCH_BYTES,

@@ -24,6 +24,7 @@ MAMBA_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 MAMBA_MAX_FUSED_D_CONV = 4
 MAMBA_FAULT_SCAN_WAIT = 2
 MAMBA_FAULT_GEMM_WAIT = 4
+MAMBA_FAULT_DELTA_WAIT = 8
 
 LIB_PATH = _build.LIB_PATH
 

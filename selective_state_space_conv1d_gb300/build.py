@@ -19,11 +19,11 @@ LIB_NAME = "libmamba_ssm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.cu", "conv1d.cu", "scan_prefill.cu", "ssm_step.cu", "noalloc.cu", "decode_graph.cu", "m3_step.cu",
-           "m3_prepare.cu", "selftest.cu", "gemm.cu", "rmsnorm.cu", "gated_delta_step.cu", "head_norm.cu"]
+           "m3_prepare.cu", "selftest.cu", "gemm.cu", "rmsnorm.cu", "gated_delta_chunk.cu", "gated_delta_step.cu", "head_norm.cu"]
 # scan_inst.cu is compiled once per (storage dtype, d_state): small parallel units
 SCAN_INST = [(bf16, n) for n in (1, 2, 4, 8, 16, 32, 64) for bf16 in (0, 1)]
 HEADERS = [os.path.join(CSRC, h) for h in ("async_copy.cuh", "device_math.cuh", "gated_delta.cuh", "launch.h",
-                                              "m3_math.cuh", "scan_kernel.cuh")] + [
+                                              "m3_math.cuh", "scan_kernel.cuh", "tcgen05.cuh")] + [
     os.path.join(INCLUDE, "mamba_ssm.h")
 ]
 

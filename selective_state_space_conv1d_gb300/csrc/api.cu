@@ -464,7 +464,9 @@ int mamba_device_faults(int clear) {
   if (v3 < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the Mamba-3 watchdog failed");
   const int vs = mamba::read_selftest_faults(clear != 0);
   if (vs < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the self-test watchdog failed");
-  return ok(), v | v2 | v3 | vs | vg;
+  const int vd = mamba::read_delta_faults(clear != 0);
+  if (vd < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the gated-delta watchdog failed");
+  return ok(), v | v2 | v3 | vs | vg | vd;
 }
 
 int mamba_selftest_bounded_wait(int64_t limit_cycles, int complete, void* stream) {
@@ -933,7 +935,8 @@ int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, const void* q,
   if (T == 0) return copy_state(state_out, state_in, B * ns, s);
   mamba::DeviceInfo dev;
   if ((rc = current_device(&dev))) return rc;
-  const cudaError_t e = mamba::launch_gated_delta_recurrent(g, dev, s);
+  const cudaError_t e = mamba::gated_delta_takes_chunks(g) ? mamba::launch_gated_delta_chunk(g, dev, s)
+                                                           : mamba::launch_gated_delta_recurrent(g, dev, s);
   if (e != cudaSuccess) return cuda_fail("gated_delta_prefill launch", e);
   return ok();
 }

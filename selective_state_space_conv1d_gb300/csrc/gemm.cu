@@ -47,6 +47,7 @@
 #include "async_copy.cuh"
 #include "device_math.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace mamba {
 namespace {
@@ -86,17 +87,6 @@ struct GemmSmem {
   static_assert(kStages >= 2, "shared memory too small for two stages");
   static_assert(kAlloc <= kSmemLimit, "shared memory over the opt-in limit");
 };
-
-// Shared-memory matrix descriptor of a K-major tile with 128-byte swizzle:
-// rows of 64 bf16 (128 bytes), 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  uint64_t d = (uint64_t)((addr & 0x3FFFF) >> 4);
-  d |= (uint64_t)1 << 16;              // leading byte offset (unused with this swizzle)
-  d |= (uint64_t)(1024 >> 4) << 32;    // stride byte offset: 8 rows x 128 bytes
-  d |= (uint64_t)1 << 46;              // descriptor version of sm_100 and later
-  d |= (uint64_t)2 << 61;              // 128-byte swizzle
-  return d;
-}
 
 // Instruction descriptor of kind::f16: f32 accumulator, bf16 A and B, both
 // K-major, N = BN, M = 128.
@@ -153,10 +143,6 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// generic-proxy shared-memory writes visible to the tensor memory accelerator
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // distributed shared memory: this CTA's shared address in cluster rank `rank`,
 // and a 16-byte load from there
@@ -177,37 +163,6 @@ __device__ __forceinline__ float4 dsmem_ld4(uint32_t addr) {
 __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// 32 lanes x 32 columns of f32 from tensor memory, asynchronous: the registers
-// may be read only after tmem_wait on the same array.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Waits for this thread's tensor-memory loads; the registers are threaded
-// through so that no use of them is scheduled before the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
-                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
-                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
-                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-               :
-               : "memory");
 }
 
 // One 32 x 32 block of the accumulator, held one row per lane in v, to C:

@@ -297,6 +297,10 @@ struct GatedDeltaArgs {
   int64_t B, T;
   int Hk, Hv, dk, dv;
 };
+// chunks of 64 tokens on the tensor cores (dk <= 128); the recurrent kernel takes any call
+bool gated_delta_takes_chunks(const GatedDeltaArgs& a);
+cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+int read_delta_faults(bool clear);
 cudaError_t launch_gated_delta_recurrent(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // ------------------------------------------------------------ head norms ----
