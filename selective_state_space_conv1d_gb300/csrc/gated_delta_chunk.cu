@@ -5,41 +5,52 @@
 // [dv][dk] the state before it, the chunk's corrections u_i = beta_i (v_i -
 // alpha_i S_{i-1} k_i) solve a unit lower triangular system:
 //
-//   A_ij = beta_i e^{G_i - G_j} k_i.k_j (j < i),   T = (I + A)^-1
-//   P_ij = e^{G_i - G_j} q_i.k_j (j <= i)
-//   R    = beta (V - e^G K S^T)                    [64][dv]
-//   U    = T R,   Y = scale (e^G Q S^T + (P T) R)
-//   S'   = e^{G_63} S + U^T diag(e^{G_63 - G}) K
+//   A_ij = beta_i e^{G_i - G_j} k_i.k_j (j < i),   T = (I + A)^-1 diag(beta)
+//   P_ij = e^{G_i - G_j} q_i.k_j (j <= i),         W = P T
+//   R    = V - e^G K S^T                           [64][dv]
+//   U    = diag(e^{G_63 - G}) T R,   Y = scale (e^G Q S^T + W R)
+//   S'   = e^{G_63} S + U^T K
 //
-// T and P T do not depend on the state: one back substitution X (I + A) = [I; P],
-// a thread a row, gives both while the previous chunk is still in flight.  What
-// remains on the path from state to state is three products and their epilogues,
-// all held transposed, a tensor-memory lane per value component n:
+// T and W do not depend on the state: X (I + A) = [I; P] gives both while the
+// previous chunk is still in flight, solved in blocks of 16 columns: the
+// diagonal blocks of I + A are inverted by substitution (a lane a row), the
+// products with them and with the blocks beside them are warp-level tensor-core
+// products in three TF32 terms.  (A thread a row for the whole substitution read
+// A 64 times over from shared memory, 7-8 us a chunk.)  What remains on the path
+// from state to state is three products and their epilogues, all held
+// transposed, a tensor-memory lane per value component n:
 //
-//   D1 = S [K; Q]^T   128 x 128 x dk     R^T  = D1's K half, gated  (epilogue 1)
-//   D2 = R^T [T; PT]^T  128 x 128 x 64   U^T  = D2's T half         (epilogue 2)
-//   D3 = U^T K          128 x dk x 64    S'   = e^G S + D3          (epilogue 3)
+//   D1 = S [K; Q]^T     128 x 128 x dk   R^T = V^T - D1's K half    (epilogue 1)
+//   D2 = R^T [T; W]^T   128 x 128 x 64   U^T = D2's T half          (epilogue 2)
+//   D3 = U^T K          128 x dk x 64    S'  = e^G S + D3           (epilogue 3)
 //
 // S, R^T and U^T go back to tensor memory as the A operands of the next product:
 // nothing of the chain touches shared memory, and a value component's power of
 // two scale is a number per thread.  The f32 state stays in registers.
 //
-// Precision: every operand is f16 with a power-of-two scale per row, S, R, U, T
-// and P T (and f32 inputs) as two halves hi + lo (22 bits; lo.lo products are
-// dropped), bf16 keys and queries as one (exact).  Two halves in bf16 would hold
+// Precision: every operand is f16 with power-of-two scales (per row of K, Q, S
+// and R; one for T and one for W), S, R, U, T and W (and f32 inputs) as two
+// halves hi + lo (22 bits; lo.lo products are dropped), bf16 keys and queries as
+// one (exact).  Two halves in bf16 would hold
 // 16 bits: measured in simulation 4e-6 of the state, against 2e-7 here and 1e-7
 // for plain f32.  The scales keep every operand below 2^14 whatever the inputs'
-// magnitudes: S by its largest value, R by the bound max|v| + max_i(beta_i
-// e^{G_i} |k_i|_1) max|S|, U by that times the largest row sum of |T|.
+// magnitudes: S by its largest value, R by the bound max|v| + max_i(e^{G_i}
+// |k_i|_1) max|S|, T and W by their largest row sum, which bounds U.
 //
 // One CTA per (sequence, value head, 128 value components), warps specialised:
 //   0-7   epilogues 1-3, output, the state in registers (lane = component; two
 //         warps per lane quarter, each half the columns)
-//   8-11  prepare: gates x products, back substitution, [T; PT] to shared memory
-//   12-14 load: K, Q rows to scaled f16, V by cp.async, the gates
+//   8-11  prepare: A and P from [K; Q] K^T and the gates, T and W to shared memory
+//   12-14 load: tensor copies of K, Q, V tiles, K and Q to scaled f16, the gates
 //   15    issues the MMAs
+// Every warp runs straight through its part of a chunk once, so the loop bodies
+// are kept rolled where registers allow it: with everything unrolled the code
+// was 177 KB and a chunk took 17-21 us, waiting for instructions.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/mamba_ssm.h"
@@ -59,19 +70,20 @@ constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
 __device__ int g_delta_faults = 0;
 
+constexpr int kLdA = kC + 4;      // row stride of A and P in shared memory, floats
+
 // per-chunk scalars and vectors, written by the load and prepare warps
 struct Gates {
   float col_hi[kC], col_lo[kC];          // G_j + ek_j as two floats
   float row_hi[2 * kC], row_lo[2 * kC];  // G_i - ek_i (keys), G_i - eq_i (queries)
   float beta[kC];
-  float fx[kC];    // beta_i e^{G_i} 2^{-ek_i}
+  float fx[kC];    // e^{G_i} 2^{-ek_i}
   float fd[kC];    // e^{G_63 - G_i} 2^{-ek_i}
   float fq[kC];    // scale e^{G_i} 2^{-eq_i}
-  float fu[kC];    // fd_i / T's row scale                     (prepare warps)
-  float fp[kC];    // scale / (P T)'s row scale                (prepare warps)
   float total;     // e^{G_63}
-  float k_bound;   // max_i beta_i e^{G_i} |k_i|_1 (bound)
-  float u_bound[2];  // max_i fd_i sum_j |T_ij|, one of each prepare warp
+  float k_bound;   // max_i e^{G_i} |k_i|_1 (bound)
+  int t_exp, w_exp;  // T and W are held as 2^{t_exp} T, 2^{w_exp} W   (prepare warps)
+  float sum_t[4], sum_w[4];  // largest row sums, one per prepare warp
 };
 
 template <int DK, bool F32>
@@ -81,25 +93,25 @@ struct Smem {
   static constexpr int kKqTerm = kBlocks * 16384;     // [K; Q]: 128 rows x 64 f16 per block
   static constexpr int kKq = kTerms * kKqTerm;
   static constexpr int kKqStages = F32 ? 2 : 3;
-  static constexpr int kTp = 2 * 16384;               // [T; PT] hi, lo: 128 rows x 64 f16
-  static constexpr int kTpStages = F32 ? 1 : 2;
-  static constexpr int kV = kC * kM * (F32 ? 4 : 2);
-  static constexpr int kVStages = F32 ? 1 : 2;
+  static constexpr int kTp = 2 * 16384;               // [T; W] hi, lo: 128 rows x 64 f16
+  static constexpr int kV = F32 ? 0 : kC * kM * 2;    // f32 values are read where they are used
+  static constexpr int kRaw = F32 ? 0 : 2 * kC * DK * 2;  // K and Q rows as stored (bf16)
   static constexpr int kOffTp = kKqStages * kKq;
-  static constexpr int kOffV = kOffTp + kTpStages * kTp;
-  static constexpr int kOffA = kOffV + kVStages * kV;  // A, f32 [64][64]
-  static constexpr int kOffGates = kOffA + kC * kC * 4;
+  static constexpr int kOffV = kOffTp + kTp;
+  static constexpr int kOffRaw = kOffV + kV;
+  static constexpr int kOffA = kOffRaw + kRaw;         // A and P, f32 [64][kLdA] each
+  static constexpr int kOffGates = kOffA + 2 * kC * kLdA * 4;
   static constexpr int kOffMax = kOffGates + kGateSlots * (int)sizeof(Gates);  // [2][2][128] f32
   static constexpr int kOffExp = kOffMax + 2 * 2 * kM * 4;                     // [2][128] int
   static constexpr int kOffBar = kOffExp + 2 * 2 * kC * 4;
-  static constexpr int kBars = 2 * kKqStages + 2 * kVStages + 2 * kTpStages + 2 + 7;
+  static constexpr int kBars = 2 * kKqStages + 2 + 1 + 2 + 4 + 7;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
   static_assert(kAlloc <= 232448, "shared memory over the opt-in limit");
 };
 
-// tensor memory columns
+// tensor memory columns (two D0 buffers)
 constexpr uint32_t kColX = 0, kColQ = 64, kColU = 128, kColO = 192, kColS = 256, kColD0 = 384, kTmemCols = 512;
 
 // kind::f16, f16 A and B, f32 accumulator, M = 128; b_mn: B is MN-major
@@ -140,9 +152,17 @@ __device__ __forceinline__ float pow2(int e) {
 // (a, b) as f16 pairs hi + lo
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
+  float ra, rb;  // hi - value, exact
+  asm("{\n"
+      "  .reg .f16 l, h;\n"
+      "  mov.b32 {l, h}, %2;\n"
+      "  sub.rn.f32.f16 %0, l, %3;\n"
+      "  sub.rn.f32.f16 %1, h, %4;\n"
+      "}\n"
+      : "=f"(ra), "=f"(rb)
+      : "r"(hi), "f"(a), "f"(b));
+  const __half2 l = __floats2half2_rn(-ra, -rb);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -154,43 +174,77 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 bytes global -> shared, zeros if !valid
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-// this thread's arrival on bar once its cp.async copies have landed
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Eight values of a row as f32; zeros past `valid` of them
-template <bool F32>
-__device__ __forceinline__ void load8(float (&f)[8], const void* row, int64_t at, int valid, bool vec) {
-  if (F32) {
-    const float* p = reinterpret_cast<const float*>(row) + at;
-    if (vec && valid >= 8) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < valid ? p[i] : 0.0f;
-  } else {
-    const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(row) + at;
-    if (vec && valid >= 8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < valid ? __bfloat162float(p[i]) : 0.0f;
+// A wait that did not succeed at once.  One that runs out sets the fault and
+// abort flags; every role then runs on through its loop without waiting, so
+// that all named barriers are met and the CTA ends.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (*abort_flag) return;
+  if (!mbar_wait(bar, parity, kWaitLimit)) {
+    atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+    *abort_flag = 1;
   }
 }
 
+// a box of a three-dimensional tensor map to shared memory
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// x as two TF32 terms (11 bits each; the tensor cores ignore the bits below)
+struct Tf32x2 {
+  uint32_t hi, lo;
+  __device__ __forceinline__ void set(float x) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+  }
+};
+// D[16][8] += A[16][8] B[8][8], f32 accumulators.  The 8 values of the
+// contraction are taken in the order 0 2 4 6 1 3 5 7 on both sides: then the
+// accumulator of one product is the A operand of the next as it stands.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A operand (hi, lo) from an accumulator
+__device__ __forceinline__ void tf32_operand(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&c)[4]) {
+  const float v[4] = {c[0], c[2], c[1], c[3]};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    Tf32x2 t;
+    t.set(v[i]);
+    hi[i] = t.hi, lo[i] = t.lo;
+  }
+}
+
+__device__ __forceinline__ void unpack8(float (&f)[8], uint4 a) {  // bf16
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+
+// a base-2 logarithm la log2(e) as a 2^-40 fixed-point number, la in [-200, 0]
+__device__ __forceinline__ long long log2_fixed(float la) {
+  const float p = la * 1.44269502f;                                    // log2(e) as two floats
+  const float e = fmaf(la, 1.44269502f, -p) + la * 1.92596299e-8f;
+  return __float2ll_rn(p * 1099511627776.0f) + __float2ll_rn(e * 1099511627776.0f);
+}
+// the number as two floats
+__device__ __forceinline__ float2 fixed_split(long long x) {
+  const float hi = __ll2float_rn(x);
+  const float lo = __ll2float_rn(x - __float2ll_rn(hi));
+  return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);
+}
+
 template <int DK, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, int vec_kq, int vec_v) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, const __grid_constant__ CUtensorMap map_k,
+                                                            const __grid_constant__ CUtensorMap map_q,
+                                                            const __grid_constant__ CUtensorMap map_v, int vec_kq,
+                                                            int vec_v) {
   using L = Smem<DK, F32>;
   using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
   extern __shared__ unsigned char smem_raw[];
@@ -204,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     return b;
   };
   const uint32_t kq_full = next_bars(L::kKqStages), kq_empty = next_bars(L::kKqStages);
-  const uint32_t v_full = next_bars(L::kVStages), v_empty = next_bars(L::kVStages);
-  const uint32_t tp_full = next_bars(L::kTpStages), tp_empty = next_bars(L::kTpStages);
-  const uint32_t d0_full = next_bars(1), d0_empty = next_bars(1);
+  const uint32_t v_full = next_bars(1), v_empty = next_bars(1);
+  const uint32_t raw_full = next_bars(1), tp_full = next_bars(1), tp_empty = next_bars(1);
+  const uint32_t d0_full = next_bars(2), d0_empty = next_bars(2);
   const uint32_t s_ready = next_bars(1), x_full = next_bars(1), r_ready = next_bars(1), u_full = next_bars(1),
                  u_ready = next_bars(1), o_full = next_bars(1), s_full = next_bars(1);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
@@ -224,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
-    for (int s = 0; s < L::kVStages; ++s) mbar_init(v_full + 8 * s, kLoadThreads), mbar_init(v_empty + 8 * s, 8);
-    for (int s = 0; s < L::kTpStages; ++s) mbar_init(tp_full + 8 * s, 4), mbar_init(tp_empty + 8 * s, 1);
-    mbar_init(d0_full, 1), mbar_init(d0_empty, 4);
+    mbar_init(v_full, vec_v ? 1 : kLoadThreads), mbar_init(v_empty, 8);
+    mbar_init(raw_full, 1), mbar_init(tp_full, 4), mbar_init(tp_empty, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, 4);
     mbar_init(s_ready, 8), mbar_init(x_full, 1), mbar_init(r_ready, 8), mbar_init(u_full, 1);
     mbar_init(u_ready, 8), mbar_init(o_full, 1), mbar_init(s_full, 1);
     *abort_flag = 0;
@@ -243,15 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   tcgen05_fence_after();
   const uint32_t tmem = *tmem_ptr;
 
-  // A wait that runs out sets the fault and abort flags; every role then runs
-  // on through its loop without waiting, so that all named barriers are met and
-  // the CTA ends.
   auto wait = [&](uint32_t bar, int phase) {
-    if (*abort_flag) return;
-    if (!mbar_wait(bar, (uint32_t)(phase & 1), kWaitLimit)) {
-      atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
-      *abort_flag = 1;
-    }
+    if (!mbar_try_wait(bar, (uint32_t)(phase & 1))) wait_slow(bar, (uint32_t)(phase & 1), abort_flag);
   };
 
   if (warp < 8) {
@@ -264,19 +311,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     float* max_v = reinterpret_cast<float*>(gbase + L::kOffMax);  // [half][128]
     float* max_s = max_v + 2 * kM;
+    const int64_t s_at = (bh * g.dv + n) * g.dk + half * HK;
+    const bool vec_s = g.dk % 4 == 0 && ((reinterpret_cast<uintptr_t>(g.state_in) | reinterpret_cast<uintptr_t>(g.state_out)) & 15) == 0;
     float s[HK];
 #pragma unroll
-    for (int j = 0; j < HK; ++j) s[j] = 0.0f;
-    if (g.state_in && live) {
-      const float* p = g.state_in + (bh * g.dv + n) * g.dk + half * HK;
-#pragma unroll
-      for (int j = 0; j < HK; ++j)
-        if (half * HK + j < g.dk) s[j] = p[j];
+    for (int j = 0; j < HK; j += 4) {
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (g.state_in && live) {
+        const float* p = g.state_in + s_at + j;
+        const int left = g.dk - half * HK - j;
+        if (vec_s) {
+          if (left > 0) x = *reinterpret_cast<const float4*>(p);
+        } else {
+          if (left > 0) x.x = p[0];
+          if (left > 1) x.y = p[1];
+          if (left > 2) x.z = p[2];
+          if (left > 3) x.w = p[3];
+        }
+      }
+      s[j] = x.x, s[j + 1] = x.y, s[j + 2] = x.z, s[j + 3] = x.w;
     }
     float s_max = 0.0f;
     int s_exp = 0;  // S is held as 2^{s_exp} S
-    // this lane's state to tensor memory, scaled, in two halves: HK / 2 columns
-    // of hi, HK / 2 of lo, then the other warp's
+    // this lane's state to tensor memory, scaled, in two halves: of every 16
+    // columns 8 of hi, 8 of lo
     auto put_state = [&]() {
       float mx = 0.0f;
 #pragma unroll
@@ -287,14 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       s_max = fmaxf(mx, max_s[(1 - half) * kM + lane_n]);
       s_exp = 13 - exponent_of(s_max);
       s_exp = s_exp > 120 ? 120 : s_exp;
-      const float c = pow2(s_exp);
+      const float2 c = make_float2(pow2(s_exp), pow2(s_exp));
 #pragma unroll
-      for (int j0 = 0; j0 < HK; j0 += 32) {
-        uint32_t hi[16], lo[16];
+      for (int j0 = 0; j0 < HK; j0 += 16) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) split2(s[j0 + 2 * j] * c, s[j0 + 2 * j + 1] * c, hi[j], lo[j]);
-        tmem_st16(t_lane + kColS + (uint32_t)(half * HK + j0 / 2), hi);
-        tmem_st16(t_lane + kColS + (uint32_t)(half * HK + HK / 2 + j0 / 2), lo);
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = __fmul2_rn(make_float2(s[j0 + 2 * j], s[j0 + 2 * j + 1]), c);
+          split2(v.x, v.y, hi[j], lo[j]);
+        }
+        tmem_st8(t_lane + kColS + (uint32_t)(half * HK + j0), hi);
+        tmem_st8(t_lane + kColS + (uint32_t)(half * HK + j0 + 8), lo);
       }
       tmem_wait_st();
       tcgen05_fence_before();
@@ -303,69 +364,81 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     };
     put_state();
 
+    const int i0 = half * 32;  // this thread's tokens of a chunk
+    const int64_t y_step = g.y_bf16 ? 2 * g.ld_y : 4 * g.ld_y;
+    char* y_at = reinterpret_cast<char*>(g.y) +
+                 ((b * g.T + i0) * g.ld_y + (int64_t)h * g.dv + n) * (g.y_bf16 ? 2 : 4);
     for (int c = 0; c < n_chunks; ++c) {
       const Gates& gt = gates[c % kGateSlots];
-      const int vs = c % L::kVStages;
-      const In* v_tile = reinterpret_cast<const In*>(gbase + L::kOffV + vs * L::kV) + (half * 32) * kM + lane_n;
-      const int i0 = half * 32;  // this thread's tokens
+      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
+      // this lane's value of token i0 + i
+      const In* v_tile = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
+      const In* v_global = reinterpret_cast<const In*>(g.v) + (b * g.T + (int64_t)c * kC + i0) * g.ld_v + (int64_t)h * g.dv + n;
+      auto value = [&](int i) {
+        if (!F32) return to_f32(v_tile[i * kM]);
+        return live && i0 + i < left ? to_f32(v_global[i * g.ld_v]) : 0.0f;
+      };
       // scale of R from its bound; the largest |v| of the lane needs the partner's tokens
-      wait(v_full + 8 * vs, c / L::kVStages);
+      if (!F32) wait(v_full, c);
       float mx = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(to_f32(v_tile[i * kM])));
+#pragma unroll 16
+      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(value(i)));
       if (mx > 3.4e38f) mx = 1.0f;
       max_v[half * kM + lane_n] = mx;
       named_barrier(3 + quad, 64);
       mx = fmaxf(mx, max_v[(1 - half) * kM + lane_n]);
       wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
-      int r_exp = 13 - exponent_of(fmaf(gt.k_bound, s_max, mx));
+      int r_exp = 9 - exponent_of(fmaf(gt.k_bound, s_max, mx));
       r_exp = r_exp > 120 ? 120 : r_exp;
-      {  // epilogue 1: R^T = beta V - fx D1
+      {  // epilogue 1: R^T = V^T - fx D1; of every 16 columns 8 of hi, 8 of lo
         const float cv = pow2(r_exp), cx = pow2(r_exp - s_exp);
-        uint32_t x[32];
         wait(x_full, c);
         tcgen05_fence_after();
-        tmem_ld32(t_lane + kColX + (uint32_t)i0, x);
-        tmem_wait(x);
-        uint32_t hi[16], lo[16];
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 16) {
+          uint32_t x[16];
+          tmem_ld16(t_lane + kColX + (uint32_t)(i0 + i), x);
+          uint32_t hi[8], lo[8];
+          float fx[16], v[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 be = *reinterpret_cast<const float4*>(&gt.beta[i0 + i]);
-          const float4 fx = *reinterpret_cast<const float4*>(&gt.fx[i0 + i]);
-          float r[4];
-          const float bes[4] = {be.x, be.y, be.z, be.w}, fxs[4] = {fx.x, fx.y, fx.z, fx.w};
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(&fx[j]) = *reinterpret_cast<const float4*>(&gt.fx[i0 + i + j]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            r[j] = bes[j] * (to_f32(v_tile[(i + j) * kM]) * cv) - fxs[j] * (__uint_as_float(x[i + j]) * cx);
-          split2(r[0], r[1], hi[i / 2], lo[i / 2]);
-          split2(r[2], r[3], hi[i / 2 + 1], lo[i / 2 + 1]);
+          for (int j = 0; j < 16; ++j) v[j] = value(i + j);
+          tmem_wait(x);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 t = __fmul2_rn(make_float2(fx[j], fx[j + 1]),
+                                        __fmul2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                                   make_float2(-cx, -cx)));
+            const float2 r = __ffma2_rn(make_float2(cv, cv), make_float2(v[j], v[j + 1]), t);
+            split2(r.x, r.y, hi[j / 2], lo[j / 2]);
+          }
+          tmem_st8(t_lane + kColX + (uint32_t)(i0 + i), hi);
+          tmem_st8(t_lane + kColX + (uint32_t)(i0 + i + 8), lo);
         }
-        tmem_st16(t_lane + kColX + (uint32_t)i0, hi);
-        tmem_st16(t_lane + kColX + (uint32_t)(i0 + 16), lo);
         tmem_wait_st();
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(r_ready), mbar_arrive(v_empty + 8 * vs);
+        if (lane == 0) {
+          mbar_arrive(r_ready);
+          if (!F32) mbar_arrive(v_empty);
+        }
       }
-      int u_exp;  // epilogue 2: U^T, decayed to the chunk's end
-      {
-        uint32_t x[32];
+      {  // epilogue 2: U^T, already decayed to the chunk's end
         wait(u_full, c);
         tcgen05_fence_after();
-        tmem_ld32(t_lane + kColU + (uint32_t)i0, x);
-        u_exp = exponent_of(fmaxf(gt.u_bound[0], gt.u_bound[1])) + 1;
-        const float cu = pow2(-u_exp);
-        tmem_wait(x);
-        uint32_t hi[16], lo[16];
+#pragma unroll 1
+        for (int i = i0; i < i0 + 32; i += 16) {
+          uint32_t x[16], hi[8], lo[8];
+          tmem_ld16(t_lane + kColU + (uint32_t)i, x);
+          tmem_wait(x);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 fu = *reinterpret_cast<const float4*>(&gt.fu[i0 + i]);
-          split2(__uint_as_float(x[i]) * (fu.x * cu), __uint_as_float(x[i + 1]) * (fu.y * cu), hi[i / 2], lo[i / 2]);
-          split2(__uint_as_float(x[i + 2]) * (fu.z * cu), __uint_as_float(x[i + 3]) * (fu.w * cu), hi[i / 2 + 1],
-                 lo[i / 2 + 1]);
+          for (int j = 0; j < 8; ++j)
+            split2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), hi[j], lo[j]);
+          tmem_st8(t_lane + kColU + (uint32_t)i, hi);
+          tmem_st8(t_lane + kColU + (uint32_t)(i + 8), lo);
         }
-        tmem_st16(t_lane + kColU + (uint32_t)i0, hi);
-        tmem_st16(t_lane + kColU + (uint32_t)(i0 + 16), lo);
         tmem_wait_st();
         tcgen05_fence_before();
         __syncwarp();
@@ -374,27 +447,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       {  // output, while D3 is in flight
         wait(o_full, c);
         tcgen05_fence_after();
-        const float cq = pow2(-s_exp), cp = pow2(-r_exp);
-        const int64_t row0 = b * g.T + (int64_t)c * kC + i0;
-        const int left = (int)(g.T - (int64_t)c * kC) - i0;  // tokens of this half inside the sequence
+        const float cq = pow2(-s_exp), cw = g.scale * pow2(-r_exp - gt.w_exp);
+        const int rows = live ? left : 0;
+        char* p = y_at;
+#pragma unroll 1
+        for (int i = i0; i < i0 + 32; i += 8) {
+          uint32_t xq[8], xo[8];
+          tmem_ld8(t_lane + kColQ + (uint32_t)i, xq);
+          tmem_ld8(t_lane + kColO + (uint32_t)i, xo);
+          float fq[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-          uint32_t xq[16], xo[16];
-          tmem_ld16(t_lane + kColQ + (uint32_t)(i0 + i), xq);
-          tmem_ld16(t_lane + kColO + (uint32_t)(i0 + i), xo);
+          for (int j = 0; j < 8; j += 4)
+            *reinterpret_cast<float4*>(&fq[j]) = *reinterpret_cast<const float4*>(&gt.fq[i + j]);
           tmem_wait(xq);
           tmem_wait(xo);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float o = gt.fq[i0 + i + j] * (__uint_as_float(xq[j]) * cq) +
-                            gt.fp[i0 + i + j] * (__uint_as_float(xo[j]) * cp);
-            if (live && i + j < left)
-              store_out(g.y, (row0 + i + j) * g.ld_y + (int64_t)h * g.dv + n, g.y_bf16, o);
+          for (int j = 0; j < 8; ++j) {
+            const float o = fmaf(__uint_as_float(xo[j]), cw, fq[j] * (__uint_as_float(xq[j]) * cq));
+            if (i + j < rows) {
+              if (g.y_bf16)
+                *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(o);
+              else
+                *reinterpret_cast<float*>(p) = o;
+            }
+            p += y_step;
           }
         }
+        y_at += kC * y_step;
       }
       {  // epilogue 3: S = e^G S + D3
-        const float total = gt.total, cd = pow2(u_exp - r_exp);
+        const float total = gt.total, cd = pow2(-r_exp - gt.t_exp);
         wait(s_full, c);
         tcgen05_fence_after();
 #pragma unroll
@@ -403,38 +485,58 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           tmem_ld16(t_lane + kColS + (uint32_t)(half * HK + j0), x);
           tmem_wait(x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]) * cd);
+          for (int j = 0; j < 16; j += 2) {
+            const float2 t = __ffma2_rn(
+                make_float2(total, total), make_float2(s[j0 + j], s[j0 + j + 1]),
+                __fmul2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cd, cd)));
+            s[j0 + j] = t.x, s[j0 + j + 1] = t.y;
+          }
         }
         if (c + 1 < n_chunks) put_state();
       }
     }
     if (g.state_out && live) {
-      float* p = g.state_out + (bh * g.dv + n) * g.dk + half * HK;
 #pragma unroll
-      for (int j = 0; j < HK; ++j)
-        if (half * HK + j < g.dk) p[j] = s[j];
+      for (int j = 0; j < HK; j += 4) {
+        float* p = g.state_out + s_at + j;
+        const int left = g.dk - half * HK - j;
+        if (vec_s) {
+          if (left > 0) *reinterpret_cast<float4*>(p) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        } else {
+          if (left > 0) p[0] = s[j];
+          if (left > 1) p[1] = s[j + 1];
+          if (left > 2) p[2] = s[j + 2];
+          if (left > 3) p[3] = s[j + 3];
+        }
+      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ prepare ----
     const int quad = warp & 3;
-    const int row = quad * 32 + lane;       // row of [K; Q] and of [T; PT]
+    const int row = quad * 32 + lane;       // row of [K; Q]
     const bool is_t = quad < 2;             // warp-uniform
+    const bool upper = quad & 1;            // tokens 32-63: the rows with columns past 31
     const int i = row & (kC - 1);           // token
-    const uint32_t t_d0 = tmem + ((uint32_t)(quad * 32) << 16) + kColD0;
     float* a_s = reinterpret_cast<float*>(gbase + L::kOffA);
+    float* p_s = a_s + kC * kLdA;
+    // of [T; W] this warp solves rows 16 rt .. of T and rows 16 rw .. of W: the
+    // work of a row block grows with its index, the two together do not
+    const int rt = quad, rw = 3 - quad;
+    const int fr = lane / 4, fc = 2 * (lane % 4);  // accumulator fragment: rows fr, fr + 8, columns fc, fc + 1
     for (int c = 0; c < n_chunks; ++c) {
       Gates& gt = gates[c % kGateSlots];
-      const int st = c % L::kTpStages;
-      float2 x[32];  // this row, pairs of columns
+      const uint32_t t_d0 = tmem + ((uint32_t)(quad * 32) << 16) + kColD0 + (uint32_t)(64 * (c & 1));
       wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
-      wait(d0_full, c);
+      wait(d0_full + 8 * (c & 1), c / 2);
       tcgen05_fence_after();
+      named_barrier(1, 128);  // the previous chunk's A and P are read
       {
         const float rh = gt.row_hi[row], rl = gt.row_lo[row];
         const float scale_row = is_t ? gt.beta[i] : 1.0f;
         const int last = is_t ? i - 1 : i;  // A is strictly lower, P lower
-#pragma unroll
-        for (int j0 = 0; j0 < kC; j0 += 32) {
+        float* dst = (is_t ? a_s : p_s) + i * kLdA;
+#pragma unroll 1
+        for (int j0 = 0; j0 < (upper ? kC : 32); j0 += 32) {
           uint32_t d[32];
           tmem_ld32(t_d0 + (uint32_t)j0, d);
           tmem_wait(d);
@@ -443,303 +545,439 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             const float4 ch = *reinterpret_cast<const float4*>(&gt.col_hi[j0 + j]);
             const float4 cl = *reinterpret_cast<const float4*>(&gt.col_lo[j0 + j]);
             const float chs[4] = {ch.x, ch.y, ch.z, ch.w}, cls[4] = {cl.x, cl.y, cl.z, cl.w};
-            float v[4];
+            float o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float w = ex2_approx((rh - chs[e]) + (rl - cls[e]));
-              v[e] = j0 + j + e <= last ? __uint_as_float(d[j + e]) * w * scale_row : 0.0f;
+            for (int e = 0; e < 4; e += 2) {
+              const float2 w = __fadd2_rn(__fadd2_rn(make_float2(rh, rh), make_float2(-chs[e], -chs[e + 1])),
+                                          __fadd2_rn(make_float2(rl, rl), make_float2(-cls[e], -cls[e + 1])));
+              const float2 v = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
+                                                     make_float2(ex2_approx(w.x), ex2_approx(w.y))),
+                                          make_float2(scale_row, scale_row));
+              o[e] = j0 + j + e <= last ? v.x : 0.0f;
+              o[e + 1] = j0 + j + e + 1 <= last ? v.y : 0.0f;
             }
-            x[(j0 + j) / 2] = make_float2(v[0], v[1]);
-            x[(j0 + j) / 2 + 1] = make_float2(v[2], v[3]);
+            *reinterpret_cast<float4*>(dst + j0 + j) = make_float4(o[0], o[1], o[2], o[3]);
           }
         }
-        tcgen05_fence_before();
+      }
+      tcgen05_fence_before();
+      named_barrier(1, 128);
+      if (lane == 0) mbar_arrive(d0_empty + 8 * (c & 1));
+      {
+        // the inverse of diagonal block `quad` of I + A over the block itself, a
+        // lane a row (16-31 repeat 0-15): X (I + A) = I, columns from the last
+        float* blk = a_s + 16 * quad * (kLdA + 1);
+        const int r = lane & 15;
+        float2 x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = make_float2(2 * q == r ? 1.0f : 0.0f, 2 * q + 1 == r ? 1.0f : 0.0f);
+#pragma unroll
+        for (int k = 15; k >= 1; --k) {
+          const float nx = (k & 1) ? -x[k / 2].y : -x[k / 2].x;
+#pragma unroll
+          for (int q = 0; q < (k + 3) / 4; ++q) {
+            const float4 a = *reinterpret_cast<const float4*>(blk + k * kLdA + 4 * q);
+            x[2 * q] = __ffma2_rn(make_float2(nx, nx), make_float2(a.x, a.y), x[2 * q]);
+            if (4 * q + 2 < k) x[2 * q + 1] = __ffma2_rn(make_float2(nx, nx), make_float2(a.z, a.w), x[2 * q + 1]);
+          }
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(d0_empty);
-      }
-      // A to shared memory (16-byte granule q of row i at q ^ (i % 8)), once
-      // the previous chunk's substitution has read its own
-      named_barrier(1, 128);
-      if (is_t) {
+        if (lane < 16) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          *reinterpret_cast<float4*>(a_s + i * kC + 4 * (q ^ (i & 7))) =
-              make_float4(x[2 * q].x, x[2 * q].y, x[2 * q + 1].x, x[2 * q + 1].y);
-          x[2 * q] = make_float2(4 * q == i ? 1.0f : 0.0f, 4 * q + 1 == i ? 1.0f : 0.0f);
-          x[2 * q + 1] = make_float2(4 * q + 2 == i ? 1.0f : 0.0f, 4 * q + 3 == i ? 1.0f : 0.0f);
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(blk + r * kLdA + 4 * q) =
+                make_float4(x[2 * q].x, x[2 * q].y, x[2 * q + 1].x, x[2 * q + 1].y);
         }
       }
       named_barrier(1, 128);
-      // X (I + A) = [I; P], columns from the last: x_k is final once every
-      // column after it has been taken off; rows 0-31 have nothing past column 31
-      auto eliminate = [&](int k) {
-        const float xk = (k & 1) ? x[k / 2].y : x[k / 2].x;
-        const float2 nx = make_float2(-xk, -xk);
+      // X (I + A) = [I; P] by blocks of 16 columns, the last first: X_k = B_k D_k,
+      // then B_j -= X_k A_kj for the blocks before it
+      float t[8][4], w[8][4];
 #pragma unroll
-        for (int q = 0; q < (k + 3) / 4; ++q) {
-          const float4 a = *reinterpret_cast<const float4*>(a_s + k * kC + 4 * (q ^ (k & 7)));
-          x[2 * q] = __ffma2_rn(nx, make_float2(a.x, a.y), x[2 * q]);
-          if (4 * q + 2 < k) x[2 * q + 1] = __ffma2_rn(nx, make_float2(a.z, a.w), x[2 * q + 1]);
+      for (int nt = 0; nt < 8; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[nt][e] = 0.0f, w[nt][e] = 0.0f;
+        if (nt / 2 <= rw) {
+          const float2 lo = *reinterpret_cast<const float2*>(p_s + (16 * rw + fr) * kLdA + 8 * nt + fc);
+          const float2 hi = *reinterpret_cast<const float2*>(p_s + (16 * rw + fr + 8) * kLdA + 8 * nt + fc);
+          w[nt][0] = lo.x, w[nt][1] = lo.y, w[nt][2] = hi.x, w[nt][3] = hi.y;
         }
-      };
-      if (quad & 1) {
-#pragma unroll
-        for (int k = kC - 1; k >= 32; --k) eliminate(k);
+        if (nt / 2 == rt) {  // the identity times D
+          const float2 lo = *reinterpret_cast<const float2*>(a_s + (16 * rt + fr) * kLdA + 8 * nt + fc);
+          const float2 hi = *reinterpret_cast<const float2*>(a_s + (16 * rt + fr + 8) * kLdA + 8 * nt + fc);
+          t[nt][0] = lo.x, t[nt][1] = lo.y, t[nt][2] = hi.x, t[nt][3] = hi.y;
+        }
       }
 #pragma unroll
-      for (int k = 31; k >= 1; --k) eliminate(k);
-      // row scale, two halves, to shared memory
-      float sum = 0.0f;
+      for (int k = 3; k >= 0; --k) {
+        const bool do_t = k <= rt, do_w = k <= rw;  // warp-uniform
+        if (!do_t && !do_w) continue;
+        uint32_t th[2][4], tl[2][4], wh[2][4], wl[2][4];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) sum += fabsf(x[q].x) + fabsf(x[q].y);
-      const int e = 13 - exponent_of(sum);
-      const float cs = pow2(e), inv = pow2(-(e < -126 ? -126 : (e > 127 ? 127 : e)));
-      if (c >= L::kTpStages) wait(tp_empty + 8 * st, c / L::kTpStages + 1);
-      if (is_t) {
-        gt.fu[i] = gt.fd[i] * inv;
-        const float bound = gt.fd[i] * sum;
-        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(bound));
-        if (lane == 0) gt.u_bound[quad] = __uint_as_float(top);
-      } else {
-        gt.fp[i] = g.scale * inv;
+        for (int j = k; j >= 0; --j) {  // j == k: times the inverse of the diagonal block
+          Tf32x2 bm[2][2][2];  // [k8][n8][row pair]
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                bm[kk][nn][e].set((j < k ? -1.0f : 1.0f) * a_s[(16 * k + 8 * kk + fc + e) * kLdA + 16 * j + 8 * nn + fr]);
+          auto product = [&](float (&x)[8][4], uint32_t (&xh)[2][4], uint32_t (&xl)[2][4], bool solved) {
+            float acc[2][4];
+#pragma unroll
+            for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nn][e] = j < k ? x[2 * j + nn][e] : 0.0f;
+            if (j == k) {
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) tf32_operand(xh[kk], xl[kk], x[2 * k + kk]);
+            }
+            if (j < k || !solved) {
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int nn = 0; nn < 2; ++nn) {
+                  mma_tf32(acc[nn], xl[kk], bm[kk][nn][0].hi, bm[kk][nn][1].hi);
+                  mma_tf32(acc[nn], xh[kk], bm[kk][nn][0].lo, bm[kk][nn][1].lo);
+                  mma_tf32(acc[nn], xh[kk], bm[kk][nn][0].hi, bm[kk][nn][1].hi);
+                }
+#pragma unroll
+              for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[2 * j + nn][e] = acc[nn][e];
+              if (j == k) {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) tf32_operand(xh[kk], xl[kk], x[2 * k + kk]);
+              }
+            }
+          };
+          if (do_t) product(t, th, tl, k == rt);
+          if (do_w) product(w, wh, wl, false);
+        }
       }
-      const uint32_t dst = base + L::kOffTp + st * L::kTp + (uint32_t)(row * 128);
+      // T's columns times beta, its rows decayed to the chunk's end; one scale for
+      // T and one for W, from the largest row sum of each
+      {
+        const float d0 = gt.fd[16 * rt + fr], d1 = gt.fd[16 * rt + fr + 8];
+        float st0 = 0.0f, st1 = 0.0f, sw0 = 0.0f, sw1 = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t hi[4], lo[4];
+        for (int nt = 0; nt < 8; ++nt) {
+          const float2 be = *reinterpret_cast<const float2*>(&gt.beta[8 * nt + fc]);
+          t[nt][0] *= be.x * d0, t[nt][1] *= be.y * d0, t[nt][2] *= be.x * d1, t[nt][3] *= be.y * d1;
+          w[nt][0] *= be.x, w[nt][1] *= be.y, w[nt][2] *= be.x, w[nt][3] *= be.y;
+          st0 += fabsf(t[nt][0]) + fabsf(t[nt][1]), st1 += fabsf(t[nt][2]) + fabsf(t[nt][3]);
+          sw0 += fabsf(w[nt][0]) + fabsf(w[nt][1]), sw1 += fabsf(w[nt][2]) + fabsf(w[nt][3]);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split2(x[4 * q + j].x * cs, x[4 * q + j].y * cs, hi[j], lo[j]);
-        const uint32_t at = dst + (uint32_t)((q ^ (row & 7)) << 4);
-        st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
-        st_shared16(at + 16384, lo[0], lo[1], lo[2], lo[3]);
+        for (int o = 1; o < 4; o <<= 1) {
+          st0 += __shfl_xor_sync(0xffffffffu, st0, o), st1 += __shfl_xor_sync(0xffffffffu, st1, o);
+          sw0 += __shfl_xor_sync(0xffffffffu, sw0, o), sw1 += __shfl_xor_sync(0xffffffffu, sw1, o);
+        }
+        const unsigned mt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(st0, st1)));
+        const unsigned mw = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sw0, sw1)));
+        if (lane == 0) gt.sum_t[quad] = __uint_as_float(mt), gt.sum_w[quad] = __uint_as_float(mw);
+      }
+      named_barrier(1, 128);
+      {
+        const float4 a = *reinterpret_cast<const float4*>(gt.sum_t), d = *reinterpret_cast<const float4*>(gt.sum_w);
+        int te = 3 - exponent_of(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+        int we = 3 - exponent_of(fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)));
+        te = te > 100 ? 100 : te, we = we > 100 ? 100 : we;
+        if (c > 0) wait(tp_empty, c - 1);
+        if (quad == 0 && lane == 0) gt.t_exp = te, gt.w_exp = we;
+        const float ct = pow2(te), cw = pow2(we);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // rows 16 rt + fr + 8 e of T, 64 + 16 rw + fr + 8 e of [T; W]; granule nt at nt ^ (row % 8)
+            const uint32_t at = base + L::kOffTp + (uint32_t)((fr + 8 * e) * 128 + ((nt ^ fr) << 4) + fc * 2);
+            uint32_t hi, lo;
+            split2(t[nt][2 * e] * ct, t[nt][2 * e + 1] * ct, hi, lo);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + rt * 2048), "r"(hi) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + rt * 2048 + 16384), "r"(lo) : "memory");
+            split2(w[nt][2 * e] * cw, w[nt][2 * e + 1] * cw, hi, lo);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8192 + rw * 2048), "r"(hi) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8192 + rw * 2048 + 16384), "r"(lo) : "memory");
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tp_full + 8 * st);
+      if (lane == 0) mbar_arrive(tp_full);
     }
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------------- load ----
     const int lw = warp - 12, lt = threadIdx.x - 12 * 32;
     constexpr int kLanes = DK / 8;           // lanes per row
     constexpr int kRowsPer = 32 / kLanes;    // rows per warp and pass
+    constexpr int kStep = kLoadWarps * kRowsPer;  // rows per pass
     const int sub = lane / kLanes, col = (lane % kLanes) * 8;
     const float neg_A = -expf(g.A_log[h]);
     const float dt_bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
     const int valid = g.dk - col;            // of this lane's eight components
+    const In* k_base = reinterpret_cast<const In*>(g.k) + b * g.T * g.ld_k + (int64_t)hk * g.dk;
+    const In* q_base = reinterpret_cast<const In*>(g.q) + b * g.T * g.ld_q + (int64_t)hk * g.dk;
+    const In* v_base = reinterpret_cast<const In*>(g.v) + b * g.T * g.ld_v + (int64_t)h * g.dv + tile * kM;
+    const In* a_base = reinterpret_cast<const In*>(g.a) + b * g.T * g.ld_a + h;
+    const In* b_base = reinterpret_cast<const In*>(g.b) + b * g.T * g.ld_b + h;
+    const bool staged = !F32 && vec_kq;      // K and Q through tensor copies
+    auto tokens = [&](int c) { return (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC); };
+    // K and Q rows of chunk c (tokens past the end read as zero)
+    auto copy_kq = [&](int c) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(raw_full, 2 * kC * DK * 2);
+        tma_load_3d(base + L::kOffRaw, &map_k, hk * g.dk, c * kC, (int)b, raw_full);
+        tma_load_3d(base + L::kOffRaw + kC * DK * 2, &map_q, hk * g.dk, c * kC, (int)b, raw_full);
+      }
+    };
+    float a_next[2] = {0.0f, 0.0f}, b_next[2] = {0.0f, 0.0f};
+    auto fetch_gates = [&](int c) {  // tokens lane and lane + 32 (warp 13)
+      const int left = tokens(c);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        const int64_t t = (int64_t)c * kC + i;
+        a_next[u] = i < left ? to_f32(a_base[t * g.ld_a]) : 0.0f;
+        b_next[u] = i < left ? to_f32(b_base[t * g.ld_b]) : 0.0f;
+      }
+    };
+    if (staged && lw == 0) copy_kq(0);
+    if (lw == 1) fetch_gates(0);
     for (int c = 0; c < n_chunks; ++c) {
-      const int ks = c % L::kKqStages, vs = c % L::kVStages;
-      const int64_t t0 = (int64_t)c * kC;
-      const int left = (int)(g.T - t0 < kC ? g.T - t0 : kC);
-      const int64_t row0 = b * g.T + t0;
+      const int ks = c % L::kKqStages;
+      const int left = tokens(c);
       int* exps = reinterpret_cast<int*>(gbase + L::kOffExp) + (c & 1) * 2 * kC;
+      if (staged) wait(raw_full, c);
       if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
       // K (rows 0-63) and Q (64-127), each row scaled to [2^13, 2^14)
+      // kBatch rows' loads and reductions are in flight together
       constexpr int kBatch = F32 ? 4 : 8;
-      constexpr int kStep = kLoadWarps * kRowsPer;  // rows per pass
 #pragma unroll 1
-      for (int p0 = 0; p0 * kStep < 2 * kC; p0 += kBatch) {
-        float f[kBatch][8];
+      for (int r0 = lw * kRowsPer + sub; r0 < 2 * kC; r0 += kBatch * kStep) {  // as often for every lane of a warp
+        float f[kBatch][8], mx[kBatch];
+        if (staged) {
+          uint4 x[kBatch];
 #pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          const int r = (p0 + p) * kStep + lw * kRowsPer + sub;
-          const int i = r & (kC - 1);
-          const bool in = i < left && valid > 0 && r < 2 * kC;
-          const void* src = r < kC ? g.k : g.q;
-          const int64_t ld = r < kC ? g.ld_k : g.ld_q;
-          load8<F32>(f[p], src, in ? (row0 + i) * ld + (int64_t)hk * g.dk + col : 0, in ? valid : 0, vec_kq);
+          for (int p = 0; p < kBatch; ++p) {
+            const int r = r0 + p * kStep < 2 * kC ? r0 + p * kStep : r0;
+            x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + r * DK * 2 + col * 2);
+          }
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) {
+            // columns past dk are another head's, rows past the end zero
+            if (valid <= 0) x[p] = make_uint4(0, 0, 0, 0);
+            unpack8(f[p], x[p]);
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) {
+            const int r = r0 + p * kStep, i = r & (kC - 1);
+            const bool in = i < left && r < 2 * kC;
+            const int64_t t = in ? (int64_t)c * kC + i : 0;
+            const In* src = (r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
+            if (F32 && vec_kq) {
+              float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+              if (in && valid > 0) lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + 4);
+              f[p][0] = lo.x, f[p][1] = lo.y, f[p][2] = lo.z, f[p][3] = lo.w;
+              f[p][4] = hi.x, f[p][5] = hi.y, f[p][6] = hi.z, f[p][7] = hi.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[p][j] = in && j < valid ? to_f32(src[j]) : 0.0f;
+            }
+          }
         }
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
-          const int r = (p0 + p) * kStep + lw * kRowsPer + sub;
-          float mx = 0.0f;
+          mx[p] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(f[p][j]));
+          for (int j = 0; j < 8; ++j) mx[p] = fmaxf(mx[p], fabsf(f[p][j]));
+        }
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          int e = 13 - exponent_of(mx);
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p) {
+          const int r = r0 + p * kStep;
+          int e = 13 - exponent_of(mx[p]);
           e = e > 120 ? 120 : e;  // a zero row: 120, so that its bound below is nothing
-          if (r >= 2 * kC) continue;  // a lane past the last row; the shuffles are behind it
-          if (col == 0) exps[r] = e;
           const float cs = pow2(e);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            const float2 v = __fmul2_rn(make_float2(f[p][2 * j], f[p][2 * j + 1]), make_float2(cs, cs));
             if (F32) {
-              split2(f[p][2 * j] * cs, f[p][2 * j + 1] * cs, hi[j], lo[j]);
+              split2(v.x, v.y, hi[j], lo[j]);
             } else {
-              const __half2 t = __floats2half2_rn(f[p][2 * j] * cs, f[p][2 * j + 1] * cs);
+              const __half2 t = __floats2half2_rn(v.x, v.y);
               hi[j] = *reinterpret_cast<const uint32_t*>(&t);
             }
           }
-          const uint32_t at = base + ks * L::kKq + (uint32_t)((col / 64) * 16384 + r * 128 +
-                                                              ((((col & 63) / 8) ^ (r & 7)) << 4));
-          st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
-          if (F32) st_shared16(at + L::kKqTerm, lo[0], lo[1], lo[2], lo[3]);
+          if (r < 2 * kC) {
+            if (col == 0) exps[r] = e;
+            const uint32_t at =
+                base + ks * L::kKq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
+            st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
+            if (F32) st_shared16(at + L::kKqTerm, lo[0], lo[1], lo[2], lo[3]);
+          }
         }
       }
       fence_proxy_async_smem();
-      named_barrier(2, kLoadThreads);  // every row's exponent is there
-      if (lw == 0) {
-        // the gates of tokens lane and lane + 32: base-2 logarithms, summed in 64
-        // bits and kept as two floats, so that differences of far-decayed tokens
-        // keep 32-bit accuracy.  alpha below 2^-256 is 0 in f32 all the same.
+      named_barrier(2, kLoadThreads);  // every row's exponent is there, the raw rows are read
+      if (staged && lw == 0 && c + 1 < n_chunks) copy_kq(c + 1);
+      if (lw == 1) {
+        // the gates of tokens lane and lane + 32: base-2 logarithms summed in
+        // 64-bit fixed point and kept as two floats, so that differences of
+        // far-decayed tokens keep 32-bit accuracy.  alpha below e^-200 is 0 in
+        // f32 all the same.
         Gates& gt = gates[c % kGateSlots];
-        double G[2];
+        long long G[2];
         float be[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int i = lane + 32 * u;
-          const bool in = i < left;
-          const float a = in ? to_f32(reinterpret_cast<const In*>(g.a)[(row0 + i) * g.ld_a + h]) : 0.0f;
-          const float bb = in ? to_f32(reinterpret_cast<const In*>(g.b)[(row0 + i) * g.ld_b + h]) : 0.0f;
-          const float la = gdr_log_alpha(a, dt_bias, neg_A);
-          G[u] = in ? (double)(la < -200.0f ? -200.0f : la) * 1.4426950408889634 : 0.0;
-          be[u] = in ? gdr_beta(bb) : 0.0f;
+          const bool in = lane + 32 * u < left;
+          const float la = gdr_log_alpha(a_next[u], dt_bias, neg_A);
+          G[u] = in ? log2_fixed(la < -200.0f ? -200.0f : la) : 0;
+          be[u] = in ? gdr_beta(b_next[u]) : 0.0f;
+        }
+        if (c + 1 < n_chunks) fetch_gates(c + 1);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double t = __shfl_up_sync(0xffffffffu, G[u], o);
+        for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const long long t = __shfl_up_sync(0xffffffffu, G[u], o);
             if (lane >= o) G[u] += t;
           }
         }
         G[1] += __shfl_sync(0xffffffffu, G[0], 31);
-        const double last = __shfl_sync(0xffffffffu, G[1], 31);
+        const long long last = __shfl_sync(0xffffffffu, G[1], 31);
         float kb = 0.0f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int i = lane + 32 * u;
           const int ek = exps[i], eq = exps[kC + i];
-          const double cj = G[u] + (double)ek, rk = G[u] - (double)ek, rq = G[u] - (double)eq;
-          const float eg = ex2_approx((float)G[u]);
-          gt.col_hi[i] = (float)cj, gt.col_lo[i] = (float)(cj - (double)(float)cj);
-          gt.row_hi[i] = (float)rk, gt.row_lo[i] = (float)(rk - (double)(float)rk);
-          gt.row_hi[kC + i] = (float)rq, gt.row_lo[kC + i] = (float)(rq - (double)(float)rq);
+          const float2 cj = fixed_split(G[u] + ((long long)ek << 40)), rk = fixed_split(G[u] - ((long long)ek << 40)),
+                       rq = fixed_split(G[u] - ((long long)eq << 40));
+          const float eg = ex2_approx(__ll2float_rn(G[u]) * 9.094947017729282e-13f);
+          gt.col_hi[i] = cj.x, gt.col_lo[i] = cj.y;
+          gt.row_hi[i] = rk.x, gt.row_lo[i] = rk.y;
+          gt.row_hi[kC + i] = rq.x, gt.row_lo[kC + i] = rq.y;
           gt.beta[i] = be[u];
-          gt.fx[i] = be[u] * eg * pow2(-ek);
-          gt.fd[i] = ex2_approx((float)(last - G[u])) * pow2(-ek);
+          gt.fx[i] = eg * pow2(-ek);
+          gt.fd[i] = ex2_approx(__ll2float_rn(last - G[u]) * 9.094947017729282e-13f) * pow2(-ek);
           gt.fq[i] = g.scale * eg * pow2(-eq);
           // |k|_1 <= DK max|k| < DK 2^{14 - ek}
-          kb = fmaxf(kb, be[u] * eg * (float)DK * pow2(14 - ek));
+          kb = fmaxf(kb, eg * (float)DK * pow2(14 - ek));
         }
         const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(kb));
-        if (lane == 0) gt.k_bound = __uint_as_float(top), gt.total = ex2_approx((float)last);
+        if (lane == 0)
+          gt.k_bound = __uint_as_float(top), gt.total = ex2_approx(__ll2float_rn(last) * 9.094947017729282e-13f);
       }
       mbar_arrive(kq_full + 8 * ks);
-      // V: straight to shared memory
-      if (c >= L::kVStages) wait(v_empty + 8 * vs, c / L::kVStages + 1);
-      {
-        const uint32_t dst = base + L::kOffV + vs * L::kV;
-        const In* src = reinterpret_cast<const In*>(g.v) + (int64_t)h * g.dv + tile * kM;
-        const int cols = g.dv - tile * kM < kM ? g.dv - tile * kM : kM;
-        constexpr int kPer = 16 / (int)sizeof(In);  // values per granule
-        constexpr int kGr = kM / kPer;
+      // V (bf16); rows past the sequence's end are zero, columns past the head's
+      // are lanes that nothing reads
+      if (!F32 && (!vec_v || lw == 0)) {
+        if (c > 0) wait(v_empty, c - 1);
         if (vec_v) {
-#pragma unroll 4
-          for (int e = lt; e < kC * kGr; e += kLoadThreads) {
-            const int r = e / kGr, q = e % kGr;
-            const bool in = r < left && q * kPer < cols;
-            cp_async16(dst + (uint32_t)(e * 16), in ? src + (row0 + r) * g.ld_v + q * kPer : src, in);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(v_full, kC * kM * 2);
+            tma_load_3d(base + L::kOffV, &map_v, h * g.dv + tile * kM, c * kC, (int)b, v_full);
           }
-          cp_async_arrive(v_full + 8 * vs);
         } else {
-          In* d = reinterpret_cast<In*>(gbase + L::kOffV + vs * L::kV);
+          const int cols = g.dv - tile * kM < kM ? g.dv - tile * kM : kM;
+          In* v_dst = reinterpret_cast<In*>(gbase + L::kOffV);
+#pragma unroll 4
           for (int e = lt; e < kC * kM; e += kLoadThreads) {
             const int r = e / kM, q = e % kM;
-            d[e] = r < left && q < cols ? src[(row0 + r) * g.ld_v + q] : from_f32<In>(0.0f);
+            v_dst[e] = r < left && q < cols ? v_base[((int64_t)c * kC + r) * g.ld_v + q] : from_f32<In>(0.0f);
           }
-          mbar_arrive(v_full + 8 * vs);
+          mbar_arrive(v_full);
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // --------------------------------------------------------------- MMAs ----
     if (lane == 0) {
       constexpr uint32_t id64 = idesc_f16(64, false), id3 = idesc_f16(DK, true);
-      constexpr int HK = DK / 2;
-      // column of S's values 16 ks ..: half by half, hi then lo
-      auto s_col = [](int ks, int lo) { return (uint32_t)((16 * ks / HK) * HK + (16 * ks % HK) / 2 + lo * (HK / 2)); };
-      auto r_col = [](int ks, int lo) { return (uint32_t)((ks / 2) * 32 + (ks % 2) * 8 + lo * 16); };
       // [K; Q] K^T of chunk c, for the prepare warps
       auto issue_d0 = [&](int c) {
-        const int ks = c % L::kKqStages;
-        const uint32_t kq = base + ks * L::kKq;
-        wait(kq_full + 8 * ks, c / L::kKqStages);
-        if (c > 0) wait(d0_empty, c - 1);
+        const uint32_t kq = base + (c % L::kKqStages) * L::kKq;
+        wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
+        if (c > 1) wait(d0_empty + 8 * (c & 1), c / 2 - 1);
         tcgen05_fence_after();
         uint32_t acc = 0;
-#pragma unroll
+#pragma unroll 1
         for (int term = 0; term < (F32 ? 3 : 1); ++term) {
-          const int a_lo = term == 1, b_lo = term == 2;
+          const uint32_t ka = kq + (term == 1 ? L::kKqTerm : 0), kb = kq + (term == 2 ? L::kKqTerm : 0);
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k) {
-            const uint64_t ad = smem_desc(kq + a_lo * L::kKqTerm + (k / 4) * 16384) + 2 * (k % 4);
-            const uint64_t bd = smem_desc(kq + b_lo * L::kKqTerm + (k / 4) * 16384) + 2 * (k % 4);
-            mma_ss(tmem + kColD0, ad, bd, id64, acc);
+            mma_ss(tmem + kColD0 + 64 * (c & 1), smem_desc(ka + (k / 4) * 16384) + 2 * (k % 4),
+                   smem_desc(kb + (k / 4) * 16384) + 2 * (k % 4), id64, acc);
             acc = 1;
           }
         }
-        mma_commit(d0_full);
+        mma_commit(d0_full + 8 * (c & 1));
       };
       issue_d0(0);
       for (int c = 0; c < n_chunks; ++c) {
-        const int ks = c % L::kKqStages, st = c % L::kTpStages;
-        const uint32_t kq = base + ks * L::kKq, tp = base + L::kOffTp + st * L::kTp;
+        const int ks = c % L::kKqStages;
+        const uint32_t kq = base + ks * L::kKq, tp = base + L::kOffTp;
         wait(s_ready, c);
         tcgen05_fence_after();
         // D1: S_hi K_hi + S_lo K_hi (+ S_hi K_lo); keys first, the queries'
-        // half runs under epilogue 1
-#pragma unroll
+        // half runs under epilogue 1.  A's halves: 8 columns hi, 8 lo of every 16
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           uint32_t acc = 0;
-#pragma unroll
+#pragma unroll 1
           for (int term = 0; term < (F32 ? 3 : 2); ++term) {
-            const int s_lo = term == 1, k_lo = term == 2;
+            const uint32_t ad = tmem + kColS + (term == 1 ? 8 : 0);
+            const uint32_t bd = kq + (term == 2 ? L::kKqTerm : 0) + part * 8192;
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
-              const uint64_t bd =
-                  smem_desc(kq + k_lo * L::kKqTerm + (k / 4) * 16384 + part * 8192) + 2 * (k % 4);
-              mma_ts(tmem + (part ? kColQ : kColX), tmem + kColS + s_col(k, s_lo), bd, id64, acc);
+              mma_ts(tmem + (part ? kColQ : kColX), ad + 16 * k, smem_desc(bd + (k / 4) * 16384) + 2 * (k % 4), id64, acc);
               acc = 1;
             }
           }
           if (part == 0) mma_commit(x_full);
         }
-        // one chunk ahead; the prepare warps have long read this chunk's
+        // one chunk ahead; two accumulators, so the prepare warps need not be
+        // done with this chunk's
         if (c + 1 < n_chunks) issue_d0(c + 1);
-        wait(tp_full + 8 * st, c / L::kTpStages);
+        wait(tp_full, c);
         wait(r_ready, c);
         tcgen05_fence_after();
-        // D2: R_hi T_hi + R_hi T_lo + R_lo T_hi; T's half first
-#pragma unroll
+        // D2: R_hi T_hi + R_hi T_lo + R_lo T_hi; T's half first, W's under epilogue 2
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           uint32_t acc = 0;
-#pragma unroll
+#pragma unroll 1
           for (int term = 0; term < 3; ++term) {
-            const int r_lo = term == 2, t_lo = term == 1;
+            const uint32_t ad = tmem + kColX + (term == 2 ? 8 : 0);
+            const uint64_t bd = smem_desc(tp + (term == 1 ? 16384 : 0) + part * 8192);
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {
-              const uint64_t bd = smem_desc(tp + t_lo * 16384 + part * 8192) + 2 * k;
-              mma_ts(tmem + (part ? kColO : kColU), tmem + kColX + r_col(k, r_lo), bd, id64, acc);
+              mma_ts(tmem + (part ? kColO : kColU), ad + 16 * k, bd + 2 * k, id64, acc);
               acc = 1;
             }
           }
           mma_commit(part ? o_full : u_full);
         }
-        mma_commit(tp_empty + 8 * st);
+        mma_commit(tp_empty);
         wait(u_ready, c);
         tcgen05_fence_after();
         // D3: U_hi K_hi + U_lo K_hi (+ U_hi K_lo); K's rows are the contraction
-        {
-          uint32_t acc = 0;
+        uint32_t acc = 0;
+#pragma unroll 1
+        for (int term = 0; term < (F32 ? 3 : 2); ++term) {
+          const uint32_t ad = tmem + kColU + (term == 1 ? 8 : 0);
+          const uint64_t bd = smem_desc(kq + (term == 2 ? L::kKqTerm : 0), 16384);
 #pragma unroll
-          for (int term = 0; term < (F32 ? 3 : 2); ++term) {
-            const int u_lo = term == 1, k_lo = term == 2;
-#pragma unroll
-            for (int k = 0; k < kC / 16; ++k) {
-              const uint64_t bd = smem_desc(kq + k_lo * L::kKqTerm + k * 2048, 16384);
-              mma_ts(tmem + kColS, tmem + kColU + r_col(k, u_lo), bd, id3, acc);
-              acc = 1;
-            }
+          for (int k = 0; k < kC / 16; ++k) {
+            mma_ts(tmem + kColS, ad + 16 * k, bd + 128 * k, id3, acc);
+            acc = 1;
           }
         }
         mma_commit(s_full);
@@ -759,6 +997,42 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+// cuTensorMapEncodeTiled from the driver, looked up once
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !p) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// [B][T][cols] bf16, rows ld apart: boxes of 64 tokens of one sequence x `box`
+// columns, starting at any multiple of 8 columns; outside it reads as zero.
+// False if the layout has no such map (then the element-wise path loads it).
+bool make_map(CUtensorMap* map, const void* p, int64_t B, int64_t T, int64_t cols, int64_t ld, int d, int box) {
+  if (reinterpret_cast<uintptr_t>(p) % 16 || ld % 8 || d % 8 || T * ld * 2 >= (int64_t(1) << 40) || T > INT32_MAX - kC ||
+      cols > INT32_MAX - box)
+    return false;
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(T * ld * 2)};
+  const cuuint32_t boxes[3] = {(cuuint32_t)box, (cuuint32_t)kC, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DK, bool F32>
 cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
   auto kern = chunk_kernel<DK, F32>;
@@ -772,15 +1046,19 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     __atomic_store_n(&configured[dev], 1, __ATOMIC_RELAXED);
   }
-  const int es = F32 ? 4 : 2;
-  auto rows16 = [&](const void* p, int64_t ld, int d) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0 && (d * es) % 16 == 0;
-  };
-  const int vec_kq = rows16(a.k, a.ld_k, a.dk) && rows16(a.q, a.ld_q, a.dk) && a.dk % 8 == 0;
-  const int vec_v = rows16(a.v, a.ld_v, a.dv);
+  CUtensorMap mk = {}, mq = {}, mv = {};
+  int vec_kq, vec_v = 0;
+  if (F32) {
+    auto rows16 = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0; };
+    vec_kq = rows16(a.k, a.ld_k) && rows16(a.q, a.ld_q) && a.dk % 8 == 0;
+  } else {
+    const int64_t kc = (int64_t)a.Hk * a.dk, vc = (int64_t)a.Hv * a.dv;
+    vec_kq = make_map(&mk, a.k, a.B, a.T, kc, a.ld_k, a.dk, DK) && make_map(&mq, a.q, a.B, a.T, kc, a.ld_q, a.dk, DK);
+    vec_v = make_map(&mv, a.v, a.B, a.T, vc, a.ld_v, a.dv, kM);
+  }
   const int64_t ctas = a.B * a.Hv * ((a.dv + kM - 1) / kM);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, vec_kq, vec_v);
+  kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, vec_kq, vec_v);
   return cudaGetLastError();
 }
 
