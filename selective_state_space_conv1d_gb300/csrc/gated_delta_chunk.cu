@@ -34,14 +34,15 @@
 // one (exact).  Two halves in bf16 would hold
 // 16 bits: measured in simulation 4e-6 of the state, against 2e-7 here and 1e-7
 // for plain f32.  The scales keep every operand below 2^14 whatever the inputs'
-// magnitudes: S by its largest value, R by the bound max|v| + max_i(e^{G_i}
-// |k_i|_1) max|S|, T and W by their largest row sum, which bounds U.
+// magnitudes: S and R by their largest values (per value component), T and W by
+// their largest row sum, which bounds U.
 //
 // One CTA per (sequence, value head, 128 value components), warps specialised:
 //   0-7   epilogues 1-3, output, the state in registers (lane = component; two
 //         warps per lane quarter, each half the columns)
 //   8-11  prepare: A and P from [K; Q] K^T and the gates, T and W to shared memory
-//   12-14 load: tensor copies of K, Q, V tiles, K and Q to scaled f16, the gates
+//   12-13 load: tensor copies of K, Q, V tiles, K and Q to scaled f16
+//   14    the gates
 //   15    issues the MMAs
 // Every warp runs straight through its part of a chunk once, so the loop bodies
 // are kept rolled where registers allow it: with everything unrolled the code
@@ -64,7 +65,7 @@ namespace {
 constexpr int kC = 64;            // tokens per chunk
 constexpr int kM = 128;           // value components per CTA
 constexpr int kThreads = 16 * 32;
-constexpr int kLoadWarps = 3, kLoadThreads = 32 * kLoadWarps, kMmaWarp = 15;
+constexpr int kLoadWarps = 2, kLoadThreads = 32 * kLoadWarps, kGateWarp = 14, kMmaWarp = 15;
 constexpr int kGateSlots = 4;
 constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
@@ -72,7 +73,7 @@ __device__ int g_delta_faults = 0;
 
 constexpr int kLdA = kC + 4;      // row stride of A and P in shared memory, floats
 
-// per-chunk scalars and vectors, written by the load and prepare warps
+// per-chunk scalars and vectors, written by the gate and prepare warps
 struct Gates {
   float col_hi[kC], col_lo[kC];          // G_j + ek_j as two floats
   float row_hi[2 * kC], row_lo[2 * kC];  // G_i - ek_i (keys), G_i - eq_i (queries)
@@ -80,9 +81,11 @@ struct Gates {
   float fx[kC];    // e^{G_i} 2^{-ek_i}
   float fd[kC];    // e^{G_63 - G_i} 2^{-ek_i}
   float fq[kC];    // scale e^{G_i} 2^{-eq_i}
+  float past[32];  // e^{G_31 - G_j} 2^{-ek_j}, j < 32
+  float since[2][32];  // -beta_i e^{G_i - G_31} 2^{-ek_i}, e^{G_i - G_31} 2^{-eq_i}, i = 32 ..
   float total;     // e^{G_63}
-  float k_bound;   // max_i e^{G_i} |k_i|_1 (bound)
   int t_exp, w_exp;  // T and W are held as 2^{t_exp} T, 2^{w_exp} W   (prepare warps)
+  float pad;
   float sum_t[4], sum_w[4];  // largest row sums, one per prepare warp
 };
 
@@ -174,6 +177,13 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// four 8 x 8 matrices of 16-bit values, lane l holding two of row l / 4 of each
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 // A wait that did not succeed at once.  One that runs out sets the fault and
 // abort flags; every role then runs on through its loop without waiting, so
 // that all named barriers are met and the CTA ends.
@@ -227,18 +237,29 @@ __device__ __forceinline__ void unpack8(float (&f)[8], uint4 a) {  // bf16
   for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 
-// a base-2 logarithm la log2(e) as a 2^-40 fixed-point number, la in [-200, 0]
-__device__ __forceinline__ long long log2_fixed(float la) {
-  const float p = la * 1.44269502f;                                    // log2(e) as two floats
-  const float e = fmaf(la, 1.44269502f, -p) + la * 1.92596299e-8f;
-  return __float2ll_rn(p * 1099511627776.0f) + __float2ll_rn(e * 1099511627776.0f);
+// A number as the unevaluated sum of two floats
+struct Two {
+  float h, l;
+};
+// log2(e) la
+__device__ __forceinline__ Two two_log2(float la) {
+  const float p = la * 1.44269502f;  // log2(e) is 1.44269502 + 1.92596299e-8
+  return Two{p, fmaf(la, 1.44269502f, -p) + la * 1.92596299e-8f};
 }
-// the number as two floats
-__device__ __forceinline__ float2 fixed_split(long long x) {
-  const float hi = __ll2float_rn(x);
-  const float lo = __ll2float_rn(x - __float2ll_rn(hi));
-  return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+  const float s = a.h + b.h, t = s - a.h;
+  const float e = (a.h - (s - t)) + (b.h - t) + (a.l + b.l);
+  const float h = s + e;
+  return Two{h, e - (h - s)};
 }
+__device__ __forceinline__ Two two_shfl_up(Two a, int o) {
+  return Two{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+}
+__device__ __forceinline__ Two two_shfl(Two a, int lane) {
+  return Two{__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
+// 2^(a - b)
+__device__ __forceinline__ float two_exp2(Two a, Two b) { return ex2_approx((a.h - b.h) + (a.l - b.l)); }
 
 template <int DK, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, const __grid_constant__ CUtensorMap map_k,
@@ -277,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   const int n_chunks = (int)((g.T + kC - 1) / kC);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
+    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, kLoadThreads + 32), mbar_init(kq_empty + 8 * s, 1);
     mbar_init(v_full, vec_v ? 1 : kLoadThreads), mbar_init(v_empty, 8);
     mbar_init(raw_full, 1), mbar_init(tp_full, 4), mbar_init(tp_empty, 1);
     for (int s = 0; s < 2; ++s) mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, 4);
@@ -331,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       s[j] = x.x, s[j + 1] = x.y, s[j + 2] = x.z, s[j + 3] = x.w;
     }
-    float s_max = 0.0f;
     int s_exp = 0;  // S is held as 2^{s_exp} S
     // this lane's state to tensor memory, scaled, in two halves: of every 16
     // columns 8 of hi, 8 of lo
@@ -342,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (mx > 3.4e38f) mx = 1.0f;  // not finite: the component is lost, any scale will do
       max_s[half * kM + lane_n] = mx;
       named_barrier(3 + quad, 64);
-      s_max = fmaxf(mx, max_s[(1 - half) * kM + lane_n]);
-      s_exp = 13 - exponent_of(s_max);
+      s_exp = 13 - exponent_of(fmaxf(mx, max_s[(1 - half) * kM + lane_n]));
       s_exp = s_exp > 120 ? 120 : s_exp;
       const float2 c = make_float2(pow2(s_exp), pow2(s_exp));
 #pragma unroll
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     put_state();
 
     const int i0 = half * 32;  // this thread's tokens of a chunk
-    const int64_t y_step = g.y_bf16 ? 2 * g.ld_y : 4 * g.ld_y;
+    const uint32_t y_step = (uint32_t)g.ld_y * (g.y_bf16 ? 2 : 4);  // bytes; a chunk's rows fit 32 bits
     char* y_at = reinterpret_cast<char*>(g.y) +
                  ((b * g.T + i0) * g.ld_y + (int64_t)h * g.dv + n) * (g.y_bf16 ? 2 : 4);
     for (int c = 0; c < n_chunks; ++c) {
@@ -378,41 +397,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         if (!F32) return to_f32(v_tile[i * kM]);
         return live && i0 + i < left ? to_f32(v_global[i * g.ld_v]) : 0.0f;
       };
-      // scale of R from its bound; the largest |v| of the lane needs the partner's tokens
-      if (!F32) wait(v_full, c);
-      float mx = 0.0f;
-#pragma unroll 16
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(value(i)));
-      if (mx > 3.4e38f) mx = 1.0f;
-      max_v[half * kM + lane_n] = mx;
-      named_barrier(3 + quad, 64);
-      mx = fmaxf(mx, max_v[(1 - half) * kM + lane_n]);
-      wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
-      int r_exp = 9 - exponent_of(fmaf(gt.k_bound, s_max, mx));
-      r_exp = r_exp > 120 ? 120 : r_exp;
+      int r_exp;  // R is held as 2^{r_exp} R
       {  // epilogue 1: R^T = V^T - fx D1; of every 16 columns 8 of hi, 8 of lo
-        const float cv = pow2(r_exp), cx = pow2(r_exp - s_exp);
+        wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
+        if (!F32) wait(v_full, c);
+        const float cx = pow2(-s_exp);
+        float2 r[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = make_float2(value(2 * j), value(2 * j + 1));
         wait(x_full, c);
         tcgen05_fence_after();
-#pragma unroll 1
+        float mx = 0.0f;
+#pragma unroll
         for (int i = 0; i < 32; i += 16) {
           uint32_t x[16];
           tmem_ld16(t_lane + kColX + (uint32_t)(i0 + i), x);
-          uint32_t hi[8], lo[8];
-          float fx[16], v[16];
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(&fx[j]) = *reinterpret_cast<const float4*>(&gt.fx[i0 + i + j]);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = value(i + j);
           tmem_wait(x);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 t = __fmul2_rn(make_float2(fx[j], fx[j + 1]),
-                                        __fmul2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
-                                                   make_float2(-cx, -cx)));
-            const float2 r = __ffma2_rn(make_float2(cv, cv), make_float2(v[j], v[j + 1]), t);
-            split2(r.x, r.y, hi[j / 2], lo[j / 2]);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 fx = *reinterpret_cast<const float4*>(&gt.fx[i0 + i + j]);
+            const float2 f[2] = {make_float2(fx.x, fx.y), make_float2(fx.z, fx.w)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2& t = r[(i + j) / 2 + e];
+              t = __ffma2_rn(__fmul2_rn(f[e], make_float2(-cx, -cx)),
+                             make_float2(__uint_as_float(x[j + 2 * e]), __uint_as_float(x[j + 2 * e + 1])), t);
+              mx = fmaxf(fmaxf(mx, fabsf(t.x)), fabsf(t.y));
+            }
+          }
+        }
+        if (mx > 3.4e38f) mx = 1.0f;
+        max_v[half * kM + lane_n] = mx;
+        named_barrier(3 + quad, 64);  // the other 32 tokens of the lane
+        r_exp = 9 - exponent_of(fmaxf(mx, max_v[(1 - half) * kM + lane_n]));
+        r_exp = r_exp > 120 ? 120 : r_exp;
+        const float cr = pow2(r_exp);
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 t = __fmul2_rn(r[i / 2 + j], make_float2(cr, cr));
+            split2(t.x, t.y, hi[j], lo[j]);
           }
           tmem_st8(t_lane + kColX + (uint32_t)(i0 + i), hi);
           tmem_st8(t_lane + kColX + (uint32_t)(i0 + i + 8), lo);
@@ -448,32 +474,44 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         wait(o_full, c);
         tcgen05_fence_after();
         const float cq = pow2(-s_exp), cw = g.scale * pow2(-r_exp - gt.w_exp);
-        const int rows = live ? left : 0;
-        char* p = y_at;
+        const int rows = live ? left - i0 : 0;  // of this thread's 32 tokens
 #pragma unroll 1
-        for (int i = i0; i < i0 + 32; i += 8) {
+        for (int i = 0; i < 32; i += 8) {
           uint32_t xq[8], xo[8];
-          tmem_ld8(t_lane + kColQ + (uint32_t)i, xq);
-          tmem_ld8(t_lane + kColO + (uint32_t)i, xo);
-          float fq[8];
+          tmem_ld8(t_lane + kColQ + (uint32_t)(i0 + i), xq);
+          tmem_ld8(t_lane + kColO + (uint32_t)(i0 + i), xo);
+          float2 o[4];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4)
-            *reinterpret_cast<float4*>(&fq[j]) = *reinterpret_cast<const float4*>(&gt.fq[i + j]);
+          for (int j = 0; j < 8; j += 4) {
+            const float4 fq = *reinterpret_cast<const float4*>(&gt.fq[i0 + i + j]);
+            o[j / 2] = __fmul2_rn(make_float2(fq.x, fq.y), make_float2(cq, cq));
+            o[j / 2 + 1] = __fmul2_rn(make_float2(fq.z, fq.w), make_float2(cq, cq));
+          }
           tmem_wait(xq);
           tmem_wait(xo);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float o = fmaf(__uint_as_float(xo[j]), cw, fq[j] * (__uint_as_float(xq[j]) * cq));
-            if (i + j < rows) {
-              if (g.y_bf16)
-                *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(o);
-              else
-                *reinterpret_cast<float*>(p) = o;
+          for (int j = 0; j < 4; ++j)
+            o[j] = __ffma2_rn(make_float2(__uint_as_float(xo[2 * j]), __uint_as_float(xo[2 * j + 1])), make_float2(cw, cw),
+                              __fmul2_rn(o[j], make_float2(__uint_as_float(xq[2 * j]), __uint_as_float(xq[2 * j + 1]))));
+          uint32_t at = (uint32_t)i * y_step;
+          if (g.y_bf16) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              const __nv_bfloat162 w = __floats2bfloat162_rn(o[j / 2].x, o[j / 2].y);
+              if (i + j < rows) *reinterpret_cast<__nv_bfloat16*>(y_at + at) = w.x;
+              at += y_step;
+              if (i + j + 1 < rows) *reinterpret_cast<__nv_bfloat16*>(y_at + at) = w.y;
+              at += y_step;
             }
-            p += y_step;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (i + j < rows) *reinterpret_cast<float*>(y_at + at) = (j & 1) ? o[j / 2].y : o[j / 2].x;
+              at += y_step;
+            }
           }
         }
-        y_at += kC * y_step;
+        y_at += (int64_t)kC * y_step;
       }
       {  // epilogue 3: S = e^G S + D3
         const float total = gt.total, cd = pow2(-r_exp - gt.t_exp);
@@ -531,33 +569,49 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       tcgen05_fence_after();
       named_barrier(1, 128);  // the previous chunk's A and P are read
       {
-        const float rh = gt.row_hi[row], rl = gt.row_lo[row];
-        const float scale_row = is_t ? gt.beta[i] : 1.0f;
-        const int last = is_t ? i - 1 : i;  // A is strictly lower, P lower
+        // -A and P to shared memory, a row per thread
         float* dst = (is_t ? a_s : p_s) + i * kLdA;
-#pragma unroll 1
-        for (int j0 = 0; j0 < (upper ? kC : 32); j0 += 32) {
-          uint32_t d[32];
-          tmem_ld32(t_d0 + (uint32_t)j0, d);
+        const uint32_t t_diag = t_d0 + (upper ? 32 : 0);
+        uint32_t d[32];
+        if (upper) {
+          // the 32 columns before these rows' own: the decay factors at token 31
+          const float since = gt.since[is_t ? 0 : 1][lane];
+          tmem_ld32(t_d0, d);
           tmem_wait(d);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 ch = *reinterpret_cast<const float4*>(&gt.col_hi[j0 + j]);
-            const float4 cl = *reinterpret_cast<const float4*>(&gt.col_lo[j0 + j]);
-            const float chs[4] = {ch.x, ch.y, ch.z, ch.w}, cls[4] = {cl.x, cl.y, cl.z, cl.w};
-            float o[4];
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const float2 w = __fadd2_rn(__fadd2_rn(make_float2(rh, rh), make_float2(-chs[e], -chs[e + 1])),
-                                          __fadd2_rn(make_float2(rl, rl), make_float2(-cls[e], -cls[e + 1])));
-              const float2 v = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
-                                                     make_float2(ex2_approx(w.x), ex2_approx(w.y))),
-                                          make_float2(scale_row, scale_row));
-              o[e] = j0 + j + e <= last ? v.x : 0.0f;
-              o[e + 1] = j0 + j + e + 1 <= last ? v.y : 0.0f;
-            }
-            *reinterpret_cast<float4*>(dst + j0 + j) = make_float4(o[0], o[1], o[2], o[3]);
+            const float4 past = *reinterpret_cast<const float4*>(&gt.past[j]);
+            const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(past.x, past.y), make_float2(since, since)),
+                                         make_float2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])));
+            const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(past.z, past.w), make_float2(since, since)),
+                                         make_float2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])));
+            *reinterpret_cast<float4*>(dst + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
           }
+          dst += 32;
+        }
+        tmem_ld32(t_diag, d);
+        const float rh = gt.row_hi[row], rl = gt.row_lo[row];
+        const float scale_row = is_t ? -gt.beta[i] : 1.0f;
+        const int last = is_t ? lane - 1 : lane;  // A is strictly lower, P lower
+        const float* col_hi = gt.col_hi + (upper ? 32 : 0);
+        const float* col_lo = gt.col_lo + (upper ? 32 : 0);
+        tmem_wait(d);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 ch = *reinterpret_cast<const float4*>(col_hi + j), cl = *reinterpret_cast<const float4*>(col_lo + j);
+          const float chs[4] = {ch.x, ch.y, ch.z, ch.w}, cls[4] = {cl.x, cl.y, cl.z, cl.w};
+          float o[4];
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float2 w = __fadd2_rn(__fadd2_rn(make_float2(rh, rh), make_float2(-chs[e], -chs[e + 1])),
+                                        __fadd2_rn(make_float2(rl, rl), make_float2(-cls[e], -cls[e + 1])));
+            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
+                                                   make_float2(ex2_approx(w.x), ex2_approx(w.y))),
+                                        make_float2(scale_row, scale_row));
+            o[e] = j + e <= last ? v.x : 0.0f;
+            o[e + 1] = j + e + 1 <= last ? v.y : 0.0f;
+          }
+          *reinterpret_cast<float4*>(dst + j) = make_float4(o[0], o[1], o[2], o[3]);
         }
       }
       tcgen05_fence_before();
@@ -573,12 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         for (int q = 0; q < 8; ++q) x[q] = make_float2(2 * q == r ? 1.0f : 0.0f, 2 * q + 1 == r ? 1.0f : 0.0f);
 #pragma unroll
         for (int k = 15; k >= 1; --k) {
-          const float nx = (k & 1) ? -x[k / 2].y : -x[k / 2].x;
+          const float xk = (k & 1) ? x[k / 2].y : x[k / 2].x;
 #pragma unroll
           for (int q = 0; q < (k + 3) / 4; ++q) {
             const float4 a = *reinterpret_cast<const float4*>(blk + k * kLdA + 4 * q);
-            x[2 * q] = __ffma2_rn(make_float2(nx, nx), make_float2(a.x, a.y), x[2 * q]);
-            if (4 * q + 2 < k) x[2 * q + 1] = __ffma2_rn(make_float2(nx, nx), make_float2(a.z, a.w), x[2 * q + 1]);
+            x[2 * q] = __ffma2_rn(make_float2(xk, xk), make_float2(a.x, a.y), x[2 * q]);
+            if (4 * q + 2 < k) x[2 * q + 1] = __ffma2_rn(make_float2(xk, xk), make_float2(a.z, a.w), x[2 * q + 1]);
           }
         }
         __syncwarp();
@@ -591,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       named_barrier(1, 128);
       // X (I + A) = [I; P] by blocks of 16 columns, the last first: X_k = B_k D_k,
-      // then B_j -= X_k A_kj for the blocks before it
+      // then B_j += X_k (-A_kj) for the blocks before it
       float t[8][4], w[8][4];
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
@@ -622,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                bm[kk][nn][e].set((j < k ? -1.0f : 1.0f) * a_s[(16 * k + 8 * kk + fc + e) * kLdA + 16 * j + 8 * nn + fr]);
+                bm[kk][nn][e].set(a_s[(16 * k + 8 * kk + fc + e) * kLdA + 16 * j + 8 * nn + fr]);
           auto product = [&](float (&x)[8][4], uint32_t (&xh)[2][4], uint32_t (&xl)[2][4], bool solved) {
             float acc[2][4];
 #pragma unroll
@@ -687,41 +741,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         if (c > 0) wait(tp_empty, c - 1);
         if (quad == 0 && lane == 0) gt.t_exp = te, gt.w_exp = we;
         const float ct = pow2(te), cw = pow2(we);
+        // lane l addresses row l % 8 of matrix l / 8: rows 0-7 and 8-15 of one
+        // granule of 8 columns, then of the next; granule q of row r at q ^ (r % 8)
+        const uint32_t at = base + L::kOffTp + (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * 128 +
+                                                          ((((lane >> 4) & 1) ^ (lane & 7)) << 4));
+        const uint32_t at_t = at + rt * 2048, at_w = at + 8192 + rw * 2048;
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
+        for (int nt = 0; nt < 8; nt += 2) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // rows 16 rt + fr + 8 e of T, 64 + 16 rw + fr + 8 e of [T; W]; granule nt at nt ^ (row % 8)
-            const uint32_t at = base + L::kOffTp + (uint32_t)((fr + 8 * e) * 128 + ((nt ^ fr) << 4) + fc * 2);
-            uint32_t hi, lo;
-            split2(t[nt][2 * e] * ct, t[nt][2 * e + 1] * ct, hi, lo);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + rt * 2048), "r"(hi) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + rt * 2048 + 16384), "r"(lo) : "memory");
-            split2(w[nt][2 * e] * cw, w[nt][2 * e + 1] * cw, hi, lo);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8192 + rw * 2048), "r"(hi) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8192 + rw * 2048 + 16384), "r"(lo) : "memory");
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = __fmul2_rn(make_float2(t[nt + e / 2][2 * (e & 1)], t[nt + e / 2][2 * (e & 1) + 1]),
+                                        make_float2(ct, ct));
+            split2(v.x, v.y, hi[e], lo[e]);
           }
+          stmatrix4(at_t ^ (uint32_t)(nt << 4), hi);
+          stmatrix4((at_t ^ (uint32_t)(nt << 4)) + 16384, lo);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = __fmul2_rn(make_float2(w[nt + e / 2][2 * (e & 1)], w[nt + e / 2][2 * (e & 1) + 1]),
+                                        make_float2(cw, cw));
+            split2(v.x, v.y, hi[e], lo[e]);
+          }
+          stmatrix4(at_w ^ (uint32_t)(nt << 4), hi);
+          stmatrix4((at_w ^ (uint32_t)(nt << 4)) + 16384, lo);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(tp_full);
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < kGateWarp) {
     // --------------------------------------------------------------- load ----
     const int lw = warp - 12, lt = threadIdx.x - 12 * 32;
     constexpr int kLanes = DK / 8;           // lanes per row
     constexpr int kRowsPer = 32 / kLanes;    // rows per warp and pass
     constexpr int kStep = kLoadWarps * kRowsPer;  // rows per pass
     const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-    const float neg_A = -expf(g.A_log[h]);
-    const float dt_bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
     const int valid = g.dk - col;            // of this lane's eight components
     const In* k_base = reinterpret_cast<const In*>(g.k) + b * g.T * g.ld_k + (int64_t)hk * g.dk;
     const In* q_base = reinterpret_cast<const In*>(g.q) + b * g.T * g.ld_q + (int64_t)hk * g.dk;
     const In* v_base = reinterpret_cast<const In*>(g.v) + b * g.T * g.ld_v + (int64_t)h * g.dv + tile * kM;
-    const In* a_base = reinterpret_cast<const In*>(g.a) + b * g.T * g.ld_a + h;
-    const In* b_base = reinterpret_cast<const In*>(g.b) + b * g.T * g.ld_b + h;
     const bool staged = !F32 && vec_kq;      // K and Q through tensor copies
     auto tokens = [&](int c) { return (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC); };
     // K and Q rows of chunk c (tokens past the end read as zero)
@@ -732,19 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         tma_load_3d(base + L::kOffRaw + kC * DK * 2, &map_q, hk * g.dk, c * kC, (int)b, raw_full);
       }
     };
-    float a_next[2] = {0.0f, 0.0f}, b_next[2] = {0.0f, 0.0f};
-    auto fetch_gates = [&](int c) {  // tokens lane and lane + 32 (warp 13)
-      const int left = tokens(c);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = lane + 32 * u;
-        const int64_t t = (int64_t)c * kC + i;
-        a_next[u] = i < left ? to_f32(a_base[t * g.ld_a]) : 0.0f;
-        b_next[u] = i < left ? to_f32(b_base[t * g.ld_b]) : 0.0f;
-      }
-    };
     if (staged && lw == 0) copy_kq(0);
-    if (lw == 1) fetch_gates(0);
     for (int c = 0; c < n_chunks; ++c) {
       const int ks = c % L::kKqStages;
       const int left = tokens(c);
@@ -754,55 +802,87 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       // K (rows 0-63) and Q (64-127), each row scaled to [2^13, 2^14)
       // kBatch rows' loads and reductions are in flight together
       constexpr int kBatch = F32 ? 4 : 8;
+      static_assert(2 * kC % (kBatch * kStep) == 0, "whole batches");
 #pragma unroll 1
-      for (int r0 = lw * kRowsPer + sub; r0 < 2 * kC; r0 += kBatch * kStep) {  // as often for every lane of a warp
-        float f[kBatch][8], mx[kBatch];
-        if (staged) {
+      for (int r0 = lw * kRowsPer + sub; r0 < 2 * kC; r0 += kBatch * kStep) {
+        float f[kBatch][8];
+        int ex[kBatch];  // floor(log2) of the row's largest value
+        if constexpr (!F32) {
           uint4 x[kBatch];
+          if (staged) {
 #pragma unroll
-          for (int p = 0; p < kBatch; ++p) {
-            const int r = r0 + p * kStep < 2 * kC ? r0 + p * kStep : r0;
-            x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + r * DK * 2 + col * 2);
+            for (int p = 0; p < kBatch; ++p) {
+              x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + (r0 + p * kStep) * DK * 2 + col * 2);
+              if (valid <= 0) x[p] = make_uint4(0, 0, 0, 0);  // columns past dk are another head's
+            }
+          } else {
+#pragma unroll 1
+            for (int p = 0; p < kBatch; ++p) {
+              const int r = r0 + p * kStep, i = r & (kC - 1);
+              const int64_t t = (int64_t)c * kC + i;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
+              uint32_t e[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) e[j] = i < left && j < valid ? src[j] : 0;
+              // by way of the rows' place in the staging buffer (this thread's own granules)
+              *reinterpret_cast<uint4*>(gbase + L::kOffRaw + r * DK * 2 + col * 2) =
+                  make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+            }
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+              x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + (r0 + p * kStep) * DK * 2 + col * 2);
+          }
+          // bit patterns of |x| order as the values do; two rows share a word
+#pragma unroll
+          for (int p = 0; p < kBatch; p += 2) {
+            uint32_t m[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              m[u] = __vmaxu2(__vmaxu2(x[p + u].x & 0x7fff7fffu, x[p + u].y & 0x7fff7fffu),
+                              __vmaxu2(x[p + u].z & 0x7fff7fffu, x[p + u].w & 0x7fff7fffu));
+            uint32_t both = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+            ex[p] = (int)((both >> 7) & 255) - 127;
+            ex[p + 1] = (int)(both >> 23) - 127;
           }
 #pragma unroll
-          for (int p = 0; p < kBatch; ++p) {
-            // columns past dk are another head's, rows past the end zero
-            if (valid <= 0) x[p] = make_uint4(0, 0, 0, 0);
-            unpack8(f[p], x[p]);
-          }
+          for (int p = 0; p < kBatch; ++p) unpack8(f[p], x[p]);
         } else {
 #pragma unroll
           for (int p = 0; p < kBatch; ++p) {
             const int r = r0 + p * kStep, i = r & (kC - 1);
-            const bool in = i < left && r < 2 * kC;
+            const bool in = i < left;
             const int64_t t = in ? (int64_t)c * kC + i : 0;
-            const In* src = (r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
-            if (F32 && vec_kq) {
+            const float* src = reinterpret_cast<const float*>(r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
+            if (vec_kq) {
               float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
-              if (in && valid > 0) lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + 4);
+              if (in && valid > 0) lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
               f[p][0] = lo.x, f[p][1] = lo.y, f[p][2] = lo.z, f[p][3] = lo.w;
               f[p][4] = hi.x, f[p][5] = hi.y, f[p][6] = hi.z, f[p][7] = hi.w;
             } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) f[p][j] = in && j < valid ? to_f32(src[j]) : 0.0f;
+              for (int j = 0; j < 8; ++j) f[p][j] = in && j < valid ? src[j] : 0.0f;
             }
           }
+          float mx[kBatch];
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) {
+            mx[p] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mx[p] = fmaxf(mx[p], fabsf(f[p][j]));
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) ex[p] = exponent_of(mx[p]);
         }
-#pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          mx[p] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mx[p] = fmaxf(mx[p], fabsf(f[p][j]));
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-          for (int p = 0; p < kBatch; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
           const int r = r0 + p * kStep;
-          int e = 13 - exponent_of(mx[p]);
-          e = e > 120 ? 120 : e;  // a zero row: 120, so that its bound below is nothing
+          const int e = ex[p] < -107 ? 120 : 13 - ex[p];
           const float cs = pow2(e);
           uint32_t hi[4], lo[4];
 #pragma unroll
@@ -815,66 +895,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
               hi[j] = *reinterpret_cast<const uint32_t*>(&t);
             }
           }
-          if (r < 2 * kC) {
-            if (col == 0) exps[r] = e;
-            const uint32_t at =
-                base + ks * L::kKq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
-            st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
-            if (F32) st_shared16(at + L::kKqTerm, lo[0], lo[1], lo[2], lo[3]);
-          }
+          if (col == 0) exps[r] = e;
+          const uint32_t at =
+              base + ks * L::kKq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
+          st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
+          if (F32) st_shared16(at + L::kKqTerm, lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_proxy_async_smem();
-      named_barrier(2, kLoadThreads);  // every row's exponent is there, the raw rows are read
+      named_barrier(2, kLoadThreads + 32);  // every row's exponent is there, the raw rows are read
       if (staged && lw == 0 && c + 1 < n_chunks) copy_kq(c + 1);
-      if (lw == 1) {
-        // the gates of tokens lane and lane + 32: base-2 logarithms summed in
-        // 64-bit fixed point and kept as two floats, so that differences of
-        // far-decayed tokens keep 32-bit accuracy.  alpha below e^-200 is 0 in
-        // f32 all the same.
-        Gates& gt = gates[c % kGateSlots];
-        long long G[2];
-        float be[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bool in = lane + 32 * u < left;
-          const float la = gdr_log_alpha(a_next[u], dt_bias, neg_A);
-          G[u] = in ? log2_fixed(la < -200.0f ? -200.0f : la) : 0;
-          be[u] = in ? gdr_beta(b_next[u]) : 0.0f;
-        }
-        if (c + 1 < n_chunks) fetch_gates(c + 1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const long long t = __shfl_up_sync(0xffffffffu, G[u], o);
-            if (lane >= o) G[u] += t;
-          }
-        }
-        G[1] += __shfl_sync(0xffffffffu, G[0], 31);
-        const long long last = __shfl_sync(0xffffffffu, G[1], 31);
-        float kb = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = lane + 32 * u;
-          const int ek = exps[i], eq = exps[kC + i];
-          const float2 cj = fixed_split(G[u] + ((long long)ek << 40)), rk = fixed_split(G[u] - ((long long)ek << 40)),
-                       rq = fixed_split(G[u] - ((long long)eq << 40));
-          const float eg = ex2_approx(__ll2float_rn(G[u]) * 9.094947017729282e-13f);
-          gt.col_hi[i] = cj.x, gt.col_lo[i] = cj.y;
-          gt.row_hi[i] = rk.x, gt.row_lo[i] = rk.y;
-          gt.row_hi[kC + i] = rq.x, gt.row_lo[kC + i] = rq.y;
-          gt.beta[i] = be[u];
-          gt.fx[i] = eg * pow2(-ek);
-          gt.fd[i] = ex2_approx(__ll2float_rn(last - G[u]) * 9.094947017729282e-13f) * pow2(-ek);
-          gt.fq[i] = g.scale * eg * pow2(-eq);
-          // |k|_1 <= DK max|k| < DK 2^{14 - ek}
-          kb = fmaxf(kb, eg * (float)DK * pow2(14 - ek));
-        }
-        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(kb));
-        if (lane == 0)
-          gt.k_bound = __uint_as_float(top), gt.total = ex2_approx(__ll2float_rn(last) * 9.094947017729282e-13f);
-      }
       mbar_arrive(kq_full + 8 * ks);
       // V (bf16); rows past the sequence's end are zero, columns past the head's
       // are lanes that nothing reads
@@ -896,6 +926,76 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           mbar_arrive(v_full);
         }
       }
+    }
+  } else if (warp == kGateWarp) {
+    // -------------------------------------------------------------- gates ----
+    // tokens lane and lane + 32 of a chunk: base-2 logarithms of alpha, summed and
+    // kept as two floats each, so that differences between far-decayed tokens keep
+    // 32-bit accuracy.  alpha below e^-200 is 0 in f32 all the same.
+    const float neg_A = -expf(g.A_log[h]);
+    const float dt_bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
+    const In* a_base = reinterpret_cast<const In*>(g.a) + b * g.T * g.ld_a + h;
+    const In* b_base = reinterpret_cast<const In*>(g.b) + b * g.T * g.ld_b + h;
+    float a_next[2], b_next[2];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t t = (int64_t)c * kC + lane + 32 * u;
+        a_next[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
+        b_next[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
+      }
+    };
+    fetch(0);
+    for (int c = 0; c < n_chunks; ++c) {
+      Two G[2];
+      float be[2];
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        const float a = u ? a_next[1] : a_next[0], bb = u ? b_next[1] : b_next[0];
+        const float la = gdr_log_alpha(a, dt_bias, neg_A);
+        Two x = two_log2(la < -200.0f ? -200.0f : la);
+        const float y = gdr_beta(bb);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const Two t = two_shfl_up(x, o), sum = two_add(x, t);
+          if (lane >= o) x = sum;
+        }
+        if (u)
+          G[1] = x, be[1] = y;
+        else
+          G[0] = x, be[0] = y;
+      }
+      if (c + 1 < n_chunks) fetch(c + 1);
+      const Two mid = two_shfl(G[0], 31);
+      G[1] = two_add(G[1], mid);
+      const Two last = two_shfl(G[1], 31);
+      const int* exps = reinterpret_cast<const int*>(gbase + L::kOffExp) + (c & 1) * 2 * kC;
+      Gates& gt = gates[c % kGateSlots];
+      named_barrier(2, kLoadThreads + 32);  // the rows' exponents are there, this slot's last readers gone
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        const float ek = (float)exps[i], eq = (float)exps[kC + i];
+        const float ik = pow2(-exps[i]), iq = pow2(-exps[kC + i]);
+        const Two cj = two_add(G[u], Two{ek, 0.0f}), rk = two_add(G[u], Two{-ek, 0.0f}), rq = two_add(G[u], Two{-eq, 0.0f});
+        const float eg = ex2_approx(G[u].h + G[u].l);
+        gt.col_hi[i] = cj.h, gt.col_lo[i] = cj.l;
+        gt.row_hi[i] = rk.h, gt.row_lo[i] = rk.l;
+        gt.row_hi[kC + i] = rq.h, gt.row_lo[kC + i] = rq.l;
+        gt.beta[i] = be[u];
+        gt.fx[i] = eg * ik;
+        gt.fd[i] = two_exp2(last, G[u]) * ik;
+        gt.fq[i] = g.scale * eg * iq;
+        if (u == 0) {
+          gt.past[lane] = two_exp2(mid, G[0]) * ik;
+        } else {
+          const float e = two_exp2(G[1], mid);
+          gt.since[0][lane] = -be[1] * e * ik;
+          gt.since[1][lane] = e * iq;
+        }
+      }
+      if (lane == 0) gt.total = ex2_approx(last.h + last.l);
+      mbar_arrive(kq_full + 8 * (c % L::kKqStages));
     }
   } else {
     // --------------------------------------------------------------- MMAs ----
@@ -1064,7 +1164,10 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-bool gated_delta_takes_chunks(const GatedDeltaArgs& a) { return a.dk <= 128 && a.T > 16; }
+// The chunks' output offsets inside a chunk are 32 bits.
+bool gated_delta_takes_chunks(const GatedDeltaArgs& a) {
+  return a.dk <= 128 && a.T > 16 && a.ld_y < (int64_t(1) << 23);
+}
 
 cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   (void)dev;
