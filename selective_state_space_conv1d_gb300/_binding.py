@@ -86,6 +86,8 @@ class _MambaLayer(ctypes.Structure):
 def load(path: str | None = None):
     """Load libmamba_ssm.so (built in-tree by build.py) and declare its ABI."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -618,52 +620,73 @@ MAMBA_NORM_L2 = 1
 MAMBA_ROTARY_INTERLEAVED = 2
 
 
-def _heads_ld(t, name, lead, H, d, dtype=None):
-    """Row stride of a [*lead, H, d] tensor (H * d dense columns per row, rows
-    (b*T + t)*ld apart); d is None for a [*lead, H] tensor."""
-    shape = (*lead, H) if d is None else (*lead, H, d)
-    if tuple(t.shape) != shape:
+def _heads_ld(t, name, shape, n_lead, cols, dtype):
+    """Row stride of a tensor of `shape`, [B, heads..] (n_lead 1) or [B, T,
+    heads..] (2), whose rows are `cols` dense columns, row (b, t) at (b*T + t)*ld.
+    The one-token calls are bound by such checks on the host: a contiguous
+    tensor is recognised without reading its strides."""
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    st, cols = t.stride(), H if d is None else H * d
-    n = len(lead)
-    if d is not None and ((d > 1 and st[-1] != 1) or (H > 1 and st[n] != d)) or d is None and H > 1 and st[n] != 1:
-        raise ValueError(f"{name}: heads must be dense inside a row, got strides {st}")
-    if n == 1:
-        return st[0] if lead[0] > 1 else cols
-    Bsz, T = lead
-    if T > 1:
-        if Bsz > 1 and st[0] != T * st[1]:
-            raise ValueError(f"{name}: batch stride {st[0]} != T * row stride {T * st[1]}")
-        return st[1]
-    return st[0] if Bsz > 1 else cols
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return cols
+    st = t.stride()
+    dense = 1
+    for i in range(len(shape) - 1, n_lead - 1, -1):
+        if shape[i] > 1 and st[i] != dense:
+            raise ValueError(f"{name}: heads must be dense inside a row, got strides {st}")
+        dense *= shape[i]
+    if n_lead == 1 or shape[1] == 1:
+        return st[0] if shape[0] > 1 else cols
+    if shape[0] > 1 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"{name}: batch stride {st[0]} != T * row stride {shape[1] * st[1]}")
+    return st[1]
 
 
-def _same_device(like, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+def _current_stream(stream, like):
+    """As _stream, for a CUDA tensor, without building a Stream object."""
+    import torch
+
+    if stream is None:
+        if not like.is_cuda:
+            raise ValueError(f"expected CUDA tensors, got one on {like.device}")
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead):
+def _f32_dense(t, name, shape):
+    """Pointer of an optional contiguous float32 tensor of `shape`."""
+    import torch
+
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 {shape} tensor, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, n_lead):
     """Shapes, dtypes and strides of a gated-delta call, checked before any
-    launch.  Returns (Hk, Hv, dk, dv, the activations' C arguments, the rest)."""
-    n = len(lead)
-    if q.dim() != n + 2 or v.dim() != n + 2:
-        raise ValueError(f"q and v must have {n + 2} dimensions, got {tuple(q.shape)} and {tuple(v.shape)}")
-    (Hk, dk), (Hv, dv) = q.shape[n:], v.shape[n:]
-    dt = v.dtype
-    acts = []
-    for name, t, H, d in (("q", q, Hk, dk), ("k", k, Hk, dk), ("v", v, Hv, dv), ("a", a, Hv, None),
-                          ("b", b, Hv, None)):
-        acts += [_ptr(t), _heads_ld(t, name, lead, H, d, dt)]
-    ld_y = _heads_ld(y, "y", lead, Hv, dv)
-    _f32_param(A_log, "A_log", (Hv,))
-    _f32_param(dt_bias, "dt_bias", (Hv,))
-    _same_device(v, y=y, q=q, k=k, a=a, b=b, A_log=A_log, dt_bias=dt_bias)
-    s = float(dk) ** -0.5 if scale is None else float(scale)
-    return Hk, Hv, dk, dv, [_ptr(y), ld_y, _dtype_code(y), *acts, _dtype_code(v), _ptr(A_log), _ptr(dt_bias), s]
+    launch (a tensor on another device is refused by the C ABI).  Returns (lead,
+    Hk, Hv, dk, dv, dtype code, the C arguments up to scale)."""
+    sq, sv = tuple(q.shape), tuple(v.shape)
+    if len(sq) != n_lead + 2 or len(sv) != n_lead + 2:
+        raise ValueError(f"q and v must have {n_lead + 2} dimensions, got {sq} and {sv}")
+    lead = sv[:n_lead]
+    Hk, dk = sq[n_lead:]
+    Hv, dv = sv[n_lead:]
+    if sq[:n_lead] != lead:
+        raise ValueError(f"q has shape {sq}, v {sv}")
+    dt, sa, kc, vc = v.dtype, lead + (Hv,), Hk * dk, Hv * dv
+    code = _dtype_code(v)
+    args = (y.data_ptr(), _heads_ld(y, "y", sv, n_lead, vc, y.dtype), code if y.dtype is dt else _dtype_code(y),
+            q.data_ptr(), _heads_ld(q, "q", sq, n_lead, kc, dt), k.data_ptr(), _heads_ld(k, "k", sq, n_lead, kc, dt),
+            v.data_ptr(), _heads_ld(v, "v", sv, n_lead, vc, dt), a.data_ptr(), _heads_ld(a, "a", sa, n_lead, Hv, dt),
+            b.data_ptr(), _heads_ld(b, "b", sa, n_lead, Hv, dt), code, _f32_dense(A_log, "A_log", (Hv,)),
+            _f32_dense(dt_bias, "dt_bias", (Hv,)), dk ** -0.5 if scale is None else scale)
+    return lead, Hk, Hv, dk, dv, code, args
 
 
 def mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, dtype_code=MAMBA_BF16) -> int:
@@ -682,33 +705,26 @@ def mamba_gated_delta_prefill(y, q, k, v, a, b, A_log, dt_bias=None, state_in=No
     and beta's pre-activations); A_log, dt_bias: [Hv] f32; states
     [B, Hv, dv, dk] f32 (state_out may be state_in).  scale: dk ** -0.5 if None.
     workspace: a uint8 scratch tensor (default: one kept per stream)."""
-    lead = tuple(v.shape[:2])
-    Hk, Hv, dk, dv, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead)
-    Bsz, T = lead
-    for name, s in (("state_in", state_in), ("state_out", state_out)):
-        _f32_param(s, name, (Bsz, Hv, dv, dk))
-    _same_device(v, state_in=state_in, state_out=state_out, workspace=workspace)
-    st = _stream(stream, v)
+    (Bsz, T), Hk, Hv, dk, dv, code, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, 2)
+    ss = (Bsz, Hv, dv, dk)
+    s_in, s_out = _f32_dense(state_in, "state_in", ss), _f32_dense(state_out, "state_out", ss)
+    st = _current_stream(stream, v)
+    lib = load()
     if workspace is None:
-        need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, _dtype_code(v)) if Hk and Hv else 0
+        need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, code) if Hk and Hv else 0
         workspace = _workspace(v.device, need, st) if need else None
     ws, nbytes = (_ptr(workspace), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
-    _check(load().mamba_gated_delta_prefill(*args, _ptr(state_in), _ptr(state_out), Bsz, T, Hk, Hv, dk, dv, ws,
-                                            nbytes, st))
+    _check(lib.mamba_gated_delta_prefill(*args, s_in, s_out, Bsz, T, Hk, Hv, dk, dv, ws, nbytes, st))
 
 
 def mamba_gated_delta_step_batched(y, q, k, v, a, b, A_log, dt_bias, state, layer, *, scale=None, stream=None):
     """One T=1 step of the gated delta rule in place on slab `layer` of state
     [n_layers, B, Hv, dv, dk]; q, k: [B, Hk, dk]; v, y: [B, Hv, dv]; a, b: [B, Hv]
     (row-strided views allowed)."""
-    lead = tuple(v.shape[:1])
-    Hk, Hv, dk, dv, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, lead)
-    if state.dim() != 5:
-        raise ValueError("state must be a [n_layers, B, Hv, dv, dk] tensor")
-    _f32_param(state, "state", (state.shape[0], lead[0], Hv, dv, dk))
-    _same_device(v, state=state)
-    _check(load().mamba_gated_delta_step_batched(*args, _ptr(state), int(layer), state.shape[0], lead[0], Hk, Hv, dk,
-                                                 dv, _stream(stream, v)))
+    (Bsz,), Hk, Hv, dk, dv, _, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, 1)
+    n_layers = state.shape[0] if state.dim() == 5 else 0
+    _check(load().mamba_gated_delta_step_batched(*args, _f32_dense(state, "state", (n_layers, Bsz, Hv, dv, dk)), layer,
+                                                 n_layers, Bsz, Hk, Hv, dk, dv, _current_stream(stream, v)))
 
 
 def mamba_qk_norm_rotary(q_out, k_out, q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, *,
@@ -722,44 +738,49 @@ def mamba_qk_norm_rotary(q_out, k_out, q, k, q_weight=None, k_weight=None, inv_f
 
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out must be given together")
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
+    sq = tuple(q.shape)
+    if len(sq) != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be 4-D [B, T, heads, d] tensors")
-    Bsz, T, Hq, d = q.shape
-    Hk = k.shape[2] if k is not None else 0
-    lead = (Bsz, T)
-    args = [_ptr(q_out), _heads_ld(q_out, "q_out", lead, Hq, d)]
-    args += [_ptr(k_out), _heads_ld(k_out, "k_out", lead, Hk, d, q_out.dtype)] if k is not None else [None, 0]
-    args += [_dtype_code(q_out), _ptr(q), _heads_ld(q, "q", lead, Hq, d)]
-    args += [_ptr(k), _heads_ld(k, "k", lead, Hk, d, q.dtype)] if k is not None else [None, 0]
-    _f32_param(q_weight, "q_weight", (d,))
-    _f32_param(k_weight, "k_weight", (d,))
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a 1-D tensor [rot / 2]")
-    _f32_param(inv_freq, "inv_freq")
-    rot = 2 * inv_freq.shape[0] if inv_freq is not None else 0
-    if positions is not None and (positions.dtype != torch.int64 or tuple(positions.shape) != lead
+    Bsz, T, Hq, d = sq
+    dt, dto = q.dtype, q_out.dtype
+    qp = (q_out.data_ptr(), _heads_ld(q_out, "q_out", sq, 2, Hq * d, dto))
+    qi = (q.data_ptr(), _heads_ld(q, "q", sq, 2, Hq * d, dt))
+    Hk, kp, ki = 0, (None, 0), (None, 0)
+    if k is not None:
+        Hk = k.shape[2]
+        sk = (Bsz, T, Hk, d)
+        kp = (k_out.data_ptr(), _heads_ld(k_out, "k_out", sk, 2, Hk * d, dto))
+        ki = (k.data_ptr(), _heads_ld(k, "k", sk, 2, Hk * d, dt))
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D tensor [rot / 2]")
+        rot = 2 * inv_freq.shape[0]
+    if positions is not None and (positions.dtype is not torch.int64 or positions.shape != (Bsz, T)
                                   or not positions.is_contiguous()):
-        raise ValueError(f"positions must be a contiguous int64 {lead} tensor")
-    _same_device(q, q_out=q_out, k_out=k_out, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
-                 positions=positions)
+        raise ValueError(f"positions must be a contiguous int64 {(Bsz, T)} tensor")
     flags = (MAMBA_NORM_L2 if l2 else 0) | (MAMBA_ROTARY_INTERLEAVED if interleaved else 0)
-    _check(load().mamba_qk_norm_rotary(*args, _dtype_code(q), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), rot,
-                                       _ptr(positions), float(eps), flags, Bsz, T, Hq, Hk, d, _stream(stream, q)))
+    code = _dtype_code(q)
+    _check(load().mamba_qk_norm_rotary(*qp, *kp, code if dto is dt else _dtype_code(q_out), *qi, *ki, code,
+                                       _f32_dense(q_weight, "q_weight", (d,)), _f32_dense(k_weight, "k_weight", (d,)),
+                                       _f32_dense(inv_freq, "inv_freq", (rot // 2,)), rot, _ptr(positions), eps,
+                                       flags, Bsz, T, Hq, Hk, d, _current_stream(stream, q)))
 
 
 def mamba_head_norm_gated(out, y, z=None, weight=None, *, eps=1e-5, stream=None):
     """out = y / sqrt(mean(y^2) + eps) * weight * SiLU(z) per head of d; out, y, z:
     [B, T, H, d] (z may be None, out may be y), weight [d] f32 or None."""
-    if y.dim() != 4:
-        raise ValueError(f"y must be a 4-D [B, T, H, d] tensor, got {tuple(y.shape)}")
-    Bsz, T, H, d = y.shape
-    lead = (Bsz, T)
-    ld_z = _heads_ld(z, "z", lead, H, d, y.dtype) if z is not None else 0
-    _f32_param(weight, "weight", (d,))
-    _same_device(y, out=out, z=z, weight=weight)
-    _check(load().mamba_head_norm_gated(_ptr(out), _heads_ld(out, "out", lead, H, d), _dtype_code(out), _ptr(y),
-                                        _heads_ld(y, "y", lead, H, d), _ptr(z), ld_z, _dtype_code(y), _ptr(weight),
-                                        float(eps), Bsz * T, H, d, _stream(stream, y)))
+    sy = tuple(y.shape)
+    if len(sy) != 4:
+        raise ValueError(f"y must be a 4-D [B, T, H, d] tensor, got {sy}")
+    Bsz, T, H, d = sy
+    dt, cols = y.dtype, H * d
+    ld_z = _heads_ld(z, "z", sy, 2, cols, dt) if z is not None else 0
+    code = _dtype_code(y)
+    _check(load().mamba_head_norm_gated(out.data_ptr(), _heads_ld(out, "out", sy, 2, cols, out.dtype),
+                                        code if out.dtype is dt else _dtype_code(out), y.data_ptr(),
+                                        _heads_ld(y, "y", sy, 2, cols, dt), _ptr(z), ld_z, code,
+                                        _f32_dense(weight, "weight", (d,)), eps, Bsz * T, H, d, _current_stream(stream, y)))
 
 
 LAYER_WEIGHTS = ("norm_w", "in_proj_w", "conv_w", "conv_b", "x_proj_w", "dt_proj_w", "dt_bias", "A_log", "D",

@@ -6,50 +6,49 @@
 // alpha_i S_{i-1} k_i) solve a unit lower triangular system:
 //
 //   A_ij = beta_i e^{G_i - G_j} k_i.k_j (j < i),   T = (I + A)^-1 diag(beta)
-//   P_ij = e^{G_i - G_j} q_i.k_j (j <= i),         W = P T
+//   P_ij = scale e^{G_i - G_j} q_i.k_j (j <= i)
 //   R    = V - e^G K S^T                           [64][dv]
-//   U    = diag(e^{G_63 - G}) T R,   Y = scale (e^G Q S^T + W R)
-//   S'   = e^{G_63} S + U^T K
+//   U    = T R,   Y = scale e^G Q S^T + P U
+//   S'   = e^{G_63} S + (diag(e^{G_63 - G}) U)^T K
 //
-// T and W do not depend on the state: X (I + A) = [I; P] gives both while the
-// previous chunk is still in flight, solved in blocks of 16 columns: the
-// diagonal blocks of I + A are inverted by substitution (a lane a row), the
-// products with them and with the blocks beside them are warp-level tensor-core
-// products in three TF32 terms.  (A thread a row for the whole substitution read
-// A 64 times over from shared memory, 7-8 us a chunk.)  What remains on the path
-// from state to state is three products and their epilogues, all held
-// transposed, a tensor-memory lane per value component n:
+// T and P do not depend on the state: they are made while the previous chunk is
+// still in flight.  X (I + A) = I is solved in blocks of 16 columns: the diagonal
+// blocks of I + A are inverted by substitution (a lane a row, D_k), then
+// Y_j = B_j - sum_{k > j} Y_k (D_k A_kj), X_k = Y_k D_k in warp-level tensor-core
+// products.  (A thread a row for the whole substitution read A 64 times over from
+// shared memory, 7-8 us a chunk; in f32 arithmetic by blocks it was 4.7.)  What
+// remains on the path from state to state is three products and their epilogues,
+// all held transposed, a tensor-memory lane per value component n:
 //
-//   D1 = S [K; Q]^T     128 x 128 x dk   R^T = V^T - D1's K half    (epilogue 1)
-//   D2 = R^T [T; W]^T   128 x 128 x 64   U^T = D2's T half          (epilogue 2)
-//   D3 = U^T K          128 x dk x 64    S'  = e^G S + D3           (epilogue 3)
+//   D1 = S K^T    128 x 64 x dk      R^T = V^T - e^G D1                  (epilogue 1)
+//   D2 = R^T T^T  128 x 64 x 64      U^T, and U^T decayed to the end     (epilogue 2)
+//   D3 = U^T K    128 x dk x 64      S'  = e^G S + D3                    (epilogue 3)
+//
+// The output's two products, S Q^T and U^T P^T, run under epilogues 2 and 3.
 //
 // S, R^T and U^T go back to tensor memory as the A operands of the next product:
-// nothing of the chain touches shared memory, and a value component's power of
-// two scale is a number per thread.  The f32 state stays in registers.
+// nothing of the chain touches shared memory.  The f32 state stays in registers.
 //
-// Precision: every operand is f16 with power-of-two scales (per row of K, Q, S
-// and R; one for T and one for W), S, R, U, T and W (and f32 inputs) as two
-// halves hi + lo (22 bits; lo.lo products are dropped), bf16 keys and queries as
-// one (exact).  Two halves in bf16 would hold
-// 16 bits: measured in simulation 4e-6 of the state, against 2e-7 here and 1e-7
-// for plain f32.  The scales keep every operand below 2^14 whatever the inputs'
-// magnitudes: S and R by their largest values (per value component), T and W by
-// their largest row sum, which bounds U.
+// Precision: f32 operands are the sum of three bf16 terms (24 bits, f32's range,
+// so no scaling and no look at the data), bf16 keys and queries one.  Of the nine
+// products of two such sums the six above 2^-24 are taken.  Two f16 halves with
+// power-of-two scales hold 22 bits for fewer products, but finding the scales
+// (maxima over lanes and rows, the keys converted) took twice the instructions,
+// and instructions are what bounds a chunk: 10.3 thousand cycles against _CYC_.
+// The output of bf16 tensors, which feeds back into nothing, takes the products
+// above 2^-16 alone.
 //
 // One CTA per (sequence, value head, 128 value components), warps specialised:
-//   0-7   epilogues 1-3, output, the state in registers (lane = component; two
-//         warps per lane quarter, each half the columns)
-//   8-11  prepare: A and P from [K; Q] K^T and the gates, T and W to shared memory
-//   12-13 load: tensor copies of K, Q, V tiles, K and Q to scaled f16
-//   14    the gates
-//   15    issues the MMAs
-// Every warp runs straight through its part of a chunk once, so the loop bodies
-// are kept rolled where registers allow it: with everything unrolled the code
-// was 177 KB and a chunk took 17-21 us, waiting for instructions.
+//   0-15  epilogues 1-3, output, the state in registers (lane = component; four
+//         warps per lane quarter, each a quarter of the columns)
+//   16-23 prepare: A and P from [K; Q] K^T and the gates, T and P to shared memory;
+//         a chain of small dependent steps, longer than the path from state to
+//         state, so two groups of four take the chunks in turn
+//   24    the gates
+//   25    issues the MMAs
+//   26-27 load: tensor copies, or f32 / unaligned tensors by hand
 #include <cuda.h>
 #include <cudaTypedefs.h>
-#include <cuda_fp16.h>
 
 #include <atomic>
 #include <type_traits>
@@ -64,62 +63,69 @@ namespace {
 
 constexpr int kC = 64;            // tokens per chunk
 constexpr int kM = 128;           // value components per CTA
-constexpr int kThreads = 16 * 32;
-constexpr int kLoadWarps = 2, kLoadThreads = 32 * kLoadWarps, kGateWarp = 14, kMmaWarp = 15;
+constexpr int kMainWarps = 16, kPrepWarps = 8, kLoadWarps = 2;
+constexpr int kParts = kMainWarps / 4;  // warps that share a lane quarter of tensor memory
+constexpr int kTok = kC / kParts;       // tokens of a chunk per such warp
+constexpr int kGateWarp = kMainWarps + kPrepWarps, kMmaWarp = kGateWarp + 1, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kGroupWarps = kPrepWarps / 2, kGroupThreads = 32 * kGroupWarps, kLoadThreads = 32 * kLoadWarps;
 constexpr int kGateSlots = 4;
+constexpr int kLdA = kC + 4;      // row stride of A and P in shared memory, floats
 constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
 __device__ int g_delta_faults = 0;
 
-constexpr int kLdA = kC + 4;      // row stride of A and P in shared memory, floats
-
-// per-chunk scalars and vectors, written by the gate and prepare warps
+// per-chunk scalars and vectors, written by the gate warp
 struct Gates {
-  float col_hi[kC], col_lo[kC];          // G_j + ek_j as two floats
-  float row_hi[2 * kC], row_lo[2 * kC];  // G_i - ek_i (keys), G_i - eq_i (queries)
+  float hi[kC], lo[kC];  // G_i (base 2) as two floats
   float beta[kC];
-  float fx[kC];    // e^{G_i} 2^{-ek_i}
-  float fd[kC];    // e^{G_63 - G_i} 2^{-ek_i}
-  float fq[kC];    // scale e^{G_i} 2^{-eq_i}
-  float past[32];  // e^{G_31 - G_j} 2^{-ek_j}, j < 32
-  float since[2][32];  // -beta_i e^{G_i - G_31} 2^{-ek_i}, e^{G_i - G_31} 2^{-eq_i}, i = 32 ..
-  float total;     // e^{G_63}
-  int t_exp, w_exp;  // T and W are held as 2^{t_exp} T, 2^{w_exp} W   (prepare warps)
-  float pad;
-  float sum_t[4], sum_w[4];  // largest row sums, one per prepare warp
+  float eg[kC];     // e^{G_i}
+  float egs[kC];    // scale e^{G_i}
+  float fd[kC];     // e^{G_63 - G_i}
+  float past[32];   // e^{G_31 - G_j}, j < 32
+  float since[32];  // e^{G_i - G_31}, i = 32 ..
+  float total;      // e^{G_63}
+  float pad[3];
 };
 
 template <int DK, bool F32>
 struct Smem {
-  static constexpr int kTerms = F32 ? 2 : 1;          // halves of K and Q
+  static constexpr int kTerms = F32 ? 3 : 1;          // bf16 terms of K and Q
   static constexpr int kBlocks = DK / 64;
-  static constexpr int kKqTerm = kBlocks * 16384;     // [K; Q]: 128 rows x 64 f16 per block
+  static constexpr int kKqTerm = kBlocks * 16384;     // [K; Q]: 128 rows x 64 bf16 per block
   static constexpr int kKq = kTerms * kKqTerm;
-  static constexpr int kKqStages = F32 ? 2 : 3;
-  static constexpr int kTp = 2 * 16384;               // [T; W] hi, lo: 128 rows x 64 f16
+  static constexpr int kKqStages = F32 ? (DK == 64 ? 2 : 1) : 3;
+  static constexpr int kT = 3 * 8192;                 // T in three terms: 64 rows x 64 bf16
+  static constexpr int kPTerms = F32 ? 3 : 2;
+  static constexpr int kP = kPTerms * 8192;           // P
   static constexpr int kV = F32 ? 0 : kC * kM * 2;    // f32 values are read where they are used
-  static constexpr int kRaw = F32 ? 0 : 2 * kC * DK * 2;  // K and Q rows as stored (bf16)
-  static constexpr int kOffTp = kKqStages * kKq;
-  static constexpr int kOffV = kOffTp + kTp;
-  static constexpr int kOffRaw = kOffV + kV;
-  static constexpr int kOffA = kOffRaw + kRaw;         // A and P, f32 [64][kLdA] each
+  static constexpr int kOffT = kKqStages * kKq;
+  static constexpr int kPBuffers = F32 ? 2 : 3;
+  static constexpr int kAhead = F32 ? 1 : 2;          // chunks that are prepared ahead
+  static constexpr int kOffP = kOffT + kT;
+  static constexpr int kOffV = kOffP + kPBuffers * kP;
+  static constexpr int kOffA = kOffV + kV;            // A, f32 [64][kLdA], of each group
   static constexpr int kOffGates = kOffA + 2 * kC * kLdA * 4;
-  static constexpr int kOffMax = kOffGates + kGateSlots * (int)sizeof(Gates);  // [2][2][128] f32
-  static constexpr int kOffExp = kOffMax + 2 * 2 * kM * 4;                     // [2][128] int
-  static constexpr int kOffBar = kOffExp + 2 * 2 * kC * 4;
-  static constexpr int kBars = 2 * kKqStages + 2 + 1 + 2 + 4 + 7;
+  static constexpr int kOffBar = kOffGates + kGateSlots * (int)sizeof(Gates);
+  static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 7;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
   static_assert(kAlloc <= 232448, "shared memory over the opt-in limit");
 };
 
-// tensor memory columns (two D0 buffers)
-constexpr uint32_t kColX = 0, kColQ = 64, kColU = 128, kColO = 192, kColS = 256, kColD0 = 384, kTmemCols = 512;
+// Tensor memory columns.  D1 is replaced by R's first two terms, later by those of
+// the decayed U.  S's three terms take 1.5 dk columns from kColS, where D3 (dk
+// columns) replaces them; R's third terms, then the decayed U's, and U's take the
+// place of S's third, which only D1 reads.  (With f32 tensors the queries' product
+// reads those too: then R's third terms take the output's place.)
+constexpr uint32_t kColX = 0, kColQ = 64, kColU = 128, kColO = 192, kColS = 256, kColThird = 384, kColU3 = 416,
+                   kColD0 = 448, kTmemCols = 512;
 
-// kind::f16, f16 A and B, f32 accumulator, M = 128; b_mn: B is MN-major
-__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+// kind::f16, bf16 A and B, f32 accumulator, M = 128; b_mn: B is MN-major
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kM >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -144,37 +150,48 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// floor(log2 x) of a positive float (-127 for zero and denormals, 128 for inf)
-__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255) - 127; }
-// 2^e, e clamped to the normal range
-__device__ __forceinline__ float pow2(int e) {
-  e = e < -126 ? -126 : (e > 127 ? 127 : e);
-  return __uint_as_float((uint32_t)(e + 127) << 23);
+// (a, b) as three bf16 pairs, each the rounding of what the ones before leave
+__device__ __forceinline__ void split3(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  float ra, rb;
+  asm("{\n"
+      "  .reg .b16 l, h;\n"
+      "  cvt.rn.bf16x2.f32 %0, %4, %3;\n"
+      "  mov.b32 {l, h}, %0;\n"
+      "  sub.rn.f32.bf16 %1, l, %3;\n"
+      "  sub.rn.f32.bf16 %2, h, %4;\n"
+      "}\n"
+      : "=&r"(t0), "=&f"(ra), "=&f"(rb)
+      : "f"(a), "f"(b));
+  ra = -ra, rb = -rb;
+  asm("{\n"
+      "  .reg .b16 l, h;\n"
+      "  cvt.rn.bf16x2.f32 %0, %4, %3;\n"
+      "  mov.b32 {l, h}, %0;\n"
+      "  sub.rn.f32.bf16 %1, l, %3;\n"
+      "  sub.rn.f32.bf16 %2, h, %4;\n"
+      "}\n"
+      : "=&r"(t1), "=&f"(a), "=&f"(b)
+      : "f"(ra), "f"(rb));
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t2) : "f"(-a), "f"(-b));
 }
 
-// (a, b) as f16 pairs hi + lo
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  float ra, rb;  // hi - value, exact
+// and as two
+__device__ __forceinline__ void split2(float a, float b, uint32_t& t0, uint32_t& t1) {
+  float ra, rb;
   asm("{\n"
-      "  .reg .f16 l, h;\n"
-      "  mov.b32 {l, h}, %2;\n"
-      "  sub.rn.f32.f16 %0, l, %3;\n"
-      "  sub.rn.f32.f16 %1, h, %4;\n"
+      "  .reg .b16 l, h;\n"
+      "  cvt.rn.bf16x2.f32 %0, %4, %3;\n"
+      "  mov.b32 {l, h}, %0;\n"
+      "  sub.rn.f32.bf16 %1, l, %3;\n"
+      "  sub.rn.f32.bf16 %2, h, %4;\n"
       "}\n"
-      : "=f"(ra), "=f"(rb)
-      : "r"(hi), "f"(a), "f"(b));
-  const __half2 l = __floats2half2_rn(-ra, -rb);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+      : "=&r"(t0), "=&f"(ra), "=&f"(rb)
+      : "f"(a), "f"(b));
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t1) : "f"(-ra), "f"(-rb));
 }
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // four 8 x 8 matrices of 16-bit values, lane l holding two of row l / 4 of each
@@ -183,58 +200,60 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4])
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+// D[16][8] += A[16][16] B[16][8]
+__device__ __forceinline__ void mma_sync(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  elect.sync _|p, 0xffffffff;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
+// True once the phase of parity `parity` has completed, false after about a
+// millisecond: until then the warp sleeps in the barrier's hardware.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return done != 0;
+}
 
 // A wait that did not succeed at once.  One that runs out sets the fault and
 // abort flags; every role then runs on through its loop without waiting, so
 // that all named barriers are met and the CTA ends.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (*abort_flag) return;
-  if (!mbar_wait(bar, parity, kWaitLimit)) {
-    atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
-    *abort_flag = 1;
+  const long long t0 = clock64();
+  while (!mbar_sleep(bar, parity)) {
+    if (clock64() - t0 > kWaitLimit) {
+      atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+      *abort_flag = 1;
+      return;
+    }
   }
-}
-
-// a box of a three-dimensional tensor map to shared memory
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-// x as two TF32 terms (11 bits each; the tensor cores ignore the bits below)
-struct Tf32x2 {
-  uint32_t hi, lo;
-  __device__ __forceinline__ void set(float x) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
-  }
-};
-// D[16][8] += A[16][8] B[8][8], f32 accumulators.  The 8 values of the
-// contraction are taken in the order 0 2 4 6 1 3 5 7 on both sides: then the
-// accumulator of one product is the A operand of the next as it stands.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// A operand (hi, lo) from an accumulator
-__device__ __forceinline__ void tf32_operand(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&c)[4]) {
-  const float v[4] = {c[0], c[2], c[1], c[3]};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    Tf32x2 t;
-    t.set(v[i]);
-    hi[i] = t.hi, lo[i] = t.lo;
-  }
-}
-
-__device__ __forceinline__ void unpack8(float (&f)[8], uint4 a) {  // bf16
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 
 // A number as the unevaluated sum of two floats
@@ -261,11 +280,40 @@ __device__ __forceinline__ Two two_shfl(Two a, int lane) {
 // 2^(a - b)
 __device__ __forceinline__ float two_exp2(Two a, Two b) { return ex2_approx((a.h - b.h) + (a.l - b.l)); }
 
+// boxes of four-dimensional tensor maps from and to shared memory
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(w), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// The products of two sums of terms, smallest first, as (term of a, term of b) in
+// two bits each.  Three terms by one: 3, or the first 2; three by three: the 6
+// above 2^-24, or the 3 above 2^-16.
+template <bool THREE>
+__device__ __forceinline__ constexpr void term_pair(int i, int& a, int& b) {
+  if (THREE) {
+    // (0,2) (2,0) (1,1) (0,1) (1,0) (0,0)
+    a = (0x118 >> (2 * i)) & 3, b = (0x052 >> (2 * i)) & 3;
+  } else {
+    a = 2 - i, b = 0;
+  }
+}
+
 template <int DK, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_q,
-                                                            const __grid_constant__ CUtensorMap map_v, int vec_kq,
-                                                            int vec_v) {
+                                                            const __grid_constant__ CUtensorMap map_v,
+                                                            const __grid_constant__ CUtensorMap map_y, int vec_kq,
+                                                            int vec_v, int vec_y) {
   using L = Smem<DK, F32>;
   using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
   extern __shared__ unsigned char smem_raw[];
@@ -279,11 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     return b;
   };
   const uint32_t kq_full = next_bars(L::kKqStages), kq_empty = next_bars(L::kKqStages);
-  const uint32_t v_full = next_bars(1), v_empty = next_bars(1);
-  const uint32_t raw_full = next_bars(1), tp_full = next_bars(1), tp_empty = next_bars(1);
-  const uint32_t d0_full = next_bars(2), d0_empty = next_bars(2);
-  const uint32_t s_ready = next_bars(1), x_full = next_bars(1), r_ready = next_bars(1), u_full = next_bars(1),
-                 u_ready = next_bars(1), o_full = next_bars(1), s_full = next_bars(1);
+  const uint32_t gate_full = next_bars(kGateSlots), gate_empty = next_bars(kGateSlots);
+  const uint32_t v_full = next_bars(1), v_empty = next_bars(1), t_full = next_bars(1);
+  // of the chunk's parity: a group of prepare warps sees every other chunk
+  const uint32_t t_empty = next_bars(2), d0_full = next_bars(2), d0_empty = next_bars(2);
+  const uint32_t p_full = next_bars(L::kPBuffers), p_empty = next_bars(L::kPBuffers), o_empty = next_bars(1);
+  const uint32_t s_ready = next_bars(1), x_full = next_bars(1), r_ready = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1), s_full = next_bars(1);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
   Gates* gates = reinterpret_cast<Gates*>(gbase + L::kOffGates);
@@ -298,12 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   const int n_chunks = (int)((g.T + kC - 1) / kC);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, kLoadThreads + 32), mbar_init(kq_empty + 8 * s, 1);
-    mbar_init(v_full, vec_v ? 1 : kLoadThreads), mbar_init(v_empty, 8);
-    mbar_init(raw_full, 1), mbar_init(tp_full, 4), mbar_init(tp_empty, 1);
-    for (int s = 0; s < 2; ++s) mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, 4);
-    mbar_init(s_ready, 8), mbar_init(x_full, 1), mbar_init(r_ready, 8), mbar_init(u_full, 1);
-    mbar_init(u_ready, 8), mbar_init(o_full, 1), mbar_init(s_full, 1);
+    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, vec_kq ? 1 : kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
+    for (int s = 0; s < kGateSlots; ++s) mbar_init(gate_full + 8 * s, 32), mbar_init(gate_empty + 8 * s, kMainWarps + kGroupWarps);
+    mbar_init(v_full, vec_v ? 1 : kLoadThreads), mbar_init(v_empty, kMainWarps);
+    mbar_init(t_full, kGroupWarps), mbar_init(o_empty, kMainWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(t_empty + 8 * s, 1), mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, kGroupWarps);
+    for (int s = 0; s < L::kPBuffers; ++s) mbar_init(p_full + 8 * s, kGroupWarps / 2), mbar_init(p_empty + 8 * s, 1);
+    mbar_init(s_ready, kMainWarps), mbar_init(x_full, 1), mbar_init(r_ready, kMainWarps);
+    mbar_init(u_full, 1), mbar_init(u_ready, kMainWarps), mbar_init(o_full, 1), mbar_init(s_full, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -319,20 +370,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   const uint32_t tmem = *tmem_ptr;
 
   auto wait = [&](uint32_t bar, int phase) {
-    if (!mbar_try_wait(bar, (uint32_t)(phase & 1))) wait_slow(bar, (uint32_t)(phase & 1), abort_flag);
+    if (!mbar_sleep(bar, (uint32_t)(phase & 1))) wait_slow(bar, (uint32_t)(phase & 1), abort_flag);
   };
 
-  if (warp < 8) {
+  if (warp < kMainWarps) {
     // ---------------------------------------------------------- epilogues ----
-    constexpr int HK = DK / 2;  // key components per thread
-    const int quad = warp & 3, half = warp >> 2;
+    constexpr int HK = DK / kParts;  // key components per thread
+    const int quad = warp & 3, part = warp >> 2;
     const int lane_n = quad * 32 + lane;
     const int n = tile * kM + lane_n;
     const bool live = n < g.dv;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-    float* max_v = reinterpret_cast<float*>(gbase + L::kOffMax);  // [half][128]
-    float* max_s = max_v + 2 * kM;
-    const int64_t s_at = (bh * g.dv + n) * g.dk + half * HK;
+    const int64_t s_at = (bh * g.dv + n) * g.dk + part * HK;
     const bool vec_s = g.dk % 4 == 0 && ((reinterpret_cast<uintptr_t>(g.state_in) | reinterpret_cast<uintptr_t>(g.state_out)) & 15) == 0;
     float s[HK];
 #pragma unroll
@@ -340,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (g.state_in && live) {
         const float* p = g.state_in + s_at + j;
-        const int left = g.dk - half * HK - j;
+        const int left = g.dk - part * HK - j;
         if (vec_s) {
           if (left > 0) x = *reinterpret_cast<const float4*>(p);
         } else {
@@ -352,42 +401,91 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       s[j] = x.x, s[j + 1] = x.y, s[j + 2] = x.z, s[j + 3] = x.w;
     }
-    int s_exp = 0;  // S is held as 2^{s_exp} S
-    // this lane's state to tensor memory, scaled, in two halves: of every 16
-    // columns 8 of hi, 8 of lo
-    auto put_state = [&]() {
-      float mx = 0.0f;
-#pragma unroll
-      for (int j = 0; j < HK; ++j) mx = fmaxf(mx, fabsf(s[j]));
-      if (mx > 3.4e38f) mx = 1.0f;  // not finite: the component is lost, any scale will do
-      max_s[half * kM + lane_n] = mx;
-      named_barrier(3 + quad, 64);
-      s_exp = 13 - exponent_of(fmaxf(mx, max_s[(1 - half) * kM + lane_n]));
-      s_exp = s_exp > 120 ? 120 : s_exp;
-      const float2 c = make_float2(pow2(s_exp), pow2(s_exp));
-#pragma unroll
-      for (int j0 = 0; j0 < HK; j0 += 16) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 v = __fmul2_rn(make_float2(s[j0 + 2 * j], s[j0 + 2 * j + 1]), c);
-          split2(v.x, v.y, hi[j], lo[j]);
-        }
-        tmem_st8(t_lane + kColS + (uint32_t)(half * HK + j0), hi);
-        tmem_st8(t_lane + kColS + (uint32_t)(half * HK + j0 + 8), lo);
-      }
-      tmem_wait_st();
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_ready);
-    };
-    put_state();
-
-    const int i0 = half * 32;  // this thread's tokens of a chunk
+    const int i0 = part * kTok;  // this thread's tokens of a chunk
     const uint32_t y_step = (uint32_t)g.ld_y * (g.y_bf16 ? 2 : 4);  // bytes; a chunk's rows fit 32 bits
     char* y_at = reinterpret_cast<char*>(g.y) +
                  ((b * g.T + i0) * g.ld_y + (int64_t)h * g.dv + n) * (g.y_bf16 ? 2 : 4);
-    for (int c = 0; c < n_chunks; ++c) {
+    auto arrive = [&](uint32_t bar) {
+      tmem_wait_st();
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // chunk c's output; it comes in the next chunk while D2 is in flight, so that
+    // the path from state to state does not wait for it
+    auto output = [&](int c) {
+      const Gates& gt = gates[c % kGateSlots];
+      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
+      wait(o_full, c);
+      tcgen05_fence_after();
+      const int rows = live ? left - i0 : 0;  // of this thread's tokens
+      // staged over the chunk's values, which epilogue 1 of the next chunk has just
+      // taken (the last chunk's own are long gone too), for a tensor store; or
+      // stored from here
+      __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(gbase + L::kOffV) + i0 * kM + lane_n;
+#pragma unroll 1
+      for (int i = 0; i < kTok; i += 8) {
+        uint32_t xq[8], xo[8];
+        tmem_ld8(t_lane + kColQ + (uint32_t)(i0 + i), xq);
+        tmem_ld8(t_lane + kColO + (uint32_t)(i0 + i), xo);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) *reinterpret_cast<float4*>(&o[j]) = *reinterpret_cast<const float4*>(&gt.egs[i0 + i + j]);
+        tmem_wait(xq);
+        tmem_wait(xo);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf(o[j], __uint_as_float(xq[j]), __uint_as_float(xo[j]));
+        if (!F32 && vec_y) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const __nv_bfloat162 w = __floats2bfloat162_rn(o[j], o[j + 1]);
+            stage[(i + j) * kM] = w.x, stage[(i + j + 1) * kM] = w.y;
+          }
+          continue;
+        }
+        uint32_t at = (uint32_t)i * y_step;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (i + j < rows) {
+            if (g.y_bf16)
+              *reinterpret_cast<__nv_bfloat16*>(y_at + at) = __float2bfloat16_rn(o[j]);
+            else
+              *reinterpret_cast<float*>(y_at + at) = o[j];
+          }
+          at += y_step;
+        }
+      }
+      y_at += (int64_t)kC * y_step;
+      if (!F32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_empty);
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty), mbar_arrive(gate_empty + 8 * (c % kGateSlots));
+    };
+#pragma unroll 1
+    for (int c = 0; c <= n_chunks; ++c) {
+      if (F32 && c > 0) wait(o_full, c - 1);  // U's third terms are read
+      if (c < n_chunks) {
+        // S to tensor memory: of this warp's HK columns of D3's place the first
+        // half the first terms, the rest the second; the third terms beyond D3
+        const uint32_t at = t_lane + kColS + (uint32_t)(part * HK), at2 = t_lane + kColS + (uint32_t)(DK + part * HK / 2);
+#pragma unroll
+        for (int j0 = 0; j0 < HK; j0 += 16) {
+          uint32_t t0[8], t1[8], t2[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) split3(s[j0 + 2 * j], s[j0 + 2 * j + 1], t0[j], t1[j], t2[j]);
+          tmem_st8(at + (uint32_t)(j0 / 2), t0);
+          tmem_st8(at + (uint32_t)(HK / 2 + j0 / 2), t1);
+          tmem_st8(at2 + (uint32_t)(j0 / 2), t2);
+        }
+        arrive(s_ready);
+      }
+      if (!F32 && c == n_chunks) wait(v_full, c);  // the output before the last has left its place
+      if (c > 0 && (F32 || c == n_chunks)) output(c - 1);
+      if (c == n_chunks) break;
       const Gates& gt = gates[c % kGateSlots];
       const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
       // this lane's value of token i0 + i
@@ -397,147 +495,90 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         if (!F32) return to_f32(v_tile[i * kM]);
         return live && i0 + i < left ? to_f32(v_global[i * g.ld_v]) : 0.0f;
       };
-      int r_exp;  // R is held as 2^{r_exp} R
-      {  // epilogue 1: R^T = V^T - fx D1; of every 16 columns 8 of hi, 8 of lo
-        wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
+      {  // epilogue 1: R^T = V^T - e^G D1
+        wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
         if (!F32) wait(v_full, c);
-        const float cx = pow2(-s_exp);
-        float2 r[16];
+        static_assert(kTok == 16, "one tensor-memory load");
+        float r[kTok];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = make_float2(value(2 * j), value(2 * j + 1));
+        for (int j = 0; j < kTok; ++j) r[j] = value(j);
         wait(x_full, c);
         tcgen05_fence_after();
-        float mx = 0.0f;
+        uint32_t x[kTok];
+        tmem_ld16(t_lane + kColX + (uint32_t)i0, x);
+        tmem_wait(x);
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-          uint32_t x[16];
-          tmem_ld16(t_lane + kColX + (uint32_t)(i0 + i), x);
-          tmem_wait(x);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 fx = *reinterpret_cast<const float4*>(&gt.fx[i0 + i + j]);
-            const float2 f[2] = {make_float2(fx.x, fx.y), make_float2(fx.z, fx.w)};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float2& t = r[(i + j) / 2 + e];
-              t = __ffma2_rn(__fmul2_rn(f[e], make_float2(-cx, -cx)),
-                             make_float2(__uint_as_float(x[j + 2 * e]), __uint_as_float(x[j + 2 * e + 1])), t);
-              mx = fmaxf(fmaxf(mx, fabsf(t.x)), fabsf(t.y));
-            }
-          }
+        for (int j = 0; j < kTok; j += 4) {
+          const float4 eg = *reinterpret_cast<const float4*>(&gt.eg[i0 + j]);
+          r[j] = fmaf(-eg.x, __uint_as_float(x[j]), r[j]);
+          r[j + 1] = fmaf(-eg.y, __uint_as_float(x[j + 1]), r[j + 1]);
+          r[j + 2] = fmaf(-eg.z, __uint_as_float(x[j + 2]), r[j + 2]);
+          r[j + 3] = fmaf(-eg.w, __uint_as_float(x[j + 3]), r[j + 3]);
         }
-        if (mx > 3.4e38f) mx = 1.0f;
-        max_v[half * kM + lane_n] = mx;
-        named_barrier(3 + quad, 64);  // the other 32 tokens of the lane
-        r_exp = 9 - exponent_of(fmaxf(mx, max_v[(1 - half) * kM + lane_n]));
-        r_exp = r_exp > 120 ? 120 : r_exp;
-        const float cr = pow2(r_exp);
+        uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 t = __fmul2_rn(r[i / 2 + j], make_float2(cr, cr));
-            split2(t.x, t.y, hi[j], lo[j]);
-          }
-          tmem_st8(t_lane + kColX + (uint32_t)(i0 + i), hi);
-          tmem_st8(t_lane + kColX + (uint32_t)(i0 + i + 8), lo);
-        }
-        tmem_wait_st();
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(r_ready);
-          if (!F32) mbar_arrive(v_empty);
+        for (int j = 0; j < 8; ++j) split3(r[2 * j], r[2 * j + 1], t0[j], t1[j], t2[j]);
+        tmem_st8(t_lane + kColX + (uint32_t)i0, t0);
+        tmem_st8(t_lane + kColX + (uint32_t)(i0 + 8), t1);
+        tmem_st8(t_lane + (F32 ? kColO + (uint32_t)i0 : kColThird + (uint32_t)(8 * part)), t2);
+        arrive(r_ready);
+      }
+      if (!F32) {
+        if (c > 0) {
+          // every warp has its values before one writes its output there
+          named_barrier(5, 32 * kMainWarps);
+          output(c - 1);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_empty);
         }
       }
-      {  // epilogue 2: U^T, already decayed to the chunk's end
+      {  // epilogue 2: U^T for the output, and decayed to the chunk's end for S
         wait(u_full, c);
         tcgen05_fence_after();
-#pragma unroll 1
-        for (int i = i0; i < i0 + 32; i += 16) {
-          uint32_t x[16], hi[8], lo[8];
-          tmem_ld16(t_lane + kColU + (uint32_t)i, x);
-          tmem_wait(x);
+        uint32_t x[16], t0[8], t1[8], t2[8];
+        tmem_ld16(t_lane + kColU + (uint32_t)i0, x);
+        tmem_wait(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            split2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), hi[j], lo[j]);
-          tmem_st8(t_lane + kColU + (uint32_t)i, hi);
-          tmem_st8(t_lane + kColU + (uint32_t)(i + 8), lo);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 fd = *reinterpret_cast<const float4*>(&gt.fd[i0 + 2 * j]);
+          split3(fd.x * __uint_as_float(x[2 * j]), fd.y * __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
+          split3(fd.z * __uint_as_float(x[2 * j + 2]), fd.w * __uint_as_float(x[2 * j + 3]), t0[j + 1], t1[j + 1], t2[j + 1]);
         }
-        tmem_wait_st();
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_ready);
-      }
-      {  // output, while D3 is in flight
-        wait(o_full, c);
-        tcgen05_fence_after();
-        const float cq = pow2(-s_exp), cw = g.scale * pow2(-r_exp - gt.w_exp);
-        const int rows = live ? left - i0 : 0;  // of this thread's 32 tokens
-#pragma unroll 1
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t xq[8], xo[8];
-          tmem_ld8(t_lane + kColQ + (uint32_t)(i0 + i), xq);
-          tmem_ld8(t_lane + kColO + (uint32_t)(i0 + i), xo);
-          float2 o[4];
+        tmem_st8(t_lane + kColX + (uint32_t)i0, t0);
+        tmem_st8(t_lane + kColX + (uint32_t)(i0 + 8), t1);
+        tmem_st8(t_lane + kColThird + (uint32_t)(8 * part), t2);
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 fq = *reinterpret_cast<const float4*>(&gt.fq[i0 + i + j]);
-            o[j / 2] = __fmul2_rn(make_float2(fq.x, fq.y), make_float2(cq, cq));
-            o[j / 2 + 1] = __fmul2_rn(make_float2(fq.z, fq.w), make_float2(cq, cq));
-          }
-          tmem_wait(xq);
-          tmem_wait(xo);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = __ffma2_rn(make_float2(__uint_as_float(xo[2 * j]), __uint_as_float(xo[2 * j + 1])), make_float2(cw, cw),
-                              __fmul2_rn(o[j], make_float2(__uint_as_float(xq[2 * j]), __uint_as_float(xq[2 * j + 1]))));
-          uint32_t at = (uint32_t)i * y_step;
-          if (g.y_bf16) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const __nv_bfloat162 w = __floats2bfloat162_rn(o[j / 2].x, o[j / 2].y);
-              if (i + j < rows) *reinterpret_cast<__nv_bfloat16*>(y_at + at) = w.x;
-              at += y_step;
-              if (i + j + 1 < rows) *reinterpret_cast<__nv_bfloat16*>(y_at + at) = w.y;
-              at += y_step;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (i + j < rows) *reinterpret_cast<float*>(y_at + at) = (j & 1) ? o[j / 2].y : o[j / 2].x;
-              at += y_step;
-            }
-          }
+        for (int j = 0; j < 8; ++j) {
+          if (F32)
+            split3(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
+          else
+            split2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
         }
-        y_at += (int64_t)kC * y_step;
+        tmem_st8(t_lane + kColU + (uint32_t)i0, t0);
+        tmem_st8(t_lane + kColU + (uint32_t)(i0 + 8), t1);
+        if (F32) tmem_st8(t_lane + kColU3 + (uint32_t)(8 * part), t2);
+        arrive(u_ready);
       }
       {  // epilogue 3: S = e^G S + D3
-        const float total = gt.total, cd = pow2(-r_exp - gt.t_exp);
+        const float total = gt.total;
         wait(s_full, c);
         tcgen05_fence_after();
 #pragma unroll
         for (int j0 = 0; j0 < HK; j0 += 16) {
           uint32_t x[16];
-          tmem_ld16(t_lane + kColS + (uint32_t)(half * HK + j0), x);
+          tmem_ld16(t_lane + kColS + (uint32_t)(part * HK + j0), x);
           tmem_wait(x);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 t = __ffma2_rn(
-                make_float2(total, total), make_float2(s[j0 + j], s[j0 + j + 1]),
-                __fmul2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cd, cd)));
-            s[j0 + j] = t.x, s[j0 + j + 1] = t.y;
-          }
+          for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]));
         }
-        if (c + 1 < n_chunks) put_state();
       }
     }
     if (g.state_out && live) {
 #pragma unroll
       for (int j = 0; j < HK; j += 4) {
         float* p = g.state_out + s_at + j;
-        const int left = g.dk - half * HK - j;
+        const int left = g.dk - part * HK - j;
         if (vec_s) {
           if (left > 0) *reinterpret_cast<float4*>(p) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         } else {
@@ -548,383 +589,284 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kGateWarp) {
     // ------------------------------------------------------------ prepare ----
     const int quad = warp & 3;
+    const int group = (warp - kMainWarps) >> 2;  // takes chunks group, group + 2, ..
+    const int bar_id = 1 + group;
     const int row = quad * 32 + lane;       // row of [K; Q]
     const bool is_t = quad < 2;             // warp-uniform
     const bool upper = quad & 1;            // tokens 32-63: the rows with columns past 31
     const int i = row & (kC - 1);           // token
-    float* a_s = reinterpret_cast<float*>(gbase + L::kOffA);
-    float* p_s = a_s + kC * kLdA;
-    // of [T; W] this warp solves rows 16 rt .. of T and rows 16 rw .. of W: the
-    // work of a row block grows with its index, the two together do not
-    const int rt = quad, rw = 3 - quad;
+    float* a_s = reinterpret_cast<float*>(gbase + L::kOffA) + group * kC * kLdA;
+    // The blocks (k, j) of D and N = -D A, in three terms, take A's place: block
+    // k (k + 1) / 2 + j, terms of 512 bytes, rows of 32 bytes whose 16-byte
+    // granules change places every four rows
+    const uint32_t n_s = base + L::kOffA + (uint32_t)(group * kC * kLdA * 4);
+    auto block_at = [&](int k, int j) { return n_s + (uint32_t)((k * (k + 1) / 2 + j) * 1536); };
+    const int rb = quad;  // T's block of 16 rows that this warp solves
     const int fr = lane / 4, fc = 2 * (lane % 4);  // accumulator fragment: rows fr, fr + 8, columns fc, fc + 1
-    for (int c = 0; c < n_chunks; ++c) {
-      Gates& gt = gates[c % kGateSlots];
-      const uint32_t t_d0 = tmem + ((uint32_t)(quad * 32) << 16) + kColD0 + (uint32_t)(64 * (c & 1));
-      wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);  // the gates
-      wait(d0_full + 8 * (c & 1), c / 2);
+    // this lane's row for ldmatrix: matrices (k 0-7, n 0-7), (k 8-15, n 0-7), (k 0-7, n 8-15), ..
+    const uint32_t ld_row = (uint32_t)(lane & 15), ld_at = ld_row * 32 + ((((uint32_t)lane >> 4) ^ ((ld_row >> 2) & 1)) << 4);
+    // acc += x m over three terms each, the small and the large products in two
+    // chains (one is 20 cycles long, 66 while tcgen05 products are in flight)
+    auto product = [&](float (&acc)[2][4], const uint32_t (&x)[3][4], const uint32_t (&m)[3][4]) {
+      float small[2][4];
+#pragma unroll
+      for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) small[nn][e] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < 6; ++p) {
+        int ta, tb;
+        term_pair<true>(p, ta, tb);
+#pragma unroll
+        for (int nn = 0; nn < 2; ++nn) mma_sync(p < 3 ? small[nn] : acc[nn], x[ta], m[tb][2 * nn], m[tb][2 * nn + 1]);
+      }
+#pragma unroll
+      for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nn][e] += small[nn][e];
+    };
+    // the A operand of a 16 x 16 block held as two accumulators
+    auto operand = [&](uint32_t (&x)[3][4], const float (&c)[2][4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split3(c[e / 2][2 * (e & 1)], c[e / 2][2 * (e & 1) + 1], x[0][e], x[1][e], x[2][e]);
+    };
+    // T and P are zero above the diagonal blocks
+    for (int e = threadIdx.x - 32 * kMainWarps; e < (L::kT + L::kPBuffers * L::kP) / 16; e += 2 * kGroupThreads)
+      *reinterpret_cast<uint4*>(gbase + L::kOffT + e * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    named_barrier(3, 2 * kGroupThreads);
+#pragma unroll 1
+    for (int c = group; c < n_chunks; c += 2) {
+      const Gates& gt = gates[c % kGateSlots];
+      const uint32_t t_d0 = tmem + ((uint32_t)(quad * 32) << 16) + kColD0;
+      wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
+      wait(d0_full + 8 * group, c / 2);
       tcgen05_fence_after();
-      named_barrier(1, 128);  // the previous chunk's A and P are read
+      named_barrier(bar_id, kGroupThreads);  // the previous chunk's blocks are read
       {
-        // -A and P to shared memory, a row per thread
-        float* dst = (is_t ? a_s : p_s) + i * kLdA;
-        const uint32_t t_diag = t_d0 + (upper ? 32 : 0);
-        uint32_t d[32];
+        // a row per thread: -A in f32, P in its terms (granule q of row r at
+        // q ^ (r % 8))
+        const int pb = c % L::kPBuffers;
+        if (!is_t && c >= L::kPBuffers) wait(p_empty + 8 * pb, c / L::kPBuffers - 1);
+        float* dst = a_s + i * kLdA;
+        const uint32_t dst_p = base + L::kOffP + pb * L::kP + (uint32_t)(i * 128);
+        auto put8 = [&](int j, const float (&o)[8]) {
+          if (is_t) {
+            *reinterpret_cast<float4*>(dst + j) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(dst + j + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          } else {
+            uint32_t t[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (F32)
+                split3(o[2 * e], o[2 * e + 1], t[0][e], t[1][e], t[2][e]);
+              else
+                split2(o[2 * e], o[2 * e + 1], t[0][e], t[1][e]);
+            }
+            const uint32_t at = dst_p + (uint32_t)(((j / 8) ^ (i & 7)) << 4);
+#pragma unroll
+            for (int e = 0; e < L::kPTerms; ++e)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + e * 8192), "r"(t[e][0]), "r"(t[e][1]),
+                           "r"(t[e][2]), "r"(t[e][3])
+                           : "memory");
+          }
+        };
+        const float scale_row = is_t ? -gt.beta[i] : g.scale;
         if (upper) {
           // the 32 columns before these rows' own: the decay factors at token 31
-          const float since = gt.since[is_t ? 0 : 1][lane];
-          tmem_ld32(t_d0, d);
+          const float since = gt.since[lane] * scale_row;
+#pragma unroll 1
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t d[8];
+            float o[8];
+            tmem_ld8(t_d0 + (uint32_t)j, d);
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(&o[e]) = *reinterpret_cast<const float4*>(&gt.past[j + e]);
+            tmem_wait(d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= since * __uint_as_float(d[e]);
+            put8(j, o);
+          }
+        }
+        const float rh = gt.hi[i], rl = gt.lo[i];
+        const int jd = upper ? 32 : 0;
+#pragma unroll 1
+        for (int j = jd; j < jd + 32; j += 8) {
+          const int last = (is_t ? i - 1 : i) - j;  // A is strictly lower, P lower
+          uint32_t d[8];
+          tmem_ld8(t_d0 + (uint32_t)j, d);
+          float o[8], cl[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(&o[e]) = *reinterpret_cast<const float4*>(&gt.hi[j + e]);
+            *reinterpret_cast<float4*>(&cl[e]) = *reinterpret_cast<const float4*>(&gt.lo[j + e]);
+          }
           tmem_wait(d);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 past = *reinterpret_cast<const float4*>(&gt.past[j]);
-            const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(past.x, past.y), make_float2(since, since)),
-                                         make_float2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])));
-            const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(past.z, past.w), make_float2(since, since)),
-                                         make_float2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])));
-            *reinterpret_cast<float4*>(dst + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          for (int e = 0; e < 8; ++e) {
+            const float w = ex2_approx((rh - o[e]) + (rl - cl[e])) * scale_row;
+            o[e] = e <= last ? __uint_as_float(d[e]) * w : 0.0f;
           }
-          dst += 32;
+          put8(j, o);
         }
-        tmem_ld32(t_diag, d);
-        const float rh = gt.row_hi[row], rl = gt.row_lo[row];
-        const float scale_row = is_t ? -gt.beta[i] : 1.0f;
-        const int last = is_t ? lane - 1 : lane;  // A is strictly lower, P lower
-        const float* col_hi = gt.col_hi + (upper ? 32 : 0);
-        const float* col_lo = gt.col_lo + (upper ? 32 : 0);
-        tmem_wait(d);
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 ch = *reinterpret_cast<const float4*>(col_hi + j), cl = *reinterpret_cast<const float4*>(col_lo + j);
-          const float chs[4] = {ch.x, ch.y, ch.z, ch.w}, cls[4] = {cl.x, cl.y, cl.z, cl.w};
-          float o[4];
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 w = __fadd2_rn(__fadd2_rn(make_float2(rh, rh), make_float2(-chs[e], -chs[e + 1])),
-                                        __fadd2_rn(make_float2(rl, rl), make_float2(-cls[e], -cls[e + 1])));
-            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
-                                                   make_float2(ex2_approx(w.x), ex2_approx(w.y))),
-                                        make_float2(scale_row, scale_row));
-            o[e] = j + e <= last ? v.x : 0.0f;
-            o[e + 1] = j + e + 1 <= last ? v.y : 0.0f;
-          }
-          *reinterpret_cast<float4*>(dst + j) = make_float4(o[0], o[1], o[2], o[3]);
-        }
+        if (!is_t) fence_proxy_async_smem();
       }
       tcgen05_fence_before();
-      named_barrier(1, 128);
-      if (lane == 0) mbar_arrive(d0_empty + 8 * (c & 1));
+      named_barrier(bar_id, kGroupThreads);
+      if (lane == 0) {
+        mbar_arrive(d0_empty + 8 * group);
+        if (!is_t) mbar_arrive(p_full + 8 * (c % L::kPBuffers));
+      }
+      // the inverse of diagonal block `quad` of I + A over the block itself, a lane
+      // a row (16-31 repeat 0-15): X (I + A) = I, columns from the last
+      float* blk = a_s + 16 * quad * (kLdA + 1);
       {
-        // the inverse of diagonal block `quad` of I + A over the block itself, a
-        // lane a row (16-31 repeat 0-15): X (I + A) = I, columns from the last
-        float* blk = a_s + 16 * quad * (kLdA + 1);
         const int r = lane & 15;
-        float2 x[8];
+        float x[16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = make_float2(2 * q == r ? 1.0f : 0.0f, 2 * q + 1 == r ? 1.0f : 0.0f);
+        for (int q = 0; q < 16; ++q) x[q] = q == r ? 1.0f : 0.0f;
 #pragma unroll
         for (int k = 15; k >= 1; --k) {
-          const float xk = (k & 1) ? x[k / 2].y : x[k / 2].x;
 #pragma unroll
-          for (int q = 0; q < (k + 3) / 4; ++q) {
-            const float4 a = *reinterpret_cast<const float4*>(blk + k * kLdA + 4 * q);
-            x[2 * q] = __ffma2_rn(make_float2(xk, xk), make_float2(a.x, a.y), x[2 * q]);
-            if (4 * q + 2 < k) x[2 * q + 1] = __ffma2_rn(make_float2(xk, xk), make_float2(a.z, a.w), x[2 * q + 1]);
+          for (int q = 0; q < k; q += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(blk + k * kLdA + q);
+            x[q] = fmaf(x[k], a.x, x[q]);
+            if (q + 1 < k) x[q + 1] = fmaf(x[k], a.y, x[q + 1]);
+            if (q + 2 < k) x[q + 2] = fmaf(x[k], a.z, x[q + 2]);
+            if (q + 3 < k) x[q + 3] = fmaf(x[k], a.w, x[q + 3]);
           }
         }
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(blk + r * kLdA + 4 * q) =
-                make_float4(x[2 * q].x, x[2 * q].y, x[2 * q + 1].x, x[2 * q + 1].y);
+          for (int q = 0; q < 16; q += 4)
+            *reinterpret_cast<float4*>(blk + r * kLdA + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
         }
       }
-      named_barrier(1, 128);
-      // X (I + A) = [I; P] by blocks of 16 columns, the last first: X_k = B_k D_k,
-      // then B_j += X_k (-A_kj) for the blocks before it
-      float t[8][4], w[8][4];
+      named_barrier(bar_id, kGroupThreads);
+      {
+        // N_kj = D_k (-A_kj) below the diagonal, blocks (1,0) (2,0) (2,1) (3,0) (3,1)
+        // (3,2) by warps 3 0 1 2 3 0; then those and the D_k, in three terms over A
+        uint32_t dt[3][4], nt[2][3][4];
+        auto load_block = [&](float (&x)[2][4], const float* m) {
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
+          for (int nn = 0; nn < 2; ++nn) {
+            const float2 lo = *reinterpret_cast<const float2*>(m + fr * kLdA + 8 * nn + fc);
+            const float2 hi = *reinterpret_cast<const float2*>(m + (fr + 8) * kLdA + 8 * nn + fc);
+            x[nn][0] = lo.x, x[nn][1] = lo.y, x[nn][2] = hi.x, x[nn][3] = hi.y;
+          }
+        };
+        float x[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[nt][e] = 0.0f, w[nt][e] = 0.0f;
-        if (nt / 2 <= rw) {
-          const float2 lo = *reinterpret_cast<const float2*>(p_s + (16 * rw + fr) * kLdA + 8 * nt + fc);
-          const float2 hi = *reinterpret_cast<const float2*>(p_s + (16 * rw + fr + 8) * kLdA + 8 * nt + fc);
-          w[nt][0] = lo.x, w[nt][1] = lo.y, w[nt][2] = hi.x, w[nt][3] = hi.y;
+        for (int u = 0; u < 2; ++u) {
+          const int p = (quad + 1) % 4 + 4 * u;
+          if (p >= 6) continue;
+          const int k = p < 1 ? 1 : p < 3 ? 2 : 3, j = p - k * (k - 1) / 2;
+          load_block(x, a_s + 16 * k * (kLdA + 1));
+          const float* m = a_s + 16 * k * kLdA + 16 * j;
+          uint32_t xt[3][4], mt[3][4];
+#pragma unroll
+          for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              split3(m[(8 * kk + fc) * kLdA + 8 * nn + fr], m[(8 * kk + fc + 1) * kLdA + 8 * nn + fr], mt[0][2 * nn + kk],
+                     mt[1][2 * nn + kk], mt[2][2 * nn + kk]);
+          operand(xt, x);
+#pragma unroll
+          for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nn][e] = 0.0f;
+          product(x, xt, mt);
+          operand(nt[u], x);
         }
-        if (nt / 2 == rt) {  // the identity times D
-          const float2 lo = *reinterpret_cast<const float2*>(a_s + (16 * rt + fr) * kLdA + 8 * nt + fc);
-          const float2 hi = *reinterpret_cast<const float2*>(a_s + (16 * rt + fr + 8) * kLdA + 8 * nt + fc);
-          t[nt][0] = lo.x, t[nt][1] = lo.y, t[nt][2] = hi.x, t[nt][3] = hi.y;
+        load_block(x, blk);
+        operand(dt, x);
+        named_barrier(bar_id, kGroupThreads);  // A is read
+        // lane l addresses row l % 8 of matrix l / 8: rows 0-7, 8-15 of columns 0-7, then of 8-15
+#pragma unroll
+        for (int e = 0; e < 3; ++e) stmatrix4(block_at(quad, quad) + 512 * e + ld_at, dt[e]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int p = (quad + 1) % 4 + 4 * u;
+          if (p >= 6) continue;
+          const int k = p < 1 ? 1 : p < 3 ? 2 : 3, j = p - k * (k - 1) / 2;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) stmatrix4(block_at(k, j) + 512 * e + ld_at, nt[u][e]);
         }
       }
+      named_barrier(bar_id, kGroupThreads);  // D and N are there
+      {
+        // rows 16 rb .. of T = X diag(beta): the identity's first step is a copy of
+        // N's blocks, its last of D's
+        float x[4][2][4];
+        auto load_terms = [&](float (&v)[2][4], uint32_t m) {  // the sum of a block's terms
 #pragma unroll
-      for (int k = 3; k >= 0; --k) {
-        const bool do_t = k <= rt, do_w = k <= rw;  // warp-uniform
-        if (!do_t && !do_w) continue;
-        uint32_t th[2][4], tl[2][4], wh[2][4], wl[2][4];
+          for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
-        for (int j = k; j >= 0; --j) {  // j == k: times the inverse of the diagonal block
-          Tf32x2 bm[2][2][2];  // [k8][n8][row pair]
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t r = (uint32_t)(fr + 8 * e), at = m + r * 32 + ((((uint32_t)nn) ^ ((r >> 2) & 1)) << 4) + fc * 2;
+              float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                bm[kk][nn][e].set(a_s[(16 * k + 8 * kk + fc + e) * kLdA + 16 * j + 8 * nn + fr]);
-          auto product = [&](float (&x)[8][4], uint32_t (&xh)[2][4], uint32_t (&xl)[2][4], bool solved) {
-            float acc[2][4];
-#pragma unroll
-            for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nn][e] = j < k ? x[2 * j + nn][e] : 0.0f;
-            if (j == k) {
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) tf32_operand(xh[kk], xl[kk], x[2 * k + kk]);
-            }
-            if (j < k || !solved) {
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int nn = 0; nn < 2; ++nn) {
-                  mma_tf32(acc[nn], xl[kk], bm[kk][nn][0].hi, bm[kk][nn][1].hi);
-                  mma_tf32(acc[nn], xh[kk], bm[kk][nn][0].lo, bm[kk][nn][1].lo);
-                  mma_tf32(acc[nn], xh[kk], bm[kk][nn][0].hi, bm[kk][nn][1].hi);
-                }
-#pragma unroll
-              for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[2 * j + nn][e] = acc[nn][e];
-              if (j == k) {
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) tf32_operand(xh[kk], xl[kk], x[2 * k + kk]);
+              for (int t = 2; t >= 0; --t) {
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at + 512 * t) : "memory");
+                lo += __uint_as_float(w << 16), hi += __uint_as_float(w & 0xffff0000u);
               }
+              v[nn][2 * e] = lo, v[nn][2 * e + 1] = hi;
             }
-          };
-          if (do_t) product(t, th, tl, k == rt);
-          if (do_w) product(w, wh, wl, false);
-        }
-      }
-      // T's columns times beta, its rows decayed to the chunk's end; one scale for
-      // T and one for W, from the largest row sum of each
-      {
-        const float d0 = gt.fd[16 * rt + fr], d1 = gt.fd[16 * rt + fr + 8];
-        float st0 = 0.0f, st1 = 0.0f, sw0 = 0.0f, sw1 = 0.0f;
+        };
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-          const float2 be = *reinterpret_cast<const float2*>(&gt.beta[8 * nt + fc]);
-          t[nt][0] *= be.x * d0, t[nt][1] *= be.y * d0, t[nt][2] *= be.x * d1, t[nt][3] *= be.y * d1;
-          w[nt][0] *= be.x, w[nt][1] *= be.y, w[nt][2] *= be.x, w[nt][3] *= be.y;
-          st0 += fabsf(t[nt][0]) + fabsf(t[nt][1]), st1 += fabsf(t[nt][2]) + fabsf(t[nt][3]);
-          sw0 += fabsf(w[nt][0]) + fabsf(w[nt][1]), sw1 += fabsf(w[nt][2]) + fabsf(w[nt][3]);
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k][nn][e] = 0.0f;
+          if (k <= rb) load_terms(x[k], block_at(rb, k));
         }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          st0 += __shfl_xor_sync(0xffffffffu, st0, o), st1 += __shfl_xor_sync(0xffffffffu, st1, o);
-          sw0 += __shfl_xor_sync(0xffffffffu, sw0, o), sw1 += __shfl_xor_sync(0xffffffffu, sw1, o);
-        }
-        const unsigned mt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(st0, st1)));
-        const unsigned mw = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sw0, sw1)));
-        if (lane == 0) gt.sum_t[quad] = __uint_as_float(mt), gt.sum_w[quad] = __uint_as_float(mw);
-      }
-      named_barrier(1, 128);
-      {
-        const float4 a = *reinterpret_cast<const float4*>(gt.sum_t), d = *reinterpret_cast<const float4*>(gt.sum_w);
-        int te = 3 - exponent_of(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
-        int we = 3 - exponent_of(fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)));
-        te = te > 100 ? 100 : te, we = we > 100 ? 100 : we;
-        if (c > 0) wait(tp_empty, c - 1);
-        if (quad == 0 && lane == 0) gt.t_exp = te, gt.w_exp = we;
-        const float ct = pow2(te), cw = pow2(we);
-        // lane l addresses row l % 8 of matrix l / 8: rows 0-7 and 8-15 of one
-        // granule of 8 columns, then of the next; granule q of row r at q ^ (r % 8)
-        const uint32_t at = base + L::kOffTp + (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * 128 +
-                                                          ((((lane >> 4) & 1) ^ (lane & 7)) << 4));
-        const uint32_t at_t = at + rt * 2048, at_w = at + 8192 + rw * 2048;
+        for (int k = 2; k >= 0; --k) {
+          if (k >= rb) continue;  // warp-uniform
+          uint32_t xt[3][4];
+          operand(xt, x[k]);
 #pragma unroll
-        for (int nt = 0; nt < 8; nt += 2) {
-          uint32_t hi[4], lo[4];
+          for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = __fmul2_rn(make_float2(t[nt + e / 2][2 * (e & 1)], t[nt + e / 2][2 * (e & 1) + 1]),
-                                        make_float2(ct, ct));
-            split2(v.x, v.y, hi[e], lo[e]);
+            for (int e = 0; e < 4; ++e) x[k][nn][e] = 0.0f;  // replaced by Y_k D_k
+#pragma unroll
+          for (int u = 1; u <= k + 1; ++u) {  // the next block first, the diagonal's last
+            const int j = u <= k ? k - u : k;
+            uint32_t m[3][4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldmatrix4_trans(m[e], block_at(k, j) + 512 * e + ld_at);
+            product(x[j], xt, m);
           }
-          stmatrix4(at_t ^ (uint32_t)(nt << 4), hi);
-          stmatrix4((at_t ^ (uint32_t)(nt << 4)) + 16384, lo);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = __fmul2_rn(make_float2(w[nt + e / 2][2 * (e & 1)], w[nt + e / 2][2 * (e & 1) + 1]),
-                                        make_float2(cw, cw));
-            split2(v.x, v.y, hi[e], lo[e]);
-          }
-          stmatrix4(at_w ^ (uint32_t)(nt << 4), hi);
-          stmatrix4((at_w ^ (uint32_t)(nt << 4)) + 16384, lo);
         }
+        // columns times beta, in three terms to shared memory
+        const uint32_t at = base + L::kOffT + (uint32_t)(rb * 2048) +
+                            (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * 128 + ((((lane >> 4) & 1) ^ (lane & 7)) << 4));
+        if (c > 0) wait(t_empty + 8 * ((c - 1) & 1), (c - 1) / 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k > rb) continue;
+          uint32_t xt[3][4];
+#pragma unroll
+          for (int nn = 0; nn < 2; ++nn) {
+            const float2 be = *reinterpret_cast<const float2*>(&gt.beta[16 * k + 8 * nn + fc]);
+            x[k][nn][0] *= be.x, x[k][nn][1] *= be.y, x[k][nn][2] *= be.x, x[k][nn][3] *= be.y;
+          }
+          operand(xt, x[k]);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) stmatrix4((at ^ (uint32_t)(k << 5)) + e * 8192, xt[e]);
+        }
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tp_full);
-    }
-  } else if (warp < kGateWarp) {
-    // --------------------------------------------------------------- load ----
-    const int lw = warp - 12, lt = threadIdx.x - 12 * 32;
-    constexpr int kLanes = DK / 8;           // lanes per row
-    constexpr int kRowsPer = 32 / kLanes;    // rows per warp and pass
-    constexpr int kStep = kLoadWarps * kRowsPer;  // rows per pass
-    const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-    const int valid = g.dk - col;            // of this lane's eight components
-    const In* k_base = reinterpret_cast<const In*>(g.k) + b * g.T * g.ld_k + (int64_t)hk * g.dk;
-    const In* q_base = reinterpret_cast<const In*>(g.q) + b * g.T * g.ld_q + (int64_t)hk * g.dk;
-    const In* v_base = reinterpret_cast<const In*>(g.v) + b * g.T * g.ld_v + (int64_t)h * g.dv + tile * kM;
-    const bool staged = !F32 && vec_kq;      // K and Q through tensor copies
-    auto tokens = [&](int c) { return (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC); };
-    // K and Q rows of chunk c (tokens past the end read as zero)
-    auto copy_kq = [&](int c) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(raw_full, 2 * kC * DK * 2);
-        tma_load_3d(base + L::kOffRaw, &map_k, hk * g.dk, c * kC, (int)b, raw_full);
-        tma_load_3d(base + L::kOffRaw + kC * DK * 2, &map_q, hk * g.dk, c * kC, (int)b, raw_full);
-      }
-    };
-    if (staged && lw == 0) copy_kq(0);
-    for (int c = 0; c < n_chunks; ++c) {
-      const int ks = c % L::kKqStages;
-      const int left = tokens(c);
-      int* exps = reinterpret_cast<int*>(gbase + L::kOffExp) + (c & 1) * 2 * kC;
-      if (staged) wait(raw_full, c);
-      if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
-      // K (rows 0-63) and Q (64-127), each row scaled to [2^13, 2^14)
-      // kBatch rows' loads and reductions are in flight together
-      constexpr int kBatch = F32 ? 4 : 8;
-      static_assert(2 * kC % (kBatch * kStep) == 0, "whole batches");
-#pragma unroll 1
-      for (int r0 = lw * kRowsPer + sub; r0 < 2 * kC; r0 += kBatch * kStep) {
-        float f[kBatch][8];
-        int ex[kBatch];  // floor(log2) of the row's largest value
-        if constexpr (!F32) {
-          uint4 x[kBatch];
-          if (staged) {
-#pragma unroll
-            for (int p = 0; p < kBatch; ++p) {
-              x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + (r0 + p * kStep) * DK * 2 + col * 2);
-              if (valid <= 0) x[p] = make_uint4(0, 0, 0, 0);  // columns past dk are another head's
-            }
-          } else {
-#pragma unroll 1
-            for (int p = 0; p < kBatch; ++p) {
-              const int r = r0 + p * kStep, i = r & (kC - 1);
-              const int64_t t = (int64_t)c * kC + i;
-              const uint16_t* src = reinterpret_cast<const uint16_t*>(r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
-              uint32_t e[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) e[j] = i < left && j < valid ? src[j] : 0;
-              // by way of the rows' place in the staging buffer (this thread's own granules)
-              *reinterpret_cast<uint4*>(gbase + L::kOffRaw + r * DK * 2 + col * 2) =
-                  make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-            }
-#pragma unroll
-            for (int p = 0; p < kBatch; ++p)
-              x[p] = *reinterpret_cast<const uint4*>(gbase + L::kOffRaw + (r0 + p * kStep) * DK * 2 + col * 2);
-          }
-          // bit patterns of |x| order as the values do; two rows share a word
-#pragma unroll
-          for (int p = 0; p < kBatch; p += 2) {
-            uint32_t m[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              m[u] = __vmaxu2(__vmaxu2(x[p + u].x & 0x7fff7fffu, x[p + u].y & 0x7fff7fffu),
-                              __vmaxu2(x[p + u].z & 0x7fff7fffu, x[p + u].w & 0x7fff7fffu));
-            uint32_t both = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
-            ex[p] = (int)((both >> 7) & 255) - 127;
-            ex[p + 1] = (int)(both >> 23) - 127;
-          }
-#pragma unroll
-          for (int p = 0; p < kBatch; ++p) unpack8(f[p], x[p]);
-        } else {
-#pragma unroll
-          for (int p = 0; p < kBatch; ++p) {
-            const int r = r0 + p * kStep, i = r & (kC - 1);
-            const bool in = i < left;
-            const int64_t t = in ? (int64_t)c * kC + i : 0;
-            const float* src = reinterpret_cast<const float*>(r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
-            if (vec_kq) {
-              float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
-              if (in && valid > 0) lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
-              f[p][0] = lo.x, f[p][1] = lo.y, f[p][2] = lo.z, f[p][3] = lo.w;
-              f[p][4] = hi.x, f[p][5] = hi.y, f[p][6] = hi.z, f[p][7] = hi.w;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) f[p][j] = in && j < valid ? src[j] : 0.0f;
-            }
-          }
-          float mx[kBatch];
-#pragma unroll
-          for (int p = 0; p < kBatch; ++p) {
-            mx[p] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mx[p] = fmaxf(mx[p], fabsf(f[p][j]));
-          }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int p = 0; p < kBatch; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
-#pragma unroll
-          for (int p = 0; p < kBatch; ++p) ex[p] = exponent_of(mx[p]);
-        }
-#pragma unroll
-        for (int p = 0; p < kBatch; ++p) {
-          const int r = r0 + p * kStep;
-          const int e = ex[p] < -107 ? 120 : 13 - ex[p];
-          const float cs = pow2(e);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 v = __fmul2_rn(make_float2(f[p][2 * j], f[p][2 * j + 1]), make_float2(cs, cs));
-            if (F32) {
-              split2(v.x, v.y, hi[j], lo[j]);
-            } else {
-              const __half2 t = __floats2half2_rn(v.x, v.y);
-              hi[j] = *reinterpret_cast<const uint32_t*>(&t);
-            }
-          }
-          if (col == 0) exps[r] = e;
-          const uint32_t at =
-              base + ks * L::kKq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
-          st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
-          if (F32) st_shared16(at + L::kKqTerm, lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      named_barrier(2, kLoadThreads + 32);  // every row's exponent is there, the raw rows are read
-      if (staged && lw == 0 && c + 1 < n_chunks) copy_kq(c + 1);
-      mbar_arrive(kq_full + 8 * ks);
-      // V (bf16); rows past the sequence's end are zero, columns past the head's
-      // are lanes that nothing reads
-      if (!F32 && (!vec_v || lw == 0)) {
-        if (c > 0) wait(v_empty, c - 1);
-        if (vec_v) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(v_full, kC * kM * 2);
-            tma_load_3d(base + L::kOffV, &map_v, h * g.dv + tile * kM, c * kC, (int)b, v_full);
-          }
-        } else {
-          const int cols = g.dv - tile * kM < kM ? g.dv - tile * kM : kM;
-          In* v_dst = reinterpret_cast<In*>(gbase + L::kOffV);
-#pragma unroll 4
-          for (int e = lt; e < kC * kM; e += kLoadThreads) {
-            const int r = e / kM, q = e % kM;
-            v_dst[e] = r < left && q < cols ? v_base[((int64_t)c * kC + r) * g.ld_v + q] : from_f32<In>(0.0f);
-          }
-          mbar_arrive(v_full);
-        }
+        mbar_arrive(t_full);
+        mbar_arrive(gate_empty + 8 * (c % kGateSlots));
       }
     }
   } else if (warp == kGateWarp) {
@@ -949,147 +891,244 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     for (int c = 0; c < n_chunks; ++c) {
       Two G[2];
       float be[2];
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        const float a = u ? a_next[1] : a_next[0], bb = u ? b_next[1] : b_next[0];
-        const float la = gdr_log_alpha(a, dt_bias, neg_A);
-        Two x = two_log2(la < -200.0f ? -200.0f : la);
-        const float y = gdr_beta(bb);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const Two t = two_shfl_up(x, o), sum = two_add(x, t);
-          if (lane >= o) x = sum;
-        }
-        if (u)
-          G[1] = x, be[1] = y;
-        else
-          G[0] = x, be[0] = y;
+      for (int u = 0; u < 2; ++u) {
+        const float la = gdr_log_alpha(a_next[u], dt_bias, neg_A);
+        G[u] = two_log2(la < -200.0f ? -200.0f : la);
+        be[u] = gdr_beta(b_next[u]);
       }
       if (c + 1 < n_chunks) fetch(c + 1);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const Two sum = two_add(G[u], two_shfl_up(G[u], o));
+          if (lane >= o) G[u] = sum;
+        }
+      }
       const Two mid = two_shfl(G[0], 31);
       G[1] = two_add(G[1], mid);
       const Two last = two_shfl(G[1], 31);
-      const int* exps = reinterpret_cast<const int*>(gbase + L::kOffExp) + (c & 1) * 2 * kC;
       Gates& gt = gates[c % kGateSlots];
-      named_barrier(2, kLoadThreads + 32);  // the rows' exponents are there, this slot's last readers gone
+      if (c >= kGateSlots) wait(gate_empty + 8 * (c % kGateSlots), c / kGateSlots + 1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = lane + 32 * u;
-        const float ek = (float)exps[i], eq = (float)exps[kC + i];
-        const float ik = pow2(-exps[i]), iq = pow2(-exps[kC + i]);
-        const Two cj = two_add(G[u], Two{ek, 0.0f}), rk = two_add(G[u], Two{-ek, 0.0f}), rq = two_add(G[u], Two{-eq, 0.0f});
-        const float eg = ex2_approx(G[u].h + G[u].l);
-        gt.col_hi[i] = cj.h, gt.col_lo[i] = cj.l;
-        gt.row_hi[i] = rk.h, gt.row_lo[i] = rk.l;
-        gt.row_hi[kC + i] = rq.h, gt.row_lo[kC + i] = rq.l;
+        gt.hi[i] = G[u].h, gt.lo[i] = G[u].l;
         gt.beta[i] = be[u];
-        gt.fx[i] = eg * ik;
-        gt.fd[i] = two_exp2(last, G[u]) * ik;
-        gt.fq[i] = g.scale * eg * iq;
-        if (u == 0) {
-          gt.past[lane] = two_exp2(mid, G[0]) * ik;
-        } else {
-          const float e = two_exp2(G[1], mid);
-          gt.since[0][lane] = -be[1] * e * ik;
-          gt.since[1][lane] = e * iq;
-        }
+        const float eg = ex2_approx(G[u].h + G[u].l);
+        gt.eg[i] = eg, gt.egs[i] = g.scale * eg;
+        gt.fd[i] = two_exp2(last, G[u]);
       }
+      gt.past[lane] = two_exp2(mid, G[0]);
+      gt.since[lane] = two_exp2(G[1], mid);
       if (lane == 0) gt.total = ex2_approx(last.h + last.l);
-      mbar_arrive(kq_full + 8 * (c % L::kKqStages));
+      mbar_arrive(gate_full + 8 * (c % kGateSlots));
     }
-  } else {
+  } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMAs ----
-    if (lane == 0) {
-      constexpr uint32_t id64 = idesc_f16(64, false), id3 = idesc_f16(DK, true);
-      // [K; Q] K^T of chunk c, for the prepare warps
-      auto issue_d0 = [&](int c) {
-        const uint32_t kq = base + (c % L::kKqStages) * L::kKq;
-        wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
-        if (c > 1) wait(d0_empty + 8 * (c & 1), c / 2 - 1);
-        tcgen05_fence_after();
-        uint32_t acc = 0;
-#pragma unroll 1
-        for (int term = 0; term < (F32 ? 3 : 1); ++term) {
-          const uint32_t ka = kq + (term == 1 ? L::kKqTerm : 0), kb = kq + (term == 2 ? L::kKqTerm : 0);
+    // The whole warp runs the loop, so that descriptors stay uniform, and one
+    // elected lane issues: by a lane of a branch of its own a product took 50
+    // cycles to issue and 32 to run.
+    const bool elected = elect_one();
+    constexpr uint32_t id64 = idesc_bf16(64, false), id3 = idesc_bf16(DK, true);
+    constexpr int HK = DK / kParts;
+    // products with K or Q; the output's without the smallest for bf16 tensors
+    constexpr int kPairs = F32 ? 6 : 3, kSkipQ = F32 ? 0 : 1, kSkipP = F32 ? 0 : 3;
+    const uint64_t kq0 = smem_desc(base), kq0_mn = smem_desc(base, 16384), t0 = smem_desc(base + L::kOffT), p0 = smem_desc(base + L::kOffP);
+    auto commit = [&](uint32_t bar) {
+      if (elected) mma_commit(bar);
+    };
+    // [K; Q] K^T of chunk c, for the prepare warps
+    auto issue_d0 = [&](int c) {
+      const uint64_t kq = kq0 + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
+      wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
+      if (c > 0) wait(d0_empty + 8 * ((c - 1) & 1), (c - 1) / 2);
+      tcgen05_fence_after();
 #pragma unroll
-          for (int k = 0; k < DK / 16; ++k) {
-            mma_ss(tmem + kColD0 + 64 * (c & 1), smem_desc(ka + (k / 4) * 16384) + 2 * (k % 4),
-                   smem_desc(kb + (k / 4) * 16384) + 2 * (k % 4), id64, acc);
-            acc = 1;
-          }
-        }
-        mma_commit(d0_full + 8 * (c & 1));
-      };
-      issue_d0(0);
-      for (int c = 0; c < n_chunks; ++c) {
-        const int ks = c % L::kKqStages;
-        const uint32_t kq = base + ks * L::kKq, tp = base + L::kOffTp;
-        wait(s_ready, c);
-        tcgen05_fence_after();
-        // D1: S_hi K_hi + S_lo K_hi (+ S_hi K_lo); keys first, the queries'
-        // half runs under epilogue 1.  A's halves: 8 columns hi, 8 lo of every 16
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint32_t acc = 0;
-#pragma unroll 1
-          for (int term = 0; term < (F32 ? 3 : 2); ++term) {
-            const uint32_t ad = tmem + kColS + (term == 1 ? 8 : 0);
-            const uint32_t bd = kq + (term == 2 ? L::kKqTerm : 0) + part * 8192;
+      for (int p = 0; p < (F32 ? 6 : 1); ++p) {
+        int ta = 0, tb = 0;
+        if (F32) term_pair<true>(p, ta, tb);
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-              mma_ts(tmem + (part ? kColQ : kColX), ad + 16 * k, smem_desc(bd + (k / 4) * 16384) + 2 * (k % 4), id64, acc);
-              acc = 1;
-            }
-          }
-          if (part == 0) mma_commit(x_full);
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint64_t at = kq + (k / 4) * 1024 + 2 * (k % 4);
+          if (elected) mma_ss(tmem + kColD0, at + ta * (L::kKqTerm / 16), at + tb * (L::kKqTerm / 16), id64, p > 0 || k > 0);
         }
-        // one chunk ahead; two accumulators, so the prepare warps need not be
-        // done with this chunk's
-        if (c + 1 < n_chunks) issue_d0(c + 1);
-        wait(tp_full, c);
-        wait(r_ready, c);
-        tcgen05_fence_after();
-        // D2: R_hi T_hi + R_hi T_lo + R_lo T_hi; T's half first, W's under epilogue 2
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint32_t acc = 0;
-#pragma unroll 1
-          for (int term = 0; term < 3; ++term) {
-            const uint32_t ad = tmem + kColX + (term == 2 ? 8 : 0);
-            const uint64_t bd = smem_desc(tp + (term == 1 ? 16384 : 0) + part * 8192);
-#pragma unroll
-            for (int k = 0; k < kC / 16; ++k) {
-              mma_ts(tmem + (part ? kColO : kColU), ad + 16 * k, bd + 2 * k, id64, acc);
-              acc = 1;
-            }
-          }
-          mma_commit(part ? o_full : u_full);
-        }
-        mma_commit(tp_empty);
-        wait(u_ready, c);
-        tcgen05_fence_after();
-        // D3: U_hi K_hi + U_lo K_hi (+ U_hi K_lo); K's rows are the contraction
-        uint32_t acc = 0;
-#pragma unroll 1
-        for (int term = 0; term < (F32 ? 3 : 2); ++term) {
-          const uint32_t ad = tmem + kColU + (term == 1 ? 8 : 0);
-          const uint64_t bd = smem_desc(kq + (term == 2 ? L::kKqTerm : 0), 16384);
-#pragma unroll
-          for (int k = 0; k < kC / 16; ++k) {
-            mma_ts(tmem + kColS, ad + 16 * k, bd + 128 * k, id3, acc);
-            acc = 1;
-          }
-        }
-        mma_commit(s_full);
-        mma_commit(kq_empty + 8 * ks);
       }
-      // the last commit has arrived (and with it every MMA is done) before
-      // tensor memory is freed and the barriers go away
-      const int last = n_chunks - 1;
-      if (!mbar_wait(kq_empty + 8 * (last % L::kKqStages), (uint32_t)(last / L::kKqStages) & 1, kWaitLimit))
-        atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+      commit(d0_full + 8 * (c & 1));
+    };
+    // S times the keys (0) or the queries (1)
+    auto issue_d1 = [&](int c, int part) {
+      const uint64_t kq = kq0 + (uint64_t)((c % L::kKqStages) * (L::kKq / 16) + part * 512);
+      const uint32_t d = tmem + (part ? kColQ : kColX);
+      const int first = part ? kSkipQ : 0;
+#pragma unroll
+      for (int p = first; p < kPairs; ++p) {
+        int ta = 0, tb = 0;
+        term_pair<F32>(p, ta, tb);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint32_t w = (16 * k % HK) / 2, q = 16 * k / HK;
+          const uint32_t ad = (ta < 2 ? ta * (HK / 2) : DK) + w + q * (ta < 2 ? HK : HK / 2);
+          if (elected)
+            mma_ts(d, tmem + kColS + ad, kq + tb * (L::kKqTerm / 16) + (k / 4) * 1024 + 2 * (k % 4), id64, p > first || k > 0);
+        }
+      }
+    };
+    issue_d0(0);
+    for (int c = 0; c < n_chunks; ++c) {
+      wait(s_ready, c);
+      tcgen05_fence_after();
+      issue_d1(c, 0);
+      commit(x_full);
+      if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
+      if (F32) {  // S's third terms make room for the decayed U's
+        if (c > 0) wait(o_empty, c - 1);
+        issue_d1(c, 1);
+      }
+      wait(t_full, c);
+      wait(r_ready, c);
+      tcgen05_fence_after();
+#pragma unroll
+      for (int p = 0; p < 6; ++p) {  // D2 = R T^T
+        int ta = 0, tb = 0;
+        term_pair<true>(p, ta, tb);
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : F32 ? kColO + 16 * k : kColThird + 8 * k;
+          if (elected) mma_ts(tmem + kColU, tmem + ad, t0 + tb * 512 + 2 * k, id64, p > 0 || k > 0);
+        }
+      }
+      commit(u_full);
+      commit(t_empty + 8 * (c & 1));
+      if (!F32) {  // the queries' product, under epilogue 2
+        if (c > 0) wait(o_empty, c - 1);
+        tcgen05_fence_after();
+        issue_d1(c, 1);
+      }
+      wait(u_ready, c);
+      tcgen05_fence_after();
+      // D3 = U K; K's rows are the contraction
+      const uint64_t kq_mn = kq0_mn + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        int ta = 0, tb = 0;
+        term_pair<F32>(p, ta, tb);
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : kColThird + 8 * k;
+          if (elected) mma_ts(tmem + kColS, tmem + ad, kq_mn + tb * (L::kKqTerm / 16) + 128 * k, id3, p > 0 || k > 0);
+        }
+      }
+      commit(s_full);
+      commit(kq_empty + 8 * (c % L::kKqStages));
+      // the output's U P^T, under epilogue 3
+      wait(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
+      const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
+#pragma unroll
+      for (int p = kSkipP; p < 6; ++p) {
+        int ta = 0, tb = 0;
+        term_pair<true>(p, ta, tb);
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
+          if (elected) mma_ts(tmem + kColO, tmem + ad, pd + tb * 512 + 2 * k, id64, p > kSkipP || k > 0);
+        }
+      }
+      commit(o_full);
+      commit(p_empty + 8 * (c % L::kPBuffers));
+      if (c + L::kAhead < n_chunks) issue_d0(c + L::kAhead);
     }
-    __syncwarp();
+    // the last commit has arrived (and with it every MMA is done) before
+    // tensor memory is freed and the barriers go away
+    const int last = n_chunks - 1;
+    if (!mbar_wait(p_empty + 8 * (last % L::kPBuffers), (uint32_t)(last / L::kPBuffers) & 1, kWaitLimit))
+      atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+  } else {
+    // --------------------------------------------------------------- load ----
+    const int lt = threadIdx.x - 32 * kLoadWarp;
+    const In* k_base = reinterpret_cast<const In*>(g.k) + b * g.T * g.ld_k + (int64_t)hk * g.dk;
+    const In* q_base = reinterpret_cast<const In*>(g.q) + b * g.T * g.ld_q + (int64_t)hk * g.dk;
+    const In* v_base = reinterpret_cast<const In*>(g.v) + b * g.T * g.ld_v + (int64_t)h * g.dv + tile * kM;
+    // chunk c's output from its place over the values
+    auto store_y = [&](int c) {
+      if (lt == 0) {
+        tma_store_4d(&map_y, base + L::kOffV, tile * kM, h, c * kC, (int)b);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      }
+      // the other path's element-wise loads write there next
+      if (!vec_v) named_barrier(4, kLoadThreads);
+    };
+    for (int c = 0; c < n_chunks; ++c) {
+      const int ks = c % L::kKqStages;
+      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
+      const uint32_t kq = base + ks * L::kKq;
+      if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
+      if (vec_kq) {
+        // tokens past the end and components past dk read as zero
+        if (lt == 0) {
+          mbar_arrive_expect_tx(kq_full + 8 * ks, L::kKqTerm);
+#pragma unroll
+          for (int kb = 0; kb < L::kBlocks; ++kb) {
+            tma_load_4d(kq + kb * 16384, &map_k, 64 * kb, hk, c * kC, (int)b, kq_full + 8 * ks);
+            tma_load_4d(kq + kb * 16384 + 8192, &map_q, 64 * kb, hk, c * kC, (int)b, kq_full + 8 * ks);
+          }
+        }
+      } else {
+        // by hand, eight components of a row at a time: K rows 0-63, Q 64-127;
+        // granule q of row r at q ^ (r % 8)
+#pragma unroll 1
+        for (int e = lt; e < 2 * kC * (DK / 8); e += kLoadThreads) {
+          const int r = e / (DK / 8), col = e % (DK / 8) * 8, i = r & (kC - 1);
+          const int valid = i < left ? g.dk - col : 0;
+          const int64_t t = (int64_t)c * kC + i;
+          const In* src = (r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = j < valid ? to_f32(src[j]) : 0.0f;
+          const uint32_t at = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
+          uint32_t x[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) split3(f[2 * j], f[2 * j + 1], x[0][j], x[1][j], x[2][j]);
+#pragma unroll
+          for (int p = 0; p < L::kTerms; ++p)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
+                         "r"(x[p][2]), "r"(x[p][3])
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(kq_full + 8 * ks);
+      }
+      // V (bf16); tokens past the sequence's end and components past dv are zero
+      if (!F32) {
+        if (c > 0) wait(v_empty, c - 1);
+        if (vec_y && c > 1) store_y(c - 2);
+        if (vec_v) {
+          if (lt == 0) {
+            mbar_arrive_expect_tx(v_full, kC * kM * 2);
+            tma_load_4d(base + L::kOffV, &map_v, tile * kM, h, c * kC, (int)b, v_full);
+          }
+        } else {
+          const int cols = g.dv - tile * kM < kM ? g.dv - tile * kM : kM;
+          In* v_dst = reinterpret_cast<In*>(gbase + L::kOffV);
+#pragma unroll 4
+          for (int e = lt; e < kC * kM; e += kLoadThreads) {
+            const int r = e / kM, q = e % kM;
+            v_dst[e] = r < left && q < cols ? v_base[((int64_t)c * kC + r) * g.ld_v + q] : from_f32<In>(0.0f);
+          }
+          mbar_arrive(v_full);
+        }
+      }
+    }
+    if (!F32) {  // the last two chunks' outputs
+      wait(v_empty, n_chunks - 1);
+      if (vec_y && n_chunks > 1) store_y(n_chunks - 2);
+      if (!vec_v || lt == 0) mbar_arrive(v_full);
+      wait(v_empty, n_chunks);
+      if (vec_y) store_y(n_chunks - 1);
+      if (lt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -1115,24 +1154,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return f;
 }
 
-// [B][T][cols] bf16, rows ld apart: boxes of 64 tokens of one sequence x `box`
-// columns, starting at any multiple of 8 columns; outside it reads as zero.
-// False if the layout has no such map (then the element-wise path loads it).
-bool make_map(CUtensorMap* map, const void* p, int64_t B, int64_t T, int64_t cols, int64_t ld, int d, int box) {
-  if (reinterpret_cast<uintptr_t>(p) % 16 || ld % 8 || d % 8 || T * ld * 2 >= (int64_t(1) << 40) || T > INT32_MAX - kC ||
-      cols > INT32_MAX - box)
-    return false;
+// Tensor maps over bf16 rows ld apart, of [B][T] tokens; outside them everything
+// reads as zero.  False if the layout has no such map (then the element-wise path
+// loads it).
+bool mappable(const void* p, int64_t T, int64_t ld, int d) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && d % 8 == 0 && T * ld * 2 < (int64_t(1) << 40) &&
+         T <= INT32_MAX - kC;
+}
+// [B][T][H][d] by boxes of 64 (swizzled) or 128 components of one head of 64 tokens
+bool make_map_heads(CUtensorMap* map, const void* p, int64_t B, int64_t T, int H, int d, int64_t ld, int box = 64) {
   auto enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)T, (cuuint64_t)B};
-  const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(T * ld * 2)};
-  const cuuint32_t boxes[3] = {(cuuint32_t)box, (cuuint32_t)kC, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, boxes, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+  if (!enc || !mappable(p, T, ld, d)) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)(d * 2), (cuuint64_t)(ld * 2), (cuuint64_t)(T * ld * 2)};
+  const cuuint32_t boxes[4] = {(cuuint32_t)box, 1, (cuuint32_t)kC, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
 template <int DK, bool F32>
 cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
   auto kern = chunk_kernel<DK, F32>;
@@ -1146,19 +1186,16 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     __atomic_store_n(&configured[dev], 1, __ATOMIC_RELAXED);
   }
-  CUtensorMap mk = {}, mq = {}, mv = {};
-  int vec_kq, vec_v = 0;
-  if (F32) {
-    auto rows16 = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0; };
-    vec_kq = rows16(a.k, a.ld_k) && rows16(a.q, a.ld_q) && a.dk % 8 == 0;
-  } else {
-    const int64_t kc = (int64_t)a.Hk * a.dk, vc = (int64_t)a.Hv * a.dv;
-    vec_kq = make_map(&mk, a.k, a.B, a.T, kc, a.ld_k, a.dk, DK) && make_map(&mq, a.q, a.B, a.T, kc, a.ld_q, a.dk, DK);
-    vec_v = make_map(&mv, a.v, a.B, a.T, vc, a.ld_v, a.dv, kM);
+  CUtensorMap mk = {}, mq = {}, mv = {}, my = {};
+  int vec_kq = 0, vec_v = 0, vec_y = 0;
+  if (!F32) {
+    vec_kq = make_map_heads(&mk, a.k, a.B, a.T, a.Hk, a.dk, a.ld_k) && make_map_heads(&mq, a.q, a.B, a.T, a.Hk, a.dk, a.ld_q);
+    vec_v = make_map_heads(&mv, a.v, a.B, a.T, a.Hv, a.dv, a.ld_v, kM);
+    vec_y = a.y_bf16 && make_map_heads(&my, a.y, a.B, a.T, a.Hv, a.dv, a.ld_y, kM);
   }
   const int64_t ctas = a.B * a.Hv * ((a.dv + kM - 1) / kM);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, vec_kq, vec_v);
+  kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, my, vec_kq, vec_v, vec_y);
   return cudaGetLastError();
 }
 

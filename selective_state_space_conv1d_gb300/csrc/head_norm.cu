@@ -15,7 +15,7 @@
 // product's rounding is 0.03 rad), so the lane holds inv_freq as a 64-bit
 // fraction of a turn and multiplies in integers: whole turns overflow out of
 // the word exactly, for either sign, and its high half is the angle to 2^-32
-// turns.  The table entry's own error is 2^-53 turns times the position.
+// turns.  The table entry's own error is 2^-64 turns times the position.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,19 +27,47 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// inv_freq (radians per position) as a 2^-64 fraction of a turn; whole turns
-// per position do not matter, positions being integers
+// inv_freq (radians per position) as a 2^-64 fraction of a turn: its 24-bit
+// significand times 2^64 / (2 pi), shifted by its exponent.  Whole turns per
+// position do not matter, positions being integers, and fall off the top.
 __device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
-  double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= rint(t);                                          // in [-1/2, 1/2]
-  return (uint64_t)__double2ll_rn(t * 9223372036854775808.0) << 1;
+  constexpr uint64_t kInv2Pi = 2935890503282001226ull;  // 2^64 / (2 pi), to the nearest
+  const uint32_t bits = __float_as_uint(inv_freq);
+  const int field = (int)((bits >> 23) & 255);
+  const uint32_t m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
+  const int right = 150 - (field ? field : 1);  // inv_freq = m 2^-right
+  const uint64_t lo = (uint64_t)m * (uint32_t)kInv2Pi, hi = (uint64_t)m * (uint32_t)(kInv2Pi >> 32) + (lo >> 32);
+  // the product is hi 2^32 + (lo mod 2^32), 86 bits
+  const uint64_t low = (hi << 32) | (uint32_t)lo, high = hi >> 32;
+  uint64_t t;
+  if (right >= 64)
+    t = right < 128 ? high >> (right - 64) : 0;
+  else if (right > 0)
+    t = (low >> right) | (high << (64 - right));
+  else
+    t = right > -64 ? low << -right : 0;
+  return (bits >> 31) ? 0 - t : t;
 }
 
+// Cosine and sine of position x turns.  The product's high word is the angle to
+// 2^-32 of a turn; its nearest quarter is taken off as an integer, and what is
+// left, at most an eighth of a turn either way, goes through the Taylor series
+// (the first terms left out are below 2^-25).
 __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turns) {
-  const int32_t hi = (int32_t)(((uint64_t)position * turns) >> 32);  // signed: [-1/2, 1/2) turn
-  float s, c;
-  sincospif((float)hi * 4.656612873077393e-10f, &s, &c);  // 2^-31: half-turns
-  return make_float2(c, s);
+  const uint32_t hi = (uint32_t)(((uint64_t)position * turns) >> 32);
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
+  const float t = (float)(int32_t)(hi - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const float t2 = t * t;
+  float s = fmaf(t2, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
+  s = fmaf(t2, s, 8.3333333e-3f);
+  s = fmaf(t2, s, -1.6666667e-1f);
+  s = fmaf(t2 * t, s, t);
+  float c = fmaf(t2, 2.4801587e-5f, -1.3888889e-3f);  // 1/8!, -1/6!
+  c = fmaf(t2, c, 4.1666667e-2f);
+  c = fmaf(t2, c, -0.5f);
+  c = fmaf(t2, c, 1.0f);
+  const float x = (quarter & 1) ? s : c, y = (quarter & 1) ? c : s;
+  return make_float2(((quarter + 1) & 2) ? -x : x, (quarter & 2) ? -y : y);
 }
 
 template <typename T>
@@ -250,22 +278,27 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadNormArgs 
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = g.weight && in ? __ldg(g.weight + c + i) : 1.0f;
   // unit u is head u % H of token u / H; a CTA takes per_group strides of kGroups
+  // units, so one division a group and then a step from unit to unit
   const int64_t base = (int64_t)blockIdx.x * kGroups * per_group + threadIdx.x / G;
+  int64_t row = base < 0x7fffffff ? (int64_t)((uint32_t)base / (uint32_t)g.H) : base / g.H;
+  int h = (int)(base - row * g.H);
   for (int s = 0; s < per_group; s += kHeads) {
     Vec8<IN> ry[kHeads], rz[kHeads];
+    int64_t rows[kHeads];
+    int hs[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-      const int64_t u = base + (int64_t)(s + j) * kGroups;
-      if (s + j < per_group && u < units && in) {
-        const int64_t row = u / g.H, h = u % g.H;
+      rows[j] = row, hs[j] = h;
+      if (s + j < per_group && base + (int64_t)(s + j) * kGroups < units && in) {
         ry[j].load(reinterpret_cast<const IN*>(g.y) + row * g.ld_y + h * g.d + c);
         if (g.z) rz[j].load(reinterpret_cast<const IN*>(g.z) + row * g.ld_z + h * g.d + c);
       }
+      h += kGroups;
+      while (h >= g.H) h -= g.H, ++row;
     }
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-      const int64_t u = base + (int64_t)(s + j) * kGroups;
-      if (s + j >= per_group || u >= units) break;  // uniform in the group
+      if (s + j >= per_group || base + (int64_t)(s + j) * kGroups >= units) break;  // uniform in the group
       float f[8];
       if (in) {
         ry[j].unpack(f);
@@ -288,8 +321,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadNormArgs 
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= silu_f(z[i]);
         }
-        const int64_t row = u / g.H, h = u % g.H;
-        store8(reinterpret_cast<OUT*>(g.out) + row * g.ld_out + h * g.d + c, f);
+        store8(reinterpret_cast<OUT*>(g.out) + rows[j] * g.ld_out + hs[j] * g.d + c, f);
       }
     }
   }
