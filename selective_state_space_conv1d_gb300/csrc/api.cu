@@ -922,6 +922,8 @@ int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, const void* q,
   int rc;
   if ((rc = gated_delta_sizes(B, T, Hk, Hv, dk, dv))) return rc;
   if (workspace_bytes < 0) return fail(MAMBA_ERR_INVALID_ARG, "negative workspace_bytes");
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return fail(MAMBA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (B == 0) return ok();
   const int64_t ns = Hv * dv * dk;
   mamba::GatedDeltaArgs g{y,  ld_y, 0,       q,     ld_q,     k,         ld_k, v, ld_v,    a,       ld_a,    b,      ld_b,
@@ -935,8 +937,9 @@ int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, const void* q,
   if (T == 0) return copy_state(state_out, state_in, B * ns, s);
   mamba::DeviceInfo dev;
   if ((rc = current_device(&dev))) return rc;
-  const cudaError_t e = mamba::gated_delta_takes_chunks(g) ? mamba::launch_gated_delta_chunk(g, dev, s)
-                                                           : mamba::launch_gated_delta_recurrent(g, dev, s);
+  const cudaError_t e = mamba::gated_delta_takes_chunks(g)
+                            ? mamba::launch_gated_delta_chunk(g, dev, workspace, workspace_bytes, s)
+                            : mamba::launch_gated_delta_recurrent(g, dev, s);
   if (e != cudaSuccess) return cuda_fail("gated_delta_prefill launch", e);
   return ok();
 }
@@ -945,8 +948,14 @@ int64_t mamba_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int6
                                           int in_dtype) {
   int rc;
   if ((rc = gated_delta_sizes(B, T, Hk, Hv, dk, dv)) || (rc = check_dtype("in_dtype", in_dtype))) return rc;
+  mamba::GatedDeltaArgs g{};
+  g.B = B, g.T = T, g.Hk = (int)Hk, g.Hv = (int)Hv, g.dk = (int)dk, g.dv = (int)dv;
+  g.in_bf16 = in_dtype == MAMBA_BF16;
   ok();
-  return 0;
+  if (B == 0 || !mamba::gated_delta_takes_chunks(g)) return 0;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  return mamba::gated_delta_chunk_workspace(g, dev);
 }
 
 int mamba_gated_delta_step_batched(void* y, int64_t ld_y, int y_dtype, const void* q, int64_t ld_q, const void* k,

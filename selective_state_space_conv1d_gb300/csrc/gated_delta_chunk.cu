@@ -38,7 +38,9 @@
 // The output of bf16 tensors, which feeds back into nothing, takes the products
 // above 2^-16 alone.
 //
-// One CTA per (sequence, value head, 128 value components), warps specialised:
+// An item is a (sequence, value head, 128 value components); its chunks follow one
+// another.  How items and their chunks are laid over the SMs: see Plan.  A CTA's
+// warps are specialised:
 //   0-15  epilogues 1-3, output, the state in registers (lane = component; four
 //         warps per lane quarter, each a quarter of the columns)
 //   16-23 prepare: A and P from [K; Q] K^T and the gates, T and P to shared memory;
@@ -112,6 +114,89 @@ struct Smem {
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
   static_assert(kAlloc <= 232448, "shared memory over the opt-in limit");
+};
+
+// How the work is laid over CTAs (one an SM).
+//  kWide: items in order, every CTA an equal run of their chunks, so that an item
+//    may begin in one CTA and end in the next.  A CTA first runs the beginning of
+//    its last item and leaves the state for the next CTA, then its whole items,
+//    then the end of its first: by then the state it needs has long been there
+//    (the CTA before started with it), and no two items wait in a circle.
+//  Few items, long sequences: each is cut into `parts` of equal length, for which
+//  three launches are made.
+//  kAheadPass: the state at the end of every part but the last, the first part from
+//    state_in (with its output), the others from zero; and, as one more item per
+//    head, the part's linear map Phi of the state before it (the same recurrence
+//    with values of zero, from the identity).
+//  (join_kernel: state before part p + 1 = (state before part p) Phi_p + that.)
+//  kPartsPass: the parts but the first again, from their states, with their output.
+enum { kWide = 0, kAheadPass = 1, kPartsPass = 2 };
+struct Plan {
+  int mode;
+  int n_chunks;      // of a sequence
+  int tiles, items;  // of 128 value components; B Hv tiles
+  int parts, part_len;
+  float* states;     // kWide: [CTA][128][dk]; else [parts - 1][B Hv][dv][dk], the state before parts 1 ..
+  float* phi;        // [parts - 2][B Hv][dk][dk], of parts 1 ..
+  int* flags;        // kWide: [CTA], set when its state is there
+};
+
+// A CTA's chunks in the order in which it runs them: the beginning of an item
+// (a_len chunks), b_count whole items, the end of an item (or a part of one).
+struct Schedule {
+  int a_item, a_len, b_first, b_count, t_item, t_begin, t_len, total;
+  bool phi, quiet;  // a part's map instead of its values; no output
+};
+__device__ __forceinline__ Schedule make_schedule(const Plan& p, int heads) {
+  Schedule s = {};
+  const int n = p.n_chunks;
+  if (p.mode == kWide) {
+    const int64_t all = (int64_t)p.items * n;
+    const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+    const int first = (int)(lo / n), last = (int)(hi / n);  // last: the item that hi lies in
+    const int lo_c = (int)(lo % n), hi_c = (int)(hi % n);
+    s.b_first = first + (lo_c > 0), s.b_count = last - s.b_first;
+    if (s.b_count < 0) {  // all inside one item
+      s.b_count = 0, s.t_item = first, s.t_begin = lo_c, s.t_len = hi_c - lo_c;
+    } else {
+      s.a_item = last, s.a_len = hi_c;
+      if (lo_c > 0) s.t_item = first, s.t_begin = lo_c, s.t_len = n - lo_c;
+    }
+  } else {
+    const int values = p.items * (p.parts - 1);  // CTAs that run values; the others run Phi
+    int i = (int)blockIdx.x, part;
+    if (i < values) {
+      s.t_item = i % p.items, part = i / p.items + (p.mode == kPartsPass);
+      s.quiet = p.mode == kAheadPass && part > 0;
+    } else {
+      i -= values;
+      s.t_item = i % heads * p.tiles, part = 1 + i / heads;
+      s.phi = s.quiet = true;
+    }
+    s.t_begin = part * p.part_len;
+    s.t_len = n - s.t_begin < p.part_len ? n - s.t_begin : p.part_len;
+  }
+  s.total = s.a_len + s.b_count * n + s.t_len;
+  return s;
+}
+struct Cursor {
+  int item, c, begin, end, b_left;
+  __device__ __forceinline__ void start(const Schedule& s, int n) {
+    b_left = s.b_count + 1;  // as if before the whole items
+    item = s.a_item, c = begin = 0, end = s.a_len;
+    if (s.a_len == 0) piece(s, n);
+  }
+  __device__ __forceinline__ void piece(const Schedule& s, int n) {
+    if (--b_left > 0) {
+      item = s.b_first + s.b_count - b_left, begin = 0, end = n;
+    } else {
+      item = s.t_item, begin = s.t_begin, end = s.t_begin + s.t_len;
+    }
+    c = begin;
+  }
+  __device__ __forceinline__ void next(const Schedule& s, int n) {
+    if (++c >= end) piece(s, n);
+  }
 };
 
 // Tensor memory columns.  D1 is replaced by R's first two terms, later by those of
@@ -313,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
                                                             const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ CUtensorMap map_v,
                                                             const __grid_constant__ CUtensorMap map_y, int vec_kq,
-                                                            int vec_v, int vec_y) {
+                                                            int vec_v, int vec_y, const Plan plan) {
   using L = Smem<DK, F32>;
   using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
   extern __shared__ unsigned char smem_raw[];
@@ -338,13 +423,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   Gates* gates = reinterpret_cast<Gates*>(gbase + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int tiles = (g.dv + kM - 1) / kM;
-  const int tile = blockIdx.x % tiles;
-  const int64_t bh = blockIdx.x / tiles;
-  const int h = (int)(bh % g.Hv);
-  const int64_t b = bh / g.Hv;
-  const int hk = h / (g.Hv / g.Hk);
-  const int n_chunks = (int)((g.T + kC - 1) / kC);
+  const int n_all = plan.n_chunks;
+  const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
+  const int n_chunks = sched.total;  // that this CTA runs
+  struct Item {
+    int tile, h, hk;
+    int64_t b, bh;
+  };
+  auto item_of = [&](const Cursor& k) {
+    const int bh = k.item / plan.tiles, h = bh % g.Hv;
+    return Item{k.item % plan.tiles, h, h / (g.Hv / g.Hk), bh / g.Hv, bh};
+  };
+  auto tokens_of = [&](const Cursor& k) { return (int)(g.T - (int64_t)k.c * kC < kC ? g.T - (int64_t)k.c * kC : kC); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, vec_kq ? 1 : kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
@@ -378,33 +468,99 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     constexpr int HK = DK / kParts;  // key components per thread
     const int quad = warp & 3, part = warp >> 2;
     const int lane_n = quad * 32 + lane;
-    const int n = tile * kM + lane_n;
-    const bool live = n < g.dv;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-    const int64_t s_at = (bh * g.dv + n) * g.dk + part * HK;
-    const bool vec_s = g.dk % 4 == 0 && ((reinterpret_cast<uintptr_t>(g.state_in) | reinterpret_cast<uintptr_t>(g.state_out)) & 15) == 0;
     float s[HK];
+    // four of this lane's values of a [..][dk] state, `left` of them inside it
+    auto load_state = [&](const float* src, bool vec) {
 #pragma unroll
-    for (int j = 0; j < HK; j += 4) {
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (g.state_in && live) {
-        const float* p = g.state_in + s_at + j;
+      for (int j = 0; j < HK; j += 4) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int left = g.dk - part * HK - j;
-        if (vec_s) {
-          if (left > 0) x = *reinterpret_cast<const float4*>(p);
+        if (src) {
+          const float* p = src + part * HK + j;
+          if (vec) {
+            if (left > 0) x = *reinterpret_cast<const float4*>(p);
+          } else {
+            if (left > 0) x.x = p[0];
+            if (left > 1) x.y = p[1];
+            if (left > 2) x.z = p[2];
+            if (left > 3) x.w = p[3];
+          }
+        }
+        s[j] = x.x, s[j + 1] = x.y, s[j + 2] = x.z, s[j + 3] = x.w;
+      }
+    };
+    auto store_state = [&](float* dst, bool vec) {
+#pragma unroll
+      for (int j = 0; j < HK; j += 4) {
+        float* p = dst + part * HK + j;
+        const int left = g.dk - part * HK - j;
+        if (vec) {
+          if (left > 0) *reinterpret_cast<float4*>(p) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         } else {
-          if (left > 0) x.x = p[0];
-          if (left > 1) x.y = p[1];
-          if (left > 2) x.z = p[2];
-          if (left > 3) x.w = p[3];
+          if (left > 0) p[0] = s[j];
+          if (left > 1) p[1] = s[j + 1];
+          if (left > 2) p[2] = s[j + 2];
+          if (left > 3) p[3] = s[j + 3];
         }
       }
-      s[j] = x.x, s[j + 1] = x.y, s[j + 2] = x.z, s[j + 3] = x.w;
-    }
+    };
+    auto vec_state = [&](const float* p) { return g.dk % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    const int64_t all_states = g.B * g.Hv * (int64_t)g.dv * g.dk;
+    // the state before the cursor's piece
+    auto enter = [&](const Cursor& k, const Item& it) {
+      const int n = it.tile * kM + lane_n;
+      const int64_t row = (it.bh * g.dv + n) * g.dk;
+      if (sched.phi) {
+#pragma unroll
+        for (int j = 0; j < HK; ++j) s[j] = part * HK + j == lane_n ? 1.0f : 0.0f;
+        return;
+      }
+      const float* src = g.state_in ? g.state_in + row : nullptr;
+      if (plan.mode == kWide && k.begin > 0) {  // the CTA before has run the item's beginning
+        volatile int* flag = plan.flags + blockIdx.x - 1;
+        const long long t0 = clock64();
+        while (*flag == 0 && !*abort_flag) {
+          if (clock64() - t0 > kWaitLimit) {
+            atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+            *abort_flag = 1;
+          }
+          __nanosleep(200);
+        }
+        __threadfence();
+        src = plan.states + ((int64_t)(blockIdx.x - 1) * kM + lane_n) * g.dk;
+      } else if (plan.mode == kAheadPass && k.begin > 0) {
+        src = nullptr;
+      } else if (plan.mode == kPartsPass) {
+        src = plan.states + (k.begin / plan.part_len - 1) * all_states + row;
+      }
+      load_state(n < g.dv ? src : nullptr, vec_state(src));
+    };
+    // and after it
+    auto leave = [&](const Cursor& k, const Item& it) {
+      const int n = it.tile * kM + lane_n;
+      const int64_t row = (it.bh * g.dv + n) * g.dk;
+      const int p = plan.mode == kWide ? 0 : k.begin / plan.part_len;
+      if (sched.phi) {
+        float* dst = plan.phi + (((p - 1) * g.B * g.Hv + it.bh) * g.dk + lane_n) * g.dk;
+        if (lane_n < g.dk) store_state(dst, vec_state(dst));
+      } else if (plan.mode == kAheadPass) {
+        float* dst = plan.states + p * all_states + row;
+        if (n < g.dv) store_state(dst, vec_state(dst));
+      } else if (k.end < n_all && plan.mode == kWide) {
+        store_state(plan.states + ((int64_t)blockIdx.x * kM + lane_n) * g.dk, vec_state(plan.states));
+        __threadfence();
+        named_barrier(5, 32 * kMainWarps);
+        if (threadIdx.x == 0) atomicExch(plan.flags + blockIdx.x, 1);
+      } else if (k.end == n_all && g.state_out) {
+        float* dst = g.state_out + row;
+        if (n < g.dv) store_state(dst, vec_state(dst));
+      }
+    };
     const int i0 = part * kTok;  // this thread's tokens of a chunk
     const uint32_t y_step = (uint32_t)g.ld_y * (g.y_bf16 ? 2 : 4);  // bytes; a chunk's rows fit 32 bits
-    char* y_at = reinterpret_cast<char*>(g.y) +
-                 ((b * g.T + i0) * g.ld_y + (int64_t)h * g.dv + n) * (g.y_bf16 ? 2 : 4);
+    char* y_at = nullptr;  // of the chunk whose output is to come: this thread's first token
+    int y_rows = 0;        // this thread's tokens inside the sequence
     auto arrive = [&](uint32_t bar) {
       tmem_wait_st();
       tcgen05_fence_before();
@@ -415,10 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // the path from state to state does not wait for it
     auto output = [&](int c) {
       const Gates& gt = gates[c % kGateSlots];
-      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
       wait(o_full, c);
       tcgen05_fence_after();
-      const int rows = live ? left - i0 : 0;  // of this thread's tokens
       // staged over the chunk's values, which epilogue 1 of the next chunk has just
       // taken (the last chunk's own are long gone too), for a tensor store; or
       // stored from here
@@ -446,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         uint32_t at = (uint32_t)i * y_step;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (i + j < rows) {
+          if (i + j < y_rows) {
             if (g.y_bf16)
               *reinterpret_cast<__nv_bfloat16*>(y_at + at) = __float2bfloat16_rn(o[j]);
             else
@@ -455,7 +609,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           at += y_step;
         }
       }
-      y_at += (int64_t)kC * y_step;
       if (!F32) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -465,10 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty), mbar_arrive(gate_empty + 8 * (c % kGateSlots));
     };
+    Cursor at_chunk;
+    at_chunk.start(sched, n_all);
 #pragma unroll 1
     for (int c = 0; c <= n_chunks; ++c) {
+      const Item it = item_of(at_chunk);
       if (F32 && c > 0) wait(o_full, c - 1);  // U's third terms are read
       if (c < n_chunks) {
+        if (at_chunk.c == at_chunk.begin) enter(at_chunk, it);
         // S to tensor memory: of this warp's HK columns of D3's place the first
         // half the first terms, the rest the second; the third terms beyond D3
         const uint32_t at = t_lane + kColS + (uint32_t)(part * HK), at2 = t_lane + kColS + (uint32_t)(DK + part * HK / 2);
@@ -487,13 +644,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (c > 0 && (F32 || c == n_chunks)) output(c - 1);
       if (c == n_chunks) break;
       const Gates& gt = gates[c % kGateSlots];
-      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
+      const int n = it.tile * kM + lane_n;
+      const int rows = n < g.dv ? tokens_of(at_chunk) - i0 : 0;
+      const int64_t row0 = it.b * g.T + (int64_t)at_chunk.c * kC + i0;
       // this lane's value of token i0 + i
       const In* v_tile = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
-      const In* v_global = reinterpret_cast<const In*>(g.v) + (b * g.T + (int64_t)c * kC + i0) * g.ld_v + (int64_t)h * g.dv + n;
+      const In* v_global = reinterpret_cast<const In*>(g.v) + row0 * g.ld_v + (int64_t)it.h * g.dv + n;
       auto value = [&](int i) {
+        if (sched.phi) return 0.0f;
         if (!F32) return to_f32(v_tile[i * kM]);
-        return live && i0 + i < left ? to_f32(v_global[i * g.ld_v]) : 0.0f;
+        return i < rows ? to_f32(v_global[i * g.ld_v]) : 0.0f;
       };
       {  // epilogue 1: R^T = V^T - e^G D1
         wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
@@ -573,21 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]));
         }
       }
-    }
-    if (g.state_out && live) {
-#pragma unroll
-      for (int j = 0; j < HK; j += 4) {
-        float* p = g.state_out + s_at + j;
-        const int left = g.dk - part * HK - j;
-        if (vec_s) {
-          if (left > 0) *reinterpret_cast<float4*>(p) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-        } else {
-          if (left > 0) p[0] = s[j];
-          if (left > 1) p[1] = s[j + 1];
-          if (left > 2) p[2] = s[j + 2];
-          if (left > 3) p[3] = s[j + 3];
-        }
-      }
+      if (at_chunk.c + 1 == at_chunk.end) leave(at_chunk, it);
+      y_at = reinterpret_cast<char*>(g.y) + (row0 * g.ld_y + (int64_t)it.h * g.dv + n) * (g.y_bf16 ? 2 : 4);
+      y_rows = sched.quiet ? 0 : rows;
+      at_chunk.next(sched, n_all);
     }
   } else if (warp < kGateWarp) {
     // ------------------------------------------------------------ prepare ----
@@ -874,22 +1023,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // tokens lane and lane + 32 of a chunk: base-2 logarithms of alpha, summed and
     // kept as two floats each, so that differences between far-decayed tokens keep
     // 32-bit accuracy.  alpha below e^-200 is 0 in f32 all the same.
-    const float neg_A = -expf(g.A_log[h]);
-    const float dt_bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
-    const In* a_base = reinterpret_cast<const In*>(g.a) + b * g.T * g.ld_a + h;
-    const In* b_base = reinterpret_cast<const In*>(g.b) + b * g.T * g.ld_b + h;
-    float a_next[2], b_next[2];
-    auto fetch = [&](int c) {
+    float a_next[2], b_next[2], A_next, bias_next;
+    Cursor at_chunk;
+    at_chunk.start(sched, n_all);
+    auto fetch = [&]() {
+      const Item it = item_of(at_chunk);
+      const In* a_base = reinterpret_cast<const In*>(g.a) + it.b * g.T * g.ld_a + it.h;
+      const In* b_base = reinterpret_cast<const In*>(g.b) + it.b * g.T * g.ld_b + it.h;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t t = (int64_t)c * kC + lane + 32 * u;
+        const int64_t t = (int64_t)at_chunk.c * kC + lane + 32 * u;
         a_next[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
         b_next[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
       }
+      A_next = g.A_log[it.h];
+      bias_next = g.dt_bias ? g.dt_bias[it.h] : 0.0f;
+      at_chunk.next(sched, n_all);
     };
-    fetch(0);
+    fetch();
     for (int c = 0; c < n_chunks; ++c) {
       Two G[2];
+      const float neg_A = -expf(A_next), dt_bias = bias_next;
       float be[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -897,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         G[u] = two_log2(la < -200.0f ? -200.0f : la);
         be[u] = gdr_beta(b_next[u]);
       }
-      if (c + 1 < n_chunks) fetch(c + 1);
+      if (c + 1 < n_chunks) fetch();
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
@@ -1047,22 +1201,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   } else {
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
-    const In* k_base = reinterpret_cast<const In*>(g.k) + b * g.T * g.ld_k + (int64_t)hk * g.dk;
-    const In* q_base = reinterpret_cast<const In*>(g.q) + b * g.T * g.ld_q + (int64_t)hk * g.dk;
-    const In* v_base = reinterpret_cast<const In*>(g.v) + b * g.T * g.ld_v + (int64_t)h * g.dv + tile * kM;
+    Cursor at_chunk, stored;  // the chunk to load, and the one whose output is to be stored
+    at_chunk.start(sched, n_all), stored.start(sched, n_all);
     // chunk c's output from its place over the values
-    auto store_y = [&](int c) {
-      if (lt == 0) {
-        tma_store_4d(&map_y, base + L::kOffV, tile * kM, h, c * kC, (int)b);
+    auto store_y = [&]() {
+      if (lt == 0 && !sched.quiet) {
+        const Item it = item_of(stored);
+        tma_store_4d(&map_y, base + L::kOffV, it.tile * kM, it.h, stored.c * kC, (int)it.b);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       }
       // the other path's element-wise loads write there next
       if (!vec_v) named_barrier(4, kLoadThreads);
+      stored.next(sched, n_all);
     };
     for (int c = 0; c < n_chunks; ++c) {
       const int ks = c % L::kKqStages;
-      const int left = (int)(g.T - (int64_t)c * kC < kC ? g.T - (int64_t)c * kC : kC);
+      const Item it = item_of(at_chunk);
+      const int left = tokens_of(at_chunk), t0 = at_chunk.c * kC;
+      const In* k_base = reinterpret_cast<const In*>(g.k) + (it.b * g.T + t0) * g.ld_k + (int64_t)it.hk * g.dk;
+      const In* q_base = reinterpret_cast<const In*>(g.q) + (it.b * g.T + t0) * g.ld_q + (int64_t)it.hk * g.dk;
+      const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
       const uint32_t kq = base + ks * L::kKq;
       if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
       if (vec_kq) {
@@ -1071,8 +1230,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           mbar_arrive_expect_tx(kq_full + 8 * ks, L::kKqTerm);
 #pragma unroll
           for (int kb = 0; kb < L::kBlocks; ++kb) {
-            tma_load_4d(kq + kb * 16384, &map_k, 64 * kb, hk, c * kC, (int)b, kq_full + 8 * ks);
-            tma_load_4d(kq + kb * 16384 + 8192, &map_q, 64 * kb, hk, c * kC, (int)b, kq_full + 8 * ks);
+            tma_load_4d(kq + kb * 16384, &map_k, 64 * kb, it.hk, t0, (int)it.b, kq_full + 8 * ks);
+            tma_load_4d(kq + kb * 16384 + 8192, &map_q, 64 * kb, it.hk, t0, (int)it.b, kq_full + 8 * ks);
           }
         }
       } else {
@@ -1082,8 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         for (int e = lt; e < 2 * kC * (DK / 8); e += kLoadThreads) {
           const int r = e / (DK / 8), col = e % (DK / 8) * 8, i = r & (kC - 1);
           const int valid = i < left ? g.dk - col : 0;
-          const int64_t t = (int64_t)c * kC + i;
-          const In* src = (r < kC ? k_base + t * g.ld_k : q_base + t * g.ld_q) + col;
+          const In* src = (r < kC ? k_base + (int64_t)i * g.ld_k : q_base + (int64_t)i * g.ld_q) + col;
           float f[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] = j < valid ? to_f32(src[j]) : 0.0f;
@@ -1103,30 +1261,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       // V (bf16); tokens past the sequence's end and components past dv are zero
       if (!F32) {
         if (c > 0) wait(v_empty, c - 1);
-        if (vec_y && c > 1) store_y(c - 2);
+        if (vec_y && c > 1) store_y();
         if (vec_v) {
           if (lt == 0) {
             mbar_arrive_expect_tx(v_full, kC * kM * 2);
-            tma_load_4d(base + L::kOffV, &map_v, tile * kM, h, c * kC, (int)b, v_full);
+            tma_load_4d(base + L::kOffV, &map_v, it.tile * kM, it.h, t0, (int)it.b, v_full);
           }
         } else {
-          const int cols = g.dv - tile * kM < kM ? g.dv - tile * kM : kM;
+          const int cols = g.dv - it.tile * kM < kM ? g.dv - it.tile * kM : kM;
           In* v_dst = reinterpret_cast<In*>(gbase + L::kOffV);
 #pragma unroll 4
           for (int e = lt; e < kC * kM; e += kLoadThreads) {
             const int r = e / kM, q = e % kM;
-            v_dst[e] = r < left && q < cols ? v_base[((int64_t)c * kC + r) * g.ld_v + q] : from_f32<In>(0.0f);
+            v_dst[e] = r < left && q < cols ? v_base[(int64_t)r * g.ld_v + q] : from_f32<In>(0.0f);
           }
           mbar_arrive(v_full);
         }
       }
+      at_chunk.next(sched, n_all);
     }
     if (!F32) {  // the last two chunks' outputs
       wait(v_empty, n_chunks - 1);
-      if (vec_y && n_chunks > 1) store_y(n_chunks - 2);
+      if (vec_y && n_chunks > 1) store_y();
       if (!vec_v || lt == 0) mbar_arrive(v_full);
       wait(v_empty, n_chunks);
-      if (vec_y) store_y(n_chunks - 1);
+      if (vec_y) store_y();
       if (lt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
@@ -1173,8 +1332,48 @@ bool make_map_heads(CUtensorMap* map, const void* p, int64_t B, int64_t T, int H
              CU_TENSOR_MAP_INTERLEAVE_NONE, box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// states [parts - 1][heads][dv][dk], phi [parts - 2][heads][dk][dk]: states[p] +=
+// states[p - 1] phi[p - 1] for p = 1 .. parts - 2, kJoinRows rows of a head per CTA
+constexpr int kJoinRows = 16, kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(float* states, const float* phi, int heads, int dv, int dk, int parts) {
+  __shared__ float x[kJoinRows][128 + 4];
+  const int row_tiles = (dv + kJoinRows - 1) / kJoinRows;
+  const int head = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kJoinRows;
+  const int64_t step = (int64_t)heads * dv * dk;
+  float* s = states + ((int64_t)head * dv + r0) * dk;
+  const int k = threadIdx.x % 128, rows = (threadIdx.x / 128) * (kJoinRows / 2);  // column, first of 8 rows
+  const bool in = k < dk;
+  for (int i = threadIdx.x; i < kJoinRows * dk; i += kJoinThreads)
+    x[i / dk][i % dk] = r0 + i / dk < dv ? s[(int64_t)(i / dk) * dk + i % dk] : 0.0f;
+  for (int p = 1; p <= parts - 2; ++p) {
+    const float* f = phi + ((int64_t)(p - 1) * heads + head) * dk * dk + k;
+    float* next = s + p * step;
+    float acc[kJoinRows / 2];
+#pragma unroll
+    for (int r = 0; r < kJoinRows / 2; ++r)
+      acc[r] = in && r0 + rows + r < dv ? next[(int64_t)(rows + r) * dk + k] : 0.0f;
+    __syncthreads();
+    if (in) {
+#pragma unroll 8
+      for (int j = 0; j < dk; ++j) {
+        const float v = f[(int64_t)j * dk];
+#pragma unroll
+        for (int r = 0; r < kJoinRows / 2; ++r) acc[r] = fmaf(x[rows + r][j], v, acc[r]);
+      }
+    }
+    __syncthreads();
+    if (in) {
+#pragma unroll
+      for (int r = 0; r < kJoinRows / 2; ++r) {
+        x[rows + r][k] = acc[r];
+        if (r0 + rows + r < dv) next[(int64_t)(rows + r) * dk + k] = acc[r];
+      }
+    }
+  }
+}
+
 template <int DK, bool F32>
-cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
+cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cudaStream_t stream) {
   auto kern = chunk_kernel<DK, F32>;
   constexpr int smem = Smem<DK, F32>::kAlloc;
   static int configured[64];
@@ -1193,24 +1392,92 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, cudaStream_t stream) {
     vec_v = make_map_heads(&mv, a.v, a.B, a.T, a.Hv, a.dv, a.ld_v, kM);
     vec_y = a.y_bf16 && make_map_heads(&my, a.y, a.B, a.T, a.Hv, a.dv, a.ld_y, kM);
   }
-  const int64_t ctas = a.B * a.Hv * ((a.dv + kM - 1) / kM);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, my, vec_kq, vec_v, vec_y);
-  return cudaGetLastError();
+  auto launch = [&](const Plan& plan, int ctas) {
+    kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, my, vec_kq, vec_v, vec_y, plan);
+    return cudaGetLastError();
+  };
+  if (plan.mode == kWide) {
+    if (plan.flags && (e = cudaMemsetAsync(plan.flags, 0, (size_t)ctas * sizeof(int), stream)) != cudaSuccess) return e;
+    return launch(plan, ctas);
+  }
+  const int heads = (int)(a.B * a.Hv);
+  if ((e = launch(plan, plan.items * (plan.parts - 1) + heads * (plan.parts - 2))) != cudaSuccess) return e;
+  const int row_tiles = (a.dv + kJoinRows - 1) / kJoinRows;
+  join_kernel<<<(unsigned)(heads * row_tiles), kJoinThreads, 0, stream>>>(plan.states, plan.phi, heads, a.dv, a.dk, plan.parts);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  Plan second = plan;
+  second.mode = kPartsPass;
+  return launch(second, plan.items * (plan.parts - 1));
+}
+
+// The layout of a call over `sms` SMs, and the scratch that it wants; with less
+// (ws_bytes) items are not cut.  Returns the CTAs of a kWide launch.
+//
+// An item's chunk takes ~5.4 us, a join's step ~3 us.  Cutting few items into P
+// parts makes n chunks in a row 2 n / P and P - 2 joins, if the parts' CTAs and the
+// maps' fit the SMs: 16 heads of 256 chunks 1380 us whole, 6 parts _LONG_ us.
+int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
+  *p = Plan{};
+  p->n_chunks = (int)((a.T + kC - 1) / kC);
+  p->tiles = (a.dv + kM - 1) / kM;
+  const int64_t heads = a.B * a.Hv, items = heads * p->tiles;
+  p->items = (int)items;
+  *want = 0;
+  auto round256 = [](int64_t b) { return (b + 255) / 256 * 256; };
+  if (items > sms && items % sms) {
+    const int64_t states = (int64_t)sms * kM * a.dk * 4;
+    *want = round256(states) + round256(sms * (int64_t)sizeof(int));
+    if (ws && ws_bytes >= *want) {
+      p->states = reinterpret_cast<float*>(ws);
+      p->flags = reinterpret_cast<int*>(ws + round256(states));
+      return sms;
+    }
+    return p->items;
+  }
+  int best = 1;
+  double best_us = 0.9 * 5.4 * p->n_chunks;  // worth three launches for a tenth
+  for (int parts = 3; parts <= p->n_chunks && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
+    const int len = (p->n_chunks + parts - 1) / parts;
+    if ((parts - 1) * len >= p->n_chunks) continue;  // the last part would be empty
+    const double us = 2 * 5.4 * len + 3.0 * (parts - 2) + 10;
+    if (us < best_us) best = parts, best_us = us;
+  }
+  if (best > 1) {
+    const int64_t states = heads * a.dv * a.dk * 4 * (best - 1), phi = heads * a.dk * a.dk * 4 * (int64_t)(best - 2);
+    *want = round256(states) + round256(phi);
+    if (ws && ws_bytes >= *want) {
+      p->mode = kAheadPass;
+      p->parts = best, p->part_len = (p->n_chunks + best - 1) / best;
+      p->states = reinterpret_cast<float*>(ws);
+      p->phi = reinterpret_cast<float*>(ws + round256(states));
+    }
+  }
+  return p->items;
 }
 
 }  // namespace
 
-// The chunks' output offsets inside a chunk are 32 bits.
+// Items and chunk numbers, and output offsets inside a chunk, are 32 bits.
 bool gated_delta_takes_chunks(const GatedDeltaArgs& a) {
-  return a.dk <= 128 && a.T > 16 && a.ld_y < (int64_t(1) << 23);
+  return a.dk <= 128 && a.T > 16 && a.ld_y < (int64_t(1) << 23) && a.T < (int64_t(1) << 30) &&
+         a.B * a.Hv * ((a.dv + kM - 1) / kM) < (int64_t(1) << 30);
 }
 
-cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  (void)dev;
+int64_t gated_delta_chunk_workspace(const GatedDeltaArgs& a, const DeviceInfo& dev) {
+  Plan plan;
+  int64_t want = 0;
+  make_plan(a, dev.sm_count, 0, nullptr, &plan, &want);
+  return want;
+}
+
+cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, void* ws, int64_t ws_bytes,
+                                     cudaStream_t stream) {
   if (a.B <= 0 || a.Hv <= 0 || a.dv <= 0) return cudaSuccess;
-  if (a.dk <= 64) return a.in_bf16 ? launch_chunk<64, false>(a, stream) : launch_chunk<64, true>(a, stream);
-  return a.in_bf16 ? launch_chunk<128, false>(a, stream) : launch_chunk<128, true>(a, stream);
+  Plan plan;
+  int64_t want = 0;
+  const int ctas = make_plan(a, dev.sm_count, ws_bytes, static_cast<char*>(ws), &plan, &want);
+  if (a.dk <= 64) return a.in_bf16 ? launch_chunk<64, false>(a, plan, ctas, stream) : launch_chunk<64, true>(a, plan, ctas, stream);
+  return a.in_bf16 ? launch_chunk<128, false>(a, plan, ctas, stream) : launch_chunk<128, true>(a, plan, ctas, stream);
 }
 
 int read_delta_faults(bool clear) {

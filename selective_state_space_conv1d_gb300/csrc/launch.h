@@ -299,7 +299,9 @@ struct GatedDeltaArgs {
 };
 // chunks of 64 tokens on the tensor cores (dk <= 128); the recurrent kernel takes any call
 bool gated_delta_takes_chunks(const GatedDeltaArgs& a);
-cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+int64_t gated_delta_chunk_workspace(const GatedDeltaArgs& a, const DeviceInfo& dev);
+cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& dev, void* ws, int64_t ws_bytes,
+                                     cudaStream_t stream);
 int read_delta_faults(bool clear);
 cudaError_t launch_gated_delta_recurrent(const GatedDeltaArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 

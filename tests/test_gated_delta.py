@@ -406,3 +406,42 @@ def test_long_prefills_of_few_heads(cuda_lib, B, Hk, Hv, T, dk, dv):
     x["dt_bias"] -= 4  # slow decays: the first tokens still count at the end
     y, s = run_prefill(x)
     check(x, y, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,Hv,T,dk,dv,dtype,y32", [
+    (2, 90, 90, 200, 64, 64, "bf16", False), (3, 26, 52, 330, 128, 136, "bf16", False), (1, 200, 200, 70, 128, 64, "bf16", True),
+    (2, 79, 79, 140, 64, 64, "f32", False), (4, 60, 60, 65, 40, 8, "bf16", False),
+])
+def test_more_items_than_sms(cuda_lib, B, Hk, Hv, T, dk, dv, dtype, y32):
+    """Items that begin on one SM and end on the next; and the same without scratch, one item a CTA."""
+    x = make(61, B, T, Hk, Hv, dk, dv, dtype, device="cuda")
+    x["dt_bias"] -= 3
+    y, s = run_prefill(x, y_dtype=torch.float32 if y32 else None)
+    check(x, y, s)
+    y2, s2 = torch.empty_like(y), torch.empty_like(s)
+    m.mamba_gated_delta_prefill(y2, x["q"], x["k"], x["v"], x["a"], x["b"], x["A_log"], x["dt_bias"], x["state_in"], s2,
+                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(s, s2)  # the state is handed over in full
+    assert m.mamba_device_faults() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,Hv,T,dk,dv,dtype,state", [
+    (1, 2, 2, 2048, 128, 128, "bf16", True), (1, 1, 3, 1990, 64, 128, "bf16", False), (1, 2, 4, 1200, 96, 200, "bf16", True),
+    (2, 3, 3, 1111, 64, 64, "f32", True), (1, 1, 1, 1025, 128, 40, "f32", False), (1, 8, 16, 3000, 128, 128, "bf16", True),
+])
+def test_sequences_cut_into_parts(cuda_lib, B, Hk, Hv, T, dk, dv, dtype, state):
+    x = make(71, B, T, Hk, Hv, dk, dv, dtype, state=state, device="cuda")
+    x["dt_bias"] -= 4
+    assert m.mamba_gated_delta_workspace_bytes(B, T, Hk, Hv, dk, dv, 1 if dtype == "bf16" else 0) > 0
+    y, s = run_prefill(x)
+    check(x, y, s)
+    y1, s1 = run_prefill(x)
+    assert torch.equal(y, y1) and torch.equal(s, s1)
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")  # too little: one pass over the sequence
+    m.mamba_gated_delta_prefill(y1, x["q"], x["k"], x["v"], x["a"], x["b"], x["A_log"], x["dt_bias"], x["state_in"], s1,
+                                workspace=ws)
+    torch.cuda.synchronize()
+    check(x, y1, s1)
