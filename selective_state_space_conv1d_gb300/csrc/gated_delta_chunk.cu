@@ -561,6 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     const uint32_t y_step = (uint32_t)g.ld_y * (g.y_bf16 ? 2 : 4);  // bytes; a chunk's rows fit 32 bits
     char* y_at = nullptr;  // of the chunk whose output is to come: this thread's first token
     int y_rows = 0;        // this thread's tokens inside the sequence
+    char* y_next = nullptr;       // the same of the current chunk
+    const In* v_global = nullptr; // and of its values
+    bool live = false;            // this lane is a value component
     auto arrive = [&](uint32_t bar) {
       tmem_wait_st();
       tcgen05_fence_before();
@@ -622,10 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     at_chunk.start(sched, n_all);
 #pragma unroll 1
     for (int c = 0; c <= n_chunks; ++c) {
-      const Item it = item_of(at_chunk);
       if (F32 && c > 0) wait(o_full, c - 1);  // U's third terms are read
       if (c < n_chunks) {
-        if (at_chunk.c == at_chunk.begin) enter(at_chunk, it);
+        if (at_chunk.c == at_chunk.begin) {
+          const Item it = item_of(at_chunk);
+          enter(at_chunk, it);
+          const int n = it.tile * kM + lane_n;
+          const int64_t row0 = it.b * g.T + (int64_t)at_chunk.c * kC + i0, col = (int64_t)it.h * g.dv + n;
+          live = n < g.dv;
+          y_next = reinterpret_cast<char*>(g.y) + (row0 * g.ld_y + col) * (g.y_bf16 ? 2 : 4);
+          v_global = reinterpret_cast<const In*>(g.v) + row0 * g.ld_v + col;
+        }
         // S to tensor memory: of this warp's HK columns of D3's place the first
         // half the first terms, the rest the second; the third terms beyond D3
         const uint32_t at = t_lane + kColS + (uint32_t)(part * HK), at2 = t_lane + kColS + (uint32_t)(DK + part * HK / 2);
@@ -644,12 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (c > 0 && (F32 || c == n_chunks)) output(c - 1);
       if (c == n_chunks) break;
       const Gates& gt = gates[c % kGateSlots];
-      const int n = it.tile * kM + lane_n;
-      const int rows = n < g.dv ? tokens_of(at_chunk) - i0 : 0;
-      const int64_t row0 = it.b * g.T + (int64_t)at_chunk.c * kC + i0;
+      const int rows = live ? tokens_of(at_chunk) - i0 : 0;
       // this lane's value of token i0 + i
       const In* v_tile = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
-      const In* v_global = reinterpret_cast<const In*>(g.v) + row0 * g.ld_v + (int64_t)it.h * g.dv + n;
       auto value = [&](int i) {
         if (sched.phi) return 0.0f;
         if (!F32) return to_f32(v_tile[i * kM]);
@@ -733,9 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]));
         }
       }
-      if (at_chunk.c + 1 == at_chunk.end) leave(at_chunk, it);
-      y_at = reinterpret_cast<char*>(g.y) + (row0 * g.ld_y + (int64_t)it.h * g.dv + n) * (g.y_bf16 ? 2 : 4);
-      y_rows = sched.quiet ? 0 : rows;
+      if (at_chunk.c + 1 == at_chunk.end) leave(at_chunk, item_of(at_chunk));
+      y_at = y_next, y_rows = sched.quiet ? 0 : rows;
+      y_next += (int64_t)kC * y_step;
+      if (F32) v_global += (int64_t)kC * g.ld_v;
       at_chunk.next(sched, n_all);
     }
   } else if (warp < kGateWarp) {
@@ -1026,18 +1034,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     float a_next[2], b_next[2], A_next, bias_next;
     Cursor at_chunk;
     at_chunk.start(sched, n_all);
+    const In* a_base = nullptr;
+    const In* b_base = nullptr;
     auto fetch = [&]() {
-      const Item it = item_of(at_chunk);
-      const In* a_base = reinterpret_cast<const In*>(g.a) + it.b * g.T * g.ld_a + it.h;
-      const In* b_base = reinterpret_cast<const In*>(g.b) + it.b * g.T * g.ld_b + it.h;
+      if (at_chunk.c == at_chunk.begin) {
+        const Item it = item_of(at_chunk);
+        a_base = reinterpret_cast<const In*>(g.a) + it.b * g.T * g.ld_a + it.h;
+        b_base = reinterpret_cast<const In*>(g.b) + it.b * g.T * g.ld_b + it.h;
+        A_next = g.A_log[it.h];
+        bias_next = g.dt_bias ? g.dt_bias[it.h] : 0.0f;
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t t = (int64_t)at_chunk.c * kC + lane + 32 * u;
         a_next[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
         b_next[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
       }
-      A_next = g.A_log[it.h];
-      bias_next = g.dt_bias ? g.dt_bias[it.h] : 0.0f;
       at_chunk.next(sched, n_all);
     };
     fetch();
@@ -1333,42 +1345,85 @@ bool make_map_heads(CUtensorMap* map, const void* p, int64_t B, int64_t T, int H
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // states [parts - 1][heads][dv][dk], phi [parts - 2][heads][dk][dk]: states[p] +=
-// states[p - 1] phi[p - 1] for p = 1 .. parts - 2, kJoinRows rows of a head per CTA
-constexpr int kJoinRows = 16, kJoinThreads = 256;
+// states[p - 1] phi[p - 1] for p = 1 .. parts - 2, kJoinRows rows of a head per CTA.
+// The rows stay in shared memory and the next map is on its way while this one is
+// multiplied: a thread sums 8 rows x 4 columns over an eighth of the map's rows (two
+// wide loads for 32 multiplies), and the eighths are added up over the used map.
+constexpr int kJoinRows = 16, kJoinThreads = 512, kJoinSplit = 8, kJoinLd = 128;
+constexpr int kJoinSmem = (2 * 128 * kJoinLd + 128 * kJoinRows) * 4;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(float* states, const float* phi, int heads, int dv, int dk, int parts) {
-  __shared__ float x[kJoinRows][128 + 4];
+  extern __shared__ float join_smem[];
+  float* maps = join_smem;                   // [2][dk][kJoinLd]
+  float* x = join_smem + 2 * 128 * kJoinLd;  // [128][kJoinRows]: column j of the rows
   const int row_tiles = (dv + kJoinRows - 1) / kJoinRows;
   const int head = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kJoinRows;
   const int64_t step = (int64_t)heads * dv * dk;
   float* s = states + ((int64_t)head * dv + r0) * dk;
-  const int k = threadIdx.x % 128, rows = (threadIdx.x / 128) * (kJoinRows / 2);  // column, first of 8 rows
-  const bool in = k < dk;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int c0 = lane * 4, q0 = warp % 2 * 8, split = warp / 2;  // columns, rows, eighth
+  const int j0 = split * dk / kJoinSplit, j1 = (split + 1) * dk / kJoinSplit;
+  auto fetch = [&](int p) {  // phi[p - 1], 16 bytes at a time where its rows allow
+    const float* f = phi + ((int64_t)(p - 1) * heads + head) * dk * dk;
+    float* to = maps + (p & 1) * 128 * kJoinLd;
+    if (dk % 4 == 0) {
+      if (c0 < dk)
+        for (int j = warp; j < dk; j += kJoinThreads / 32) cp_async16(smem_u32(to + j * kJoinLd + c0), f + j * dk + c0);
+    } else {
+      for (int j = warp; j < dk; j += kJoinThreads / 32)
+        for (int c = lane; c < dk; c += 32) to[j * kJoinLd + c] = f[j * dk + c];
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (parts > 2) fetch(1);
   for (int i = threadIdx.x; i < kJoinRows * dk; i += kJoinThreads)
-    x[i / dk][i % dk] = r0 + i / dk < dv ? s[(int64_t)(i / dk) * dk + i % dk] : 0.0f;
+    x[i % dk * kJoinRows + i / dk] = r0 + i / dk < dv ? s[(int64_t)(i / dk) * dk + i % dk] : 0.0f;
+  // The sums that this thread joins and keeps: row `warp`, columns c0 .. c0 + 3.
+  const bool mine = r0 + warp < dv;
   for (int p = 1; p <= parts - 2; ++p) {
-    const float* f = phi + ((int64_t)(p - 1) * heads + head) * dk * dk + k;
-    float* next = s + p * step;
-    float acc[kJoinRows / 2];
+    if (p + 1 <= parts - 2) fetch(p + 1);
+    float* next = s + p * step + (int64_t)warp * dk + c0;
+    float sum[4];
 #pragma unroll
-    for (int r = 0; r < kJoinRows / 2; ++r)
-      acc[r] = in && r0 + rows + r < dv ? next[(int64_t)(rows + r) * dk + k] : 0.0f;
+    for (int c = 0; c < 4; ++c) sum[c] = mine && c0 + c < dk ? next[c] : 0.0f;
+    if (p + 1 <= parts - 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    if (in) {
-#pragma unroll 8
-      for (int j = 0; j < dk; ++j) {
-        const float v = f[(int64_t)j * dk];
+    float* m = maps + (p & 1) * 128 * kJoinLd;
+    float acc[8][4] = {};
+#pragma unroll 4
+    for (int j = j0; j < j1; ++j) {
+      const float4 f = *reinterpret_cast<const float4*>(m + j * kJoinLd + c0);
+      const float4 u = *reinterpret_cast<const float4*>(x + j * kJoinRows + q0);
+      const float4 v = *reinterpret_cast<const float4*>(x + j * kJoinRows + q0 + 4);
+      const float fs[4] = {f.x, f.y, f.z, f.w}, xs[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int r = 0; r < kJoinRows / 2; ++r) acc[r] = fmaf(x[rows + r][j], v, acc[r]);
-      }
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(xs[r], fs[c], acc[r][c]);
     }
+    __syncthreads();  // the map and the rows are read
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      *reinterpret_cast<float4*>(m + (split * kJoinRows + q0 + r) * kJoinLd + c0) =
+          make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     __syncthreads();
-    if (in) {
 #pragma unroll
-      for (int r = 0; r < kJoinRows / 2; ++r) {
-        x[rows + r][k] = acc[r];
-        if (r0 + rows + r < dv) next[(int64_t)(rows + r) * dk + k] = acc[r];
-      }
+    for (int e = 0; e < kJoinSplit; ++e) {
+      const float4 f = *reinterpret_cast<const float4*>(m + (e * kJoinRows + warp) * kJoinLd + c0);
+      sum[0] += f.x, sum[1] += f.y, sum[2] += f.z, sum[3] += f.w;
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c0 + c < dk) {
+        x[(c0 + c) * kJoinRows + warp] = sum[c];
+        if (mine) next[c] = sum[c];
+      }
+    __syncthreads();
   }
 }
 
@@ -1382,7 +1437,9 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!__atomic_load_n(&configured[dev], __ATOMIC_RELAXED)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem)) != cudaSuccess)
+      return e;
     __atomic_store_n(&configured[dev], 1, __ATOMIC_RELAXED);
   }
   CUtensorMap mk = {}, mq = {}, mv = {}, my = {};
@@ -1403,7 +1460,7 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
   const int heads = (int)(a.B * a.Hv);
   if ((e = launch(plan, plan.items * (plan.parts - 1) + heads * (plan.parts - 2))) != cudaSuccess) return e;
   const int row_tiles = (a.dv + kJoinRows - 1) / kJoinRows;
-  join_kernel<<<(unsigned)(heads * row_tiles), kJoinThreads, 0, stream>>>(plan.states, plan.phi, heads, a.dv, a.dk, plan.parts);
+  join_kernel<<<(unsigned)(heads * row_tiles), kJoinThreads, kJoinSmem, stream>>>(plan.states, plan.phi, heads, a.dv, a.dk, plan.parts);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   Plan second = plan;
   second.mode = kPartsPass;
