@@ -6,10 +6,12 @@
 //   head_norm_gated  y / sqrt(mean y^2 + eps) w SiLU(z) for every head of y
 //
 // Bound: HBM (each value read once and written once).  A group of G = d / 8
-// lanes (8, 16 or 32) holds a head, 8 values per lane (16-byte accesses), so
-// the sum is a butterfly and the rotation's partner sits in the same lane
-// (interleaved pairs) or in one other lane (halves).  A group keeps its
-// token's cosines and sines in registers and goes over heads with them.
+// lanes (8, 16 or 32) holds a head, 8 values per lane, so the sum is a butterfly.
+// A lane's values are two runs of four, for pairs in halves the four of the low
+// half and their partners in the high half: a turn stays inside the lane, and the
+// lane needs the cosines and sines of four pairs (a lane of eight neighbours would
+// need eight, and its partners through shuffles).  A group keeps its token's
+// cosines and sines in registers and goes over the heads with them.
 //
 // Angles: position inv_freq loses its low bits in f32 (at position 10^6 the
 // product's rounding is 0.03 rad), so the lane holds inv_freq as a 64-bit
@@ -25,7 +27,12 @@
 namespace mamba {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads and resident CTAs per SM of the two vector kernels: small CTAs, several
+// heads' loads each, and as many CTAs as the registers allow.  32768 tokens, d = 128:
+// 24 heads of q and k 70.9 us (256 threads, 4 heads, 3 CTAs: 78.6), a norm of 40
+// heads 160 us (256 threads, 4 heads, 3 CTAs: 215).
+constexpr int kQkThreads = 128, kQkCtas = 7;
+constexpr int kHnThreads = 64, kHnCtas = 16;
 
 // inv_freq (radians per position) as a 2^-64 fraction of a turn: its 24-bit
 // significand times 2^64 / (2 pi), shifted by its exponent.  Whole turns per
@@ -76,6 +83,10 @@ template <>
 struct Vec8<__nv_bfloat16> {
   uint4 raw;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* p2) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p2);
+    raw = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -88,9 +99,10 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p) { load(p, p + 4); }
+  __device__ __forceinline__ void load(const float* p, const float* p2) {
     a = *reinterpret_cast<const float4*>(p);
-    b = *(reinterpret_cast<const float4*>(p) + 1);
+    b = *reinterpret_cast<const float4*>(p2);
   }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
@@ -98,75 +110,77 @@ struct Vec8<float> {
   }
 };
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) { *reinterpret_cast<uint4*>(p) = pack8(f); }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, __nv_bfloat16* p2, const float (&f)[8]) {
+  const uint4 w = pack8(f);
+  *reinterpret_cast<uint2*>(p) = make_uint2(w.x, w.y);
+  *reinterpret_cast<uint2*>(p2) = make_uint2(w.z, w.w);
+}
+__device__ __forceinline__ void store8(float* p, float* p2, const float (&f)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+  *reinterpret_cast<float4*>(p2) = make_float4(f[4], f[5], f[6], f[7]);
 }
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) { store8(p, p + 4, f); }
 
 // One group of G lanes: one token, heads [h0, h0 + per_group) of the Hq + Hk.
 // kHeads heads' loads are in flight together.  The weights of the lane's 8
 // components are re-read per head (L1) rather than held for both q and k.
-template <typename IN, typename OUT, int G, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs g, int per_group, int slices) {
+// HALVES: pairs (i, rot / 2 + i); else neighbours, or no turns.
+template <typename IN, typename OUT, int G, bool HALVES>
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_norm_kernel(const QkNormArgs g, int per_group, int slices, float inv_n) {
   grid_dependency_begin();
-  constexpr int kHeads = 4;
-  constexpr int kGroups = kThreads / G;
+  constexpr int kHeads = sizeof(IN) == 2 ? 6 : 3;
+  constexpr int kGroups = kQkThreads / G;
   const int lane = threadIdx.x % G;
   const int64_t unit = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
   const int64_t rows = g.B * g.T;
-  const int64_t row_raw = unit / slices;
+  const int64_t row_raw = slices == 1 ? unit : unit / slices;
   const bool live = row_raw < rows;
   const int64_t row = live ? row_raw : rows - 1;  // idle groups stay for the shuffles
   const int heads = g.Hq + g.Hk;
-  const int h0 = (int)(unit % slices) * per_group;
+  const int h0 = slices == 1 ? 0 : (int)(unit % slices) * per_group;
   const int h1 = h0 + per_group < heads ? h0 + per_group : heads;
-  const int c = 8 * lane;
-  const bool in = c < g.d;  // d % 8 == 0
+  const bool in = 8 * lane < g.d;          // d % 8 == 0
+  const bool turned = 8 * lane < g.rot;    // rot % 8 == 0
+  const int c = HALVES && turned ? 4 * lane : 8 * lane;
+  const int c2 = HALVES && turned ? g.rot / 2 + c : c + 4;
 
-  // this token's turns for the lane's components
-  const bool turned = c < g.rot;
-  const int half = g.rot / 2;
-  float cs[8], sn[8];
-  int partner = threadIdx.x % 32;
+  // this token's turns for the lane's four pairs
+  float cs[4], sn[4];
   if (g.rot > 0) {
-    if (INTERLEAVED) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 a = make_float2(1.0f, 0.0f);
-        if (turned) a = cos_sin(g.positions ? g.positions[row] : row % g.T, turns_per_position(g.inv_freq[c / 2 + i]));
-        cs[i] = a.x, sn[i] = a.y;
-      }
-    } else {
-      const bool low = c < half;
-      if (turned) partner += low ? half / 8 : -(half / 8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float2 a = make_float2(1.0f, 0.0f);
-        if (turned)
-          a = cos_sin(g.positions ? g.positions[row] : row % g.T,
-                      turns_per_position(g.inv_freq[(low ? c : c - half) + i]));
-        cs[i] = a.x, sn[i] = low ? -a.y : a.y;  // x cos - y sin below, y cos + x sin above
-      }
+    for (int i = 0; i < 4; ++i) {
+      float2 a = make_float2(1.0f, 0.0f);
+      if (turned) a = cos_sin(g.positions ? g.positions[row] : row % g.T, turns_per_position(g.inv_freq[4 * lane + i]));
+      cs[i] = a.x, sn[i] = a.y;
     }
   }
+  const IN* q = reinterpret_cast<const IN*>(g.q) + row * g.ld_q;
+  const IN* k = reinterpret_cast<const IN*>(g.k) + row * g.ld_k - (int64_t)g.Hq * g.d;
+  OUT* q_out = reinterpret_cast<OUT*>(g.q_out) + row * g.ld_qo;
+  OUT* k_out = reinterpret_cast<OUT*>(g.k_out) + row * g.ld_ko - (int64_t)g.Hq * g.d;
 
   for (int h = h0; h < h1; h += kHeads) {
     Vec8<IN> raw[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int hh = h + j < h1 ? h + j : h1 - 1;
-      const IN* p = hh < g.Hq ? reinterpret_cast<const IN*>(g.q) + row * g.ld_q + (int64_t)hh * g.d
-                              : reinterpret_cast<const IN*>(g.k) + row * g.ld_k + (int64_t)(hh - g.Hq) * g.d;
-      if (in) raw[j].load(p + c);
+      const IN* p = (hh < g.Hq ? q : k) + hh * g.d;
+      if (in) {
+        if constexpr (HALVES)
+          raw[j].load(p + c, p + c2);
+        else
+          raw[j].load(p + c);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
@@ -184,35 +198,32 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs g, i
       const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << ((threadIdx.x % 32) / G * G);
 #pragma unroll
       for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      const float inv = rsqrtf((g.l2 ? ss : ss / (float)g.d) + g.eps);
+      const float inv = rsqrtf(fmaf(ss, inv_n, g.eps));
       const bool is_q = h + j < g.Hq;
       const float* w = is_q ? g.q_weight : g.k_weight;
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= inv;
       if (w && in) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= __ldg(w + c + i);
+        const float4 lo = __ldg(reinterpret_cast<const float4*>(w + c)), hi = __ldg(reinterpret_cast<const float4*>(w + c2));
+        f[0] *= lo.x, f[1] *= lo.y, f[2] *= lo.z, f[3] *= lo.w;
+        f[4] *= hi.x, f[5] *= hi.y, f[6] *= hi.z, f[7] *= hi.w;
       }
       if (g.rot > 0) {
-        if (INTERLEAVED) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = f[2 * i], y = f[2 * i + 1];
-            f[2 * i] = fmaf(-y, sn[i], x * cs[i]);
-            f[2 * i + 1] = fmaf(x, sn[i], y * cs[i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(mask, f[i], partner);
-            f[i] = turned ? fmaf(o, sn[i], f[i] * cs[i]) : f[i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          float& a = f[HALVES ? i : 2 * i];
+          float& b = f[HALVES ? 4 + i : 2 * i + 1];
+          const float x = a, y = b;
+          a = fmaf(-y, sn[i], x * cs[i]);
+          b = fmaf(x, sn[i], y * cs[i]);
         }
       }
       if (in && live) {
-        OUT* p = is_q ? reinterpret_cast<OUT*>(g.q_out) + row * g.ld_qo + (int64_t)(h + j) * g.d
-                      : reinterpret_cast<OUT*>(g.k_out) + row * g.ld_ko + (int64_t)(h + j - g.Hq) * g.d;
-        store8(p + c, f);
+        OUT* p = (is_q ? q_out : k_out) + (h + j) * g.d;
+        if constexpr (HALVES)
+          store8(p + c, p + c2, f);
+        else
+          store8(p + c, f);
       }
     }
   }
@@ -266,10 +277,10 @@ __global__ void __launch_bounds__(32 * kAnyWarps) qk_norm_any_kernel(const QkNor
 }
 
 template <typename IN, typename OUT, int G>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadNormArgs g, int64_t units, int per_group) {
+__global__ void __launch_bounds__(kHnThreads, kHnCtas) head_norm_kernel(const HeadNormArgs g, int64_t units, int per_group) {
   grid_dependency_begin();
-  constexpr int kHeads = 4;
-  constexpr int kGroups = kThreads / G;
+  constexpr int kHeads = sizeof(IN) == 2 ? 2 : 1;
+  constexpr int kGroups = kHnThreads / G;
   const int lane = threadIdx.x % G;
   const int c = 8 * lane;
   const bool in = c < g.d;
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const Hea
 
 // 8-value accesses: base, row stride and head size keep every head's groups aligned
 bool vec8(const void* p, int64_t ld, int d, int es) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (es == 2 ? 16 : 16) == 0 && (ld * es) % 16 == 0 && d % 8 == 0);
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0 && d % 8 == 0);
 }
 
 template <typename IN, typename OUT, int G>
@@ -371,12 +382,13 @@ cudaError_t launch_qk_g(const QkNormArgs& a, int sms, cudaStream_t stream) {
   if (slices < 1) slices = 1;
   const int per_group = (int)((heads + slices - 1) / slices);
   slices = (heads + per_group - 1) / per_group;
-  const int64_t ctas = (rows * slices + kThreads / G - 1) / (kThreads / G);
+  const int64_t ctas = (rows * slices + kQkThreads / G - 1) / (kQkThreads / G);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)ctas), block(kThreads);
-  if (a.interleaved)
-    return launch_pdl(true, qk_norm_kernel<IN, OUT, G, true>, grid, block, 0, stream, a, per_group, (int)slices);
-  return launch_pdl(true, qk_norm_kernel<IN, OUT, G, false>, grid, block, 0, stream, a, per_group, (int)slices);
+  const dim3 grid((unsigned)ctas), block(kQkThreads);
+  const float inv_n = a.l2 ? 1.0f : 1.0f / (float)a.d;
+  if (a.interleaved || a.rot == 0)
+    return launch_pdl(true, qk_norm_kernel<IN, OUT, G, false>, grid, block, 0, stream, a, per_group, (int)slices, inv_n);
+  return launch_pdl(true, qk_norm_kernel<IN, OUT, G, true>, grid, block, 0, stream, a, per_group, (int)slices, inv_n);
 }
 
 template <typename IN, typename OUT>
@@ -384,8 +396,8 @@ cudaError_t launch_qk_t(const QkNormArgs& a, int sms, cudaStream_t stream) {
   const int ei = sizeof(IN), eo = sizeof(OUT);
   const bool vec = vec8(a.Hq ? a.q : nullptr, a.ld_q, a.d, ei) && vec8(a.Hk ? a.k : nullptr, a.ld_k, a.d, ei) &&
                    vec8(a.Hq ? a.q_out : nullptr, a.ld_qo, a.d, eo) &&
-                   vec8(a.Hk ? a.k_out : nullptr, a.ld_ko, a.d, eo) && a.d % 8 == 0 &&
-                   (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0);
+                   vec8(a.Hk ? a.k_out : nullptr, a.ld_ko, a.d, eo) && vec8(a.q_weight, 0, a.d, 4) &&
+                   vec8(a.k_weight, 0, a.d, 4) && a.d % 8 == 0 && a.rot % 8 == 0;
   if (!vec) {
     const int64_t ctas = (a.B * a.T * (a.Hq + a.Hk) + kAnyWarps - 1) / kAnyWarps;
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -399,12 +411,12 @@ cudaError_t launch_qk_t(const QkNormArgs& a, int sms, cudaStream_t stream) {
 template <typename IN, typename OUT, int G>
 cudaError_t launch_hn_g(const HeadNormArgs& a, int sms, cudaStream_t stream) {
   const int64_t units = a.rows * a.H;
-  constexpr int kGroups = kThreads / G;
-  // four heads per group once that still fills every SM
-  const int per_group = units >= (int64_t)sms * 4 * kGroups * 4 ? 4 : 1;
+  constexpr int kGroups = kHnThreads / G;
+  // eight heads per group once that still fills every SM
+  const int per_group = units >= (int64_t)sms * kHnCtas * kGroups * 8 ? 8 : 1;
   const int64_t ctas = (units + kGroups * per_group - 1) / (kGroups * per_group);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_pdl(true, head_norm_kernel<IN, OUT, G>, dim3((unsigned)ctas), dim3(kThreads), 0, stream, a, units,
+  return launch_pdl(true, head_norm_kernel<IN, OUT, G>, dim3((unsigned)ctas), dim3(kHnThreads), 0, stream, a, units,
                     per_group);
 }
 
