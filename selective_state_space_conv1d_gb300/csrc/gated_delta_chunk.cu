@@ -1227,6 +1227,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (!vec_v) named_barrier(4, kLoadThreads);
       stored.next(sched, n_all);
     };
+    // a row of four values that 16-byte accesses reach
+    const bool wide_kq = g.dk % 4 == 0 && g.ld_k % 4 == 0 && g.ld_q % 4 == 0 &&
+                         ((reinterpret_cast<uintptr_t>(g.k) | reinterpret_cast<uintptr_t>(g.q)) & 15) == 0;
+    // a chunk's f32 rows, which are read element-wise, to the second-level cache: the
+    // reads then take a third of the time, and the chunk before hides the rest
+    auto prefetch = [&](const Cursor& k) {
+      const Item it = item_of(k);
+      const int rows = tokens_of(k), cols = g.dv - it.tile * kM < kM ? g.dv - it.tile * kM : kM;
+      const int64_t row = it.b * g.T + (int64_t)k.c * kC;
+      auto lines = [&](const void* p, int64_t ld, int n) {
+        const float* first = reinterpret_cast<const float*>(p) + row * ld;
+        for (int e = lt; e < 4 * rows; e += kLoadThreads)
+          if (32 * (e & 3) < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(first + (e / 4) * ld + 32 * (e & 3)));
+      };
+      lines(reinterpret_cast<const float*>(g.k) + (int64_t)it.hk * g.dk, g.ld_k, g.dk);
+      lines(reinterpret_cast<const float*>(g.q) + (int64_t)it.hk * g.dk, g.ld_q, g.dk);
+      lines(reinterpret_cast<const float*>(g.v) + (int64_t)it.h * g.dv + it.tile * kM, g.ld_v, cols);
+    };
     for (int c = 0; c < n_chunks; ++c) {
       const int ks = c % L::kKqStages;
       const Item it = item_of(at_chunk);
@@ -1235,7 +1253,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       const In* q_base = reinterpret_cast<const In*>(g.q) + (it.b * g.T + t0) * g.ld_q + (int64_t)it.hk * g.dk;
       const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
       const uint32_t kq = base + ks * L::kKq;
+      if (F32 && c == 0) prefetch(at_chunk);
       if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
+      at_chunk.next(sched, n_all);
+      if (F32 && c + 1 < n_chunks) prefetch(at_chunk);
       if (vec_kq) {
         // tokens past the end and components past dk read as zero
         if (lt == 0) {
@@ -1247,25 +1268,41 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           }
         }
       } else {
-        // by hand, eight components of a row at a time: K rows 0-63, Q 64-127;
-        // granule q of row r at q ^ (r % 8)
+        // by hand, eight components of a row at a time, kBatch of these in flight per
+        // thread: K rows 0-63, Q 64-127; granule q of row r at q ^ (r % 8)
+        constexpr int kBatch = 4;
 #pragma unroll 1
-        for (int e = lt; e < 2 * kC * (DK / 8); e += kLoadThreads) {
-          const int r = e / (DK / 8), col = e % (DK / 8) * 8, i = r & (kC - 1);
-          const int valid = i < left ? g.dk - col : 0;
-          const In* src = (r < kC ? k_base + (int64_t)i * g.ld_k : q_base + (int64_t)i * g.ld_q) + col;
-          float f[8];
+        for (int e0 = lt; e0 < 2 * kC * (DK / 8); e0 += kBatch * kLoadThreads) {
+          float f[kBatch][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = j < valid ? to_f32(src[j]) : 0.0f;
-          const uint32_t at = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
-          uint32_t x[3][4];
+          for (int u = 0; u < kBatch; ++u) {
+            const int e = e0 + u * kLoadThreads, r = e / (DK / 8), col = e % (DK / 8) * 8, i = r & (kC - 1);
+            const int valid = i < left ? g.dk - col : 0;
+            const In* src = (r < kC ? k_base + (int64_t)i * g.ld_k : q_base + (int64_t)i * g.ld_q) + col;
+            if (F32 && wide_kq) {
+              float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+              if (valid > 0) a = *reinterpret_cast<const float4*>(src);
+              if (valid > 4) b = *reinterpret_cast<const float4*>(src + 4);
+              f[u][0] = a.x, f[u][1] = a.y, f[u][2] = a.z, f[u][3] = a.w;
+              f[u][4] = b.x, f[u][5] = b.y, f[u][6] = b.z, f[u][7] = b.w;
+            } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) split3(f[2 * j], f[2 * j + 1], x[0][j], x[1][j], x[2][j]);
+              for (int j = 0; j < 8; ++j) f[u][j] = j < valid ? to_f32(src[j]) : 0.0f;
+            }
+          }
 #pragma unroll
-          for (int p = 0; p < L::kTerms; ++p)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
-                         "r"(x[p][2]), "r"(x[p][3])
-                         : "memory");
+          for (int u = 0; u < kBatch; ++u) {
+            const int e = e0 + u * kLoadThreads, r = e / (DK / 8), col = e % (DK / 8) * 8;
+            const uint32_t at = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
+            uint32_t x[3][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split3(f[u][2 * j], f[u][2 * j + 1], x[0][j], x[1][j], x[2][j]);
+#pragma unroll
+            for (int p = 0; p < L::kTerms; ++p)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
+                           "r"(x[p][2]), "r"(x[p][3])
+                           : "memory");
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(kq_full + 8 * ks);
@@ -1290,7 +1327,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           mbar_arrive(v_full);
         }
       }
-      at_chunk.next(sched, n_all);
     }
     if (!F32) {  // the last two chunks' outputs
       wait(v_empty, n_chunks - 1);
@@ -1473,6 +1509,7 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
 // An item's chunk takes ~5.4 us, a join's step ~3 us.  Cutting few items into P
 // parts makes n chunks in a row 2 n / P and P - 2 joins, if the parts' CTAs and the
 // maps' fit the SMs: 16 heads of 256 chunks 1380 us whole, 6 parts _LONG_ us.
+constexpr double kChunkUs = 5.8, kJoinUs = 4.0, kPartsUs = 30.0;
 int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
   *p = Plan{};
   p->n_chunks = (int)((a.T + kC - 1) / kC);
@@ -1492,11 +1529,11 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
     return p->items;
   }
   int best = 1;
-  double best_us = 0.9 * 5.4 * p->n_chunks;  // worth three launches for a tenth
+  double best_us = 0.9 * kChunkUs * p->n_chunks;  // worth three launches for a tenth
   for (int parts = 3; parts <= p->n_chunks && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
     const int len = (p->n_chunks + parts - 1) / parts;
     if ((parts - 1) * len >= p->n_chunks) continue;  // the last part would be empty
-    const double us = 2 * 5.4 * len + 3.0 * (parts - 2) + 10;
+    const double us = 2 * kChunkUs * len + kJoinUs * (parts - 2) + kPartsUs;
     if (us < best_us) best = parts, best_us = us;
   }
   if (best > 1) {
