@@ -87,7 +87,11 @@ struct Gates {
   float past[32];   // e^{G_31 - G_j}, j < 32
   float since[32];  // e^{G_i - G_31}, i = 32 ..
   float total;      // e^{G_63}
-  float pad[3];
+  // which chunk it is, for the warps that have no registers to keep track
+  int at, begin, end;       // its number in the sequence, and those of the piece run here
+  int tile, h, b, bh;       // the item
+  int tokens;               // of the chunk inside the sequence
+  int phi, quiet, pad;      // the schedule's
 };
 
 template <int DK, bool F32>
@@ -109,7 +113,7 @@ struct Smem {
   static constexpr int kOffA = kOffV + kV;            // A, f32 [64][kLdA], of each group
   static constexpr int kOffGates = kOffA + 2 * kC * kLdA * 4;
   static constexpr int kOffBar = kOffGates + kGateSlots * (int)sizeof(Gates);
-  static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 7;
+  static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 12;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
@@ -207,7 +211,10 @@ struct Cursor {
 constexpr uint32_t kColX = 0, kColQ = 64, kColU = 128, kColO = 192, kColS = 256, kColThird = 384, kColU3 = 416,
                    kColD0 = 448, kTmemCols = 512;
 
-// kind::f16, bf16 A and B, f32 accumulator, M = 128; b_mn: B is MN-major
+// kind::f16, bf16 A and B, f32 accumulator, M = 128; b_mn: B is MN-major; A's
+// second terms, and B's where B is a sum too, are stored negated
+constexpr uint32_t kNegA = 1u << 13, kNegB = 1u << 14;
+__host__ __device__ constexpr uint32_t neg_bits(int ta, int tb) { return (ta == 1 ? kNegA : 0u) | (tb == 1 ? kNegB : 0u); }
 __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kM >> 4) << 24);
@@ -235,8 +242,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// (a, b) as three bf16 pairs, each the rounding of what the ones before leave
-__device__ __forceinline__ void split3(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+// (a, b) as three bf16 pairs, each the rounding of what the ones before leave.  The
+// remainder's instruction gives it negated, so the second pair comes out negated
+// and the third not: the tensor products take the sign back (kNegA, kNegB).
+__device__ __forceinline__ void split3n(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
   float ra, rb;
   asm("{\n"
       "  .reg .b16 l, h;\n"
@@ -247,7 +256,6 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& t0, uint32_t&
       "}\n"
       : "=&r"(t0), "=&f"(ra), "=&f"(rb)
       : "f"(a), "f"(b));
-  ra = -ra, rb = -rb;
   asm("{\n"
       "  .reg .b16 l, h;\n"
       "  cvt.rn.bf16x2.f32 %0, %4, %3;\n"
@@ -257,11 +265,16 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& t0, uint32_t&
       "}\n"
       : "=&r"(t1), "=&f"(a), "=&f"(b)
       : "f"(ra), "f"(rb));
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t2) : "f"(-a), "f"(-b));
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t2) : "f"(a), "f"(b));
+}
+// with its sign, for the warp-level products
+__device__ __forceinline__ void split3(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  split3n(a, b, t0, t1, t2);
+  t1 ^= 0x80008000u;
 }
 
 // and as two
-__device__ __forceinline__ void split2(float a, float b, uint32_t& t0, uint32_t& t1) {
+__device__ __forceinline__ void split2n(float a, float b, uint32_t& t0, uint32_t& t1) {
   float ra, rb;
   asm("{\n"
       "  .reg .b16 l, h;\n"
@@ -272,7 +285,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& t0, uint32_t&
       "}\n"
       : "=&r"(t0), "=&f"(ra), "=&f"(rb)
       : "f"(a), "f"(b));
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t1) : "f"(-ra), "f"(-rb));
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t1) : "f"(ra), "f"(rb));
 }
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
@@ -417,22 +430,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   // of the chunk's parity: a group of prepare warps sees every other chunk
   const uint32_t t_empty = next_bars(2), d0_full = next_bars(2), d0_empty = next_bars(2);
   const uint32_t p_full = next_bars(L::kPBuffers), p_empty = next_bars(L::kPBuffers), o_empty = next_bars(1);
-  const uint32_t s_ready = next_bars(1), x_full = next_bars(1), r_ready = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1), s_full = next_bars(1);
+  // in halves (the warps of parts 0, 1 and of 2, 3): the products start on the first
+  const uint32_t s_ready = next_bars(2), r_ready = next_bars(2), w_ready = next_bars(2), s_full = next_bars(2);
+  const uint32_t x_full = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
   Gates* gates = reinterpret_cast<Gates*>(gbase + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n_all = plan.n_chunks;
-  const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
-  const int n_chunks = sched.total;  // that this CTA runs
+  const int n_chunks = make_schedule(plan, (int)(g.B * g.Hv)).total;  // that this CTA runs
   struct Item {
     int tile, h, hk;
-    int64_t b, bh;
+    int64_t b;
   };
   auto item_of = [&](const Cursor& k) {
     const int bh = k.item / plan.tiles, h = bh % g.Hv;
-    return Item{k.item % plan.tiles, h, h / (g.Hv / g.Hk), bh / g.Hv, bh};
+    return Item{k.item % plan.tiles, h, h / (g.Hv / g.Hk), bh / g.Hv};
   };
   auto tokens_of = [&](const Cursor& k) { return (int)(g.T - (int64_t)k.c * kC < kC ? g.T - (int64_t)k.c * kC : kC); };
 
@@ -443,8 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     mbar_init(t_full, kGroupWarps), mbar_init(o_empty, kMainWarps);
     for (int s = 0; s < 2; ++s) mbar_init(t_empty + 8 * s, 1), mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, kGroupWarps);
     for (int s = 0; s < L::kPBuffers; ++s) mbar_init(p_full + 8 * s, kGroupWarps / 2), mbar_init(p_empty + 8 * s, 1);
-    mbar_init(s_ready, kMainWarps), mbar_init(x_full, 1), mbar_init(r_ready, kMainWarps);
-    mbar_init(u_full, 1), mbar_init(u_ready, kMainWarps), mbar_init(o_full, 1), mbar_init(s_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_ready + 8 * s, kMainWarps / 2), mbar_init(r_ready + 8 * s, kMainWarps / 2);
+      mbar_init(w_ready + 8 * s, kMainWarps / 2), mbar_init(s_full + 8 * s, 1);
+    }
+    mbar_init(x_full, 1), mbar_init(u_full, 1), mbar_init(u_ready, kMainWarps), mbar_init(o_full, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -467,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // ---------------------------------------------------------- epilogues ----
     constexpr int HK = DK / kParts;  // key components per thread
     const int quad = warp & 3, part = warp >> 2;
+    const uint32_t half = 8 * (part >> 1);  // this warp's of two barriers
     const int lane_n = quad * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     float s[HK];
@@ -507,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     };
     auto vec_state = [&](const float* p) { return g.dk % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const int64_t all_states = g.B * g.Hv * (int64_t)g.dv * g.dk;
-    // the state before the cursor's piece
-    auto enter = [&](const Cursor& k, const Item& it) {
-      const int n = it.tile * kM + lane_n;
-      const int64_t row = (it.bh * g.dv + n) * g.dk;
-      if (sched.phi) {
+    // the state before the chunk's piece
+    auto enter = [&](const Gates& k) {
+      const int n = k.tile * kM + lane_n;
+      const int64_t row = ((int64_t)k.bh * g.dv + n) * g.dk;
+      if (k.phi) {
 #pragma unroll
         for (int j = 0; j < HK; ++j) s[j] = part * HK + j == lane_n ? 1.0f : 0.0f;
         return;
@@ -537,12 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       load_state(n < g.dv ? src : nullptr, vec_state(src));
     };
     // and after it
-    auto leave = [&](const Cursor& k, const Item& it) {
-      const int n = it.tile * kM + lane_n;
-      const int64_t row = (it.bh * g.dv + n) * g.dk;
+    auto leave = [&](const Gates& k) {
+      const int n = k.tile * kM + lane_n;
+      const int64_t row = ((int64_t)k.bh * g.dv + n) * g.dk;
       const int p = plan.mode == kWide ? 0 : k.begin / plan.part_len;
-      if (sched.phi) {
-        float* dst = plan.phi + (((p - 1) * g.B * g.Hv + it.bh) * g.dk + lane_n) * g.dk;
+      if (k.phi) {
+        float* dst = plan.phi + (((p - 1) * g.B * g.Hv + k.bh) * g.dk + lane_n) * g.dk;
         if (lane_n < g.dk) store_state(dst, vec_state(dst));
       } else if (plan.mode == kAheadPass) {
         float* dst = plan.states + p * all_states + row;
@@ -559,11 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     };
     const int i0 = part * kTok;  // this thread's tokens of a chunk
     const uint32_t y_step = (uint32_t)g.ld_y * (g.y_bf16 ? 2 : 4);  // bytes; a chunk's rows fit 32 bits
-    char* y_at = nullptr;  // of the chunk whose output is to come: this thread's first token
-    int y_rows = 0;        // this thread's tokens inside the sequence
-    char* y_next = nullptr;       // the same of the current chunk
-    const In* v_global = nullptr; // and of its values
-    bool live = false;            // this lane is a value component
     auto arrive = [&](uint32_t bar) {
       tmem_wait_st();
       tcgen05_fence_before();
@@ -574,6 +587,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // the path from state to state does not wait for it
     auto output = [&](int c) {
       const Gates& gt = gates[c % kGateSlots];
+      const bool direct = F32 || !vec_y;
+      char* y_at = nullptr;
+      int y_rows = 0;
+      if (direct) {
+        const int n = gt.tile * kM + lane_n;
+        y_at = reinterpret_cast<char*>(g.y) +
+               ((gt.b * g.T + (int64_t)gt.at * kC + i0) * g.ld_y + (int64_t)gt.h * g.dv + n) * (g.y_bf16 ? 2 : 4);
+        y_rows = n < g.dv && !gt.quiet ? gt.tokens - i0 : 0;
+      }
       wait(o_full, c);
       tcgen05_fence_after();
       // staged over the chunk's values, which epilogue 1 of the next chunk has just
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         tmem_wait(xo);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = fmaf(o[j], __uint_as_float(xq[j]), __uint_as_float(xo[j]));
-        if (!F32 && vec_y) {
+        if (!direct) {
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
             const __nv_bfloat162 w = __floats2bfloat162_rn(o[j], o[j + 1]);
@@ -621,21 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty), mbar_arrive(gate_empty + 8 * (c % kGateSlots));
     };
-    Cursor at_chunk;
-    at_chunk.start(sched, n_all);
 #pragma unroll 1
     for (int c = 0; c <= n_chunks; ++c) {
+      const Gates& gt = gates[c % kGateSlots];
       if (F32 && c > 0) wait(o_full, c - 1);  // U's third terms are read
       if (c < n_chunks) {
-        if (at_chunk.c == at_chunk.begin) {
-          const Item it = item_of(at_chunk);
-          enter(at_chunk, it);
-          const int n = it.tile * kM + lane_n;
-          const int64_t row0 = it.b * g.T + (int64_t)at_chunk.c * kC + i0, col = (int64_t)it.h * g.dv + n;
-          live = n < g.dv;
-          y_next = reinterpret_cast<char*>(g.y) + (row0 * g.ld_y + col) * (g.y_bf16 ? 2 : 4);
-          v_global = reinterpret_cast<const In*>(g.v) + row0 * g.ld_v + col;
-        }
+        wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
+        if (gt.at == gt.begin) enter(gt);
         // S to tensor memory: of this warp's HK columns of D3's place the first
         // half the first terms, the rest the second; the third terms beyond D3
         const uint32_t at = t_lane + kColS + (uint32_t)(part * HK), at2 = t_lane + kColS + (uint32_t)(DK + part * HK / 2);
@@ -643,52 +657,64 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         for (int j0 = 0; j0 < HK; j0 += 16) {
           uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) split3(s[j0 + 2 * j], s[j0 + 2 * j + 1], t0[j], t1[j], t2[j]);
+          for (int j = 0; j < 8; ++j) split3n(s[j0 + 2 * j], s[j0 + 2 * j + 1], t0[j], t1[j], t2[j]);
           tmem_st8(at + (uint32_t)(j0 / 2), t0);
           tmem_st8(at + (uint32_t)(HK / 2 + j0 / 2), t1);
+          if (j0 == 0 && half == 0 && c > 0) {  // D3's second half reads the decayed U there
+            wait(s_full + 8, c - 1);
+            tcgen05_fence_after();
+          }
           tmem_st8(at2 + (uint32_t)(j0 / 2), t2);
         }
-        arrive(s_ready);
+        arrive(s_ready + half);
       }
       if (!F32 && c == n_chunks) wait(v_full, c);  // the output before the last has left its place
       if (c > 0 && (F32 || c == n_chunks)) output(c - 1);
       if (c == n_chunks) break;
-      const Gates& gt = gates[c % kGateSlots];
-      const int rows = live ? tokens_of(at_chunk) - i0 : 0;
-      // this lane's value of token i0 + i
-      const In* v_tile = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
-      auto value = [&](int i) {
-        if (sched.phi) return 0.0f;
-        if (!F32) return to_f32(v_tile[i * kM]);
-        return i < rows ? to_f32(v_global[i * g.ld_v]) : 0.0f;
-      };
       {  // epilogue 1: R^T = V^T - e^G D1
-        wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
-        if (!F32) wait(v_full, c);
         static_assert(kTok == 16, "one tensor-memory load");
         float r[kTok];
+        if (F32) {
+          const int n = gt.tile * kM + lane_n, rows = n < g.dv && !gt.phi ? gt.tokens - i0 : 0;
+          const In* v = reinterpret_cast<const In*>(g.v) + (gt.b * g.T + (int64_t)gt.at * kC + i0) * g.ld_v + (int64_t)gt.h * g.dv + n;
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) r[j] = value(j);
+          for (int j = 0; j < kTok; ++j) {
+            r[j] = j < rows ? to_f32(*v) : 0.0f;
+            v += g.ld_v;
+          }
+        } else {
+          wait(v_full, c);
+          const In* v = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
+#pragma unroll
+          for (int j = 0; j < kTok; ++j) r[j] = to_f32(v[j * kM]);
+          if (gt.phi) {
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) r[j] = 0.0f;
+          }
+        }
         wait(x_full, c);
         tcgen05_fence_after();
-        uint32_t x[kTok];
-        tmem_ld16(t_lane + kColX + (uint32_t)i0, x);
-        tmem_wait(x);
 #pragma unroll
-        for (int j = 0; j < kTok; j += 4) {
-          const float4 eg = *reinterpret_cast<const float4*>(&gt.eg[i0 + j]);
-          r[j] = fmaf(-eg.x, __uint_as_float(x[j]), r[j]);
-          r[j + 1] = fmaf(-eg.y, __uint_as_float(x[j + 1]), r[j + 1]);
-          r[j + 2] = fmaf(-eg.z, __uint_as_float(x[j + 2]), r[j + 2]);
-          r[j + 3] = fmaf(-eg.w, __uint_as_float(x[j + 3]), r[j + 3]);
+        for (int j0 = 0; j0 < kTok; j0 += 8) {  // all of it is read before the first is replaced
+          uint32_t x[8];
+          tmem_ld8(t_lane + kColX + (uint32_t)(i0 + j0), x);
+          tmem_wait(x);
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 eg = *reinterpret_cast<const float4*>(&gt.eg[i0 + j0 + j]);
+            r[j0 + j] = fmaf(-eg.x, __uint_as_float(x[j]), r[j0 + j]);
+            r[j0 + j + 1] = fmaf(-eg.y, __uint_as_float(x[j + 1]), r[j0 + j + 1]);
+            r[j0 + j + 2] = fmaf(-eg.z, __uint_as_float(x[j + 2]), r[j0 + j + 2]);
+            r[j0 + j + 3] = fmaf(-eg.w, __uint_as_float(x[j + 3]), r[j0 + j + 3]);
+          }
         }
         uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split3(r[2 * j], r[2 * j + 1], t0[j], t1[j], t2[j]);
+        for (int j = 0; j < 8; ++j) split3n(r[2 * j], r[2 * j + 1], t0[j], t1[j], t2[j]);
         tmem_st8(t_lane + kColX + (uint32_t)i0, t0);
         tmem_st8(t_lane + kColX + (uint32_t)(i0 + 8), t1);
         tmem_st8(t_lane + (F32 ? kColO + (uint32_t)i0 : kColThird + (uint32_t)(8 * part)), t2);
-        arrive(r_ready);
+        arrive(r_ready + half);
       }
       if (!F32) {
         if (c > 0) {
@@ -703,24 +729,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       {  // epilogue 2: U^T for the output, and decayed to the chunk's end for S
         wait(u_full, c);
         tcgen05_fence_after();
-        uint32_t x[16], t0[8], t1[8], t2[8];
+        uint32_t x[16];
         tmem_ld16(t_lane + kColU + (uint32_t)i0, x);
         tmem_wait(x);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 fd = *reinterpret_cast<const float4*>(&gt.fd[i0 + 2 * j]);
-          split3(fd.x * __uint_as_float(x[2 * j]), fd.y * __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
-          split3(fd.z * __uint_as_float(x[2 * j + 2]), fd.w * __uint_as_float(x[2 * j + 3]), t0[j + 1], t1[j + 1], t2[j + 1]);
+        for (int j0 = 0; j0 < 8; j0 += 4) {
+          uint32_t t0[4], t1[4], t2[4];
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const uint32_t* u = x + 2 * (j0 + j);
+            const float4 fd = *reinterpret_cast<const float4*>(&gt.fd[i0 + 2 * (j0 + j)]);
+            split3n(fd.x * __uint_as_float(u[0]), fd.y * __uint_as_float(u[1]), t0[j], t1[j], t2[j]);
+            split3n(fd.z * __uint_as_float(u[2]), fd.w * __uint_as_float(u[3]), t0[j + 1], t1[j + 1], t2[j + 1]);
+          }
+          tmem_st4(t_lane + kColX + (uint32_t)(i0 + j0), t0);
+          tmem_st4(t_lane + kColX + (uint32_t)(i0 + 8 + j0), t1);
+          tmem_st4(t_lane + kColThird + (uint32_t)(8 * part + j0), t2);
         }
-        tmem_st8(t_lane + kColX + (uint32_t)i0, t0);
-        tmem_st8(t_lane + kColX + (uint32_t)(i0 + 8), t1);
-        tmem_st8(t_lane + kColThird + (uint32_t)(8 * part), t2);
+        arrive(w_ready + half);
+        uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (F32)
-            split3(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
+            split3n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
           else
-            split2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
+            split2n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
         }
         tmem_st8(t_lane + kColU + (uint32_t)i0, t0);
         tmem_st8(t_lane + kColU + (uint32_t)(i0 + 8), t1);
@@ -729,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       {  // epilogue 3: S = e^G S + D3
         const float total = gt.total;
-        wait(s_full, c);
+        wait(s_full + half, c);
         tcgen05_fence_after();
 #pragma unroll
         for (int j0 = 0; j0 < HK; j0 += 16) {
@@ -740,11 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]));
         }
       }
-      if (at_chunk.c + 1 == at_chunk.end) leave(at_chunk, item_of(at_chunk));
-      y_at = y_next, y_rows = sched.quiet ? 0 : rows;
-      y_next += (int64_t)kC * y_step;
-      if (F32) v_global += (int64_t)kC * g.ld_v;
-      at_chunk.next(sched, n_all);
+      if (gt.at + 1 == gt.end) leave(gt);
     }
   } else if (warp < kGateWarp) {
     // ------------------------------------------------------------ prepare ----
@@ -790,11 +819,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
       for (int e = 0; e < 4; ++e) split3(c[e / 2][2 * (e & 1)], c[e / 2][2 * (e & 1) + 1], x[0][e], x[1][e], x[2][e]);
     };
-    // T and P are zero above the diagonal blocks
-    for (int e = threadIdx.x - 32 * kMainWarps; e < (L::kT + L::kPBuffers * L::kP) / 16; e += 2 * kGroupThreads)
-      *reinterpret_cast<uint4*>(gbase + L::kOffT + e * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    named_barrier(3, 2 * kGroupThreads);
 #pragma unroll 1
     for (int c = group; c < n_chunks; c += 2) {
       const Gates& gt = gates[c % kGateSlots];
@@ -819,9 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (F32)
-                split3(o[2 * e], o[2 * e + 1], t[0][e], t[1][e], t[2][e]);
+                split3n(o[2 * e], o[2 * e + 1], t[0][e], t[1][e], t[2][e]);
               else
-                split2(o[2 * e], o[2 * e + 1], t[0][e], t[1][e]);
+                split2n(o[2 * e], o[2 * e + 1], t[0][e], t[1][e]);
             }
             const uint32_t at = dst_p + (uint32_t)(((j / 8) ^ (i & 7)) << 4);
 #pragma unroll
@@ -1014,7 +1038,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             const float2 be = *reinterpret_cast<const float2*>(&gt.beta[16 * k + 8 * nn + fc]);
             x[k][nn][0] *= be.x, x[k][nn][1] *= be.y, x[k][nn][2] *= be.x, x[k][nn][3] *= be.y;
           }
-          operand(xt, x[k]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            split3n(x[k][e / 2][2 * (e & 1)], x[k][e / 2][2 * (e & 1) + 1], xt[0][e], xt[1][e], xt[2][e]);
 #pragma unroll
           for (int e = 0; e < 3; ++e) stmatrix4((at ^ (uint32_t)(k << 5)) + e * 8192, xt[e]);
         }
@@ -1032,13 +1058,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // kept as two floats each, so that differences between far-decayed tokens keep
     // 32-bit accuracy.  alpha below e^-200 is 0 in f32 all the same.
     float a_next[2], b_next[2], A_next, bias_next;
+    const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
     Cursor at_chunk;
     at_chunk.start(sched, n_all);
+    Item it = {};
     const In* a_base = nullptr;
     const In* b_base = nullptr;
     auto fetch = [&]() {
       if (at_chunk.c == at_chunk.begin) {
-        const Item it = item_of(at_chunk);
+        it = item_of(at_chunk);
         a_base = reinterpret_cast<const In*>(g.a) + it.b * g.T * g.ld_a + it.h;
         b_base = reinterpret_cast<const In*>(g.b) + it.b * g.T * g.ld_b + it.h;
         A_next = g.A_log[it.h];
@@ -1050,7 +1078,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         a_next[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
         b_next[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
       }
-      at_chunk.next(sched, n_all);
     };
     fetch();
     for (int c = 0; c < n_chunks; ++c) {
@@ -1063,6 +1090,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         G[u] = two_log2(la < -200.0f ? -200.0f : la);
         be[u] = gdr_beta(b_next[u]);
       }
+      const Cursor here = at_chunk;
+      const int tile = it.tile, h = it.h, b = (int)it.b;
+      at_chunk.next(sched, n_all);
       if (c + 1 < n_chunks) fetch();
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
@@ -1088,7 +1118,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       gt.past[lane] = two_exp2(mid, G[0]);
       gt.since[lane] = two_exp2(G[1], mid);
-      if (lane == 0) gt.total = ex2_approx(last.h + last.l);
+      if (lane == 0) {
+        gt.total = ex2_approx(last.h + last.l);
+        gt.at = here.c, gt.begin = here.begin, gt.end = here.end, gt.tokens = tokens_of(here);
+        gt.tile = tile, gt.h = h, gt.b = b, gt.bh = b * g.Hv + h;
+        gt.phi = sched.phi, gt.quiet = sched.quiet;
+      }
       mbar_arrive(gate_full + 8 * (c % kGateSlots));
     }
   } else if (warp == kMmaWarp) {
@@ -1097,7 +1132,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // elected lane issues: by a lane of a branch of its own a product took 50
     // cycles to issue and 32 to run.
     const bool elected = elect_one();
-    constexpr uint32_t id64 = idesc_bf16(64, false), id3 = idesc_bf16(DK, true);
+    constexpr uint32_t id64 = idesc_bf16(64, false);
+    // D3 in two halves of its columns, where each is a block of K
+    constexpr int kHalves = DK / 64;
+    constexpr uint32_t id3 = idesc_bf16(64, true);
     constexpr int HK = DK / kParts;
     // products with K or Q; the output's without the smallest for bf16 tensors
     constexpr int kPairs = F32 ? 6 : 3, kSkipQ = F32 ? 0 : 1, kSkipP = F32 ? 0 : 3;
@@ -1118,13 +1156,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k) {
           const uint64_t at = kq + (k / 4) * 1024 + 2 * (k % 4);
-          if (elected) mma_ss(tmem + kColD0, at + ta * (L::kKqTerm / 16), at + tb * (L::kKqTerm / 16), id64, p > 0 || k > 0);
+          if (elected) mma_ss(tmem + kColD0, at + ta * (L::kKqTerm / 16), at + tb * (L::kKqTerm / 16), id64 | neg_bits(ta, tb), p > 0 || k > 0);
         }
       }
       commit(d0_full + 8 * (c & 1));
     };
     // S times the keys (0) or the queries (1)
-    auto issue_d1 = [&](int c, int part) {
+    auto issue_d1 = [&](int c, int part, int k0, int k1) {
       const uint64_t kq = kq0 + (uint64_t)((c % L::kKqStages) * (L::kKq / 16) + part * 512);
       const uint32_t d = tmem + (part ? kColQ : kColX);
       const int first = part ? kSkipQ : 0;
@@ -1133,36 +1171,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         int ta = 0, tb = 0;
         term_pair<F32>(p, ta, tb);
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
+        for (int k = k0; k < k1; ++k) {
           const uint32_t w = (16 * k % HK) / 2, q = 16 * k / HK;
           const uint32_t ad = (ta < 2 ? ta * (HK / 2) : DK) + w + q * (ta < 2 ? HK : HK / 2);
           if (elected)
-            mma_ts(d, tmem + kColS + ad, kq + tb * (L::kKqTerm / 16) + (k / 4) * 1024 + 2 * (k % 4), id64, p > first || k > 0);
+            mma_ts(d, tmem + kColS + ad, kq + tb * (L::kKqTerm / 16) + (k / 4) * 1024 + 2 * (k % 4), id64 | neg_bits(ta, tb),
+                   p > first || k > 0);
         }
       }
     };
     issue_d0(0);
     for (int c = 0; c < n_chunks; ++c) {
-      wait(s_ready, c);
-      tcgen05_fence_after();
-      issue_d1(c, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wait(s_ready + 8 * h, c);
+        tcgen05_fence_after();
+        issue_d1(c, 0, h * (DK / 32), (h + 1) * (DK / 32));
+      }
       commit(x_full);
       if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
       if (F32) {  // S's third terms make room for the decayed U's
         if (c > 0) wait(o_empty, c - 1);
-        issue_d1(c, 1);
+        issue_d1(c, 1, 0, DK / 16);
       }
       wait(t_full, c);
-      wait(r_ready, c);
-      tcgen05_fence_after();
+      // D2 = R T^T.  T is lower triangular: 16 tokens of the contraction reach the
+      // columns from their own on
 #pragma unroll
-      for (int p = 0; p < 6; ++p) {  // D2 = R T^T
-        int ta = 0, tb = 0;
-        term_pair<true>(p, ta, tb);
+      for (int h = 0; h < 2; ++h) {
+        wait(r_ready + 8 * h, c);
+        tcgen05_fence_after();
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : F32 ? kColO + 16 * k : kColThird + 8 * k;
-          if (elected) mma_ts(tmem + kColU, tmem + ad, t0 + tb * 512 + 2 * k, id64, p > 0 || k > 0);
+        for (int p = 0; p < 6; ++p) {
+          int ta = 0, tb = 0;
+          term_pair<true>(p, ta, tb);
+#pragma unroll
+          for (int k = 2 * h; k < 2 * h + 2; ++k) {
+            const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : F32 ? kColO + 16 * k : kColThird + 8 * k;
+            if (elected)
+              mma_ts(tmem + kColU + 16 * k, tmem + ad, t0 + tb * 512 + 130 * k,
+                     idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > 0 || k > 0);
+          }
         }
       }
       commit(u_full);
@@ -1170,26 +1219,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (!F32) {  // the queries' product, under epilogue 2
         if (c > 0) wait(o_empty, c - 1);
         tcgen05_fence_after();
-        issue_d1(c, 1);
+        issue_d1(c, 1, 0, DK / 16);
       }
-      wait(u_ready, c);
-      tcgen05_fence_after();
       // D3 = U K; K's rows are the contraction
       const uint64_t kq_mn = kq0_mn + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        int ta = 0, tb = 0;
-        term_pair<F32>(p, ta, tb);
+      for (int h = 0; h < 2; ++h) {
+        wait(w_ready + 8 * h, c);
+        tcgen05_fence_after();
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : kColThird + 8 * k;
-          if (elected) mma_ts(tmem + kColS, tmem + ad, kq_mn + tb * (L::kKqTerm / 16) + 128 * k, id3, p > 0 || k > 0);
+        for (int nh = 0; nh < kHalves; ++nh) {
+#pragma unroll
+          for (int p = 0; p < kPairs; ++p) {
+            int ta = 0, tb = 0;
+            term_pair<F32>(p, ta, tb);
+#pragma unroll
+            for (int k = 2 * h; k < 2 * h + 2; ++k) {
+              const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : kColThird + 8 * k;
+              if (elected)
+                mma_ts(tmem + kColS + 64 * nh, tmem + ad, kq_mn + tb * (L::kKqTerm / 16) + 1024 * nh + 128 * k,
+                       id3 | neg_bits(ta, tb), p > 0 || k > 0);
+            }
+          }
+          if (h == 1) commit(s_full + 8 * nh);
         }
       }
-      commit(s_full);
+      if (kHalves == 1) commit(s_full + 8);
       commit(kq_empty + 8 * (c % L::kKqStages));
       // the output's U P^T, under epilogue 3
       wait(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
+      wait(u_ready, c);
+      tcgen05_fence_after();
       const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
 #pragma unroll
       for (int p = kSkipP; p < 6; ++p) {
@@ -1198,7 +1258,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {
           const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
-          if (elected) mma_ts(tmem + kColO, tmem + ad, pd + tb * 512 + 2 * k, id64, p > kSkipP || k > 0);
+          if (elected)
+            mma_ts(tmem + kColO + 16 * k, tmem + ad, pd + tb * 512 + 130 * k,
+                   idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > kSkipP || k > 0);
         }
       }
       commit(o_full);
@@ -1213,8 +1275,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   } else {
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
-    Cursor at_chunk, stored;  // the chunk to load, and the one whose output is to be stored
-    at_chunk.start(sched, n_all), stored.start(sched, n_all);
+    const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
+    Cursor at_kq, at_chunk, stored;  // the chunks to load, and the one whose output is to be stored
+    at_kq.start(sched, n_all), at_chunk.start(sched, n_all), stored.start(sched, n_all);
     // chunk c's output from its place over the values
     auto store_y = [&]() {
       if (lt == 0 && !sched.quiet) {
@@ -1245,18 +1308,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       lines(reinterpret_cast<const float*>(g.q) + (int64_t)it.hk * g.dk, g.ld_q, g.dk);
       lines(reinterpret_cast<const float*>(g.v) + (int64_t)it.h * g.dv + it.tile * kM, g.ld_v, cols);
     };
-    for (int c = 0; c < n_chunks; ++c) {
+    // the keys and queries of chunk c, the cursor's
+    auto load_kq = [&](int c) {
       const int ks = c % L::kKqStages;
-      const Item it = item_of(at_chunk);
-      const int left = tokens_of(at_chunk), t0 = at_chunk.c * kC;
+      const Item it = item_of(at_kq);
+      const int left = tokens_of(at_kq), t0 = at_kq.c * kC;
       const In* k_base = reinterpret_cast<const In*>(g.k) + (it.b * g.T + t0) * g.ld_k + (int64_t)it.hk * g.dk;
       const In* q_base = reinterpret_cast<const In*>(g.q) + (it.b * g.T + t0) * g.ld_q + (int64_t)it.hk * g.dk;
-      const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
       const uint32_t kq = base + ks * L::kKq;
-      if (F32 && c == 0) prefetch(at_chunk);
+      if (F32 && c == 0) prefetch(at_kq);
       if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
-      at_chunk.next(sched, n_all);
-      if (F32 && c + 1 < n_chunks) prefetch(at_chunk);
+      at_kq.next(sched, n_all);
+      if (F32 && c + 1 < n_chunks) prefetch(at_kq);
       if (vec_kq) {
         // tokens past the end and components past dk read as zero
         if (lt == 0) {
@@ -1296,7 +1359,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             const uint32_t at = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
             uint32_t x[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split3(f[u][2 * j], f[u][2 * j + 1], x[0][j], x[1][j], x[2][j]);
+            for (int j = 0; j < 4; ++j) split3n(f[u][2 * j], f[u][2 * j + 1], x[0][j], x[1][j], x[2][j]);
 #pragma unroll
             for (int p = 0; p < L::kTerms; ++p)
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
@@ -1307,8 +1370,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         fence_proxy_async_smem();
         mbar_arrive(kq_full + 8 * ks);
       }
+    };
+    load_kq(0);
+    for (int c = 0; c < n_chunks; ++c) {
+      // a chunk ahead of the values, whose place is free later
+      if (c + 1 < n_chunks) load_kq(c + 1);
       // V (bf16); tokens past the sequence's end and components past dv are zero
       if (!F32) {
+        const Item it = item_of(at_chunk);
+        const int left = tokens_of(at_chunk), t0 = at_chunk.c * kC;
+        const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
         if (c > 0) wait(v_empty, c - 1);
         if (vec_y && c > 1) store_y();
         if (vec_v) {
@@ -1326,6 +1397,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           }
           mbar_arrive(v_full);
         }
+        at_chunk.next(sched, n_all);
       }
     }
     if (!F32) {  // the last two chunks' outputs
