@@ -74,6 +74,7 @@ constexpr int kGroupWarps = kPrepWarps / 2, kGroupThreads = 32 * kGroupWarps, kL
 constexpr int kGateSlots = 4;
 constexpr int kLdA = kC + 4;      // row stride of A and P in shared memory, floats
 constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
+constexpr int kWaitTries = 1 << 18;          // of 4 us
 
 __device__ int g_delta_faults = 0;
 
@@ -298,6 +299,12 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4])
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
+__device__ __forceinline__ void ldmatrix4(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -323,35 +330,20 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// True once the phase of parity `parity` has completed, false after about a
-// millisecond: until then the warp sleeps in the barrier's hardware.
+// True once the phase of parity `parity` has completed, false after a while (4 us):
+// until then the warp sleeps in the barrier's hardware.
 __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n"
       "  .reg .pred p;\n"
-      "  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       "  selp.u32 %0, 1, 0, p;\n"
       "}\n"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
-}
-
-// A wait that did not succeed at once.  One that runs out sets the fault and
-// abort flags; every role then runs on through its loop without waiting, so
-// that all named barriers are met and the CTA ends.
-__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (*abort_flag) return;
-  const long long t0 = clock64();
-  while (!mbar_sleep(bar, parity)) {
-    if (clock64() - t0 > kWaitLimit) {
-      atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
-      *abort_flag = 1;
-      return;
-    }
-  }
 }
 
 // A number as the unevaluated sum of two floats
@@ -476,8 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   tcgen05_fence_after();
   const uint32_t tmem = *tmem_ptr;
 
+  // The gate, MMA and load warps' waits are counted; one that runs out sets the abort
+  // flag, and every role then runs on through its loop without waiting, so that all
+  // named barriers are met and the CTA ends.  The epilogue and prepare warps wait for
+  // those warps alone (or for what they have started and wait for themselves), so
+  // theirs only look at the flag: 12 instructions less at every wait are 3 % of a
+  // chunk, the loops being larger than the instruction cache.
+  auto wait_counted = [&](uint32_t bar, int phase) {
+#pragma unroll 1
+    for (int tries = 0; !mbar_sleep(bar, (uint32_t)(phase & 1)); ++tries) {
+      if (tries > kWaitTries) *abort_flag = 1;
+      if (*abort_flag) break;
+    }
+  };
   auto wait = [&](uint32_t bar, int phase) {
-    if (!mbar_sleep(bar, (uint32_t)(phase & 1))) wait_slow(bar, (uint32_t)(phase & 1), abort_flag);
+    while (!mbar_sleep(bar, (uint32_t)(phase & 1))) {
+      if (*abort_flag) break;
+    }
   };
 
   if (warp < kMainWarps) {
@@ -540,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         const long long t0 = clock64();
         while (*flag == 0 && !*abort_flag) {
           if (clock64() - t0 > kWaitLimit) {
-            atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
             *abort_flag = 1;
           }
           __nanosleep(200);
@@ -785,15 +791,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     const bool upper = quad & 1;            // tokens 32-63: the rows with columns past 31
     const int i = row & (kC - 1);           // token
     float* a_s = reinterpret_cast<float*>(gbase + L::kOffA) + group * kC * kLdA;
-    // The blocks (k, j) of D and N = -D A, in three terms, take A's place: block
-    // k (k + 1) / 2 + j, terms of 512 bytes, rows of 32 bytes whose 16-byte
-    // granules change places every four rows
+    // The blocks (k, j) of D and N = -D A, in three terms of 16 rows of 32 bytes, take
+    // A's place: the first two that of their block of A, the third one above the
+    // diagonal.  Rows are 17 granules of 16 bytes apart, so no two of eight share banks.
     const uint32_t n_s = base + L::kOffA + (uint32_t)(group * kC * kLdA * 4);
-    auto block_at = [&](int k, int j) { return n_s + (uint32_t)((k * (k + 1) / 2 + j) * 1536); };
+    auto term_at = [&](int k, int j, int t) {
+      int a = k, b = j, off = 32 * t;
+      if (t == 2) {
+        if (k == j)
+          a = k < 3 ? 0 : 1, b = k < 3 ? k + 1 : 2, off = 32;
+        else
+          a = j, b = k, off = 0;
+      }
+      return n_s + (uint32_t)(a * 16 * kLdA * 4 + b * 64 + off);
+    };
     const int rb = quad;  // T's block of 16 rows that this warp solves
     const int fr = lane / 4, fc = 2 * (lane % 4);  // accumulator fragment: rows fr, fr + 8, columns fc, fc + 1
     // this lane's row for ldmatrix: matrices (k 0-7, n 0-7), (k 8-15, n 0-7), (k 0-7, n 8-15), ..
-    const uint32_t ld_row = (uint32_t)(lane & 15), ld_at = ld_row * 32 + ((((uint32_t)lane >> 4) ^ ((ld_row >> 2) & 1)) << 4);
+    const uint32_t ld_at = (uint32_t)((lane & 15) * kLdA * 4 + (lane >> 4) * 16);
     // acc += x m over three terms each, the small and the large products in two
     // chains (one is 20 cycles long, 66 while tcgen05 products are in flight)
     auto product = [&](float (&acc)[2][4], const uint32_t (&x)[3][4], const uint32_t (&m)[3][4]) {
@@ -923,89 +938,62 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
-          for (int q = 0; q < 16; q += 4)
-            *reinterpret_cast<float4*>(blk + r * kLdA + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t t[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split3(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], t[0][e], t[1][e], t[2][e]);
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(term_at(quad, quad, e) + r * kLdA * 4 + 16 * q),
+                           "r"(t[e][0]), "r"(t[e][1]), "r"(t[e][2]), "r"(t[e][3])
+                           : "memory");
+          }
         }
       }
       named_barrier(bar_id, kGroupThreads);
-      {
-        // N_kj = D_k (-A_kj) below the diagonal, blocks (1,0) (2,0) (2,1) (3,0) (3,1)
-        // (3,2) by warps 3 0 1 2 3 0; then those and the D_k, in three terms over A
-        uint32_t dt[3][4], nt[2][3][4];
-        auto load_block = [&](float (&x)[2][4], const float* m) {
+      // N_kj = D_k (-A_kj) below the diagonal, blocks (1,0) (2,0) (2,1) (3,0) (3,1)
+      // (3,2) by warps 3 0 1 2 3 0
+#pragma unroll 1
+      for (int p = (quad + 1) % 4; p < 6; p += 4) {
+        const int k = p < 1 ? 1 : p < 3 ? 2 : 3, j = p - k * (k - 1) / 2;
+        const float* m = a_s + 16 * k * kLdA + 16 * j;
+        uint32_t xt[3][4], mt[3][4];
 #pragma unroll
-          for (int nn = 0; nn < 2; ++nn) {
-            const float2 lo = *reinterpret_cast<const float2*>(m + fr * kLdA + 8 * nn + fc);
-            const float2 hi = *reinterpret_cast<const float2*>(m + (fr + 8) * kLdA + 8 * nn + fc);
-            x[nn][0] = lo.x, x[nn][1] = lo.y, x[nn][2] = hi.x, x[nn][3] = hi.y;
-          }
-        };
-        float x[2][4];
+        for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int p = (quad + 1) % 4 + 4 * u;
-          if (p >= 6) continue;
-          const int k = p < 1 ? 1 : p < 3 ? 2 : 3, j = p - k * (k - 1) / 2;
-          load_block(x, a_s + 16 * k * (kLdA + 1));
-          const float* m = a_s + 16 * k * kLdA + 16 * j;
-          uint32_t xt[3][4], mt[3][4];
+          for (int kk = 0; kk < 2; ++kk)
+            split3(m[(8 * kk + fc) * kLdA + 8 * nn + fr], m[(8 * kk + fc + 1) * kLdA + 8 * nn + fr], mt[0][2 * nn + kk],
+                   mt[1][2 * nn + kk], mt[2][2 * nn + kk]);
 #pragma unroll
-          for (int nn = 0; nn < 2; ++nn)
+        for (int e = 0; e < 3; ++e) ldmatrix4(xt[e], term_at(k, k, e) + ld_at);
+        float x[2][4] = {};
+        product(x, xt, mt);
+        operand(xt, x);
+        __syncwarp();  // the block of A is read
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              split3(m[(8 * kk + fc) * kLdA + 8 * nn + fr], m[(8 * kk + fc + 1) * kLdA + 8 * nn + fr], mt[0][2 * nn + kk],
-                     mt[1][2 * nn + kk], mt[2][2 * nn + kk]);
-          operand(xt, x);
-#pragma unroll
-          for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[nn][e] = 0.0f;
-          product(x, xt, mt);
-          operand(nt[u], x);
-        }
-        load_block(x, blk);
-        operand(dt, x);
-        named_barrier(bar_id, kGroupThreads);  // A is read
-        // lane l addresses row l % 8 of matrix l / 8: rows 0-7, 8-15 of columns 0-7, then of 8-15
-#pragma unroll
-        for (int e = 0; e < 3; ++e) stmatrix4(block_at(quad, quad) + 512 * e + ld_at, dt[e]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int p = (quad + 1) % 4 + 4 * u;
-          if (p >= 6) continue;
-          const int k = p < 1 ? 1 : p < 3 ? 2 : 3, j = p - k * (k - 1) / 2;
-#pragma unroll
-          for (int e = 0; e < 3; ++e) stmatrix4(block_at(k, j) + 512 * e + ld_at, nt[u][e]);
-        }
+        for (int e = 0; e < 3; ++e) stmatrix4(term_at(k, j, e) + ld_at, xt[e]);
       }
       named_barrier(bar_id, kGroupThreads);  // D and N are there
       {
-        // rows 16 rb .. of T = X diag(beta): the identity's first step is a copy of
-        // N's blocks, its last of D's
+        // rows 16 rb .. of T = X diag(beta): the identity's first step takes N's blocks
+        // and D's as they are (the sum of the terms: a product by the identity)
         float x[4][2][4];
-        auto load_terms = [&](float (&v)[2][4], uint32_t m) {  // the sum of a block's terms
-#pragma unroll
-          for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t r = (uint32_t)(fr + 8 * e), at = m + r * 32 + ((((uint32_t)nn) ^ ((r >> 2) & 1)) << 4) + fc * 2;
-              float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-              for (int t = 2; t >= 0; --t) {
-                uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at + 512 * t) : "memory");
-                lo += __uint_as_float(w << 16), hi += __uint_as_float(w & 0xffff0000u);
-              }
-              v[nn][2 * e] = lo, v[nn][2 * e + 1] = hi;
-            }
-        };
+        const uint32_t one = (fr == fc ? 0x3f80u : 0u) | (fr == fc + 1 ? 0x3f800000u : 0u);
+        const uint32_t identity[4] = {one, 0, 0, one};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
           for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[k][nn][e] = 0.0f;
-          if (k <= rb) load_terms(x[k], block_at(rb, k));
+          if (k > rb) continue;
+#pragma unroll
+          for (int e = 2; e >= 0; --e) {
+            uint32_t m[4];
+            ldmatrix4_trans(m, term_at(rb, k, e) + ld_at);
+            mma_sync(x[k][0], identity, m[0], m[1]);
+            mma_sync(x[k][1], identity, m[2], m[3]);
+          }
         }
 #pragma unroll
         for (int k = 2; k >= 0; --k) {
@@ -1021,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             const int j = u <= k ? k - u : k;
             uint32_t m[3][4];
 #pragma unroll
-            for (int e = 0; e < 3; ++e) ldmatrix4_trans(m[e], block_at(k, j) + 512 * e + ld_at);
+            for (int e = 0; e < 3; ++e) ldmatrix4_trans(m[e], term_at(k, j, e) + ld_at);
             product(x[j], xt, m);
           }
         }
@@ -1106,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       G[1] = two_add(G[1], mid);
       const Two last = two_shfl(G[1], 31);
       Gates& gt = gates[c % kGateSlots];
-      if (c >= kGateSlots) wait(gate_empty + 8 * (c % kGateSlots), c / kGateSlots + 1);
+      if (c >= kGateSlots) wait_counted(gate_empty + 8 * (c % kGateSlots), c / kGateSlots + 1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = lane + 32 * u;
@@ -1146,8 +1134,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // [K; Q] K^T of chunk c, for the prepare warps
     auto issue_d0 = [&](int c) {
       const uint64_t kq = kq0 + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
-      wait(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
-      if (c > 0) wait(d0_empty + 8 * ((c - 1) & 1), (c - 1) / 2);
+      wait_counted(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
+      if (c > 0) wait_counted(d0_empty + 8 * ((c - 1) & 1), (c - 1) / 2);
       tcgen05_fence_after();
 #pragma unroll
       for (int p = 0; p < (F32 ? 6 : 1); ++p) {
@@ -1184,22 +1172,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     for (int c = 0; c < n_chunks; ++c) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        wait(s_ready + 8 * h, c);
+        wait_counted(s_ready + 8 * h, c);
         tcgen05_fence_after();
         issue_d1(c, 0, h * (DK / 32), (h + 1) * (DK / 32));
       }
       commit(x_full);
       if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
       if (F32) {  // S's third terms make room for the decayed U's
-        if (c > 0) wait(o_empty, c - 1);
+        if (c > 0) wait_counted(o_empty, c - 1);
         issue_d1(c, 1, 0, DK / 16);
       }
-      wait(t_full, c);
+      wait_counted(t_full, c);
       // D2 = R T^T.  T is lower triangular: 16 tokens of the contraction reach the
       // columns from their own on
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        wait(r_ready + 8 * h, c);
+        wait_counted(r_ready + 8 * h, c);
         tcgen05_fence_after();
 #pragma unroll
         for (int p = 0; p < 6; ++p) {
@@ -1217,7 +1205,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       commit(u_full);
       commit(t_empty + 8 * (c & 1));
       if (!F32) {  // the queries' product, under epilogue 2
-        if (c > 0) wait(o_empty, c - 1);
+        if (c > 0) wait_counted(o_empty, c - 1);
         tcgen05_fence_after();
         issue_d1(c, 1, 0, DK / 16);
       }
@@ -1225,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       const uint64_t kq_mn = kq0_mn + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        wait(w_ready + 8 * h, c);
+        wait_counted(w_ready + 8 * h, c);
         tcgen05_fence_after();
 #pragma unroll
         for (int nh = 0; nh < kHalves; ++nh) {
@@ -1247,8 +1235,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (kHalves == 1) commit(s_full + 8);
       commit(kq_empty + 8 * (c % L::kKqStages));
       // the output's U P^T, under epilogue 3
-      wait(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
-      wait(u_ready, c);
+      wait_counted(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
+      wait_counted(u_ready, c);
       tcgen05_fence_after();
       const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
 #pragma unroll
@@ -1270,8 +1258,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // the last commit has arrived (and with it every MMA is done) before
     // tensor memory is freed and the barriers go away
     const int last = n_chunks - 1;
-    if (!mbar_wait(p_empty + 8 * (last % L::kPBuffers), (uint32_t)(last / L::kPBuffers) & 1, kWaitLimit))
-      atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
+    wait_counted(o_full, last);
+    wait_counted(p_empty + 8 * (last % L::kPBuffers), last / L::kPBuffers);
   } else {
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
@@ -1317,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       const In* q_base = reinterpret_cast<const In*>(g.q) + (it.b * g.T + t0) * g.ld_q + (int64_t)it.hk * g.dk;
       const uint32_t kq = base + ks * L::kKq;
       if (F32 && c == 0) prefetch(at_kq);
-      if (c >= L::kKqStages) wait(kq_empty + 8 * ks, c / L::kKqStages + 1);
+      if (c >= L::kKqStages) wait_counted(kq_empty + 8 * ks, c / L::kKqStages + 1);
       at_kq.next(sched, n_all);
       if (F32 && c + 1 < n_chunks) prefetch(at_kq);
       if (vec_kq) {
@@ -1380,7 +1368,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         const Item it = item_of(at_chunk);
         const int left = tokens_of(at_chunk), t0 = at_chunk.c * kC;
         const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
-        if (c > 0) wait(v_empty, c - 1);
+        if (c > 0) wait_counted(v_empty, c - 1);
         if (vec_y && c > 1) store_y();
         if (vec_v) {
           if (lt == 0) {
@@ -1401,16 +1389,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
     }
     if (!F32) {  // the last two chunks' outputs
-      wait(v_empty, n_chunks - 1);
+      wait_counted(v_empty, n_chunks - 1);
       if (vec_y && n_chunks > 1) store_y();
       if (!vec_v || lt == 0) mbar_arrive(v_full);
-      wait(v_empty, n_chunks);
+      wait_counted(v_empty, n_chunks);
       if (vec_y) store_y();
       if (lt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
   tcgen05_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(&g_delta_faults, MAMBA_FAULT_DELTA_WAIT);
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
