@@ -385,6 +385,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+
 // The products of two sums of terms, smallest first, as (term of a, term of b) in
 // two bits each.  Three terms by one: 3, or the first 2; three by three: the 6
 // above 2^-24, or the 3 above 2^-16.
@@ -1264,64 +1270,85 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
     const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
-    Cursor at_kq, at_chunk, stored;  // the chunks to load, and the one whose output is to be stored
-    at_kq.start(sched, n_all), at_chunk.start(sched, n_all), stored.start(sched, n_all);
-    // chunk c's output from its place over the values
-    auto store_y = [&]() {
+    // A chunk's place in the tensors.  The cursor runs two chunks ahead of the values'
+    // load: that chunk's rows are prefetched, the next one's keys and queries loaded,
+    // this one's values, and the output of two before stored.
+    struct At {
+      int tile, h, hk, b, t;
+    };
+    Cursor ahead;
+    ahead.start(sched, n_all);
+    At next = {};  // the cursor's
+    auto place = [&]() {
+      if (ahead.c == ahead.begin) {
+        const Item it = item_of(ahead);
+        next = At{it.tile, it.h, it.hk, (int)it.b, ahead.c * kC};
+      } else {
+        next.t += kC;
+      }
+      ahead.next(sched, n_all);
+    };
+    // a chunk's output from its place over the values
+    auto store_y = [&](const At& at) {
       if (lt == 0 && !sched.quiet) {
-        const Item it = item_of(stored);
-        tma_store_4d(&map_y, base + L::kOffV, it.tile * kM, it.h, stored.c * kC, (int)it.b);
+        tma_store_4d(&map_y, base + L::kOffV, at.tile * kM, at.h, at.t, at.b);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       }
       // the other path's element-wise loads write there next
       if (!vec_v) named_barrier(4, kLoadThreads);
-      stored.next(sched, n_all);
     };
     // a row of four values that 16-byte accesses reach
     const bool wide_kq = g.dk % 4 == 0 && g.ld_k % 4 == 0 && g.ld_q % 4 == 0 &&
                          ((reinterpret_cast<uintptr_t>(g.k) | reinterpret_cast<uintptr_t>(g.q)) & 15) == 0;
-    // a chunk's f32 rows, which are read element-wise, to the second-level cache: the
-    // reads then take a third of the time, and the chunk before hides the rest
-    auto prefetch = [&](const Cursor& k) {
-      const Item it = item_of(k);
-      const int rows = tokens_of(k), cols = g.dv - it.tile * kM < kM ? g.dv - it.tile * kM : kM;
-      const int64_t row = it.b * g.T + (int64_t)k.c * kC;
+    // A chunk's rows to the second-level cache, ahead of their load: f32 rows, which are
+    // read element-wise, come in a third of the time (30.4 us a chunk without), and CTAs
+    // at different chunks, whose rows share no pages, wait _PFA_ us a chunk less.
+    auto prefetch = [&](const At& at) {
+      if (!F32) {
+        if (lt == 0 && vec_kq) {
+#pragma unroll
+          for (int kb = 0; kb < L::kBlocks; ++kb) {
+            tma_prefetch_4d(&map_k, 64 * kb, at.hk, at.t, at.b);
+            tma_prefetch_4d(&map_q, 64 * kb, at.hk, at.t, at.b);
+          }
+        }
+        if (lt == 0 && vec_v) tma_prefetch_4d(&map_v, at.tile * kM, at.h, at.t, at.b);
+        return;
+      }
+      const int rows = g.T - at.t < kC ? (int)(g.T - at.t) : kC, cols = g.dv - at.tile * kM < kM ? g.dv - at.tile * kM : kM;
+      const int64_t row = at.b * g.T + at.t;
       auto lines = [&](const void* p, int64_t ld, int n) {
         const float* first = reinterpret_cast<const float*>(p) + row * ld;
         for (int e = lt; e < 4 * rows; e += kLoadThreads)
           if (32 * (e & 3) < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(first + (e / 4) * ld + 32 * (e & 3)));
       };
-      lines(reinterpret_cast<const float*>(g.k) + (int64_t)it.hk * g.dk, g.ld_k, g.dk);
-      lines(reinterpret_cast<const float*>(g.q) + (int64_t)it.hk * g.dk, g.ld_q, g.dk);
-      lines(reinterpret_cast<const float*>(g.v) + (int64_t)it.h * g.dv + it.tile * kM, g.ld_v, cols);
+      lines(reinterpret_cast<const float*>(g.k) + (int64_t)at.hk * g.dk, g.ld_k, g.dk);
+      lines(reinterpret_cast<const float*>(g.q) + (int64_t)at.hk * g.dk, g.ld_q, g.dk);
+      lines(reinterpret_cast<const float*>(g.v) + (int64_t)at.h * g.dv + at.tile * kM, g.ld_v, cols);
     };
-    // the keys and queries of chunk c, the cursor's
-    auto load_kq = [&](int c) {
+    // the keys and queries of chunk c
+    auto load_kq = [&](int c, const At& at) {
       const int ks = c % L::kKqStages;
-      const Item it = item_of(at_kq);
-      const int left = tokens_of(at_kq), t0 = at_kq.c * kC;
-      const In* k_base = reinterpret_cast<const In*>(g.k) + (it.b * g.T + t0) * g.ld_k + (int64_t)it.hk * g.dk;
-      const In* q_base = reinterpret_cast<const In*>(g.q) + (it.b * g.T + t0) * g.ld_q + (int64_t)it.hk * g.dk;
       const uint32_t kq = base + ks * L::kKq;
-      if (F32 && c == 0) prefetch(at_kq);
       if (c >= L::kKqStages) wait_counted(kq_empty + 8 * ks, c / L::kKqStages + 1);
-      at_kq.next(sched, n_all);
-      if (F32 && c + 1 < n_chunks) prefetch(at_kq);
       if (vec_kq) {
         // tokens past the end and components past dk read as zero
         if (lt == 0) {
           mbar_arrive_expect_tx(kq_full + 8 * ks, L::kKqTerm);
 #pragma unroll
           for (int kb = 0; kb < L::kBlocks; ++kb) {
-            tma_load_4d(kq + kb * 16384, &map_k, 64 * kb, it.hk, t0, (int)it.b, kq_full + 8 * ks);
-            tma_load_4d(kq + kb * 16384 + 8192, &map_q, 64 * kb, it.hk, t0, (int)it.b, kq_full + 8 * ks);
+            tma_load_4d(kq + kb * 16384, &map_k, 64 * kb, at.hk, at.t, at.b, kq_full + 8 * ks);
+            tma_load_4d(kq + kb * 16384 + 8192, &map_q, 64 * kb, at.hk, at.t, at.b, kq_full + 8 * ks);
           }
         }
       } else {
         // by hand, eight components of a row at a time, kBatch of these in flight per
         // thread: K rows 0-63, Q 64-127; granule q of row r at q ^ (r % 8)
         constexpr int kBatch = 4;
+        const int left = g.T - at.t < kC ? (int)(g.T - at.t) : kC;
+        const In* k_base = reinterpret_cast<const In*>(g.k) + (at.b * g.T + at.t) * g.ld_k + (int64_t)at.hk * g.dk;
+        const In* q_base = reinterpret_cast<const In*>(g.q) + (at.b * g.T + at.t) * g.ld_q + (int64_t)at.hk * g.dk;
 #pragma unroll 1
         for (int e0 = lt; e0 < 2 * kC * (DK / 8); e0 += kBatch * kLoadThreads) {
           float f[kBatch][8];
@@ -1344,13 +1371,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
             const int e = e0 + u * kLoadThreads, r = e / (DK / 8), col = e % (DK / 8) * 8;
-            const uint32_t at = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
+            const uint32_t dst = kq + (uint32_t)((col / 64) * 16384 + r * 128 + ((((col & 63) / 8) ^ (r & 7)) << 4));
             uint32_t x[3][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split3n(f[u][2 * j], f[u][2 * j + 1], x[0][j], x[1][j], x[2][j]);
 #pragma unroll
             for (int p = 0; p < L::kTerms; ++p)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + p * L::kKqTerm), "r"(x[p][0]), "r"(x[p][1]),
                            "r"(x[p][2]), "r"(x[p][3])
                            : "memory");
           }
@@ -1359,24 +1386,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         mbar_arrive(kq_full + 8 * ks);
       }
     };
-    load_kq(0);
-    for (int c = 0; c < n_chunks; ++c) {
+    At here = {}, before = {}, two_before = {};
+    place();
+    prefetch(next);
+#pragma unroll 1
+    for (int c = -1; c < n_chunks; ++c) {
       // a chunk ahead of the values, whose place is free later
-      if (c + 1 < n_chunks) load_kq(c + 1);
+      const At after = next;
+      if (c + 1 < n_chunks) load_kq(c + 1, after);
+      if (c + 2 < n_chunks) {
+        place();
+        prefetch(next);
+      }
       // V (bf16); tokens past the sequence's end and components past dv are zero
-      if (!F32) {
-        const Item it = item_of(at_chunk);
-        const int left = tokens_of(at_chunk), t0 = at_chunk.c * kC;
-        const In* v_base = reinterpret_cast<const In*>(g.v) + (it.b * g.T + t0) * g.ld_v + (int64_t)it.h * g.dv + it.tile * kM;
+      if (!F32 && c >= 0) {
         if (c > 0) wait_counted(v_empty, c - 1);
-        if (vec_y && c > 1) store_y();
+        if (vec_y && c > 1) store_y(two_before);
         if (vec_v) {
           if (lt == 0) {
             mbar_arrive_expect_tx(v_full, kC * kM * 2);
-            tma_load_4d(base + L::kOffV, &map_v, it.tile * kM, it.h, t0, (int)it.b, v_full);
+            tma_load_4d(base + L::kOffV, &map_v, here.tile * kM, here.h, here.t, here.b, v_full);
           }
         } else {
-          const int cols = g.dv - it.tile * kM < kM ? g.dv - it.tile * kM : kM;
+          const int left = g.T - here.t < kC ? (int)(g.T - here.t) : kC;
+          const int cols = g.dv - here.tile * kM < kM ? g.dv - here.tile * kM : kM;
+          const In* v_base = reinterpret_cast<const In*>(g.v) + (here.b * g.T + here.t) * g.ld_v + (int64_t)here.h * g.dv + here.tile * kM;
           In* v_dst = reinterpret_cast<In*>(gbase + L::kOffV);
 #pragma unroll 4
           for (int e = lt; e < kC * kM; e += kLoadThreads) {
@@ -1385,15 +1419,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           }
           mbar_arrive(v_full);
         }
-        at_chunk.next(sched, n_all);
       }
+      two_before = before, before = here, here = after;
     }
     if (!F32) {  // the last two chunks' outputs
       wait_counted(v_empty, n_chunks - 1);
-      if (vec_y && n_chunks > 1) store_y();
+      if (vec_y && n_chunks > 1) store_y(two_before);
       if (!vec_v || lt == 0) mbar_arrive(v_full);
       wait_counted(v_empty, n_chunks);
-      if (vec_y) store_y();
+      if (vec_y) store_y(before);
       if (lt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
@@ -1567,10 +1601,13 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
 // The layout of a call over `sms` SMs, and the scratch that it wants; with less
 // (ws_bytes) items are not cut.  Returns the CTAs of a kWide launch.
 //
-// An item's chunk takes ~5.4 us, a join's step ~3 us.  Cutting few items into P
-// parts makes n chunks in a row 2 n / P and P - 2 joins, if the parts' CTAs and the
-// maps' fit the SMs: 16 heads of 256 chunks 1380 us whole, 6 parts _LONG_ us.
-constexpr double kChunkUs = 5.8, kJoinUs = 4.0, kPartsUs = 30.0;
+// A launch takes ~12.5 us before its second chunk (the first chunk's own chain from
+// the keys' load to the output), then 4.3 us a chunk with few CTAs and 5.3 with all
+// SMs busy; the join 3 us and 4 a step.  Cutting few items into P parts makes n chunks
+// in a row 2 n / P in two launches and P - 2 join steps, if the parts' CTAs and the
+// maps' fit the SMs: 12 heads of 64 chunks _P64_ us in parts, _W64_ whole; of 16
+// chunks _P16_ and _W16_; of 8 chunks whole, _W8_.
+constexpr double kStartUs = 12.5, kFewUs = 4.6, kFullUs = 5.0, kJoinStartUs = 3, kJoinUs = 4;
 int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
   *p = Plan{};
   p->n_chunks = (int)((a.T + kC - 1) / kC);
@@ -1579,7 +1616,11 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
   p->items = (int)items;
   *want = 0;
   auto round256 = [](int64_t b) { return (b + 255) / 256 * 256; };
-  if (items > sms && items % sms) {
+  // Whole items leave the SMs of the last round idle; cut, they cost the states' way
+  // from CTA to CTA and chunks that share no pages.  4096 tokens: 320 items 794 us cut,
+  // 895 whole; 224 items 610 and 636; 240 items 636 and 637.
+  const int64_t rounds = (items + sms - 1) / sms;
+  if (items > sms && rounds * sms * 10 > items * 13) {
     const int64_t states = (int64_t)sms * kM * a.dk * 4;
     *want = round256(states) + round256(sms * (int64_t)sizeof(int));
     if (ws && ws_bytes >= *want) {
@@ -1589,12 +1630,13 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
     }
     return p->items;
   }
+  if (items > sms) return p->items;
   int best = 1;
-  double best_us = 0.9 * kChunkUs * p->n_chunks;  // worth three launches for a tenth
+  double best_us = 0.9 * (kStartUs + kFewUs * p->n_chunks);  // worth three launches for a tenth
   for (int parts = 3; parts <= p->n_chunks && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
     const int len = (p->n_chunks + parts - 1) / parts;
     if ((parts - 1) * len >= p->n_chunks) continue;  // the last part would be empty
-    const double us = 2 * kChunkUs * len + kJoinUs * (parts - 2) + kPartsUs;
+    const double us = 2 * (kStartUs + kFullUs * len) + kJoinStartUs + kJoinUs * (parts - 2);
     if (us < best_us) best = parts, best_us = us;
   }
   if (best > 1) {
