@@ -516,9 +516,11 @@ MAMBA_API int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, cons
                                         int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
                                         void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Scratch bytes with which mamba_gated_delta_prefill spreads a long prefill of
- * few heads over every SM of the current device (0: it needs none); negative on
- * an error. */
+/* Scratch bytes with which mamba_gated_delta_prefill spreads its work evenly over
+ * the SMs of the current device: a long prefill of few heads, or more heads than
+ * SMs (0: it needs none); negative on an error.  A workspace is 16-byte aligned;
+ * with less than these bytes the call runs whole heads, with the same results up
+ * to rounding. */
 MAMBA_API int64_t mamba_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk,
                                                     int64_t dv, int in_dtype);
 
