@@ -31,12 +31,18 @@
 //
 // Precision: f32 operands are the sum of three bf16 terms (24 bits, f32's range,
 // so no scaling and no look at the data), bf16 keys and queries one.  Of the nine
-// products of two such sums the six above 2^-24 are taken.  Two f16 halves with
-// power-of-two scales hold 22 bits for fewer products, but finding the scales
-// (maxima over lanes and rows, the keys converted) took twice the instructions,
-// and instructions are what bounds a chunk: 10.3 thousand cycles against _CYC_.
-// The output of bf16 tensors, which feeds back into nothing, takes the products
-// above 2^-16 alone.
+// products of two such sums the six above 2^-24 are taken.  (Two f16 halves with
+// power-of-two scales hold 22 bits for fewer products, but finding the scales,
+// maxima over lanes and rows, took twice the instructions.)  The output of bf16
+// tensors, which feeds back into nothing, takes the products above 2^-16 alone.
+//
+// Bound: neither HBM (40 KB and 1.5 us of tensor-core time a chunk) nor the tensor
+// cores but the instructions of the epilogues and of T, on a chain of dependent
+// steps.  A chunk of 128 x 128 takes 4.95 us (10.2 thousand cycles) with at most one
+// busy SM of each pair and 5.4-5.8 with all: the loops of all roles are larger than
+// the instruction cache, which is shared in pairs.  So roles keep no more code than
+// they need (one lookup per item, short waits, sums by a product with the identity)
+// and no spills: each of these took 3 to 8 % off a chunk.
 //
 // An item is a (sequence, value head, 128 value components); its chunks follow one
 // another.  How items and their chunks are laid over the SMs: see Plan.  A CTA's
@@ -404,12 +410,15 @@ __device__ __forceinline__ constexpr void term_pair(int i, int& a, int& b) {
   }
 }
 
-template <int DK, bool F32>
+// MAPS: q, k and v come through tensor maps (bf16, dk a multiple of 8) and the states
+// are 16-byte aligned.  A kernel of its own, so that the loops of the other loads do
+// not lie between its own.
+template <int DK, bool F32, bool MAPS>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ CUtensorMap map_v,
-                                                            const __grid_constant__ CUtensorMap map_y, int vec_kq,
-                                                            int vec_v, int vec_y, const Plan plan) {
+                                                            const __grid_constant__ CUtensorMap map_y, int vec_y,
+                                                            const Plan plan) {
   using L = Smem<DK, F32>;
   using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
   extern __shared__ unsigned char smem_raw[];
@@ -449,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   auto tokens_of = [&](const Cursor& k) { return (int)(g.T - (int64_t)k.c * kC < kC ? g.T - (int64_t)k.c * kC : kC); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, vec_kq ? 1 : kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
+    for (int s = 0; s < L::kKqStages; ++s) mbar_init(kq_full + 8 * s, MAPS ? 1 : kLoadThreads), mbar_init(kq_empty + 8 * s, 1);
     for (int s = 0; s < kGateSlots; ++s) mbar_init(gate_full + 8 * s, 32), mbar_init(gate_empty + 8 * s, kMainWarps + kGroupWarps);
-    mbar_init(v_full, vec_v ? 1 : kLoadThreads), mbar_init(v_empty, kMainWarps);
+    mbar_init(v_full, MAPS ? 1 : kLoadThreads), mbar_init(v_empty, kMainWarps);
     mbar_init(t_full, kGroupWarps), mbar_init(o_empty, kMainWarps);
     for (int s = 0; s < 2; ++s) mbar_init(t_empty + 8 * s, 1), mbar_init(d0_full + 8 * s, 1), mbar_init(d0_empty + 8 * s, kGroupWarps);
     for (int s = 0; s < L::kPBuffers; ++s) mbar_init(p_full + 8 * s, kGroupWarps / 2), mbar_init(p_empty + 8 * s, 1);
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
       }
     };
-    auto vec_state = [&](const float* p) { return g.dk % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    auto vec_state = [&](const float* p) { return MAPS || (g.dk % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0); };
     const int64_t all_states = g.B * g.Hv * (int64_t)g.dv * g.dk;
     // the state before the chunk's piece
     auto enter = [&](const Gates& k) {
@@ -571,20 +580,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       const int n = k.tile * kM + lane_n;
       const int64_t row = ((int64_t)k.bh * g.dv + n) * g.dk;
       const int p = plan.mode == kWide ? 0 : k.begin / plan.part_len;
-      if (k.phi) {
-        float* dst = plan.phi + (((p - 1) * g.B * g.Hv + k.bh) * g.dk + lane_n) * g.dk;
-        if (lane_n < g.dk) store_state(dst, vec_state(dst));
-      } else if (plan.mode == kAheadPass) {
-        float* dst = plan.states + p * all_states + row;
-        if (n < g.dv) store_state(dst, vec_state(dst));
-      } else if (k.end < n_all && plan.mode == kWide) {
-        store_state(plan.states + ((int64_t)blockIdx.x * kM + lane_n) * g.dk, vec_state(plan.states));
+      const bool hand_over = k.end < n_all && plan.mode == kWide;
+      float* dst = n < g.dv ? g.state_out : nullptr;
+      if (dst) dst += row;
+      if (hand_over)
+        dst = plan.states + ((int64_t)blockIdx.x * kM + lane_n) * g.dk;
+      else if (k.phi)
+        dst = lane_n < g.dk ? plan.phi + (((p - 1) * g.B * g.Hv + k.bh) * g.dk + lane_n) * g.dk : nullptr;
+      else if (plan.mode == kAheadPass)
+        dst = n < g.dv ? plan.states + p * all_states + row : nullptr;
+      else if (k.end < n_all)
+        dst = nullptr;
+      if (dst) store_state(dst, vec_state(dst));
+      if (hand_over) {
         __threadfence();
         named_barrier(5, 32 * kMainWarps);
         if (threadIdx.x == 0) atomicExch(plan.flags + blockIdx.x, 1);
-      } else if (k.end == n_all && g.state_out) {
-        float* dst = g.state_out + row;
-        if (n < g.dv) store_state(dst, vec_state(dst));
       }
     };
     const int i0 = part * kTok;  // this thread's tokens of a chunk
@@ -1296,24 +1307,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       }
       // the other path's element-wise loads write there next
-      if (!vec_v) named_barrier(4, kLoadThreads);
+      if (!MAPS) named_barrier(4, kLoadThreads);
     };
     // a row of four values that 16-byte accesses reach
     const bool wide_kq = g.dk % 4 == 0 && g.ld_k % 4 == 0 && g.ld_q % 4 == 0 &&
                          ((reinterpret_cast<uintptr_t>(g.k) | reinterpret_cast<uintptr_t>(g.q)) & 15) == 0;
     // A chunk's rows to the second-level cache, ahead of their load: f32 rows, which are
     // read element-wise, come in a third of the time (30.4 us a chunk without), and CTAs
-    // at different chunks, whose rows share no pages, wait _PFA_ us a chunk less.
+    // at different chunks, whose rows share no pages, take 5.9 us a chunk instead of 6.5.
     auto prefetch = [&](const At& at) {
       if (!F32) {
-        if (lt == 0 && vec_kq) {
+        if (lt == 0 && MAPS) {
 #pragma unroll
           for (int kb = 0; kb < L::kBlocks; ++kb) {
             tma_prefetch_4d(&map_k, 64 * kb, at.hk, at.t, at.b);
             tma_prefetch_4d(&map_q, 64 * kb, at.hk, at.t, at.b);
           }
         }
-        if (lt == 0 && vec_v) tma_prefetch_4d(&map_v, at.tile * kM, at.h, at.t, at.b);
+        if (lt == 0 && MAPS) tma_prefetch_4d(&map_v, at.tile * kM, at.h, at.t, at.b);
         return;
       }
       const int rows = g.T - at.t < kC ? (int)(g.T - at.t) : kC, cols = g.dv - at.tile * kM < kM ? g.dv - at.tile * kM : kM;
@@ -1332,7 +1343,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       const int ks = c % L::kKqStages;
       const uint32_t kq = base + ks * L::kKq;
       if (c >= L::kKqStages) wait_counted(kq_empty + 8 * ks, c / L::kKqStages + 1);
-      if (vec_kq) {
+      if (MAPS) {
         // tokens past the end and components past dk read as zero
         if (lt == 0) {
           mbar_arrive_expect_tx(kq_full + 8 * ks, L::kKqTerm);
@@ -1402,7 +1413,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (!F32 && c >= 0) {
         if (c > 0) wait_counted(v_empty, c - 1);
         if (vec_y && c > 1) store_y(two_before);
-        if (vec_v) {
+        if (MAPS) {
           if (lt == 0) {
             mbar_arrive_expect_tx(v_full, kC * kM * 2);
             tma_load_4d(base + L::kOffV, &map_v, here.tile * kM, here.h, here.t, here.b, v_full);
@@ -1425,7 +1436,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     if (!F32) {  // the last two chunks' outputs
       wait_counted(v_empty, n_chunks - 1);
       if (vec_y && n_chunks > 1) store_y(two_before);
-      if (!vec_v || lt == 0) mbar_arrive(v_full);
+      if (!MAPS || lt == 0) mbar_arrive(v_full);
       wait_counted(v_empty, n_chunks);
       if (vec_y) store_y(before);
       if (lt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -1558,9 +1569,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(float* states, const
   }
 }
 
-template <int DK, bool F32>
-cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cudaStream_t stream) {
-  auto kern = chunk_kernel<DK, F32>;
+struct Maps {
+  CUtensorMap k, q, v, y;
+  bool inputs, y_too;  // which there are
+};
+
+template <int DK, bool F32, bool MAPS>
+cudaError_t launch_chunk(const GatedDeltaArgs& a, const Maps& maps, const Plan& plan, int ctas, cudaStream_t stream) {
+  auto kern = chunk_kernel<DK, F32, MAPS>;
   constexpr int smem = Smem<DK, F32>::kAlloc;
   static int configured[64];
   int dev = 0;
@@ -1573,15 +1589,8 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
       return e;
     __atomic_store_n(&configured[dev], 1, __ATOMIC_RELAXED);
   }
-  CUtensorMap mk = {}, mq = {}, mv = {}, my = {};
-  int vec_kq = 0, vec_v = 0, vec_y = 0;
-  if (!F32) {
-    vec_kq = make_map_heads(&mk, a.k, a.B, a.T, a.Hk, a.dk, a.ld_k) && make_map_heads(&mq, a.q, a.B, a.T, a.Hk, a.dk, a.ld_q);
-    vec_v = make_map_heads(&mv, a.v, a.B, a.T, a.Hv, a.dv, a.ld_v, kM);
-    vec_y = a.y_bf16 && make_map_heads(&my, a.y, a.B, a.T, a.Hv, a.dv, a.ld_y, kM);
-  }
   auto launch = [&](const Plan& plan, int ctas) {
-    kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, mk, mq, mv, my, vec_kq, vec_v, vec_y, plan);
+    kern<<<(unsigned)ctas, kThreads, smem, stream>>>(a, maps.k, maps.q, maps.v, maps.y, maps.y_too, plan);
     return cudaGetLastError();
   };
   if (plan.mode == kWide) {
@@ -1605,8 +1614,8 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Plan& plan, int ctas, cu
 // the keys' load to the output), then 4.3 us a chunk with few CTAs and 5.3 with all
 // SMs busy; the join 3 us and 4 a step.  Cutting few items into P parts makes n chunks
 // in a row 2 n / P in two launches and P - 2 join steps, if the parts' CTAs and the
-// maps' fit the SMs: 12 heads of 64 chunks _P64_ us in parts, _W64_ whole; of 16
-// chunks _P16_ and _W16_; of 8 chunks whole, _W8_.
+// maps' fit the SMs: 12 heads of 64 chunks 140 us in parts, 296 whole; of 16
+// chunks 71 and 86; 32 heads of 64 chunks 238 and 297.
 constexpr double kStartUs = 12.5, kFewUs = 4.6, kFullUs = 5.0, kJoinStartUs = 3, kJoinUs = 4;
 int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
   *p = Plan{};
@@ -1654,7 +1663,10 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
 
 }  // namespace
 
-// Items and chunk numbers, and output offsets inside a chunk, are 32 bits.
+// Up to 16 tokens go token by token: 40 heads of 16 tokens 18.6 us against 18.6 for
+// a chunk (8 tokens 10.5, 32 tokens 31.0 against 18.5); 8 heads 11.2 against 16.9 (32
+// tokens 18.7 and 16.8); 1024 heads 121 against 107 (12 tokens 94).  Items and chunk
+// numbers, and output offsets inside a chunk, are 32 bits.
 bool gated_delta_takes_chunks(const GatedDeltaArgs& a) {
   return a.dk <= 128 && a.T > 16 && a.ld_y < (int64_t(1) << 23) && a.T < (int64_t(1) << 30) &&
          a.B * a.Hv * ((a.dv + kM - 1) / kM) < (int64_t(1) << 30);
@@ -1673,8 +1685,21 @@ cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& 
   Plan plan;
   int64_t want = 0;
   const int ctas = make_plan(a, dev.sm_count, ws_bytes, static_cast<char*>(ws), &plan, &want);
-  if (a.dk <= 64) return a.in_bf16 ? launch_chunk<64, false>(a, plan, ctas, stream) : launch_chunk<64, true>(a, plan, ctas, stream);
-  return a.in_bf16 ? launch_chunk<128, false>(a, plan, ctas, stream) : launch_chunk<128, true>(a, plan, ctas, stream);
+  Maps maps = {};
+  if (!a.in_bf16) {
+    return a.dk <= 64 ? launch_chunk<64, true, false>(a, maps, plan, ctas, stream)
+                      : launch_chunk<128, true, false>(a, maps, plan, ctas, stream);
+  }
+  maps.inputs = make_map_heads(&maps.k, a.k, a.B, a.T, a.Hk, a.dk, a.ld_k) &&
+                make_map_heads(&maps.q, a.q, a.B, a.T, a.Hk, a.dk, a.ld_q) &&
+                make_map_heads(&maps.v, a.v, a.B, a.T, a.Hv, a.dv, a.ld_v, kM) &&
+                ((reinterpret_cast<uintptr_t>(a.state_in) | reinterpret_cast<uintptr_t>(a.state_out)) & 15) == 0;
+  maps.y_too = a.y_bf16 && make_map_heads(&maps.y, a.y, a.B, a.T, a.Hv, a.dv, a.ld_y, kM);
+  if (maps.inputs)
+    return a.dk <= 64 ? launch_chunk<64, false, true>(a, maps, plan, ctas, stream)
+                      : launch_chunk<128, false, true>(a, maps, plan, ctas, stream);
+  return a.dk <= 64 ? launch_chunk<64, false, false>(a, maps, plan, ctas, stream)
+                    : launch_chunk<128, false, false>(a, maps, plan, ctas, stream);
 }
 
 int read_delta_faults(bool clear) {
