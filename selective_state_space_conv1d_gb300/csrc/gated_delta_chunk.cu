@@ -121,7 +121,7 @@ struct Smem {
   static constexpr int kOffGates = kOffA + 2 * kC * kLdA * 4;
   static constexpr int kOffBar = kOffGates + kGateSlots * (int)sizeof(Gates);
   static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 12;
-  static constexpr int kBytes = kOffBar + 8 * kBars + 16;
+  static constexpr int kBytes = kOffBar + 8 * kBars + 64;  // and tensor memory's address, the abort flag, the schedule
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
   static_assert(kAlloc <= 232448, "shared memory over the opt-in limit");
@@ -442,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   const uint32_t x_full = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
+  Schedule& sched = *reinterpret_cast<Schedule*>(tmem_ptr + 2);
   Gates* gates = reinterpret_cast<Gates*>(gbase + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n_all = plan.n_chunks;
-  const int n_chunks = make_schedule(plan, (int)(g.B * g.Hv)).total;  // that this CTA runs
   struct Item {
     int tile, h, hk;
     int64_t b;
@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     *abort_flag = 0;
     mbar_fence_init();
   }
+  if (threadIdx.x == 32) sched = make_schedule(plan, (int)(g.B * g.Hv));
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_ptr)),
                  "r"(kTmemCols)
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *tmem_ptr;
+  const int n_chunks = sched.total;  // that this CTA runs
 
   // The gate, MMA and load warps' waits are counted; one that runs out sets the abort
   // flag, and every role then runs on through its loop without waiting, so that all
@@ -1062,43 +1064,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // tokens lane and lane + 32 of a chunk: base-2 logarithms of alpha, summed and
     // kept as two floats each, so that differences between far-decayed tokens keep
     // 32-bit accuracy.  alpha below e^-200 is 0 in f32 all the same.
-    float a_next[2], b_next[2], A_next, bias_next;
-    const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
+    float neg_A = 0.0f, dt_bias = 0.0f;
     Cursor at_chunk;
     at_chunk.start(sched, n_all);
     Item it = {};
     const In* a_base = nullptr;
     const In* b_base = nullptr;
-    auto fetch = [&]() {
+#pragma unroll 1
+    for (int c = 0; c < n_chunks; ++c) {
       if (at_chunk.c == at_chunk.begin) {
         it = item_of(at_chunk);
         a_base = reinterpret_cast<const In*>(g.a) + it.b * g.T * g.ld_a + it.h;
         b_base = reinterpret_cast<const In*>(g.b) + it.b * g.T * g.ld_b + it.h;
-        A_next = g.A_log[it.h];
-        bias_next = g.dt_bias ? g.dt_bias[it.h] : 0.0f;
+        neg_A = -expf(g.A_log[it.h]);
+        dt_bias = g.dt_bias ? g.dt_bias[it.h] : 0.0f;
       }
+      Two G[2];
+      float la[2], be[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t t = (int64_t)at_chunk.c * kC + lane + 32 * u;
-        a_next[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
-        b_next[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
+        la[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
+        be[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
       }
-    };
-    fetch();
-    for (int c = 0; c < n_chunks; ++c) {
-      Two G[2];
-      const float neg_A = -expf(A_next), dt_bias = bias_next;
-      float be[2];
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {  // once, then with the two tokens' places changed
+        const float l = gdr_log_alpha(la[0], dt_bias, neg_A), beta = gdr_beta(be[0]);
+        la[0] = la[1], be[0] = be[1];
+        la[1] = l, be[1] = beta;
+      }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float la = gdr_log_alpha(a_next[u], dt_bias, neg_A);
-        G[u] = two_log2(la < -200.0f ? -200.0f : la);
-        be[u] = gdr_beta(b_next[u]);
-      }
-      const Cursor here = at_chunk;
-      const int tile = it.tile, h = it.h, b = (int)it.b;
-      at_chunk.next(sched, n_all);
-      if (c + 1 < n_chunks) fetch();
+      for (int u = 0; u < 2; ++u) G[u] = two_log2(la[u] < -200.0f ? -200.0f : la[u]);
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
@@ -1125,10 +1121,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       gt.since[lane] = two_exp2(G[1], mid);
       if (lane == 0) {
         gt.total = ex2_approx(last.h + last.l);
-        gt.at = here.c, gt.begin = here.begin, gt.end = here.end, gt.tokens = tokens_of(here);
-        gt.tile = tile, gt.h = h, gt.b = b, gt.bh = b * g.Hv + h;
+        gt.at = at_chunk.c, gt.begin = at_chunk.begin, gt.end = at_chunk.end, gt.tokens = tokens_of(at_chunk);
+        gt.tile = it.tile, gt.h = it.h, gt.b = (int)it.b, gt.bh = (int)it.b * g.Hv + it.h;
         gt.phi = sched.phi, gt.quiet = sched.quiet;
       }
+      at_chunk.next(sched, n_all);
       mbar_arrive(gate_full + 8 * (c % kGateSlots));
     }
   } else if (warp == kMmaWarp) {
@@ -1280,7 +1277,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   } else {
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
-    const Schedule sched = make_schedule(plan, (int)(g.B * g.Hv));
     // A chunk's place in the tensors.  The cursor runs two chunks ahead of the values'
     // load: that chunk's rows are prefetched, the next one's keys and queries loaded,
     // this one's values, and the output of two before stored.
@@ -1626,10 +1622,10 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
   *want = 0;
   auto round256 = [](int64_t b) { return (b + 255) / 256 * 256; };
   // Whole items leave the SMs of the last round idle; cut, they cost the states' way
-  // from CTA to CTA and chunks that share no pages.  4096 tokens: 320 items 794 us cut,
-  // 895 whole; 224 items 610 and 636; 240 items 636 and 637.
+  // from CTA to CTA and chunks that share no pages.  4096 tokens: 320 items 719 us cut,
+  // 896 whole; 240 items 564 and 625, of 1024 tokens 175 and 177.
   const int64_t rounds = (items + sms - 1) / sms;
-  if (items > sms && rounds * sms * 10 > items * 13) {
+  if (items > sms && rounds * sms * 4 > items * 5) {
     const int64_t states = (int64_t)sms * kM * a.dk * 4;
     *want = round256(states) + round256(sms * (int64_t)sizeof(int));
     if (ws && ws_bytes >= *want) {
