@@ -38,8 +38,8 @@
 //
 // Bound: neither HBM (40 KB and 1.5 us of tensor-core time a chunk) nor the tensor
 // cores but the instructions of the epilogues and of T, on a chain of dependent
-// steps.  A chunk of 128 x 128 takes 4.95 us (10.2 thousand cycles) with at most one
-// busy SM of each pair and 5.4-5.8 with all: the loops of all roles are larger than
+// steps.  A chunk of 128 x 128 takes 4.9 us (10.1 thousand cycles) with at most one
+// busy SM of each pair and 5.4 with all: the loops of all roles are larger than
 // the instruction cache, which is shared in pairs.  So roles keep no more code than
 // they need (one lookup per item, short waits, sums by a product with the identity)
 // and no spills: each of these took 3 to 8 % off a chunk.
@@ -1310,7 +1310,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
                          ((reinterpret_cast<uintptr_t>(g.k) | reinterpret_cast<uintptr_t>(g.q)) & 15) == 0;
     // A chunk's rows to the second-level cache, ahead of their load: f32 rows, which are
     // read element-wise, come in a third of the time (30.4 us a chunk without), and CTAs
-    // at different chunks, whose rows share no pages, take 5.9 us a chunk instead of 6.5.
+    // at different chunks, whose rows share no pages, took 5.9 us a chunk
+    // instead of 6.5.
     auto prefetch = [&](const At& at) {
       if (!F32) {
         if (lt == 0 && MAPS) {
