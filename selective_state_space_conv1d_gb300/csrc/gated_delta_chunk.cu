@@ -98,7 +98,7 @@ struct Gates {
   int at, begin, end;       // its number in the sequence, and those of the piece run here
   int tile, h, b, bh;       // the item
   int tokens;               // of the chunk inside the sequence
-  int phi, quiet, pad;      // the schedule's
+  int phi, pad[2];          // the schedule's
 };
 
 template <int DK, bool F32>
@@ -136,11 +136,11 @@ struct Smem {
 //  Few items, long sequences: each is cut into `parts` of equal length, for which
 //  three launches are made.
 //  kAheadPass: the state at the end of every part but the last, the first part from
-//    state_in (with its output), the others from zero; and, as one more item per
-//    head, the part's linear map Phi of the state before it (the same recurrence
-//    with values of zero, from the identity).
+//    state_in, the others from zero; and, as one more item per head, the part's linear
+//    map Phi of the state before it (the same recurrence with values of zero, from the
+//    identity).  Nothing of the output is computed.
 //  (join_kernel: state before part p + 1 = (state before part p) Phi_p + that.)
-//  kPartsPass: the parts but the first again, from their states, with their output.
+//  kPartsPass: all parts again, from their states, with their output.
 enum { kWide = 0, kAheadPass = 1, kPartsPass = 2 };
 struct Plan {
   int mode;
@@ -148,6 +148,7 @@ struct Plan {
   int tiles, items;  // of 128 value components; B Hv tiles
   int parts, part_len;
   float* states;     // kWide: [CTA][128][dk]; else [parts - 1][B Hv][dv][dk], the state before parts 1 ..
+  float* first;      // [B Hv][dv][dk], state_in: state_out, which may lie over it, is written before all have read it
   float* phi;        // [parts - 2][B Hv][dk][dk], of parts 1 ..
   int* flags;        // kWide: [CTA], set when its state is there
 };
@@ -174,15 +175,15 @@ __device__ __forceinline__ Schedule make_schedule(const Plan& p, int heads) {
       if (lo_c > 0) s.t_item = first, s.t_begin = lo_c, s.t_len = n - lo_c;
     }
   } else {
-    const int values = p.items * (p.parts - 1);  // CTAs that run values; the others run Phi
+    s.quiet = p.mode == kAheadPass;
+    const int values = p.items * (p.parts - s.quiet);  // CTAs that run values; the others run Phi
     int i = (int)blockIdx.x, part;
     if (i < values) {
-      s.t_item = i % p.items, part = i / p.items + (p.mode == kPartsPass);
-      s.quiet = p.mode == kAheadPass && part > 0;
+      s.t_item = i % p.items, part = i / p.items;
     } else {
       i -= values;
       s.t_item = i % heads * p.tiles, part = 1 + i / heads;
-      s.phi = s.quiet = true;
+      s.phi = true;
     }
     s.t_begin = part * p.part_len;
     s.t_len = n - s.t_begin < p.part_len ? n - s.t_begin : p.part_len;
@@ -573,9 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       } else if (plan.mode == kAheadPass && k.begin > 0) {
         src = nullptr;
       } else if (plan.mode == kPartsPass) {
-        src = plan.states + (k.begin / plan.part_len - 1) * all_states + row;
+        if (k.begin > 0)
+          src = plan.states + (k.begin / plan.part_len - 1) * all_states + row;
+        else if (src)
+          src = plan.first + row;
       }
       load_state(n < g.dv ? src : nullptr, vec_state(src));
+      if (plan.mode == kAheadPass && src && n < g.dv) store_state(plan.first + row, vec_state(plan.first));
     };
     // and after it
     auto leave = [&](const Gates& k) {
@@ -612,14 +617,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // the path from state to state does not wait for it
     auto output = [&](int c) {
       const Gates& gt = gates[c % kGateSlots];
+      const bool quiet = sched.quiet;
       const bool direct = F32 || !vec_y;
       char* y_at = nullptr;
       int y_rows = 0;
-      if (direct) {
+      if (direct && !quiet) {
         const int n = gt.tile * kM + lane_n;
         y_at = reinterpret_cast<char*>(g.y) +
                ((gt.b * g.T + (int64_t)gt.at * kC + i0) * g.ld_y + (int64_t)gt.h * g.dv + n) * (g.y_bf16 ? 2 : 4);
-        y_rows = n < g.dv && !gt.quiet ? gt.tokens - i0 : 0;
+        y_rows = n < g.dv ? gt.tokens - i0 : 0;
       }
       wait(o_full, c);
       tcgen05_fence_after();
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       // stored from here
       __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(gbase + L::kOffV) + i0 * kM + lane_n;
 #pragma unroll 1
-      for (int i = 0; i < kTok; i += 8) {
+      for (int i = quiet ? kTok : 0; i < kTok; i += 8) {
         uint32_t xq[8], xo[8];
         tmem_ld8(t_lane + kColQ + (uint32_t)(i0 + i), xq);
         tmem_ld8(t_lane + kColO + (uint32_t)(i0 + i), xo);
@@ -772,17 +778,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           tmem_st4(t_lane + kColThird + (uint32_t)(8 * part + j0), t2);
         }
         arrive(w_ready + half);
-        uint32_t t0[8], t1[8], t2[8];
+        if (!sched.quiet) {
+          uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (F32)
-            split3n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
-          else
-            split2n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
+          for (int j = 0; j < 8; ++j) {
+            if (F32)
+              split3n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
+            else
+              split2n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
+          }
+          tmem_st8(t_lane + kColU + (uint32_t)i0, t0);
+          tmem_st8(t_lane + kColU + (uint32_t)(i0 + 8), t1);
+          if (F32) tmem_st8(t_lane + kColU3 + (uint32_t)(8 * part), t2);
         }
-        tmem_st8(t_lane + kColU + (uint32_t)i0, t0);
-        tmem_st8(t_lane + kColU + (uint32_t)(i0 + 8), t1);
-        if (F32) tmem_st8(t_lane + kColU3 + (uint32_t)(8 * part), t2);
         arrive(u_ready);
       }
       {  // epilogue 3: S = e^G S + D3
@@ -861,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       wait(d0_full + 8 * group, c / 2);
       tcgen05_fence_after();
       named_barrier(bar_id, kGroupThreads);  // the previous chunk's blocks are read
-      {
+      if (is_t || !sched.quiet) {
         // a row per thread: -A in f32, P in its terms (granule q of row r at
         // q ^ (r % 8))
         const int pb = c % L::kPBuffers;
@@ -1123,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         gt.total = ex2_approx(last.h + last.l);
         gt.at = at_chunk.c, gt.begin = at_chunk.begin, gt.end = at_chunk.end, gt.tokens = tokens_of(at_chunk);
         gt.tile = it.tile, gt.h = it.h, gt.b = (int)it.b, gt.bh = (int)it.b * g.Hv + it.h;
-        gt.phi = sched.phi, gt.quiet = sched.quiet;
+        gt.phi = sched.phi;
       }
       at_chunk.next(sched, n_all);
       mbar_arrive(gate_full + 8 * (c % kGateSlots));
@@ -1133,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     // The whole warp runs the loop, so that descriptors stay uniform, and one
     // elected lane issues: by a lane of a branch of its own a product took 50
     // cycles to issue and 32 to run.
-    const bool elected = elect_one();
+    const bool elected = elect_one(), quiet = sched.quiet;
     constexpr uint32_t id64 = idesc_bf16(64, false);
     // D3 in two halves of its columns, where each is a block of K
     constexpr int kHalves = DK / 64;
@@ -1194,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
       if (F32) {  // S's third terms make room for the decayed U's
         if (c > 0) wait_counted(o_empty, c - 1);
-        issue_d1(c, 1, 0, DK / 16);
+        if (!quiet) issue_d1(c, 1, 0, DK / 16);
       }
       wait_counted(t_full, c);
       // D2 = R T^T.  T is lower triangular: 16 tokens of the contraction reach the
@@ -1221,7 +1229,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (!F32) {  // the queries' product, under epilogue 2
         if (c > 0) wait_counted(o_empty, c - 1);
         tcgen05_fence_after();
-        issue_d1(c, 1, 0, DK / 16);
+        if (!quiet) issue_d1(c, 1, 0, DK / 16);
       }
       // D3 = U K; K's rows are the contraction
       const uint64_t kq_mn = kq0_mn + (uint64_t)((c % L::kKqStages) * (L::kKq / 16));
@@ -1253,16 +1261,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       wait_counted(u_ready, c);
       tcgen05_fence_after();
       const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
+      if (!quiet) {
 #pragma unroll
-      for (int p = kSkipP; p < 6; ++p) {
-        int ta = 0, tb = 0;
-        term_pair<true>(p, ta, tb);
+        for (int p = kSkipP; p < 6; ++p) {
+          int ta = 0, tb = 0;
+          term_pair<true>(p, ta, tb);
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
-          if (elected)
-            mma_ts(tmem + kColO + 16 * k, tmem + ad, pd + tb * 512 + 130 * k,
-                   idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > kSkipP || k > 0);
+          for (int k = 0; k < kC / 16; ++k) {
+            const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
+            if (elected)
+              mma_ts(tmem + kColO + 16 * k, tmem + ad, pd + tb * 512 + 130 * k,
+                     idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > kSkipP || k > 0);
+          }
         }
       }
       commit(o_full);
@@ -1601,19 +1611,19 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Maps& maps, const Plan& 
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   Plan second = plan;
   second.mode = kPartsPass;
-  return launch(second, plan.items * (plan.parts - 1));
+  return launch(second, plan.items * plan.parts);
 }
 
 // The layout of a call over `sms` SMs, and the scratch that it wants; with less
 // (ws_bytes) items are not cut.  Returns the CTAs of a kWide launch.
 //
 // A launch takes ~12.5 us before its second chunk (the first chunk's own chain from
-// the keys' load to the output), then 4.3 us a chunk with few CTAs and 5.3 with all
-// SMs busy; the join 3 us and 4 a step.  Cutting few items into P parts makes n chunks
-// in a row 2 n / P in two launches and P - 2 join steps, if the parts' CTAs and the
-// maps' fit the SMs: 12 heads of 64 chunks 140 us in parts, 296 whole; of 16
-// chunks 71 and 86; 32 heads of 64 chunks 238 and 297.
-constexpr double kStartUs = 12.5, kFewUs = 4.6, kFullUs = 5.0, kJoinStartUs = 3, kJoinUs = 4;
+// the keys' load to the output), then 4.6 us a chunk with few CTAs, 5.0 with most SMs
+// busy and 4.2 without output; the join 3 us and 4 a step.  Cutting few items into P
+// parts makes n chunks in a row n / P in each of two launches and P - 2 join steps, if
+// the parts' CTAs and the maps' fit the SMs: 12 heads of 64 chunks 128 us in parts,
+// 292 whole; of 16 chunks 66 and 83; 48 heads of 64 chunks 247 and 297.
+constexpr double kStartUs = 12.5, kFewUs = 4.6, kFullUs = 5.0, kQuietUs = 4.2, kJoinStartUs = 3, kJoinUs = 4;
 int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
   *p = Plan{};
   p->n_chunks = (int)((a.T + kC - 1) / kC);
@@ -1639,20 +1649,22 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
   if (items > sms) return p->items;
   int best = 1;
   double best_us = 0.9 * (kStartUs + kFewUs * p->n_chunks);  // worth three launches for a tenth
-  for (int parts = 3; parts <= p->n_chunks && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
+  for (int parts = 3; parts <= p->n_chunks && items * parts <= sms && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
     const int len = (p->n_chunks + parts - 1) / parts;
     if ((parts - 1) * len >= p->n_chunks) continue;  // the last part would be empty
-    const double us = 2 * (kStartUs + kFullUs * len) + kJoinStartUs + kJoinUs * (parts - 2);
+    const double us = 2 * kStartUs + (kFullUs + kQuietUs) * len + kJoinStartUs + kJoinUs * (parts - 2);
     if (us < best_us) best = parts, best_us = us;
   }
   if (best > 1) {
-    const int64_t states = heads * a.dv * a.dk * 4 * (best - 1), phi = heads * a.dk * a.dk * 4 * (int64_t)(best - 2);
-    *want = round256(states) + round256(phi);
+    const int64_t one = round256(heads * a.dv * a.dk * 4), states = heads * a.dv * a.dk * 4 * (best - 1);
+    const int64_t phi = heads * a.dk * a.dk * 4 * (int64_t)(best - 2);
+    *want = one + round256(states) + round256(phi);
     if (ws && ws_bytes >= *want) {
       p->mode = kAheadPass;
       p->parts = best, p->part_len = (p->n_chunks + best - 1) / best;
-      p->states = reinterpret_cast<float*>(ws);
-      p->phi = reinterpret_cast<float*>(ws + round256(states));
+      p->first = reinterpret_cast<float*>(ws);
+      p->states = reinterpret_cast<float*>(ws + one);
+      p->phi = reinterpret_cast<float*>(ws + one + round256(states));
     }
   }
   return p->items;

@@ -445,3 +445,16 @@ def test_sequences_cut_into_parts(cuda_lib, B, Hk, Hv, T, dk, dv, dtype, state):
                                 workspace=ws)
     torch.cuda.synchronize()
     check(x, y1, s1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,T", [("bf16", 2048), ("f32", 1999)])
+def test_parts_with_the_state_in_place(cuda_lib, dtype, T):
+    # the first part still needs the state when the last one may have written it
+    x = make(72, 1, T, 4, 8, 64, 128, dtype, state=True, device="cuda")
+    assert m.mamba_gated_delta_workspace_bytes(1, T, 4, 8, 64, 128, 1 if dtype == "bf16" else 0) > 0
+    y, s = run_prefill(x)
+    for _ in range(5):
+        state, y1 = x["state_in"].clone(), torch.empty_like(y)
+        m.mamba_gated_delta_prefill(y1, x["q"], x["k"], x["v"], x["a"], x["b"], x["A_log"], x["dt_bias"], state, state)
+        assert torch.equal(y, y1) and torch.equal(s, state)
