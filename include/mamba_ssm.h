@@ -484,7 +484,9 @@ MAMBA_API int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const floa
  * (No counterpart in the mamba-rs pages: an addition of this library, in the
  *  manner of its scan and step.)  Value head h reads key head h / (Hv / Hk).
  * Keys are taken as given: the rule contracts for |k_t| <= 1, which
- * mamba_qk_norm_rotary with MAMBA_NORM_L2 gives.
+ * mamba_qk_norm_rotary with MAMBA_NORM_L2 gives.  A NaN or an infinity of a token
+ * reaches the outputs after it, and in a prefill it may reach those of up to 15
+ * tokens before it (its group of 16), of the same head.
  *
  * mamba_gated_delta_prefill runs T tokens from a state and returns the state
  * after the last one; prefill(T1) then prefill(T2) equals prefill(T1 + T2) up

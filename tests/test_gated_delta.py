@@ -458,3 +458,22 @@ def test_parts_with_the_state_in_place(cuda_lib, dtype, T):
         state, y1 = x["state_in"].clone(), torch.empty_like(y)
         m.mamba_gated_delta_prefill(y1, x["q"], x["k"], x["v"], x["a"], x["b"], x["A_log"], x["dt_bias"], state, state)
         assert torch.equal(y, y1) and torch.equal(s, state)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "a", "b"])
+@pytest.mark.parametrize("t", [37, 64, 130])
+def test_nan_stays_in_its_head_and_group(cuda_lib, dtype, name, t):
+    x = make(73, 2, 200, 2, 4, 64, 64, dtype, state=True, device="cuda")
+    y, s = run_prefill(x)
+    x[name][1, t, 1] = float("nan")
+    y1, s1 = run_prefill(x)
+    heads = [2, 3] if name in ("q", "k") else [1]  # of the second sequence
+    others = [h for h in range(4) if h not in heads]
+    assert torch.equal(y[0], y1[0]) and torch.equal(s[0], s1[0])
+    assert torch.equal(y[1, :, others], y1[1, :, others]) and torch.equal(s[1, others], s1[1, others])
+    assert torch.equal(y[1, :t // 16 * 16], y1[1, :t // 16 * 16])
+    assert y1[1, t, heads].isnan().all()
+    if name != "q":
+        assert y1[1, t:, heads].isnan().all() and s1[1, heads].isnan().all()
