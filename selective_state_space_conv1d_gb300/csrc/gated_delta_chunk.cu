@@ -296,6 +296,20 @@ __device__ __forceinline__ void split2n(float a, float b, uint32_t& t0, uint32_t
   asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(t1) : "f"(ra), "f"(rb));
 }
 
+// (a0, a1) += (b0 c0, b1 c1) in one instruction
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c0, float c1) {
+  asm("{\n"
+      "  .reg .b64 a, b, c;\n"
+      "  mov.b64 a, {%0, %1};\n"
+      "  mov.b64 b, {%2, %3};\n"
+      "  mov.b64 c, {%4, %5};\n"
+      "  fma.rn.f32x2 a, b, c, a;\n"
+      "  mov.b64 {%0, %1}, a;\n"
+      "}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -644,7 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         tmem_wait(xq);
         tmem_wait(xo);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fmaf(o[j], __uint_as_float(xq[j]), __uint_as_float(xo[j]));
+        for (int j = 0; j < 8; j += 2) {
+          float lo = __uint_as_float(xo[j]), hi = __uint_as_float(xo[j + 1]);
+          fma2(lo, hi, o[j], o[j + 1], __uint_as_float(xq[j]), __uint_as_float(xq[j + 1]));
+          o[j] = lo, o[j + 1] = hi;
+        }
         if (!direct) {
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
@@ -733,10 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
           for (int j = 0; j < 8; j += 4) {
             const float4 eg = *reinterpret_cast<const float4*>(&gt.eg[i0 + j0 + j]);
-            r[j0 + j] = fmaf(-eg.x, __uint_as_float(x[j]), r[j0 + j]);
-            r[j0 + j + 1] = fmaf(-eg.y, __uint_as_float(x[j + 1]), r[j0 + j + 1]);
-            r[j0 + j + 2] = fmaf(-eg.z, __uint_as_float(x[j + 2]), r[j0 + j + 2]);
-            r[j0 + j + 3] = fmaf(-eg.w, __uint_as_float(x[j + 3]), r[j0 + j + 3]);
+            fma2(r[j0 + j], r[j0 + j + 1], -eg.x, -eg.y, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            fma2(r[j0 + j + 2], r[j0 + j + 3], -eg.z, -eg.w, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
           }
         }
         uint32_t t0[8], t1[8], t2[8];
@@ -803,7 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           tmem_ld16(t_lane + kColS + (uint32_t)(part * HK + j0), x);
           tmem_wait(x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(total, s[j0 + j], __uint_as_float(x[j]));
+          for (int j = 0; j < 16; j += 2) {
+            float lo = __uint_as_float(x[j]), hi = __uint_as_float(x[j + 1]);
+            fma2(lo, hi, total, total, s[j0 + j], s[j0 + j + 1]);
+            s[j0 + j] = lo, s[j0 + j + 1] = hi;
+          }
         }
       }
       if (gt.at + 1 == gt.end) leave(gt);
@@ -956,10 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
           for (int q = 0; q < k; q += 4) {
             const float4 a = *reinterpret_cast<const float4*>(blk + k * kLdA + q);
-            x[q] = fmaf(x[k], a.x, x[q]);
-            if (q + 1 < k) x[q + 1] = fmaf(x[k], a.y, x[q + 1]);
-            if (q + 2 < k) x[q + 2] = fmaf(x[k], a.z, x[q + 2]);
-            if (q + 3 < k) x[q + 3] = fmaf(x[k], a.w, x[q + 3]);
+            fma2(x[q], x[q + 1], x[k], x[k], a.x, a.y);  // zero from column k on
+            if (q + 2 < k) fma2(x[q + 2], x[q + 3], x[k], x[k], a.z, a.w);
           }
         }
         __syncwarp();
