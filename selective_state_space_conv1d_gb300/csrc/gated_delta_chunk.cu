@@ -1220,6 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
       if (F32) {  // S's third terms make room for the decayed U's
         if (c > 0) wait_counted(o_empty, c - 1);
+        tcgen05_fence_after();  // the output's loads come before the product over them
         if (!quiet) issue_d1(c, 1, 0, DK / 16);
       }
       wait_counted(t_full, c);

@@ -1,0 +1,40 @@
+"""Rules that the chunked kernel's source has to keep, checked by reading it.
+
+A wait on an mbarrier does not by itself order a thread's tensor-memory accesses
+after those that the barrier stands for: tcgen05.fence::after_thread_sync has to
+come between.  Where one is missing the results are right as long as the timing
+is, so no run shows it.
+"""
+import os
+import re
+
+import selective_state_space_conv1d_gb300 as m
+
+_CSRC = os.path.join(os.path.dirname(m.__file__), "csrc")
+
+
+def _roles():
+    """The chunk kernel's text by role: epilogues, prepare, gates, MMAs, load."""
+    with open(os.path.join(_CSRC, "gated_delta_chunk.cu")) as f:
+        text = re.sub(r"//(?! -----).*", "", f.read())  # without comments, but for the roles' headings
+    parts = re.split(r"// -{10,} (\w+) -{4}", text)
+    return dict(zip(parts[1::2], parts[2::2]))
+
+
+def _unfenced(text, wait, access):
+    """Accesses whose last wait before them has no fence between."""
+    bad, pending = [], None
+    for e in re.finditer(rf"(?P<wait>{wait})|(?P<fence>\btcgen05_fence_after\(\))|(?P<access>{access})", text):
+        if e["wait"]:
+            pending = e["wait"]
+        elif e["fence"]:
+            pending = None
+        elif pending:
+            bad.append((pending, e["access"]))
+    return bad
+
+
+def test_products_come_after_a_fence():
+    text = _roles()["MMAs"]
+    assert text.count("wait_counted(") >= 8
+    assert _unfenced(text, r"\bwait_counted\([a-z_0-9]+", r"\b(?:issue_d[01]|mma_ss|mma_ts)\(") == []
