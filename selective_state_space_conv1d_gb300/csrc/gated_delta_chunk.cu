@@ -695,7 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll 1
     for (int c = 0; c <= n_chunks; ++c) {
       const Gates& gt = gates[c % kGateSlots];
-      if (F32 && c > 0) wait(o_full, c - 1);  // U's third terms are read
+      if (F32 && c > 0) {  // U's third terms are read, where S's third come next
+        wait(o_full, c - 1);
+        tcgen05_fence_after();
+      }
       if (c < n_chunks) {
         wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
         if (gt.at == gt.begin) enter(gt);

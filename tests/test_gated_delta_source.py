@@ -38,3 +38,11 @@ def test_products_come_after_a_fence():
     text = _roles()["MMAs"]
     assert text.count("wait_counted(") >= 8
     assert _unfenced(text, r"\bwait_counted\([a-z_0-9]+", r"\b(?:issue_d[01]|mma_ss|mma_ts)\(") == []
+
+
+def test_tensor_memory_is_touched_after_a_fence():
+    """Behind the barriers that products commit to, in the warps that load and store tensor memory."""
+    for role in ("epilogues", "prepare"):
+        text = _roles()[role]
+        assert re.search(r"\bwait\((?:[xuso]|d0)_full", text)
+        assert _unfenced(text, r"\bwait\((?:[xuso]|d0)_full", r"\btmem_(?:ld|st)\d+\(") == []
