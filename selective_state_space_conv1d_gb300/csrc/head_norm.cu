@@ -292,20 +292,20 @@ __global__ void __launch_bounds__(kHnThreads, kHnCtas) head_norm_kernel(const He
   // units, so one division a group and then a step from unit to unit
   const int64_t base = (int64_t)blockIdx.x * kGroups * per_group + threadIdx.x / G;
   int64_t row = base < 0x7fffffff ? (int64_t)((uint32_t)base / (uint32_t)g.H) : base / g.H;
-  int h = (int)(base - row * g.H);
+  uint32_t h = (uint32_t)(base - row * g.H);  // below 2^31, and a step more below 2^32
   for (int s = 0; s < per_group; s += kHeads) {
     Vec8<IN> ry[kHeads], rz[kHeads];
     int64_t rows[kHeads];
-    int hs[kHeads];
+    uint32_t hs[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       rows[j] = row, hs[j] = h;
       if (s + j < per_group && base + (int64_t)(s + j) * kGroups < units && in) {
-        ry[j].load(reinterpret_cast<const IN*>(g.y) + row * g.ld_y + h * g.d + c);
-        if (g.z) rz[j].load(reinterpret_cast<const IN*>(g.z) + row * g.ld_z + h * g.d + c);
+        ry[j].load(reinterpret_cast<const IN*>(g.y) + row * g.ld_y + (int64_t)h * g.d + c);
+        if (g.z) rz[j].load(reinterpret_cast<const IN*>(g.z) + row * g.ld_z + (int64_t)h * g.d + c);
       }
       h += kGroups;
-      while (h >= g.H) h -= g.H, ++row;
+      while (h >= (uint32_t)g.H) h -= g.H, ++row;
     }
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kHnThreads, kHnCtas) head_norm_kernel(const He
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= silu_f(z[i]);
         }
-        store8(reinterpret_cast<OUT*>(g.out) + rows[j] * g.ld_out + hs[j] * g.d + c, f);
+        store8(reinterpret_cast<OUT*>(g.out) + rows[j] * g.ld_out + (int64_t)hs[j] * g.d + c, f);
       }
     }
   }
@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const Hea
   const IN* z = g.z ? reinterpret_cast<const IN*>(g.z) + row * g.ld_z + h * g.d : nullptr;
   OUT* o = reinterpret_cast<OUT*>(g.out) + row * g.ld_out + h * g.d;
   float ss = 0.0f;
-  for (int c = lane; c < g.d; c += 32) {
+  for (uint32_t c = lane; c < (uint32_t)g.d; c += 32) {
     const float v = to_f32(y[c]);
     ss = fmaf(v, v, ss);
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
   const float inv = rsqrtf(ss / (float)g.d + g.eps);
-  for (int c = lane; c < g.d; c += 32) {
+  for (uint32_t c = lane; c < (uint32_t)g.d; c += 32) {
     float v = to_f32(y[c]) * (inv * (g.weight ? g.weight[c] : 1.0f));
     if (z) v *= silu_f(to_f32(z[c]));
     o[c] = from_f32<OUT>(v);
