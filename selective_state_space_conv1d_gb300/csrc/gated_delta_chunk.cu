@@ -150,7 +150,7 @@ struct Plan {
   float* states;     // kWide: [CTA][128][dk]; else [parts - 1][B Hv][dv][dk], the state before parts 1 ..
   float* first;      // [B Hv][dv][dk], state_in: state_out, which may lie over it, is written before all have read it
   float* phi;        // [parts - 2][B Hv][dk][dk], of parts 1 ..
-  int* flags;        // kWide: [CTA], set when its state is there
+  int* flags;        // kWide: [CTA], the warps whose part of its state is there
 };
 
 // A CTA's chunks in the order in which it runs them: the beginning of an item
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (plan.mode == kWide && k.begin > 0) {  // the CTA before has run the item's beginning
         volatile int* flag = plan.flags + blockIdx.x - 1;
         const long long t0 = clock64();
-        while (*flag == 0 && !*abort_flag) {
+        while (*flag < kMainWarps && !*abort_flag) {
           if (clock64() - t0 > kWaitLimit) {
             *abort_flag = 1;
           }
@@ -614,9 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         dst = nullptr;
       if (dst) store_state(dst, vec_state(dst));
       if (hand_over) {
+        // counted warp by warp: a barrier here would depend on what the gates say, which
+        // the warps need not agree on once a wait has run out
         __threadfence();
-        named_barrier(5, 32 * kMainWarps);
-        if (threadIdx.x == 0) atomicExch(plan.flags + blockIdx.x, 1);
+        __syncwarp();
+        if (lane == 0) atomicAdd(plan.flags + blockIdx.x, 1);
       }
     };
     const int i0 = part * kTok;  // this thread's tokens of a chunk

@@ -46,3 +46,20 @@ def test_tensor_memory_is_touched_after_a_fence():
         text = _roles()[role]
         assert re.search(r"\bwait\((?:[xuso]|d0)_full", text)
         assert _unfenced(text, r"\bwait\((?:[xuso]|d0)_full", r"\btmem_(?:ld|st)\d+\(") == []
+
+
+def _lambda(text, name):
+    """The text of `auto name = [&](..) {..};`."""
+    start = text.index(f"auto {name} = [&](")
+    depth = 0
+    for i in range(text.index("{", start), len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i + 1]
+
+
+def test_no_barrier_hangs_on_what_the_gates_say():
+    """Once a wait has run out, the gates of a chunk may be unwritten and differ between warps' reads."""
+    text = _roles()["epilogues"]
+    for name in ("enter", "leave"):  # both run, or not, by the gates
+        assert "named_barrier(" not in _lambda(text, name) and "__syncthreads(" not in _lambda(text, name)
