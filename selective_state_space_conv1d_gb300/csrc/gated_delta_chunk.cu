@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     const uint32_t half = 8 * (part >> 1);  // this warp's of two barriers
     const int lane_n = quad * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-    float s[HK];
+    float s[HK] = {};
     // four of this lane's values of a [..][dk] state, `left` of them inside it
     auto load_state = [&](const float* src, bool vec) {
 #pragma unroll
@@ -562,19 +562,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
       }
     };
+    // False once a wait has run out: what was read of the gates before may then be
+    // unwritten, or of another chunk (their writer changes a slot that is in use only
+    // after it has seen the flag), and no global address is made of it.  Warps decide
+    // as one.
+    auto live = [&]() {
+      asm volatile("" ::: "memory");
+      return __all_sync(0xffffffffu, *abort_flag == 0) != 0;
+    };
     auto vec_state = [&](const float* p) { return MAPS || (g.dk % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0); };
     const int64_t all_states = g.B * g.Hv * (int64_t)g.dv * g.dk;
     // the state before the chunk's piece
     auto enter = [&](const Gates& k) {
-      const int n = k.tile * kM + lane_n;
+      const int n = k.tile * kM + lane_n, begin = k.begin;
       const int64_t row = ((int64_t)k.bh * g.dv + n) * g.dk;
+      if (!live()) return;
       if (k.phi) {
 #pragma unroll
         for (int j = 0; j < HK; ++j) s[j] = part * HK + j == lane_n ? 1.0f : 0.0f;
         return;
       }
       const float* src = g.state_in ? g.state_in + row : nullptr;
-      if (plan.mode == kWide && k.begin > 0) {  // the CTA before has run the item's beginning
+      if (plan.mode == kWide && begin > 0) {  // the CTA before has run the item's beginning
         volatile int* flag = plan.flags + blockIdx.x - 1;
         const long long t0 = clock64();
         while (*flag < kMainWarps && !*abort_flag) {
@@ -585,11 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
         __threadfence();
         src = plan.states + ((int64_t)(blockIdx.x - 1) * kM + lane_n) * g.dk;
-      } else if (plan.mode == kAheadPass && k.begin > 0) {
+      } else if (plan.mode == kAheadPass && begin > 0) {
         src = nullptr;
       } else if (plan.mode == kPartsPass) {
-        if (k.begin > 0)
-          src = plan.states + (k.begin / plan.part_len - 1) * all_states + row;
+        if (begin > 0)
+          src = plan.states + (begin / plan.part_len - 1) * all_states + row;
         else if (src)
           src = plan.first + row;
       }
@@ -600,17 +609,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     auto leave = [&](const Gates& k) {
       const int n = k.tile * kM + lane_n;
       const int64_t row = ((int64_t)k.bh * g.dv + n) * g.dk;
-      const int p = plan.mode == kWide ? 0 : k.begin / plan.part_len;
-      const bool hand_over = k.end < n_all && plan.mode == kWide;
+      const int p = plan.mode == kWide ? 0 : k.begin / plan.part_len, bh = k.bh;
+      const bool inside = k.end < n_all, hand_over = inside && plan.mode == kWide, phi = k.phi;
+      if (!live()) return;
       float* dst = n < g.dv ? g.state_out : nullptr;
       if (dst) dst += row;
       if (hand_over)
         dst = plan.states + ((int64_t)blockIdx.x * kM + lane_n) * g.dk;
-      else if (k.phi)
-        dst = lane_n < g.dk ? plan.phi + (((p - 1) * g.B * g.Hv + k.bh) * g.dk + lane_n) * g.dk : nullptr;
+      else if (phi)
+        dst = lane_n < g.dk ? plan.phi + (((p - 1) * g.B * g.Hv + bh) * g.dk + lane_n) * g.dk : nullptr;
       else if (plan.mode == kAheadPass)
         dst = n < g.dv ? plan.states + p * all_states + row : nullptr;
-      else if (k.end < n_all)
+      else if (inside)
         dst = nullptr;
       if (dst) store_state(dst, vec_state(dst));
       if (hand_over) {
@@ -642,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         y_at = reinterpret_cast<char*>(g.y) +
                ((gt.b * g.T + (int64_t)gt.at * kC + i0) * g.ld_y + (int64_t)gt.h * g.dv + n) * (g.y_bf16 ? 2 : 4);
         y_rows = n < g.dv ? gt.tokens - i0 : 0;
+        if (!live()) y_rows = 0;
       }
       wait(o_full, c);
       tcgen05_fence_after();
@@ -703,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       if (c < n_chunks) {
         wait(gate_full + 8 * (c % kGateSlots), c / kGateSlots);
-        if (gt.at == gt.begin) enter(gt);
+        if (__any_sync(0xffffffffu, gt.at == gt.begin)) enter(gt);
         // S to tensor memory: of this warp's HK columns of D3's place the first
         // half the first terms, the rest the second; the third terms beyond D3
         const uint32_t at = t_lane + kColS + (uint32_t)(part * HK), at2 = t_lane + kColS + (uint32_t)(DK + part * HK / 2);
@@ -729,8 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         static_assert(kTok == 16, "one tensor-memory load");
         float r[kTok];
         if (F32) {
-          const int n = gt.tile * kM + lane_n, rows = n < g.dv && !gt.phi ? gt.tokens - i0 : 0;
+          const int n = gt.tile * kM + lane_n;
+          int rows = n < g.dv && !gt.phi ? gt.tokens - i0 : 0;
           const In* v = reinterpret_cast<const In*>(g.v) + (gt.b * g.T + (int64_t)gt.at * kC + i0) * g.ld_v + (int64_t)gt.h * g.dv + n;
+          if (!live()) rows = 0;
 #pragma unroll
           for (int j = 0; j < kTok; ++j) {
             r[j] = j < rows ? to_f32(*v) : 0.0f;
@@ -831,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           }
         }
       }
-      if (gt.at + 1 == gt.end) leave(gt);
+      if (__any_sync(0xffffffffu, gt.at + 1 == gt.end)) leave(gt);
     }
   } else if (warp < kGateWarp) {
     // ------------------------------------------------------------ prepare ----

@@ -63,3 +63,17 @@ def test_no_barrier_hangs_on_what_the_gates_say():
     text = _roles()["epilogues"]
     for name in ("enter", "leave"):  # both run, or not, by the gates
         assert "named_barrier(" not in _lambda(text, name) and "__syncthreads(" not in _lambda(text, name)
+
+
+def test_no_address_is_made_of_an_aborted_chunk_s_gates():
+    """Each use of the gates for a global address looks at the abort flag between reading them and the access."""
+    text = _roles()["epilogues"]
+    for name in ("enter", "leave"):
+        body = _lambda(text, name)
+        read, access = body.split("if (!live()) return;")
+        assert re.search(r"\bk\.bh\b", read)
+        # k.phi of enter chooses no address
+        assert not re.search(r"\bk\.(?!phi\b)\w+", access) and not re.search(r"(?:load|store)_state\(", read)
+    output, values = _lambda(text, "output"), text[text.index("epilogue 1" if "epilogue 1" in text else "float r[kTok];"):]
+    assert re.search(r"y_rows = [^;]*gt\.tokens[^;]*;\s*if \(!live\(\)\) y_rows = 0;", output)
+    assert re.search(r"int rows = [^;]*gt\.tokens[^;]*;[^;]*;\s*if \(!live\(\)\) rows = 0;", values)
