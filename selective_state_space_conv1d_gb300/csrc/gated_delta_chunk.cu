@@ -120,7 +120,7 @@ struct Smem {
   static constexpr int kOffA = kOffV + kV;            // A, f32 [64][kLdA], of each group
   static constexpr int kOffGates = kOffA + 2 * kC * kLdA * 4;
   static constexpr int kOffBar = kOffGates + kGateSlots * (int)sizeof(Gates);
-  static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 12;
+  static constexpr int kBars = 2 * kKqStages + 2 * kGateSlots + 2 + 3 + 2 * kPBuffers + 1 + 4 + 12 + 1;
   static constexpr int kBytes = kOffBar + 8 * kBars + 64;  // and tensor memory's address, the abort flag, the schedule
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(sizeof(Gates) % 16 == 0, "gate slots must keep 16-byte alignment");
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
   const uint32_t p_full = next_bars(L::kPBuffers), p_empty = next_bars(L::kPBuffers), o_empty = next_bars(1);
   // in halves (the warps of parts 0, 1 and of 2, 3): the products start on the first
   const uint32_t s_ready = next_bars(2), r_ready = next_bars(2), w_ready = next_bars(2), s_full = next_bars(2);
-  const uint32_t x_full = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1);
+  const uint32_t x_full = next_bars(1), u_full = next_bars(1), u_ready = next_bars(1), o_full = next_bars(1), drained = next_bars(1);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
   Schedule& sched = *reinterpret_cast<Schedule*>(tmem_ptr + 2);
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       mbar_init(s_ready + 8 * s, kMainWarps / 2), mbar_init(r_ready + 8 * s, kMainWarps / 2);
       mbar_init(w_ready + 8 * s, kMainWarps / 2), mbar_init(s_full + 8 * s, 1);
     }
-    mbar_init(x_full, 1), mbar_init(u_full, 1), mbar_init(u_ready, kMainWarps), mbar_init(o_full, 1);
+    mbar_init(x_full, 1), mbar_init(u_full, 1), mbar_init(u_ready, kMainWarps), mbar_init(o_full, 1), mbar_init(drained, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -511,6 +511,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     for (int tries = 0; !mbar_sleep(bar, (uint32_t)(phase & 1)); ++tries) {
       if (tries > kWaitTries) *abort_flag = 1;
       if (*abort_flag) break;
+    }
+  };
+  // for what is in flight at the end, whatever the flag says
+  auto landed = [&](uint32_t bar, int phase) {
+#pragma unroll 1
+    for (int tries = 0; !mbar_sleep(bar, (uint32_t)(phase & 1)); ++tries) {
+      if (tries > kWaitTries) {
+        *abort_flag = 1;
+        break;
+      }
     }
   };
   auto wait = [&](uint32_t bar, int phase) {
@@ -1316,11 +1326,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       commit(p_empty + 8 * (c % L::kPBuffers));
       if (c + L::kAhead < n_chunks) issue_d0(c + L::kAhead);
     }
-    // the last commit has arrived (and with it every MMA is done) before
-    // tensor memory is freed and the barriers go away
-    const int last = n_chunks - 1;
-    wait_counted(o_full, last);
-    wait_counted(p_empty + 8 * (last % L::kPBuffers), last / L::kPBuffers);
+    // every MMA and commit is done before tensor memory is freed and the barriers go
+    // away, after a wait that ran out too
+    commit(drained);
+    landed(drained, 0);
   } else {
     // --------------------------------------------------------------- load ----
     const int lt = threadIdx.x - 32 * kLoadWarp;
@@ -1382,6 +1391,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       lines(reinterpret_cast<const float*>(g.q) + (int64_t)at.hk * g.dk, g.ld_q, g.dk);
       lines(reinterpret_cast<const float*>(g.v) + (int64_t)at.h * g.dv + at.tile * kM, g.ld_v, cols);
     };
+    // Copies that this thread has started.  Once a wait has run out it starts no more: the
+    // places may be in use, and a barrier takes no second copy before the first has landed.
+    int kq_started = 0, v_started = 0;
     // the keys and queries of chunk c
     auto load_kq = [&](int c, const At& at) {
       const int ks = c % L::kKqStages;
@@ -1389,7 +1401,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       if (c >= L::kKqStages) wait_counted(kq_empty + 8 * ks, c / L::kKqStages + 1);
       if (MAPS) {
         // tokens past the end and components past dk read as zero
-        if (lt == 0) {
+        if (lt == 0 && !*abort_flag) {
+          kq_started = c + 1;
           mbar_arrive_expect_tx(kq_full + 8 * ks, L::kKqTerm);
 #pragma unroll
           for (int kb = 0; kb < L::kBlocks; ++kb) {
@@ -1458,7 +1471,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         if (c > 0) wait_counted(v_empty, c - 1);
         if (vec_y && c > 1) store_y(two_before);
         if (MAPS) {
-          if (lt == 0) {
+          if (lt == 0 && !*abort_flag) {
+            v_started = c + 1;
             mbar_arrive_expect_tx(v_full, kC * kM * 2);
             tma_load_4d(base + L::kOffV, &map_v, here.tile * kM, here.h, here.t, here.b, v_full);
           }
@@ -1476,6 +1490,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
       }
       two_before = before, before = here, here = after;
+    }
+    if (MAPS && lt == 0 && *abort_flag) {  // nothing may land after the CTA has ended
+#pragma unroll 1
+      for (int c = kq_started > L::kKqStages ? kq_started - L::kKqStages : 0; c < kq_started; ++c)
+        landed(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
+      if (v_started > 0) landed(v_full, v_started - 1);
     }
     if (!F32) {  // the last two chunks' outputs
       wait_counted(v_empty, n_chunks - 1);

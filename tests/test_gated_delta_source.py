@@ -77,3 +77,18 @@ def test_no_address_is_made_of_an_aborted_chunk_s_gates():
     output, values = _lambda(text, "output"), text[text.index("epilogue 1" if "epilogue 1" in text else "float r[kTok];"):]
     assert re.search(r"y_rows = [^;]*gt\.tokens[^;]*;\s*if \(!live\(\)\) y_rows = 0;", output)
     assert re.search(r"int rows = [^;]*gt\.tokens[^;]*;[^;]*;\s*if \(!live\(\)\) rows = 0;", values)
+
+
+def test_nothing_is_in_flight_when_a_cta_ends():
+    """A wait that ran out leaves copies and products in flight: they are waited for before the memory is given back."""
+    mma, load = _roles()["MMAs"], _roles()["load"]
+    end = mma[mma.rindex("issue_d0("):]
+    assert re.search(r"\bcommit\(drained\);\s*landed\(drained, 0\);", end) and "wait_counted(" not in end
+    copies = [c.start() for c in re.finditer(r"\bmbar_arrive_expect_tx\(", load)]
+    assert len(copies) == 2
+    for at, name in zip(copies, ("kq", "v")):  # none is started after the flag is up
+        assert re.search(rf"if \(lt == 0 && !\*abort_flag\) \{{\s*{name}_started = c \+ 1;\s*$", load[:at])
+    rest = load[load.index("if (MAPS && lt == 0 && *abort_flag)"):]
+    assert re.search(r"landed\(kq_full", rest) and re.search(r"landed\(v_full", rest)
+    # before the barrier of the values is used for anything else
+    assert rest.index("landed(v_full") < rest.index("mbar_arrive(v_full)")
