@@ -522,7 +522,9 @@ MAMBA_API int mamba_gated_delta_prefill(void* y, int64_t ld_y, int y_dtype, cons
  * the SMs of the current device: a long prefill of few heads, or more heads than
  * SMs (0: it needs none); negative on an error.  A workspace is 16-byte aligned;
  * with less than these bytes the call runs whole heads, with the same results up
- * to rounding. */
+ * to rounding.  Contents on entry are ignored.  Calls (or replays of captured
+ * calls) that share a workspace must not overlap in time, and, a call being
+ * several launches, no two threads may be making them at once. */
 MAMBA_API int64_t mamba_gated_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk,
                                                     int64_t dv, int in_dtype);
 

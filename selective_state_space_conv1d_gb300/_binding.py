@@ -311,29 +311,98 @@ def mamba_selective_scan_workspace_bytes(Bsz, T, Di, N) -> int:
     return int(v)
 
 
-_ws_cache = {}    # (device index, stream handle) -> uint8 scratch tensor
-_ws_retired = []  # outgrown scratch tensors, kept alive (see _workspace)
+_ws_cache = {}    # (device index, stream handle) -> [lock, uint8 scratch tensor]
+_ws_retired = []  # outgrown scratch tensors, kept alive: work in flight may still use them
 
 
-def _workspace(device, nbytes, stream_handle):
-    """A scratch buffer per (device, stream), reused across calls and grown on
-    demand (at least doubling).  Calls on different streams never share one, so
-    concurrent streams cannot overwrite each other's carries.  An outgrown
-    buffer is kept alive rather than freed: a CUDA graph captured earlier may
-    still hold its address."""
+def _capturing(dev, stream_handle):
+    """Whether the stream is being captured into a CUDA graph."""
     import torch
 
-    dev = device.index if device.index is not None else torch.cuda.current_device()
-    key = (dev, int(stream_handle))
-    with _lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            size = max(nbytes, 1 << 20, 2 * buf.numel() if buf is not None else 0)
-            if buf is not None:
-                _ws_retired.append(buf)
-            buf = torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", dev))
-            _ws_cache[key] = buf
-    return buf
+    if stream_handle in (0, 1):  # the legacy default stream cannot be
+        return False
+    if stream_handle == torch._C._cuda_getCurrentRawStream(dev):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, torch.device("cuda", dev))):
+        return torch.cuda.is_current_stream_capturing()
+
+
+class _scratch:
+    """The scratch of one call, `with _scratch(..) as ws` around its C call (None
+    for no bytes).
+
+    A buffer is kept per (device, stream), grown on demand (at least doubling), and
+    locked until the call is enqueued: a call may enqueue several launches that hand
+    results on through the scratch, and the C call runs without the interpreter's
+    lock, so another thread's launches on the stream must not come between them.
+    Calls on different streams never share one.  A call that is captured gets one of
+    its own, from the graph's memory: graphs may be replayed side by side whatever
+    stream they were captured on."""
+    __slots__ = ("dev", "nbytes", "stream", "lock")
+
+    def __init__(self, device, nbytes, stream_handle):
+        import torch
+
+        self.dev = device.index if device.index is not None else torch.cuda.current_device()
+        self.nbytes, self.stream, self.lock = nbytes, int(stream_handle), None
+
+    def _new(self, nbytes):
+        import torch
+
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", self.dev))
+
+    def __enter__(self):
+        if self.nbytes <= 0:
+            return None
+        if _capturing(self.dev, self.stream):
+            return self._captured()
+        with _lock:
+            entry = _ws_cache.setdefault((self.dev, self.stream), [threading.Lock(), None])
+        lock = entry[0]
+        lock.acquire()
+        try:
+            buf = entry[1]
+            if buf is None or buf.numel() < self.nbytes:
+                new = self._new(max(self.nbytes, 1 << 20, 2 * buf.numel() if buf is not None else 0))
+                if buf is not None:
+                    _ws_retired.append(buf)
+                entry[1] = buf = new
+        except BaseException:
+            lock.release()
+            raise
+        self.lock = lock
+        return buf
+
+    def _captured(self):
+        import torch
+
+        if self.stream == torch._C._cuda_getCurrentRawStream(self.dev):
+            return self._new(self.nbytes)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, torch.device("cuda", self.dev))):
+            return self._new(self.nbytes)
+
+    def __exit__(self, *exc):
+        if self.lock is not None:
+            self.lock.release()
+            self.lock = None
+
+
+class _given:
+    """A caller's workspace (or None) in the place of a _scratch."""
+    __slots__ = ("buf",)
+
+    def __init__(self, buf):
+        self.buf = buf
+
+    def __enter__(self):
+        return self.buf
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _ptr_bytes(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def _check_scan_args(y, u, dt, Bm, Cm, A_log, D, dt_bias, z, ssm_state_in, ssm_state_out):
@@ -367,6 +436,12 @@ def _check_scan_args(y, u, dt, Bm, Cm, A_log, D, dt_bias, z, ssm_state_in, ssm_s
     return Bsz, T, Di, N
 
 
+def _scan_scratch(workspace, Bsz, T, Di, N, device, st):
+    if workspace is None:
+        return _scratch(device, mamba_selective_scan_workspace_bytes(Bsz, T, Di, N), st)
+    return _given(None if workspace is False else workspace)
+
+
 def mamba_selective_scan_prefill(y, u, dt, Bm, Cm, A_log, D=None, dt_bias=None, z=None,
                                  ssm_state_in=None, ssm_state_out=None, *, workspace=None,
                                  stream=None):
@@ -375,26 +450,20 @@ def mamba_selective_scan_prefill(y, u, dt, Bm, Cm, A_log, D=None, dt_bias=None, 
     y, u, dt, z: [B, T, Di] (row-strided views allowed); Bm, Cm: [B, T, N];
     A_log: [Di, N]; D, dt_bias: [Di]; states: [B, Di, N] f32.
     workspace: None = a cached buffer per (device, stream) sized by
-    mamba_selective_scan_workspace_bytes; False = none (one sequential pass);
-    or a uint8 cuda tensor (16-byte aligned), which the caller must not reuse
-    on another stream while this call may still be running."""
+    mamba_selective_scan_workspace_bytes (in a torch.cuda.graph capture, one of the
+    graph's own); False = none (one sequential pass); or a uint8 cuda tensor
+    (16-byte aligned), which the caller must not reuse on another stream while this
+    call may still be running, nor from another thread while it is being made."""
     Bsz, T, Di, N = _check_scan_args(y, u, dt, Bm, Cm, A_log, D, dt_bias, z, ssm_state_in, ssm_state_out)
     st = _stream(stream, u)
-    if workspace is None:
-        need = mamba_selective_scan_workspace_bytes(Bsz, T, Di, N)
-        ws = _workspace(u.device, need, st) if need > 0 else None
-    elif workspace is False:
-        ws = None
-    else:
-        ws = workspace
-    ws_ptr = ws.data_ptr() if ws is not None else None
-    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    _check(load().mamba_selective_scan_prefill(
-        _ptr(y), _rows_ld(y, "y"), _dtype_code(y), _ptr(u), _rows_ld(u, "u"),
-        _ptr(dt), _rows_ld(dt, "dt"), _ptr(z), _rows_ld(z, "z") if z is not None else 0,
-        _ptr(Bm), _rows_ld(Bm, "Bm"), _ptr(Cm), _rows_ld(Cm, "Cm"), _dtype_code(u),
-        _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(ssm_state_in), _ptr(ssm_state_out),
-        Bsz, T, Di, N, ws_ptr, ws_bytes, st))
+    scratch = _scan_scratch(workspace, Bsz, T, Di, N, u.device, st)
+    with scratch as ws:
+        _check(load().mamba_selective_scan_prefill(
+            _ptr(y), _rows_ld(y, "y"), _dtype_code(y), _ptr(u), _rows_ld(u, "u"),
+            _ptr(dt), _rows_ld(dt, "dt"), _ptr(z), _rows_ld(z, "z") if z is not None else 0,
+            _ptr(Bm), _rows_ld(Bm, "Bm"), _ptr(Cm), _rows_ld(Cm, "Cm"), _dtype_code(u),
+            _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(ssm_state_in), _ptr(ssm_state_out),
+            Bsz, T, Di, N, *_ptr_bytes(ws), st))
 
 
 def mamba_mixer_prefill(y, x, dt, Bm, Cm, conv_w, A_log, conv_b=None, D=None, dt_bias=None, z=None,
@@ -429,22 +498,15 @@ def mamba_mixer_prefill(y, x, dt, Bm, Cm, conv_w, A_log, conv_b=None, D=None, dt
         if tuple(t.shape) != (Bsz, T, N):
             raise ValueError(f"{nm} must be [B, T, N]")
     st = _stream(stream, x)
-    if workspace is None:
-        need = mamba_selective_scan_workspace_bytes(Bsz, T, Di, N)
-        ws = _workspace(x.device, need, st) if need > 0 else None
-    elif workspace is False:
-        ws = None
-    else:
-        ws = workspace
-    ws_ptr = ws.data_ptr() if ws is not None else None
-    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    _check(load().mamba_mixer_prefill(
-        _ptr(y), _rows_ld(y, "y"), _dtype_code(y), _ptr(x), _rows_ld(x, "x"),
-        _ptr(dt), _rows_ld(dt, "dt"), _ptr(z), _rows_ld(z, "z") if z is not None else 0,
-        _ptr(Bm), _rows_ld(Bm, "Bm"), _ptr(Cm), _rows_ld(Cm, "Cm"), _dtype_code(x),
-        _ptr(conv_w), _ptr(conv_b), _ptr(conv_state_in), _ptr(conv_state_out),
-        _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(ssm_state_in), _ptr(ssm_state_out),
-        Bsz, T, Di, K, N, ws_ptr, ws_bytes, st))
+    scratch = _scan_scratch(workspace, Bsz, T, Di, N, x.device, st)
+    with scratch as ws:
+        _check(load().mamba_mixer_prefill(
+            _ptr(y), _rows_ld(y, "y"), _dtype_code(y), _ptr(x), _rows_ld(x, "x"),
+            _ptr(dt), _rows_ld(dt, "dt"), _ptr(z), _rows_ld(z, "z") if z is not None else 0,
+            _ptr(Bm), _rows_ld(Bm, "Bm"), _ptr(Cm), _rows_ld(Cm, "Cm"), _dtype_code(x),
+            _ptr(conv_w), _ptr(conv_b), _ptr(conv_state_in), _ptr(conv_state_out),
+            _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(ssm_state_in), _ptr(ssm_state_out),
+            Bsz, T, Di, K, N, *_ptr_bytes(ws), st))
 
 
 def mamba3_siso_step_batched(y, x, k, q, alpha, beta, gamma, ssm_state, k_state, v_state, layer, D=None, *,
@@ -704,17 +766,15 @@ def mamba_gated_delta_prefill(y, q, k, v, a, b, A_log, dt_bias=None, state_in=No
     q, k: [B, T, Hk, dk]; v, y: [B, T, Hv, dv]; a, b: [B, T, Hv] (the decay's
     and beta's pre-activations); A_log, dt_bias: [Hv] f32; states
     [B, Hv, dv, dk] f32 (state_out may be state_in).  scale: dk ** -0.5 if None.
-    workspace: a uint8 scratch tensor (default: one kept per stream)."""
+    workspace: a uint8 scratch tensor, as for mamba_selective_scan_prefill (None:
+    one kept per stream, or the graph's own in a torch.cuda.graph capture)."""
     (Bsz, T), Hk, Hv, dk, dv, code, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, 2)
     ss = (Bsz, Hv, dv, dk)
     s_in, s_out = _f32_dense(state_in, "state_in", ss), _f32_dense(state_out, "state_out", ss)
     st = _current_stream(stream, v)
-    lib = load()
-    if workspace is None:
-        need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, code) if Hk and Hv else 0
-        workspace = _workspace(v.device, need, st) if need else None
-    ws, nbytes = (_ptr(workspace), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
-    _check(lib.mamba_gated_delta_prefill(*args, s_in, s_out, Bsz, T, Hk, Hv, dk, dv, ws, nbytes, st))
+    need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, code) if workspace is None and Hk and Hv else 0
+    with _scratch(v.device, need, st) if need else _given(workspace) as ws:
+        _check(load().mamba_gated_delta_prefill(*args, s_in, s_out, Bsz, T, Hk, Hv, dk, dv, *_ptr_bytes(ws), st))
 
 
 def mamba_gated_delta_step_batched(y, q, k, v, a, b, A_log, dt_bias, state, layer, *, scale=None, stream=None):
@@ -826,10 +886,10 @@ def mamba_layer_workspace_bytes(w, Bsz, T, eps=1e-5) -> int:
     return int(v)
 
 
-def _layer_workspace(workspace, w, Bsz, T, eps, device, st):
+def _layer_scratch(workspace, w, Bsz, T, eps, device, st):
     if workspace is None:
-        return _workspace(device, mamba_layer_workspace_bytes(w, Bsz, T, eps), st)
-    return workspace
+        return _scratch(device, mamba_layer_workspace_bytes(w, Bsz, T, eps), st)
+    return _given(workspace)
 
 
 def mamba_layer_prefill(hidden, w, conv_state_in=None, conv_state_out=None, ssm_state_in=None,
@@ -850,10 +910,9 @@ def mamba_layer_prefill(hidden, w, conv_state_in=None, conv_state_out=None, ssm_
                         (ssm_state_in, "ssm_state_in", S.d_state), (ssm_state_out, "ssm_state_out", S.d_state)):
         _f32_param(t, nm, (Bsz, S.d_inner, last))
     st = _stream(stream, hidden)
-    ws = _layer_workspace(workspace, w, Bsz, T, eps, hidden.device, st)
-    _check(load().mamba_layer_prefill(_ptr(hidden), ctypes.byref(S), _ptr(conv_state_in), _ptr(conv_state_out),
-                                      _ptr(ssm_state_in), _ptr(ssm_state_out), Bsz, T, _ptr(ws),
-                                      ws.numel() * ws.element_size(), st))
+    with _layer_scratch(workspace, w, Bsz, T, eps, hidden.device, st) as ws:
+        _check(load().mamba_layer_prefill(_ptr(hidden), ctypes.byref(S), _ptr(conv_state_in), _ptr(conv_state_out),
+                                          _ptr(ssm_state_in), _ptr(ssm_state_out), Bsz, T, *_ptr_bytes(ws), st))
 
 
 def mamba_layer_step(hidden, w, conv_state, ssm_state, layer, *, eps=1e-5, workspace=None, stream=None):
@@ -874,9 +933,9 @@ def mamba_layer_step(hidden, w, conv_state, ssm_state, layer, *, eps=1e-5, works
     if conv_state.shape[0] != ssm_state.shape[0]:
         raise ValueError("conv_state and ssm_state must have the same number of layers")
     st = _stream(stream, hidden)
-    ws = _layer_workspace(workspace, w, Bsz, 1, eps, hidden.device, st)
-    _check(load().mamba_layer_step(_ptr(hidden), ctypes.byref(S), _ptr(conv_state), _ptr(ssm_state), int(layer),
-                                   conv_state.shape[0], Bsz, _ptr(ws), ws.numel() * ws.element_size(), st))
+    with _layer_scratch(workspace, w, Bsz, 1, eps, hidden.device, st) as ws:
+        _check(load().mamba_layer_step(_ptr(hidden), ctypes.byref(S), _ptr(conv_state), _ptr(ssm_state), int(layer),
+                                       conv_state.shape[0], Bsz, *_ptr_bytes(ws), st))
 
 
 def mamba_selective_scan_prefill_noalloc(y, u, dt, Bm, Cm, A_log, D=None, dt_bias=None, z=None,
