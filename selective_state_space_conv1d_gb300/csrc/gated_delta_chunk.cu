@@ -1138,14 +1138,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t t = (int64_t)at_chunk.c * kC + lane + 32 * u;
-        la[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : -INFINITY;  // past the end: alpha 1, beta 0
-        be[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : -INFINITY;
+        la[u] = t < g.T ? to_f32(a_base[t * g.ld_a]) : 0.0f;
+        be[u] = t < g.T ? to_f32(b_base[t * g.ld_b]) : 0.0f;
       }
+      const int left = tokens_of(at_chunk) - lane;
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {  // once, then with the two tokens' places changed
         const float l = gdr_log_alpha(la[0], dt_bias, neg_A), beta = gdr_beta(be[0]);
+        const bool inside = 32 * u < left;  // past the end alpha is 1 and beta 0, whatever the head's A and bias
         la[0] = la[1], be[0] = be[1];
-        la[1] = l, be[1] = beta;
+        la[1] = inside ? l : 0.0f, be[1] = inside ? beta : 0.0f;
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) G[u] = two_log2(la[u] < -200.0f ? -200.0f : la[u]);
