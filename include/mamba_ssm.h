@@ -492,6 +492,9 @@ MAMBA_API int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const floa
  * after the last one; prefill(T1) then prefill(T2) equals prefill(T1 + T2) up
  * to rounding.
  *
+ * States and f32 outputs keep f32 accuracy, whatever the inputs' type; the value that
+ * a bf16 y is the rounding of is good to 16 bits at least.
+ *
  *   y          [B][T][Hv][dv], row (b T + t) at ld_y, dtype y_dtype     (out)
  *   q, k       [B][T][Hk][dk] at ld_q, ld_k, dtype in_dtype             (in)
  *   v          [B][T][Hv][dv] at ld_v, dtype in_dtype                   (in)

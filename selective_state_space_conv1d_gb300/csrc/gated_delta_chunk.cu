@@ -33,8 +33,9 @@
 // so no scaling and no look at the data), bf16 keys and queries one.  Of the nine
 // products of two such sums the six above 2^-24 are taken.  (Two f16 halves with
 // power-of-two scales hold 22 bits for fewer products, but finding the scales,
-// maxima over lanes and rows, took twice the instructions.)  The output of bf16
-// tensors, which feeds back into nothing, takes the products above 2^-16 alone.
+// maxima over lanes and rows, took twice the instructions.)  A bf16 output of
+// bf16 tensors with dk > 64, which feeds back into nothing, takes the products above
+// 2^-16 alone (FULL): 4e-6 off in the mean before its own rounding of 2e-3.
 //
 // Bound: neither HBM (40 KB and 1.5 us of tensor-core time a chunk) nor the tensor
 // cores but the instructions of the epilogues and of T, on a chain of dependent
@@ -101,7 +102,8 @@ struct Gates {
   int phi, pad[2];          // the schedule's
 };
 
-template <int DK, bool F32>
+// FULL: the output takes all terms of its operands
+template <int DK, bool F32, bool FULL>
 struct Smem {
   static constexpr int kTerms = F32 ? 3 : 1;          // bf16 terms of K and Q
   static constexpr int kBlocks = DK / 64;
@@ -109,11 +111,11 @@ struct Smem {
   static constexpr int kKq = kTerms * kKqTerm;
   static constexpr int kKqStages = F32 ? (DK == 64 ? 2 : 1) : 3;
   static constexpr int kT = 3 * 8192;                 // T in three terms: 64 rows x 64 bf16
-  static constexpr int kPTerms = F32 ? 3 : 2;
+  static constexpr int kPTerms = FULL ? 3 : 2;
   static constexpr int kP = kPTerms * 8192;           // P
   static constexpr int kV = F32 ? 0 : kC * kM * 2;    // f32 values are read where they are used
   static constexpr int kOffT = kKqStages * kKq;
-  static constexpr int kPBuffers = F32 ? 2 : 3;
+  static constexpr int kPBuffers = F32 || (FULL && DK > 64) ? 2 : 3;
   static constexpr int kAhead = F32 ? 1 : 2;          // chunks that are prepared ahead
   static constexpr int kOffP = kOffT + kT;
   static constexpr int kOffV = kOffP + kPBuffers * kP;
@@ -214,8 +216,9 @@ struct Cursor {
 // Tensor memory columns.  D1 is replaced by R's first two terms, later by those of
 // the decayed U.  S's three terms take 1.5 dk columns from kColS, where D3 (dk
 // columns) replaces them; R's third terms, then the decayed U's, and U's take the
-// place of S's third, which only D1 reads.  (With f32 tensors the queries' product
-// reads those too: then R's third terms take the output's place.)
+// place of S's third, which only D1 reads.  (With FULL the queries' product reads those
+// too: then R's third terms take the output's place if dk > 64; with dk <= 64 S's
+// third terms lie before kColThird.)
 constexpr uint32_t kColX = 0, kColQ = 64, kColU = 128, kColO = 192, kColS = 256, kColThird = 384, kColU3 = 416,
                    kColD0 = 448, kTmemCols = 512;
 
@@ -428,13 +431,20 @@ __device__ __forceinline__ constexpr void term_pair(int i, int& a, int& b) {
 // MAPS: q, k and v come through tensor maps (bf16, dk a multiple of 8) and the states
 // are 16-byte aligned.  A kernel of its own, so that the loops of the other loads do
 // not lie between its own.
-template <int DK, bool F32, bool MAPS>
+template <int DK, bool F32, bool MAPS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs g, const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ CUtensorMap map_v,
                                                             const __grid_constant__ CUtensorMap map_y, int vec_y,
                                                             const Plan plan) {
-  using L = Smem<DK, F32>;
+  using L = Smem<DK, F32, FULL>;
+  static_assert(FULL || !F32, "f32 tensors take all terms");
+  // The output of a chunk comes in the next one, under D2; with all its terms and dk >
+  // 64 before epilogue 1, since S's third terms leave R's no columns but the output's.
+  constexpr bool kEarly = F32 || (FULL && DK > 64);
+  // U P^T of all terms is twice as long: in the next chunk, under epilogue 1, and not
+  // before the product that it waits for (4.4 us a chunk against 4.8, 4.3 with half)
+  constexpr bool kLate = FULL && !kEarly;
   using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     auto output = [&](int c) {
       const Gates& gt = gates[c % kGateSlots];
       const bool quiet = sched.quiet;
-      const bool direct = F32 || !vec_y;
+      const bool direct = kEarly || !vec_y;
       char* y_at = nullptr;
       int y_rows = 0;
       if (direct && !quiet) {
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           at += y_step;
         }
       }
-      if (!F32) {
+      if (!kEarly) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_empty);
@@ -718,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
 #pragma unroll 1
     for (int c = 0; c <= n_chunks; ++c) {
       const Gates& gt = gates[c % kGateSlots];
-      if (F32 && c > 0) {  // U's third terms are read, where S's third come next
+      if (kEarly && c > 0) {  // U's third terms are read, where S's third come next
         wait(o_full, c - 1);
         tcgen05_fence_after();
       }
@@ -743,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
         arrive(s_ready + half);
       }
-      if (!F32 && c == n_chunks) wait(v_full, c);  // the output before the last has left its place
-      if (c > 0 && (F32 || c == n_chunks)) output(c - 1);
+      if (!kEarly && c == n_chunks) wait(v_full, c);  // the output before the last has left its place
+      if (c > 0 && (kEarly || c == n_chunks)) output(c - 1);
       if (c == n_chunks) break;
       {  // epilogue 1: R^T = V^T - e^G D1
         static_assert(kTok == 16, "one tensor-memory load");
@@ -764,6 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           const In* v = reinterpret_cast<const In*>(gbase + L::kOffV) + i0 * kM + lane_n;
 #pragma unroll
           for (int j = 0; j < kTok; ++j) r[j] = to_f32(v[j * kM]);
+          if (kEarly) {  // no output takes their place
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_empty);
+          }
           if (gt.phi) {
 #pragma unroll
             for (int j = 0; j < kTok; ++j) r[j] = 0.0f;
@@ -788,10 +802,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         for (int j = 0; j < 8; ++j) split3n(r[2 * j], r[2 * j + 1], t0[j], t1[j], t2[j]);
         tmem_st8(t_lane + kColX + (uint32_t)i0, t0);
         tmem_st8(t_lane + kColX + (uint32_t)(i0 + 8), t1);
-        tmem_st8(t_lane + (F32 ? kColO + (uint32_t)i0 : kColThird + (uint32_t)(8 * part)), t2);
+        tmem_st8(t_lane + (kEarly ? kColO + (uint32_t)i0 : kColThird + (uint32_t)(8 * part)), t2);
         arrive(r_ready + half);
       }
-      if (!F32) {
+      if (!kEarly) {
         if (c > 0) {
           // every warp has its values before one writes its output there
           named_barrier(5, 32 * kMainWarps);
@@ -826,14 +840,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            if (F32)
+            if (FULL)
               split3n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j], t2[j]);
             else
               split2n(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), t0[j], t1[j]);
           }
           tmem_st8(t_lane + kColU + (uint32_t)i0, t0);
           tmem_st8(t_lane + kColU + (uint32_t)(i0 + 8), t1);
-          if (F32) tmem_st8(t_lane + kColU3 + (uint32_t)(8 * part), t2);
+          if (FULL) tmem_st8(t_lane + kColU3 + (uint32_t)(8 * part), t2);
         }
         arrive(u_ready);
       }
@@ -932,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
             uint32_t t[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (F32)
+              if (FULL)
                 split3n(o[2 * e], o[2 * e + 1], t[0][e], t[1][e], t[2][e]);
               else
                 split2n(o[2 * e], o[2 * e + 1], t[0][e], t[1][e]);
@@ -1196,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
     constexpr uint32_t id3 = idesc_bf16(64, true);
     constexpr int HK = DK / kParts;
     // products with K or Q; the output's without the smallest for bf16 tensors
-    constexpr int kPairs = F32 ? 6 : 3, kSkipQ = F32 ? 0 : 1, kSkipP = F32 ? 0 : 3;
+    constexpr int kPairs = F32 ? 6 : 3, kSkipQ = FULL ? 0 : 1, kSkipP = FULL ? 0 : 3;
     const uint64_t kq0 = smem_desc(base), kq0_mn = smem_desc(base, 16384), t0 = smem_desc(base + L::kOffT), p0 = smem_desc(base + L::kOffP);
     auto commit = [&](uint32_t bar) {
       if (elected) mma_commit(bar);
@@ -1238,6 +1252,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         }
       }
     };
+    // the output's U P^T
+    auto issue_o = [&](int c) {
+      wait_counted(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
+      wait_counted(u_ready, c);
+      tcgen05_fence_after();
+      const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
+      if (!quiet) {
+#pragma unroll
+        for (int p = kSkipP; p < 6; ++p) {
+          int ta = 0, tb = 0;
+          term_pair<true>(p, ta, tb);
+#pragma unroll
+          for (int k = 0; k < kC / 16; ++k) {
+            const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
+            if (elected)
+              mma_ts(tmem + kColO + 16 * k, tmem + ad, pd + tb * 512 + 130 * k,
+                     idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > kSkipP || k > 0);
+          }
+        }
+      }
+      commit(o_full);
+      commit(p_empty + 8 * (c % L::kPBuffers));
+    };
     issue_d0(0);
     for (int c = 0; c < n_chunks; ++c) {
 #pragma unroll
@@ -1247,8 +1284,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         issue_d1(c, 0, h * (DK / 32), (h + 1) * (DK / 32));
       }
       commit(x_full);
+      if (kLate && c > 0) issue_o(c - 1);
       if (L::kAhead > 1 && c == 0 && n_chunks > 1) issue_d0(1);
-      if (F32) {  // S's third terms make room for the decayed U's
+      if (kEarly) {  // S's third terms make room for the decayed U's
         if (c > 0) wait_counted(o_empty, c - 1);
         tcgen05_fence_after();  // the output's loads come before the product over them
         if (!quiet) issue_d1(c, 1, 0, DK / 16);
@@ -1266,7 +1304,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
           term_pair<true>(p, ta, tb);
 #pragma unroll
           for (int k = 2 * h; k < 2 * h + 2; ++k) {
-            const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : F32 ? kColO + 16 * k : kColThird + 8 * k;
+            const uint32_t ad = ta < 2 ? kColX + 8 * ta + 16 * k : kEarly ? kColO + 16 * k : kColThird + 8 * k;
             if (elected)
               mma_ts(tmem + kColU + 16 * k, tmem + ad, t0 + tb * 512 + 130 * k,
                      idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > 0 || k > 0);
@@ -1275,7 +1313,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       commit(u_full);
       commit(t_empty + 8 * (c & 1));
-      if (!F32) {  // the queries' product, under epilogue 2
+      if (!kEarly) {  // the queries' product, under epilogue 2
         if (c > 0) wait_counted(o_empty, c - 1);
         tcgen05_fence_after();
         if (!quiet) issue_d1(c, 1, 0, DK / 16);
@@ -1305,29 +1343,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       }
       if (kHalves == 1) commit(s_full + 8);
       commit(kq_empty + 8 * (c % L::kKqStages));
-      // the output's U P^T, under epilogue 3
-      wait_counted(p_full + 8 * (c % L::kPBuffers), c / L::kPBuffers);
-      wait_counted(u_ready, c);
-      tcgen05_fence_after();
-      const uint64_t pd = p0 + (uint64_t)((c % L::kPBuffers) * (L::kP / 16));
-      if (!quiet) {
-#pragma unroll
-        for (int p = kSkipP; p < 6; ++p) {
-          int ta = 0, tb = 0;
-          term_pair<true>(p, ta, tb);
-#pragma unroll
-          for (int k = 0; k < kC / 16; ++k) {
-            const uint32_t ad = ta < 2 ? kColU + 8 * ta + 16 * k : kColU3 + 8 * k;
-            if (elected)
-              mma_ts(tmem + kColO + 16 * k, tmem + ad, pd + tb * 512 + 130 * k,
-                     idesc_bf16(kC - 16 * k, false) | neg_bits(ta, tb), p > kSkipP || k > 0);
-          }
-        }
-      }
-      commit(o_full);
-      commit(p_empty + 8 * (c % L::kPBuffers));
+      if (!kLate) issue_o(c);
       if (c + L::kAhead < n_chunks) issue_d0(c + L::kAhead);
     }
+    if (kLate) issue_o(n_chunks - 1);
     // every MMA and commit is done before tensor memory is freed and the barriers go
     // away, after a wait that ran out too
     commit(drained);
@@ -1471,7 +1490,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
       // V (bf16); tokens past the sequence's end and components past dv are zero
       if (!F32 && c >= 0) {
         if (c > 0) wait_counted(v_empty, c - 1);
-        if (vec_y && c > 1) store_y(two_before);
+        if (!kEarly && vec_y && c > 1) store_y(two_before);
         if (MAPS) {
           if (lt == 0 && !*abort_flag) {
             v_started = c + 1;
@@ -1499,7 +1518,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const GatedDeltaArgs
         landed(kq_full + 8 * (c % L::kKqStages), c / L::kKqStages);
       if (v_started > 0) landed(v_full, v_started - 1);
     }
-    if (!F32) {  // the last two chunks' outputs
+    if (!kEarly) {  // the last two chunks' outputs
       wait_counted(v_empty, n_chunks - 1);
       if (vec_y && n_chunks > 1) store_y(two_before);
       if (!MAPS || lt == 0) mbar_arrive(v_full);
@@ -1640,10 +1659,10 @@ struct Maps {
   bool inputs, y_too;  // which there are
 };
 
-template <int DK, bool F32, bool MAPS>
+template <int DK, bool F32, bool MAPS, bool FULL>
 cudaError_t launch_chunk(const GatedDeltaArgs& a, const Maps& maps, const Plan& plan, int ctas, cudaStream_t stream) {
-  auto kern = chunk_kernel<DK, F32, MAPS>;
-  constexpr int smem = Smem<DK, F32>::kAlloc;
+  auto kern = chunk_kernel<DK, F32, MAPS, FULL>;
+  constexpr int smem = Smem<DK, F32, FULL>::kAlloc;
   static int configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1755,19 +1774,26 @@ cudaError_t launch_gated_delta_chunk(const GatedDeltaArgs& a, const DeviceInfo& 
   const int ctas = make_plan(a, dev.sm_count, ws_bytes, static_cast<char*>(ws), &plan, &want);
   Maps maps = {};
   if (!a.in_bf16) {
-    return a.dk <= 64 ? launch_chunk<64, true, false>(a, maps, plan, ctas, stream)
-                      : launch_chunk<128, true, false>(a, maps, plan, ctas, stream);
+    return a.dk <= 64 ? launch_chunk<64, true, false, true>(a, maps, plan, ctas, stream)
+                      : launch_chunk<128, true, false, true>(a, maps, plan, ctas, stream);
   }
   maps.inputs = make_map_heads(&maps.k, a.k, a.B, a.T, a.Hk, a.dk, a.ld_k) &&
                 make_map_heads(&maps.q, a.q, a.B, a.T, a.Hk, a.dk, a.ld_q) &&
                 make_map_heads(&maps.v, a.v, a.B, a.T, a.Hv, a.dv, a.ld_v, kM) &&
                 ((reinterpret_cast<uintptr_t>(a.state_in) | reinterpret_cast<uintptr_t>(a.state_out)) & 15) == 0;
   maps.y_too = a.y_bf16 && make_map_heads(&maps.y, a.y, a.B, a.T, a.Hv, a.dv, a.ld_y, kM);
-  if (maps.inputs)
-    return a.dk <= 64 ? launch_chunk<64, false, true>(a, maps, plan, ctas, stream)
-                      : launch_chunk<128, false, true>(a, maps, plan, ctas, stream);
-  return a.dk <= 64 ? launch_chunk<64, false, false>(a, maps, plan, ctas, stream)
-                    : launch_chunk<128, false, false>(a, maps, plan, ctas, stream);
+  // All terms wherever y keeps 32 bits, and with dk <= 64, where they cost little (152
+  // heads of 4096 tokens 308 us against 303, 12 heads 269 and 260).  With dk > 64 they put
+  // the output on the path from state to state (12 heads of 4096 tokens 325 us against
+  // 300, 3 x 101 tokens 20.5 and 18.5), which a bf16 y, rounded to 2^-9, does not need.
+  if (a.dk <= 64)
+    return maps.inputs ? launch_chunk<64, false, true, true>(a, maps, plan, ctas, stream)
+                       : launch_chunk<64, false, false, true>(a, maps, plan, ctas, stream);
+  if (a.y_bf16)
+    return maps.inputs ? launch_chunk<128, false, true, false>(a, maps, plan, ctas, stream)
+                       : launch_chunk<128, false, false, false>(a, maps, plan, ctas, stream);
+  return maps.inputs ? launch_chunk<128, false, true, true>(a, maps, plan, ctas, stream)
+                     : launch_chunk<128, false, false, true>(a, maps, plan, ctas, stream);
 }
 
 int read_delta_faults(bool clear) {

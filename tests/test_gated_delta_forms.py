@@ -27,3 +27,43 @@ def test_a_head_that_keeps_nothing(cuda_lib, T, dtype, name):
     y, s = base.run_prefill(x)
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(s).all())
     base.check(x, y, s)
+
+
+# Error of f32 results in the mean.  A value is a sum of up to dk + 128 products (over the key components and over two
+# chunks' tokens), whose additions' and operands' errors of at most 2^-24 are independent: their root mean square is
+# at most sqrt(dk + 128) 2^-24 of the values', and keys of unit length make the rule a contraction, so errors of earlier
+# chunks do not grow.  (Sixteen bits in one operand are 2^-18 of it, four times this and more.)
+def check_rms(x, y, s):
+    ry, rs, _, _ = base.reference(x)
+    tol = (x["q"].shape[3] + 128) ** 0.5 * 2.0 ** -24
+    for what, got, ref in (("y", y, ry), ("state", s, rs)):
+        err = (got.cpu().double() - ref).square().mean().sqrt() / ref.square().mean().sqrt()
+        assert err <= tol, f"{what}: relative error {err:.2e}, allowed {tol:.2e}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Hk,Hv,dk,dv", [
+    (2, 16, 2, 4, 128, 128), (2, 17, 2, 4, 128, 128), (2, 200, 2, 4, 128, 128), (2, 17, 2, 2, 64, 64), (2, 200, 1, 2, 64, 64),
+    (1, 200, 1, 2, 96, 200), (1, 150, 2, 2, 72, 40), (1, 200, 1, 1, 200, 64), (1, 130, 1, 2, 100, 130),
+    (1, 2048, 1, 2, 128, 128), (1, 1500, 2, 2, 64, 128), (1, 200, 170, 170, 128, 64), (2, 100, 80, 80, 64, 64),
+])
+def test_f32_outputs_keep_32_bits(cuda_lib, B, T, Hk, Hv, dk, dv, dtype):
+    x = base.make(91, B, T, Hk, Hv, dk, dv, dtype, device="cuda")
+    x["dt_bias"] -= 2
+    y, s = base.run_prefill(x, y_dtype=torch.float32)
+    check_rms(x, y, s)
+
+
+@pytest.mark.gpu
+def test_the_type_of_y_changes_the_last_rounding_alone(cuda_lib):
+    """Of the f32 and the bf16 output, the latter is off by half a step at most, and both leave one state."""
+    for dk in (64, 128):
+        x = base.make(92, 1, 300, 2, 2, dk, 128, "bf16", device="cuda")
+        y, s = base.run_prefill(x)
+        y32, s32 = base.run_prefill(x, y_dtype=torch.float32)
+        assert torch.equal(s, s32)
+        # half a step, and 2^-16 of the largest term for the products that a bf16 y may do without
+        _, _, my, _ = base.reference(x)
+        tol = 2.0 ** -8 * y32.cpu().double().abs() + 2.0 ** -16 * my[:, None, :, None]
+        assert bool(((y.cpu().double() - y32.cpu().double()).abs() <= tol).all())
