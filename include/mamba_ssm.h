@@ -554,7 +554,8 @@ MAMBA_API int mamba_gated_delta_step_batched(void* y, int64_t ld_y, int y_dtype,
  *     (x, y) -> (x cos - y sin, y cos + x sin)
  * where pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
  * MAMBA_ROTARY_INTERLEAVED.  Angles are reduced exactly before they reach 32
- * bits, so far positions cost no accuracy.
+ * bits, so far positions cost no accuracy.  A frequency that is NaN or infinite makes
+ * its pair NaN.
  *
  *   q_out, k_out  [B][T][Hq][d], [B][T][Hk][d] at ld_qo, ld_ko, out_dtype (out);
  *                 may be q and k themselves (same pointer, stride and dtype)

@@ -77,6 +77,13 @@ __device__ __forceinline__ float2 cos_sin(int64_t position, uint64_t turns) {
   return make_float2(((quarter + 1) & 2) ? -x : x, (quarter & 2) ? -y : y);
 }
 
+// The turn of `position` by a frequency; NaN for one that is NaN or infinite
+__device__ __forceinline__ float2 turn(int64_t position, float inv_freq) {
+  const float2 a = cos_sin(position, turns_per_position(inv_freq));
+  const float zero = inv_freq - inv_freq;  // or NaN
+  return make_float2(a.x + zero, a.y + zero);
+}
+
 template <typename T>
 struct Vec8;
 template <>
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_norm_kernel(const QkNo
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 a = make_float2(1.0f, 0.0f);
-      if (turned) a = cos_sin(g.positions ? g.positions[row] : row % g.T, turns_per_position(g.inv_freq[4 * lane + i]));
+      if (turned) a = turn(g.positions ? g.positions[row] : row % g.T, g.inv_freq[4 * lane + i]);
       cs[i] = a.x, sn[i] = a.y;
     }
   }
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) qk_norm_any_kernel(const QkNor
       const int pair = g.interleaved ? c / 2 : c % half;
       const bool low = g.interleaved ? c % 2 == 0 : c < half;
       const float other = x[g.interleaved ? c ^ 1 : low ? c + half : c - half];
-      const float2 a = cos_sin(pos, turns_per_position(g.inv_freq[pair]));
+      const float2 a = turn(pos, g.inv_freq[pair]);
       v = fmaf(other, low ? -a.y : a.y, v * a.x);
     }
     o[c] = from_f32<OUT>(v);
