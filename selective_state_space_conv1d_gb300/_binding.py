@@ -747,7 +747,7 @@ def _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, n_lead):
             q.data_ptr(), _heads_ld(q, "q", sq, n_lead, kc, dt), k.data_ptr(), _heads_ld(k, "k", sq, n_lead, kc, dt),
             v.data_ptr(), _heads_ld(v, "v", sv, n_lead, vc, dt), a.data_ptr(), _heads_ld(a, "a", sa, n_lead, Hv, dt),
             b.data_ptr(), _heads_ld(b, "b", sa, n_lead, Hv, dt), code, _f32_dense(A_log, "A_log", (Hv,)),
-            _f32_dense(dt_bias, "dt_bias", (Hv,)), dk ** -0.5 if scale is None else scale)
+            _f32_dense(dt_bias, "dt_bias", (Hv,)), (dk or 1) ** -0.5 if scale is None else scale)
     return lead, Hk, Hv, dk, dv, code, args
 
 

@@ -67,3 +67,14 @@ def test_the_type_of_y_changes_the_last_rounding_alone(cuda_lib):
         _, _, my, _ = base.reference(x)
         tol = 2.0 ** -8 * y32.cpu().double().abs() + 2.0 ** -16 * my[:, None, :, None]
         assert bool(((y.cpu().double() - y32.cpu().double()).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dk,dv", [(0, 8), (8, 0), (0, 0)])
+def test_heads_of_no_components_are_refused_by_the_library(dk, dv):
+    x = base.make(0, 2, 5, 2, 4, max(dk, 1), max(dv, 1))
+    q, v, s = x["q"][..., :dk], x["v"][..., :dv], torch.zeros(1, 2, 4, dv, dk)
+    with pytest.raises(m.MambaError):
+        m.mamba_gated_delta_prefill(v.clone(), q, q, v, x["a"], x["b"], x["A_log"], x["dt_bias"], None, s[0], stream=0)
+    one = [t[:, 0].contiguous() for t in (v, q, q, v, x["a"], x["b"])]
+    with pytest.raises(m.MambaError):
+        m.mamba_gated_delta_step_batched(*one, x["A_log"], x["dt_bias"], s, 0, stream=0)
