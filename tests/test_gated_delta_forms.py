@@ -78,3 +78,52 @@ def test_heads_of_no_components_are_refused_by_the_library(dk, dv):
     one = [t[:, 0].contiguous() for t in (v, q, q, v, x["a"], x["b"])]
     with pytest.raises(m.MambaError):
         m.mamba_gated_delta_step_batched(*one, x["A_log"], x["dt_bias"], s, 0, stream=0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,Hv,T,dk,dv,dtype", [
+    (2, 90, 90, 200, 64, 64, "bf16"), (1, 100, 200, 70, 128, 128, "bf16"), (1, 40, 80, 150, 128, 200, "bf16"),
+    (2, 80, 80, 140, 64, 64, "f32"), (1, 160, 160, 65, 96, 72, "f32"),
+])
+def test_hand_overs_with_the_state_in_place(cuda_lib, B, Hk, Hv, T, dk, dv, dtype):
+    """More items than SMs: one begins on an SM and ends on the next, which writes the state it began from."""
+    assert m.mamba_gated_delta_workspace_bytes(B, T, Hk, Hv, dk, dv, 1 if dtype == "bf16" else 0) > 0
+    x = base.make(101, B, T, Hk, Hv, dk, dv, dtype, device="cuda")
+    x["dt_bias"] -= 3
+    y, s = base.run_prefill(x)
+    base.check(x, y, s)
+    for _ in range(3):
+        y1, s1 = base.run_prefill(x, inplace=True)
+        assert torch.equal(y, y1) and torch.equal(s, s1)
+    assert m.mamba_device_faults() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_y_far_apart(cuda_lib, dtype):
+    """A row stride past the chunked kernel's 32-bit offsets."""
+    x = base.make(102, 1, 40, 1, 2, 64, 32, dtype, device="cuda")
+    ld = 1 << 23
+    buf = torch.zeros(39 * ld + 64, dtype=base.DT[dtype], device="cuda")
+    y = buf.as_strided((1, 40, 2, 32), (40 * ld, ld, 32, 1))
+    s = torch.empty(1, 2, 32, 64, device="cuda")
+    m.mamba_gated_delta_prefill(y, x["q"], x["k"], x["v"], x["a"], x["b"], x["A_log"], x["dt_bias"], x["state_in"], s)
+    torch.cuda.synchronize()
+    base.check(x, y, s)
+    assert int(buf.count_nonzero()) <= y.numel()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinity_leaves_the_groups_before_it(cuda_lib, dtype):
+    x = base.make(103, 1, 300, 1, 2, 64, 64, dtype, device="cuda")
+    y0, s0 = base.run_prefill(x)
+    x["v"][0, 100, 0, 3] = float("inf")
+    x["v"][0, 213, 0, 9] = -float("inf")
+    y, s = base.run_prefill(x)
+    others = [n for n in range(64) if n not in (3, 9)]
+    assert torch.equal(y[:, :, 1], y0[:, :, 1]) and torch.equal(s[:, 1], s0[:, 1])
+    assert torch.equal(y[..., others], y0[..., others]) and torch.equal(s[:, :, others], s0[:, :, others])
+    for n, t in ((3, 100), (9, 213)):
+        assert torch.equal(y[0, :t // 16 * 16, 0, n], y0[0, :t // 16 * 16, 0, n])
+        assert not bool(torch.isfinite(y[0, t:, 0, n]).any()) and not bool(torch.isfinite(s[0, 0, n]).any())

@@ -39,3 +39,30 @@ def test_a_row_of_more_than_2_to_the_31_values(cuda_lib):
         at = slice(lo, lo + part)
         check(out[0, 0, at], y[0, 0, at], z[0, 0, at], None, lo)
     assert not any(bool(out[0, 0, lo:lo + part].isnan().any()) for lo in range(0, H, part))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,H,d", [
+    # heads of which every group of lanes takes eight: over 152 x 16 CTAs of 64 / (d / 8) groups
+    (52001, 3, 64), (160001, 1, 64), (11201, 7, 128), (77853, 1, 128), (13001, 3, 256), (38913, 1, 200), (20013, 5, 88),
+])
+def test_heads_past_one_for_each_group(cuda_lib, rows, H, d, dtype, in_place):
+    g = torch.Generator(device="cuda").manual_seed(d)
+    # the head after the last, as a sentinel
+    buf = torch.randn(rows * H * d + d, generator=g, device="cuda").to(DT[dtype])
+    y = buf[:rows * H * d].view(1, rows, H, d)
+    z = torch.randn(1, rows, H, d, generator=g, device="cuda").to(DT[dtype])
+    w = 1 + 0.2 * torch.randn(d, generator=g, device="cuda")
+    was, after = y.clone(), buf[rows * H * d:].clone()
+    full = buf if in_place else torch.full_like(buf, 5.0)
+    out = full[:rows * H * d].view(1, rows, H, d)
+    m.mamba_head_norm_gated(out, y, z, w)
+    torch.cuda.synchronize()
+    part = 1 << 14
+    for lo in range(0, rows, part):
+        at = slice(lo, lo + part)
+        check(out[0, at], was[0, at], z[0, at], w, lo)
+    assert torch.equal(full[rows * H * d:], after if in_place else torch.full_like(after, 5.0))
+    assert in_place or torch.equal(y, was)
