@@ -169,13 +169,9 @@ __device__ __forceinline__ Schedule make_schedule(const Plan& p, int heads) {
     const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
     const int first = (int)(lo / n), last = (int)(hi / n);  // last: the item that hi lies in
     const int lo_c = (int)(lo % n), hi_c = (int)(hi % n);
-    s.b_first = first + (lo_c > 0), s.b_count = last - s.b_first;
-    if (s.b_count < 0) {  // all inside one item
-      s.b_count = 0, s.t_item = first, s.t_begin = lo_c, s.t_len = hi_c - lo_c;
-    } else {
-      s.a_item = last, s.a_len = hi_c;
-      if (lo_c > 0) s.t_item = first, s.t_begin = lo_c, s.t_len = n - lo_c;
-    }
+    s.b_first = first + (lo_c > 0), s.b_count = last - s.b_first;  // no CTA has less than an item's chunks
+    s.a_item = last, s.a_len = hi_c;
+    if (lo_c > 0) s.t_item = first, s.t_begin = lo_c, s.t_len = n - lo_c;
   } else {
     s.quiet = p.mode == kAheadPass;
     const int values = p.items * (p.parts - s.quiet);  // CTAs that run values; the others run Phi
