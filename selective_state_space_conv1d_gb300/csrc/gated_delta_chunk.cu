@@ -1691,13 +1691,22 @@ cudaError_t launch_chunk(const GatedDeltaArgs& a, const Maps& maps, const Plan& 
 // The layout of a call over `sms` SMs, and the scratch that it wants; with less
 // (ws_bytes) items are not cut.  Returns the CTAs of a kWide launch.
 //
-// A launch takes ~12.5 us before its second chunk (the first chunk's own chain from
-// the keys' load to the output), then 4.6 us a chunk with few CTAs, 5.0 with most SMs
-// busy and 4.2 without output; the join 3 us and 4 a step.  Cutting few items into P
-// parts makes n chunks in a row n / P in each of two launches and P - 2 join steps, if
-// the parts' CTAs and the maps' fit the SMs: 12 heads of 64 chunks 128 us in parts,
-// 292 whole; of 16 chunks 66 and 83; 48 heads of 64 chunks 247 and 297.
-constexpr double kStartUs = 12.5, kFewUs = 4.6, kFullUs = 5.0, kQuietUs = 4.2, kJoinStartUs = 3, kJoinUs = 4;
+// Cutting few items into P parts makes n chunks in a row n / P in each of two launches
+// and P - 2 join steps, if the parts' CTAs and the maps' fit the SMs.  By type and key
+// size, fitted to 1 to 48 heads of 4 to 64 chunks, whole and in 3 to 32 parts (us
+// between events around a call): whole 25 + chunk n, in parts parts + 1.87 chunk n / P +
+// join (P - 2).
+// The choice was within 8 % of the best of all at each, and the same but for 1 % in the
+// mean.  12 heads of 64 x 64, 12 chunks, f32: 71 us in 6 parts, 102 whole; bf16 62 and
+// 71; of 128 x 128 f32 106 and 175; 20 chunks bf16 in 7 parts 86 and 114.
+constexpr double kStartUs = 25, kPassesUs = 1.87;
+struct PlanCosts {
+  double chunk, parts, join;
+};
+PlanCosts plan_costs(const GatedDeltaArgs& a) {
+  if (a.dk <= 64) return PlanCosts{a.in_bf16 ? 3.8 : 6.4, 38, 2.2};
+  return PlanCosts{a.in_bf16 ? 4.4 : 13.1, 47, 3.5};
+}
 int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan* p, int64_t* want) {
   *p = Plan{};
   p->n_chunks = (int)((a.T + kC - 1) / kC);
@@ -1722,11 +1731,12 @@ int make_plan(const GatedDeltaArgs& a, int sms, int64_t ws_bytes, char* ws, Plan
   }
   if (items > sms) return p->items;
   int best = 1;
-  double best_us = 0.9 * (kStartUs + kFewUs * p->n_chunks);  // worth three launches for a tenth
+  const PlanCosts cost = plan_costs(a);
+  double best_us = 0.95 * (kStartUs + cost.chunk * p->n_chunks);  // worth three launches for a twentieth
   for (int parts = 3; parts <= p->n_chunks && items * parts <= sms && items * (parts - 1) + heads * (parts - 2) <= sms; ++parts) {
     const int len = (p->n_chunks + parts - 1) / parts;
     if ((parts - 1) * len >= p->n_chunks) continue;  // the last part would be empty
-    const double us = 2 * kStartUs + (kFullUs + kQuietUs) * len + kJoinStartUs + kJoinUs * (parts - 2);
+    const double us = cost.parts + kPassesUs * cost.chunk * len + cost.join * (parts - 2);
     if (us < best_us) best = parts, best_us = us;
   }
   if (best > 1) {

@@ -127,3 +127,19 @@ def test_an_infinity_leaves_the_groups_before_it(cuda_lib, dtype):
     for n, t in ((3, 100), (9, 213)):
         assert torch.equal(y[0, :t // 16 * 16, 0, n], y0[0, :t // 16 * 16, 0, n])
         assert not bool(torch.isfinite(y[0, t:, 0, n]).any()) and not bool(torch.isfinite(s[0, 0, n]).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,Hv,T,dk,dv,dtype", [
+    (1, 48, 48, 1280, 128, 128, "f32"), (1, 2, 4, 700, 128, 128, "f32"), (1, 12, 12, 740, 64, 64, "f32"),
+    (1, 1, 1, 400, 72, 40, "f32"), (1, 2, 4, 760, 64, 64, "bf16"),
+])
+def test_sequences_that_are_cut_by_their_own_type_s_times(cuda_lib, B, Hk, Hv, T, dk, dv, dtype):
+    """A chunk of f32 tensors takes two to three times one of bf16: shorter sequences of them are worth cutting."""
+    assert m.mamba_gated_delta_workspace_bytes(B, T, Hk, Hv, dk, dv, 1 if dtype == "bf16" else 0) > 0
+    x = base.make(104, B, T, Hk, Hv, dk, dv, dtype, device="cuda")
+    x["dt_bias"] -= 4
+    y, s = base.run_prefill(x)
+    base.check(x, y, s)
+    if dtype == "f32":
+        check_rms(x, y, s)
