@@ -39,11 +39,12 @@
 //
 // Bound: neither HBM (40 KB and 1.5 us of tensor-core time a chunk) nor the tensor
 // cores but the instructions of the epilogues and of T, on a chain of dependent
-// steps.  A chunk of 128 x 128 takes 4.9 us (10.1 thousand cycles) with at most one
-// busy SM of each pair and 5.4 with all: the loops of all roles are larger than
-// the instruction cache, which is shared in pairs.  So roles keep no more code than
+// steps.  A further chunk of 128 x 128, bf16, takes 4.3 us with 12 CTAs, 4.5 with 76
+// (one of each pair of SMs) and 4.8 with all 152: the loops of all roles are larger
+// than the instruction cache, which is shared in pairs.  (64 x 64: 3.8, 3.9 and 4.4;
+// f32 6.4, 6.4 and 6.7, of 128 x 128 14.1 throughout.)  So roles keep no more code than
 // they need (one lookup per item, short waits, sums by a product with the identity)
-// and no spills: each of these took 3 to 8 % off a chunk.
+// and few spills: each of these took 3 to 8 % off a chunk.
 //
 // An item is a (sequence, value head, 128 value components); its chunks follow one
 // another.  How items and their chunks are laid over the SMs: see Plan.  A CTA's
