@@ -766,14 +766,14 @@ def mamba_gated_delta_prefill(y, q, k, v, a, b, A_log, dt_bias=None, state_in=No
     q, k: [B, T, Hk, dk]; v, y: [B, T, Hv, dv]; a, b: [B, T, Hv] (the decay's
     and beta's pre-activations); A_log, dt_bias: [Hv] f32; states
     [B, Hv, dv, dk] f32 (state_out may be state_in).  scale: dk ** -0.5 if None.
-    workspace: a uint8 scratch tensor, as for mamba_selective_scan_prefill (None:
-    one kept per stream, or the graph's own in a torch.cuda.graph capture)."""
+    workspace: as for mamba_selective_scan_prefill, of
+    mamba_gated_delta_workspace_bytes (without one whole heads run)."""
     (Bsz, T), Hk, Hv, dk, dv, code, args = _gated_delta_args(y, q, k, v, a, b, A_log, dt_bias, scale, 2)
     ss = (Bsz, Hv, dv, dk)
     s_in, s_out = _f32_dense(state_in, "state_in", ss), _f32_dense(state_out, "state_out", ss)
     st = _current_stream(stream, v)
     need = mamba_gated_delta_workspace_bytes(Bsz, T, Hk, Hv, dk, dv, code) if workspace is None and Hk and Hv else 0
-    with _scratch(v.device, need, st) if need else _given(workspace) as ws:
+    with _scratch(v.device, need, st) if need else _given(None if workspace is False else workspace) as ws:
         _check(load().mamba_gated_delta_prefill(*args, s_in, s_out, Bsz, T, Hk, Hv, dk, dv, *_ptr_bytes(ws), st))
 
 

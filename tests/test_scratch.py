@@ -44,9 +44,9 @@ def fake(monkeypatch):
     return lib
 
 
-def _call(stream):
+def _call(stream, **kw):
     q, v, a, w = torch.zeros(1, 32, 1, 8), torch.zeros(1, 32, 1, 8), torch.zeros(1, 32, 1), torch.zeros(1)
-    m.mamba_gated_delta_prefill(torch.zeros_like(v), q, q, v, a, a, w, w, stream=stream)
+    m.mamba_gated_delta_prefill(torch.zeros_like(v), q, q, v, a, a, w, w, stream=stream, **kw)
 
 
 def _threads(*calls):
@@ -82,6 +82,15 @@ def test_a_failed_call_gives_the_scratch_back(fake):
         _call(7)
     fake.mamba_gated_delta_prefill = good
     _threads(lambda: _call(7))
+
+
+def test_a_workspace_given_or_declined(fake, monkeypatch):
+    got = []
+    monkeypatch.setattr(fake, "mamba_gated_delta_prefill", lambda *a: got.append(a[-3:-1]) or 0)
+    ws = torch.zeros(8192, dtype=torch.uint8)
+    _call(7, workspace=ws)
+    _call(7, workspace=False)
+    assert got == [(ws.data_ptr(), 8192), (None, 0)] and not _binding._ws_cache
 
 
 def test_a_captured_call_keeps_none(fake, monkeypatch):
