@@ -458,6 +458,34 @@ MAMBA_API int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* 
                                 void* stream);
 
 /*
+ * A linear layer with 4-bit weights and group scales, in mamba_linear_bf16's manner:
+ *     C[m][n] = sum_k a[m][k] s[n][k / group] (q[n][k] - z[n][k / group])  (+ R[m][n])
+ * (No counterpart in the mamba-rs pages: an addition of this library.)  Differences
+ * q - z are exact and a group's sum meets its scale in f32, so the result is that of
+ * the weights as they are, to f32 rounding.  A row of the result does not depend on
+ * how many rows the call has only up to that rounding.
+ *
+ *   c         [M] rows of N at ld_c, dtype c_dtype                           (out)
+ *   a         [M] rows of K bf16 at ld_a                                     (in)
+ *   q         [N] rows of ceil(K / 32) * 16 bytes at ld_q (bytes): byte j holds the
+ *             weights k = 2 j (low half) and k = 2 j + 1, 0..15; what lies past K is
+ *             ignored                                                        (in)
+ *   scales    [N] rows of ceil(K / group) at ld_s, dtype scale_dtype         (in)
+ *   zeros     [N] rows of ceil(K / group) bytes at ld_z, 0..127, or NULL: 8  (in)
+ *   group     32, 64 or 128
+ *   residual  [M] rows of N f32 at ld_r, or NULL; may be c itself (f32, same stride)
+ * a and q must be 16-byte aligned, ld_a a multiple of 8 and ld_q of 16.  M, N, K
+ * below 2^31.  Deterministic: the order of the sums depends on the sizes only.
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL pointers, strides smaller than a row,
+ * misaligned a / q, overlap of c with an input (other than the residual as above),
+ * extent overflow; MAMBA_ERR_UNSUPPORTED for another group.
+ */
+MAMBA_API int mamba_linear_w4(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t ld_a, const uint8_t* q,
+                              int64_t ld_q, const void* scales, int64_t ld_s, int scale_dtype, const uint8_t* zeros,
+                              int64_t ld_z, int64_t group, const float* residual, int64_t ld_r, int64_t M, int64_t N,
+                              int64_t K, void* stream);
+
+/*
  * RMSNorm of the residual stream, row by row:
  *     out[m][j] = x[m][j] / sqrt(mean_j x[m][j]^2 + eps) * weight[j]
  * (inference.rs step chain F1 "Save residual + RmsNorm" with rms_norm_eps;
@@ -472,6 +500,57 @@ MAMBA_API int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* 
  */
 MAMBA_API int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const float* x, int64_t ld_x,
                             const float* weight, float eps, int64_t M, int64_t D, void* stream);
+
+/*
+ * The residual stream between two blocks, row by row: the norm after a block, its
+ * gate and residual scale, the sum, and the norm before the next block:
+ *     n   = y, or y / sqrt(mean_j y_j^2 + eps) * post_weight  (post_weight not NULL)
+ *     x'  = x + scale * gate * n                              (gate NULL: 1)
+ *     out = x' / sqrt(mean_j x'_j^2 + eps) * pre_weight
+ * (No counterpart in the mamba-rs pages, whose residual add sits in out_proj's epilogue
+ *  and whose RMSNorm in the next block's start: an addition of this library.)
+ *
+ *   x_out   [M] rows of D f32 at ld_xo; may be x itself (same stride)        (out)
+ *   out     [M] rows of D at ld_out, out_dtype, or NULL (no norm: the last block) (out)
+ *   x       [M] rows of D f32 at ld_x                                        (in)
+ *   y       [M] rows of D at ld_y, y_dtype                                   (in)
+ *   pre_weight, post_weight  [D] f32; pre_weight is NULL if and only if out is (in)
+ *   gate    rows of D at ld_gate, gate_dtype, or NULL: row m takes gate row
+ *           m / gate_rows (1: one per row, T: one per sequence of T), or the one
+ *           row there is with gate_rows 0                                    (in)
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL pointers, eps outside [0, 1], a scale that is
+ * not finite, gate_rows < 0, strides smaller than D, overlap of an output with anything
+ * (x_out with x as above excepted).
+ */
+MAMBA_API int mamba_block_norm(float* x_out, int64_t ld_xo, void* out, int64_t ld_out, int out_dtype, const float* x,
+                               int64_t ld_x, const void* y, int64_t ld_y, int y_dtype, const float* pre_weight,
+                               const float* post_weight, const void* gate, int64_t ld_gate, int gate_dtype,
+                               int64_t gate_rows, float scale, float eps, int64_t M, int64_t D, void* stream);
+
+/*
+ * What rows of logits say about tokens, with p = softmax(row):
+ *     logprob[m] = ln p[tokens[m]],  entropy[m] = -sum_v p_v ln p_v,
+ *     top_id[m][i], top_logprob[m][i]: the i-th likeliest token and its ln p
+ * (gpu_lm.rs `compute_logits` downloads the logits to sample on the host; here what an
+ *  answer needs of them is made where they are.)
+ *
+ *   logprob      [M] f32, or NULL with tokens NULL                           (out)
+ *   entropy      [M] f32, or NULL                                            (out)
+ *   top_logprob  [M][n_top] f32, top_id [M][n_top] int64 (both NULL if n_top == 0) (out)
+ *   logits       [M] rows of V at ld, dtype                                  (in)
+ *   tokens       [M] int64; a negative one asks for none (logprob 0: padding), one
+ *                from V on gives NaN                                         (in)
+ *   n_top        0..MAMBA_MAX_TOP, at most V; equal logits go by the lowest index
+ * Logits of -inf have probability 0 (ln p = -inf); a row of nothing else has entropy 0
+ * and ln p = -inf everywhere.  A NaN or +inf in a row makes its entropy and every ln p
+ * NaN, as the formula does; in the order of tokens NaN stands above +inf.
+ * Errors: MAMBA_ERR_INVALID_ARG for NULL pointers, sizes or strides out of range,
+ * overlap; MAMBA_ERR_UNSUPPORTED for n_top over MAMBA_MAX_TOP.
+ */
+#define MAMBA_MAX_TOP 32
+MAMBA_API int mamba_token_logprobs(float* logprob, float* entropy, float* top_logprob, int64_t* top_id,
+                                   const void* logits, int64_t ld, int dtype, const int64_t* tokens, int64_t n_top,
+                                   int64_t M, int64_t V, void* stream);
 
 /*
  * The gated delta rule: a recurrent layer whose state S [dv][dk] per value head

@@ -13,7 +13,10 @@ C-ABI entry points (include/mamba_ssm.h), each backed by hand-written CUDA kerne
   mamba3_siso_step_fused_batched  both in one launch (k and q never leave the SM)
   mamba3_decode_graph_create    n_steps x n_layers such tokens recorded once as a CUDA graph
   mamba_linear_bf16             a projection of the layer on the tensor cores (tcgen05)
+  mamba_linear_w4               a projection with 4-bit weights and group scales
   mamba_rmsnorm                 RMSNorm of the f32 residual stream
+  mamba_block_norm              norm after a block, gate, residual scale and sum, norm before the next
+  mamba_token_logprobs          log probabilities of given tokens, entropy, likeliest alternatives
   mamba_gated_delta_prefill     the gated delta rule over T tokens, state in/out
   mamba_gated_delta_step_batched  its T=1 step on a [n_layers][B][Hv][dv][dk] state
   mamba_qk_norm_rotary          per-head norms of queries and keys with the position rotation
@@ -41,6 +44,7 @@ from ._binding import (  # noqa: F401
     MAMBA_FAULT_DELTA_WAIT,
     MAMBA_FAULT_GEMM_WAIT,
     MAMBA_MAX_FUSED_D_CONV,
+    MAMBA_MAX_TOP,
     MAMBA_NOALLOC_SCRATCH_BYTES,
     MAMBA_NORM_L2,
     MAMBA_ROTARY_INTERLEAVED,
@@ -61,8 +65,11 @@ from ._binding import (  # noqa: F401
     mamba_layer_prefill,
     mamba_layer_step,
     mamba_layer_workspace_bytes,
+    mamba_block_norm,
     mamba_linear_bf16,
+    mamba_linear_w4,
     mamba_rmsnorm,
+    mamba_token_logprobs,
     layer_struct,
     LAYER_WEIGHTS,
     mamba_mixer_prefill,

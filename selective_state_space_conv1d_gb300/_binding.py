@@ -22,6 +22,7 @@ MAMBA_F32 = 0
 MAMBA_BF16 = 1
 MAMBA_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 MAMBA_MAX_FUSED_D_CONV = 4
+MAMBA_MAX_TOP = 32
 MAMBA_FAULT_SCAN_WAIT = 2
 MAMBA_FAULT_GEMM_WAIT = 4
 MAMBA_FAULT_DELTA_WAIT = 8
@@ -43,7 +44,10 @@ ABI_SYMBOLS = (
     "mamba3_siso_step_fused_batched",
     "mamba3_decode_graph_create",
     "mamba_linear_bf16",
+    "mamba_linear_w4",
     "mamba_rmsnorm",
+    "mamba_block_norm",
+    "mamba_token_logprobs",
     "mamba_gated_delta_prefill",
     "mamba_gated_delta_workspace_bytes",
     "mamba_gated_delta_step_batched",
@@ -126,6 +130,14 @@ def load(path: str | None = None):
         lib.mamba3_siso_step_fused_batched.restype = ctypes.c_int
         lib.mamba_linear_bf16.argtypes = [vp, i64, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
         lib.mamba_linear_bf16.restype = ctypes.c_int
+        lib.mamba_linear_w4.argtypes = [vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, vp, i64, i64, vp, i64, i64, i64,
+                                        i64, vp]
+        lib.mamba_linear_w4.restype = ctypes.c_int
+        lib.mamba_block_norm.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp, i64, i32, i64,
+                                         ctypes.c_float, ctypes.c_float, i64, i64, vp]
+        lib.mamba_block_norm.restype = ctypes.c_int
+        lib.mamba_token_logprobs.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, i64, i64, i64, vp]
+        lib.mamba_token_logprobs.restype = ctypes.c_int
         lib.mamba_rmsnorm.argtypes = [vp, i64, i32, vp, i64, vp, ctypes.c_float, i64, i64, vp]
         lib.mamba_rmsnorm.restype = ctypes.c_int
         f32 = ctypes.c_float
@@ -841,6 +853,116 @@ def mamba_head_norm_gated(out, y, z=None, weight=None, *, eps=1e-5, stream=None)
                                         code if out.dtype is dt else _dtype_code(out), y.data_ptr(),
                                         _heads_ld(y, "y", sy, 2, cols, dt), _ptr(z), ld_z, code,
                                         _f32_dense(weight, "weight", (d,)), eps, Bsz * T, H, d, _current_stream(stream, y)))
+
+
+def _rows_of(t, name, shape, dtype):
+    """Pointer and row stride of a [rows, cols] tensor of `shape` and dtype (None:
+    float32 or bfloat16), columns dense."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be dense (stride {t.stride(1)})")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def mamba_linear_w4(c, a, q, scales, zeros=None, residual=None, *, group=128, stream=None):
+    """c[M, N] = a[M, K] @ W[N, K]^T (+ residual[M, N]) with weights of 4 bits,
+    W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]).
+
+    a: bf16; q: uint8 [N, ceil(K / 32) * 16], byte j of a row holding q of k = 2j in
+    its low half and of 2j + 1 in its high half (pack_w4, quantize_w4); scales: f32
+    or bf16 [N, ceil(K / group)]; zeros: uint8 of that shape, or None (8); group: 32,
+    64 or 128; c: f32 or bf16; residual: f32 [M, N], may be c itself.  Row-strided
+    views allowed, the rows of a and q 16-byte aligned."""
+    import torch
+
+    if a.dim() != 2 or q.dim() != 2:
+        raise ValueError("a and q must be 2-D")
+    M, K = a.shape
+    N = q.shape[0]
+    sg = (N, -(-K // group) if group > 0 else 0)
+    pz, ld_z = _rows_of(zeros, "zeros", sg, torch.uint8) if zeros is not None else (None, 0)
+    pr, ld_r = _rows_of(residual, "residual", (M, N), torch.float32) if residual is not None else (None, 0)
+    _check(load().mamba_linear_w4(
+        *_rows_of(c, "c", (M, N), None), _dtype_code(c), *_rows_of(a, "a", (M, K), torch.bfloat16),
+        *_rows_of(q, "q", (N, (K + 31) // 32 * 16), torch.uint8), *_rows_of(scales, "scales", sg, None),
+        _dtype_code(scales), pz, ld_z, group, pr, ld_r, M, N, K, _current_stream(stream, a)))
+
+
+def _token_rows(t, name, shape, dtype):
+    """Pointer and row stride of a [B, T, D] or [M, D] tensor."""
+    if len(shape) == 2:
+        return _rows_of(t, name, shape, dtype)
+    return t.data_ptr(), _heads_ld(t, name, shape, 2, shape[2], t.dtype if dtype is None else dtype)
+
+
+def mamba_block_norm(x_out, out, x, y, pre_weight=None, post_weight=None, gate=None, *, scale=1.0, eps=1e-5,
+                     stream=None):
+    """The residual stream between two blocks: n = y, or RMSNorm(y) * post_weight;
+    x_out = x + scale * gate * n; out = RMSNorm(x_out) * pre_weight.
+
+    x, x_out: f32 [B, T, D] or [M, D] (x_out may be x); y, out: f32 or bf16 of that
+    shape (out and pre_weight may be None together); pre_weight, post_weight: [D]
+    f32; gate: f32 or bf16 [D], [B, D] (one per sequence) or of x's shape, or None."""
+    import torch
+
+    s = tuple(x.shape)
+    if len(s) not in (2, 3):
+        raise ValueError(f"x must be [B, T, D] or [M, D], got {s}")
+    D = s[-1]
+    M = s[0] if len(s) == 2 else s[0] * s[1]
+    po, ld_o, code_o = None, 0, 0
+    if out is not None:
+        (po, ld_o), code_o = _token_rows(out, "out", s, None), _dtype_code(out)
+    pg, ld_g, code_g, g_rows = None, 0, 0, 0
+    if gate is not None:
+        code_g = _dtype_code(gate)
+        if gate.dim() == 1:
+            pg, ld_g = _rows_of(gate.unsqueeze(0), "gate", (1, D), None)
+        elif gate.dim() == len(s):
+            (pg, ld_g), g_rows = _token_rows(gate, "gate", s, None), 1
+        else:
+            (pg, ld_g), g_rows = _rows_of(gate, "gate", (s[0], D), None), s[1]
+    _check(load().mamba_block_norm(
+        *_token_rows(x_out, "x_out", s, torch.float32), po, ld_o, code_o, *_token_rows(x, "x", s, torch.float32),
+        *_token_rows(y, "y", s, None), _dtype_code(y), _f32_dense(pre_weight, "pre_weight", (D,)),
+        _f32_dense(post_weight, "post_weight", (D,)), pg, ld_g, code_g, g_rows, scale, eps, M, D,
+        _current_stream(stream, x)))
+
+
+def mamba_token_logprobs(logprob, entropy, top_logprob, top_id, logits, tokens=None, *, stream=None):
+    """What rows of logits say about tokens: ln softmax(logits)[tokens], the entropy,
+    and the likeliest tokens with their ln p (by value, then by the lowest index).
+
+    logits: f32 or bf16 [M, V] (row-strided views allowed); tokens: int64 [M] (negative:
+    none, logprob 0); logprob, entropy: f32 [M]; top_logprob: f32 [M, n], top_id: int64
+    [M, n], n up to MAMBA_MAX_TOP.  Any output may be None (logprob with tokens,
+    top_logprob with top_id); outputs are contiguous."""
+    import torch
+
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [M, V], got {tuple(logits.shape)}")
+    M, V = logits.shape
+    n = 0
+    if top_id is not None:
+        if top_id.dim() != 2:
+            raise ValueError(f"top_id must be [M, n], got {tuple(top_id.shape)}")
+        n = top_id.shape[1]
+        if top_id.dtype is not torch.int64 or top_id.shape[0] != M or not top_id.is_contiguous():
+            raise ValueError(f"top_id must be a contiguous int64 [{M}, n] tensor")
+    if (top_id is None) != (top_logprob is None):
+        raise ValueError("top_logprob and top_id must be given together")
+    if tokens is not None and (tokens.dtype is not torch.int64 or tokens.shape != (M,) or not tokens.is_contiguous()):
+        raise ValueError(f"tokens must be a contiguous int64 [{M}] tensor")
+    _check(load().mamba_token_logprobs(
+        _f32_dense(logprob, "logprob", (M,)), _f32_dense(entropy, "entropy", (M,)),
+        _f32_dense(top_logprob, "top_logprob", (M, n)) if n else None, _ptr(top_id) if n else None,
+        *_rows_of(logits, "logits", (M, V), None), _dtype_code(logits), _ptr(tokens), n, M, V,
+        _current_stream(stream, logits)))
 
 
 LAYER_WEIGHTS = ("norm_w", "in_proj_w", "conv_w", "conv_b", "x_proj_w", "dt_proj_w", "dt_bias", "A_log", "D",

@@ -886,6 +886,114 @@ int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t
   return ok();
 }
 
+int mamba_linear_w4(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t ld_a, const uint8_t* q, int64_t ld_q,
+                    const void* scales, int64_t ld_s, int scale_dtype, const uint8_t* zeros, int64_t ld_z,
+                    int64_t group, const float* residual, int64_t ld_r, int64_t M, int64_t N, int64_t K,
+                    void* stream) {
+  int rc;
+  if ((rc = check_dtype("c_dtype", c_dtype)) || (rc = check_dtype("scale_dtype", scale_dtype))) return rc;
+  if (M < 0 || N < 0 || K < 1) return fail(MAMBA_ERR_INVALID_ARG, "sizes (M=%lld N=%lld K=%lld)", (long long)M, (long long)N, (long long)K);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MAMBA_ERR_UNSUPPORTED, "group=%lld not in {32, 64, 128}", (long long)group);
+  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || !sizes_ok(M, K) || !sizes_ok(N, K) || !sizes_ok(M, N))
+    return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if (M == 0 || N == 0) return ok();
+  if (!c || !a || !q || !scales) return fail(MAMBA_ERR_INVALID_ARG, "c, a, q and scales must not be NULL");
+  const int64_t groups = (K + group - 1) / group, row_bytes = (K + 31) / 32 * 16;
+  const int es = es_of(c_dtype);
+  View outs[] = {{"c", c, M, N, ld_c, es, 0}};
+  // the residual first: it may be c itself
+  View ins[] = {{"residual", residual, M, N, ld_r, 4, 0},
+                {"a", a, M, K, ld_a, 2, 0},
+                {"q", q, N, row_bytes, ld_q, 1, 0},
+                {"scales", scales, N, groups, ld_s, es_of(scale_dtype), 0},
+                {"zeros", zeros, N, groups, ld_z, 1, 0}};
+  if ((rc = check_views(outs, 1, ins, 5, true))) return rc;
+  if (reinterpret_cast<uintptr_t>(a) % 16 || reinterpret_cast<uintptr_t>(q) % 16 || (M > 1 && ld_a % 8) ||
+      (N > 1 && ld_q % 16))
+    return fail(MAMBA_ERR_INVALID_ARG, "a and q must be 16-byte aligned, ld_a a multiple of 8 and ld_q of 16");
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, 5, dev_id)) || (rc = check_view_pointers(outs, 1, dev_id))) return rc;
+  mamba::LinearW4Args g{c, ld_c, c_dtype == MAMBA_BF16, a, ld_a, q, ld_q, scales, ld_s, scale_dtype == MAMBA_BF16,
+                        zeros, ld_z, (int)group, residual, ld_r, M, N, K};
+  const cudaError_t e = mamba::launch_linear_w4(g, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("linear_w4 launch", e);
+  return ok();
+}
+
+int mamba_block_norm(float* x_out, int64_t ld_xo, void* out, int64_t ld_out, int out_dtype, const float* x,
+                     int64_t ld_x, const void* y, int64_t ld_y, int y_dtype, const float* pre_weight,
+                     const float* post_weight, const void* gate, int64_t ld_gate, int gate_dtype, int64_t gate_rows,
+                     float scale, float eps, int64_t M, int64_t D, void* stream) {
+  int rc;
+  if ((rc = check_dtype("out_dtype", out_dtype)) || (rc = check_dtype("y_dtype", y_dtype)) ||
+      (rc = check_dtype("gate_dtype", gate_dtype)))
+    return rc;
+  if (M < 0 || D < 1 || gate_rows < 0)
+    return fail(MAMBA_ERR_INVALID_ARG, "sizes (M=%lld D=%lld gate_rows=%lld)", (long long)M, (long long)D, (long long)gate_rows);
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(MAMBA_ERR_INVALID_ARG, "eps must be in [0, 1]");
+  if (!(scale - scale == 0.0f)) return fail(MAMBA_ERR_INVALID_ARG, "scale must be finite");
+  if (M > INT32_MAX || D > INT32_MAX || !sizes_ok(M, D)) return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if (M == 0) return ok();
+  if (!x_out || !x || !y) return fail(MAMBA_ERR_INVALID_ARG, "x_out, x and y must not be NULL");
+  if (!out != !pre_weight) return fail(MAMBA_ERR_INVALID_ARG, "out and pre_weight go together");
+  const int64_t g_rows = gate_rows == 0 ? 1 : (M + gate_rows - 1) / gate_rows;
+  View outs[] = {{"x_out", x_out, M, D, ld_xo, 4, 0}, {"out", out, M, D, ld_out, es_of(out_dtype), 0}};
+  View ins[] = {{"x", x, M, D, ld_x, 4, 0},
+                {"y", y, M, D, ld_y, es_of(y_dtype), 0},
+                {"gate", gate, g_rows, D, ld_gate, es_of(gate_dtype), 0},
+                {"pre_weight", pre_weight, 1, D, D, 4, 0},
+                {"post_weight", post_weight, 1, D, D, 4, 0}};
+  // only x may be an output's own view: y is checked against `out` as any other input
+  View y_view[] = {ins[1]}, out_view[] = {outs[1]};
+  if ((rc = check_views(outs, 2, ins, 5, true)) || (rc = check_views(out_view, 1, y_view, 1, false))) return rc;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, 5, dev_id)) || (rc = check_view_pointers(outs, 2, dev_id))) return rc;
+  mamba::BlockNormArgs n{x_out, ld_xo, out, ld_out, out_dtype == MAMBA_BF16, x, ld_x, y, ld_y, y_dtype == MAMBA_BF16,
+                         pre_weight, post_weight, gate, ld_gate, gate_dtype == MAMBA_BF16, gate_rows, scale, eps, M, D};
+  const cudaError_t e = mamba::launch_block_norm(n, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("block_norm launch", e);
+  return ok();
+}
+
+int mamba_token_logprobs(float* logprob, float* entropy, float* top_logprob, int64_t* top_id, const void* logits,
+                         int64_t ld, int dtype, const int64_t* tokens, int64_t n_top, int64_t M, int64_t V,
+                         void* stream) {
+  int rc;
+  if ((rc = check_dtype("dtype", dtype))) return rc;
+  if (M < 0 || V < 1 || n_top < 0 || n_top > V)
+    return fail(MAMBA_ERR_INVALID_ARG, "sizes (M=%lld V=%lld n_top=%lld)", (long long)M, (long long)V, (long long)n_top);
+  if (n_top > MAMBA_MAX_TOP) return fail(MAMBA_ERR_UNSUPPORTED, "n_top=%lld over %d", (long long)n_top, MAMBA_MAX_TOP);
+  if (V > INT32_MAX || M > INT32_MAX || !sizes_ok(M, V)) return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
+  if (M == 0) return ok();
+  if (!logits) return fail(MAMBA_ERR_INVALID_ARG, "logits must not be NULL");
+  if (!tokens != !logprob) return fail(MAMBA_ERR_INVALID_ARG, "tokens and logprob go together");
+  if ((n_top > 0) != (top_logprob != nullptr) || (n_top > 0) != (top_id != nullptr))
+    return fail(MAMBA_ERR_INVALID_ARG, "top_logprob and top_id go with n_top");
+  View outs[] = {{"logprob", logprob, 1, M, M, 4, 0},
+                 {"entropy", entropy, 1, M, M, 4, 0},
+                 {"top_logprob", top_logprob, 1, M * n_top, M * n_top, 4, 0},
+                 {"top_id", top_id, 1, M * n_top, M * n_top, 8, 0}};
+  View ins[] = {{"logits", logits, M, V, ld, es_of(dtype), 0}, {"tokens", tokens, 1, M, M, 8, 0}};
+  if ((rc = check_views(outs, 4, ins, 2, false))) return rc;
+  mamba::DeviceInfo dev;
+  if ((rc = current_device(&dev))) return rc;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if ((rc = check_view_pointers(ins, 2, dev_id)) || (rc = check_view_pointers(outs, 4, dev_id))) return rc;
+  mamba::TokenLogprobsArgs t{logprob, entropy, top_logprob, top_id, logits, ld, dtype == MAMBA_BF16, tokens, M, V,
+                             (int)n_top};
+  const cudaError_t e = mamba::launch_token_logprobs(t, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("token_logprobs launch", e);
+  return ok();
+}
+
 int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const float* x, int64_t ld_x, const float* weight,
                   float eps, int64_t M, int64_t D, void* stream) {
   int rc;

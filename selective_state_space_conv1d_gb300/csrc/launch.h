@@ -348,4 +348,66 @@ struct HeadNormArgs {
 };
 cudaError_t launch_head_norm_gated(const HeadNormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ------------------------------------------------- around a block: 4-bit ----
+// C[M][N] = A[M][K] . W[N][K]^T (+ R), A bf16, W in 4 bits: element k of row n is
+// scale[n][k / group] (q - zero[n][k / group]), byte j of a row holding q of k = 2 j
+// in its low half; rows of ceil(K / 32) 16 bytes at ld_q.
+struct LinearW4Args {
+  void* c;
+  int64_t ld_c;
+  int c_bf16;
+  const void* a;
+  int64_t ld_a;
+  const uint8_t* q;
+  int64_t ld_q;
+  const void* scales;
+  int64_t ld_s;
+  int s_bf16;
+  const uint8_t* zeros;  // or null (8)
+  int64_t ld_z;
+  int group;             // 32, 64 or 128
+  const float* r;        // residual [M][N] at ld_r, or null
+  int64_t ld_r;
+  int64_t M, N, K;
+};
+cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream);
+
+// x' = x + scale gate . (y, normed if post), out = x' normed (block_norm.cu)
+struct BlockNormArgs {
+  float* x_out;
+  int64_t ld_xo;
+  void* out;          // or null
+  int64_t ld_out;
+  int out_bf16;
+  const float* x;     // may be x_out
+  int64_t ld_x;
+  const void* y;
+  int64_t ld_y;
+  int y_bf16;
+  const float* pre;   // [D]; null with out
+  const float* post;  // [D] or null
+  const void* gate;   // or null
+  int64_t ld_gate;
+  int gate_bf16;
+  int64_t gate_rows;  // rows that share a row of the gate; 0: all
+  float scale, eps;
+  int64_t M, D;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// log probabilities of a token per row, entropy, the n_top likeliest (token_logprobs.cu)
+struct TokenLogprobsArgs {
+  float* logprob;        // [M] or null (with tokens)
+  float* entropy;        // [M] or null
+  float* top_logprob;    // [M][n_top]
+  int64_t* top_id;       // [M][n_top]
+  const void* logits;
+  int64_t ld;
+  int bf16;
+  const int64_t* tokens;
+  int64_t M, V;
+  int n_top;
+};
+cudaError_t launch_token_logprobs(const TokenLogprobsArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace mamba
