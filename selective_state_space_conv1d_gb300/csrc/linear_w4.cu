@@ -219,8 +219,8 @@ cudaError_t launch_group(const LinearW4Args& g, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream) {
-  (void)dev;
   if (g.M <= 0 || g.N <= 0) return cudaSuccess;
+  if (g.M > 8) return launch_gemm_w4(g, dev, stream);
   if (g.group == 32) return launch_group<32>(g, stream);
   if (g.group == 64) return launch_group<64>(g, stream);
   return launch_group<128>(g, stream);
