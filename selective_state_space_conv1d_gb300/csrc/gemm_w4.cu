@@ -48,6 +48,7 @@ constexpr int kBN = 128;    // weight rows per tile
 constexpr int kBK = 64;     // k per operand stage: one 128-byte swizzle row
 constexpr int kChunk = 128; // k per copy of weights
 constexpr int kEpiWarps = 8;
+constexpr int kReduceChunks = 3;  // a cluster's reduction takes about as long as 3 chunks
 constexpr int kSmemLimit = 232448;
 constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
@@ -61,26 +62,25 @@ struct Cfg {
   // registers per thread of the roles; their sum over the warpgroups is within what
   // the CTA is launched with (128 x 4 and 96 x 5)
   static constexpr int kRegsLoad = 40;
-  static constexpr int kRegsDq = kDqGroups == 1 ? 96 : 88;
-  static constexpr int kRegsEpi = kDqGroups == 1 ? 184 : 128;
+  static constexpr int kRegsDq = 88;
+  static constexpr int kRegsEpi = kDqGroups == 1 ? 192 : 128;
   static constexpr int kRegs = kRegsLoad + kDqGroups * kRegsDq + 2 * kRegsEpi;
   static_assert(kRegs <= (65536 / kThreads / 8 * 8) * (kThreads / 128), "more registers than a CTA has");
   static constexpr int kStageB = BT * kBK * 2;
   static constexpr int kStageA = kBN * kBK * 2;
   static constexpr int kStageQ = kBN * kChunk / 2;
-  static constexpr int kSB = BT == 256 ? 4 : (BT == 128 ? 6 : 8);
-  static constexpr int kSA = BT == 256 ? 3 : 4;
-  static constexpr int kOffA = kSB * kStageB;
-  static constexpr int kOffQ = kOffA + kSA * kStageA;
+  static constexpr int kStage = kStageB + kStageA;
+  static constexpr int kS = BT == 256 ? 4 : (BT == 128 ? 5 : 6);  // operand stages
+  static constexpr int kOffQ = kS * kStage;
   static constexpr int kSQ0 = (kSmemLimit - 1024 - 512 - kOffQ) / kStageQ;
-  static constexpr int kSQ = kSQ0 > 8 ? 8 : kSQ0;
+  static constexpr int kSQ = kSQ0 > 8 ? 8 : kSQ0;                 // weights as they are stored
   static constexpr int kOffBar = kOffQ + kSQ * kStageQ;
-  static constexpr int kBars = 2 * (kSB + kSA + kSQ) + 5;
+  static constexpr int kBars = 2 * (kS + kSQ) + 5;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base
   static constexpr int kTmemCols = 2 * BT;
   static constexpr int kPartPitch = kBN + 4;
-  static_assert(kAlloc <= kSmemLimit && kSQ >= 2, "shared memory");
+  static_assert(kAlloc <= kSmemLimit && kSQ >= 2 && kS >= 4, "shared memory");
 };
 
 template <int BT>
@@ -146,6 +146,59 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {
   return *reinterpret_cast<const __nv_bfloat162*>(&v);
 }
 
+// a row's scale of group g, 0 past its groups
+__device__ __forceinline__ float scale_at(const void* scales, int s_bf16, int64_t row, int g, int groups) {
+  if (g >= groups) return 0.0f;
+  return s_bf16 ? to_f32(static_cast<const __nv_bfloat16*>(scales)[row + g])
+                : static_cast<const float*>(scales)[row + g];
+}
+
+// a row's zero point for the b-th 32 k
+template <int GROUP>
+__device__ __forceinline__ uint32_t zero_at(const uint8_t* row, int b, int K) {
+  return row && b * 32 < K ? row[b * 32 / GROUP] & 127u : 8u;
+}
+
+// one weight row's totals down a column of C, the residual (or null) added: 16 at a
+// time, a batch's residuals read together
+template <typename T, int PAIRS>
+__device__ __forceinline__ void store_totals(T* c, int64_t ld_c, const float* r, int64_t ld_r,
+                                             const float2 (&total)[PAIRS], int cols) {
+#pragma unroll
+  for (int j0 = 0; j0 < 2 * PAIRS; j0 += 16) {
+    if (j0 >= cols) return;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = j & 1 ? total[(j0 + j) / 2].y : total[(j0 + j) / 2].x;
+    if (cols - j0 >= 16) {
+      if (r) {
+        float rv[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) rv[j] = r[j * ld_r];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += rv[j];
+        r += 16 * ld_r;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        *c = from_f32<T>(v[j]);
+        c += ld_c;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j0 + j < cols) c[j * ld_c] = from_f32<T>(r ? v[j] + r[j * ld_r] : v[j]);
+    }
+  }
+}
+
+// the stage that was written is handed to the tensor cores
+__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void fail_w4(volatile int* abort_flag) {
   atomicOr(&g_gemm_w4_faults, MAMBA_FAULT_GEMM_WAIT);
   *abort_flag = 1;
@@ -158,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
                    const uint8_t* __restrict__ zeros, int64_t ld_z, const float* r, int64_t ld_r, int M, int N, int K,
                    int splits) {
   using L = Cfg<BT>;
-  constexpr int SA = L::kSA, SB = L::kSB, SQ = L::kSQ;
+  constexpr int S = L::kS, SQ = L::kSQ;
   constexpr int kG = kChunk / GROUP;          // groups per chunk
   constexpr int kStepsPerGroup = GROUP / 16;  // products per group
   extern __shared__ unsigned char smem_raw[];
@@ -166,15 +219,15 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   const uint32_t base = (raw + 1023) & ~1023u;
   unsigned char* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::kOffBar;
-  auto b_full = [&](int s) { return bars + 8 * s; };
-  auto b_empty = [&](int s) { return bars + 8 * (SB + s); };
-  auto a_full = [&](int s) { return bars + 8 * (2 * SB + s); };
-  auto a_empty = [&](int s) { return bars + 8 * (2 * SB + SA + s); };
-  auto q_full = [&](int s) { return bars + 8 * (2 * (SB + SA) + s); };
-  auto q_empty = [&](int s) { return bars + 8 * (2 * (SB + SA) + SQ + s); };
-  auto acc_full = [&](int a) { return bars + 8 * (2 * (SB + SA + SQ) + a); };
-  auto acc_empty = [&](int a) { return bars + 8 * (2 * (SB + SA + SQ) + 2 + a); };
-  const uint32_t drain = bars + 8 * (2 * (SB + SA + SQ) + 4);
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (S + s); };
+  auto q_full = [&](int s) { return bars + 8 * (2 * S + s); };
+  auto q_empty = [&](int s) { return bars + 8 * (2 * S + SQ + s); };
+  auto mid = [&](int a) { return bars + 8 * (2 * (S + SQ) + a); };
+  auto acc_empty = [&](int a) { return bars + 8 * (2 * (S + SQ) + 2 + a); };
+  const uint32_t drain = bars + 8 * (2 * (S + SQ) + 4);
+  auto stage_b = [&](int s) { return base + (uint32_t)(s * L::kStage); };
+  auto stage_a = [&](int s) { return base + (uint32_t)(s * L::kStage + L::kStageB); };
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
 
@@ -192,20 +245,16 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < SB; ++s) {
-      mbar_init(b_full(s), 1);
-      mbar_init(b_empty(s), 1);
-    }
-    for (int s = 0; s < SA; ++s) {
-      mbar_init(a_full(s), 4);
-      mbar_init(a_empty(s), 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 5);  // the copy of the activations and four warps' weights
+      mbar_init(empty(s), 1);
     }
     for (int s = 0; s < SQ; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 4 * L::kDqGroups);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(acc_full(a), 1);
+      mbar_init(mid(a), 1);
       mbar_init(acc_empty(a), kEpiWarps);
     }
     mbar_init(drain, 1);
@@ -234,17 +283,18 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       for (int t = t_first; t < tiles && !*abort_flag; t += t_step) {
         const int m0 = t / n_tiles * BT;
         for (int ks = 2 * cb; ks < 2 * ce; ++ks, ++g) {
-          const int s = g % SB;
-          if (g >= SB && !mbar_wait(b_empty(s), (g / SB + 1) & 1, kWaitLimit)) {
+          const int s = g % S;
+          if (g >= S && !mbar_wait(empty(s), (g / S + 1) & 1, kWaitLimit)) {
             fail_w4(abort_flag);
             break;
           }
-          mbar_arrive_expect_tx(b_full(s), L::kStageB);
-          tma_load_2d(base + s * L::kStageB, &map_a, ks * kBK, m0, b_full(s));
+          mbar_arrive_expect_tx(full(s), L::kStageB);
+          tma_load_2d(stage_b(s), &map_a, ks * kBK, m0, full(s));
         }
       }
-      for (int i = g > SB ? g - SB : 0; i < g; ++i)
-        if (!mbar_wait(b_full(i % SB), (i / SB) & 1, kWaitLimit)) fail_w4(abort_flag);
+      // the copies issued land: their stages complete, unless the weights' side gave up
+      for (int i = g > S ? g - S : 0; i < g; ++i)
+        if (!mbar_wait(full(i % S), (i / S) & 1, kWaitLimit)) fail_w4(abort_flag);
     } else if (warp == 2 && lane == 0) {
       // weights
       int g = 0;
@@ -272,31 +322,30 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half, ++g) {
             if (!ok) break;
-            const int sa = g % SA, sb = g % SB;
-            if (!mbar_wait(a_full(sa), (g / SA) & 1, kWaitLimit) || !mbar_wait(b_full(sb), (g / SB) & 1, kWaitLimit)) {
+            const int s = g % S;
+            if (!mbar_wait(full(s), (g / S) & 1, kWaitLimit)) {
               ok = false;
               break;
             }
             tcgen05_fence_after();
-            const uint64_t da = smem_desc(base + L::kOffA + sa * L::kStageA), db = smem_desc(base + sb * L::kStageB);
+            const uint64_t da = smem_desc(stage_a(s)), db = smem_desc(stage_b(s));
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k) {
               const int step = half * 4 + k;
-              if (step % kStepsPerGroup == 0 && acc >= 2) {
-                if (!mbar_wait(acc_empty(acc & 1), (acc / 2 + 1) & 1, kWaitLimit)) {
+              if (step % kStepsPerGroup == 0) {
+                if (acc >= 2 && !mbar_wait(acc_empty(acc & 1), (acc / 2 + 1) & 1, kWaitLimit)) {
                   ok = false;
                   break;
                 }
                 tcgen05_fence_after();
               }
               mma_bf16(tmem + (uint32_t)((acc & 1) * BT), da + 2 * k, db + 2 * k, idesc, step % kStepsPerGroup != 0);
-              if ((step + 1) % kStepsPerGroup == 0) {
-                mma_commit(acc_full(acc & 1));
-                ++acc;
-              }
+              if ((step + 1) % kStepsPerGroup == 0) ++acc;
+              // a commit takes the issuing thread about 180 cycles: a stage's own says
+              // too that the group which ends with it is complete
+              if (GROUP == 32 && k == 1) mma_commit(mid(g & 1));
             }
-            mma_commit(a_empty(sa));
-            mma_commit(b_empty(sb));
+            mma_commit(empty(s));
           }
         }
       }
@@ -305,51 +354,71 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       if (!mbar_wait(drain, 0, kWaitLimit)) fail_w4(abort_flag);
     }
   } else if (warp < L::kEpiWarp) {
-    // nibbles to bf16: thread = weight row of the tile
+    // nibbles to bf16: thread = weight row of the tile.  A stage is handed over one
+    // turn after it was written: its stores are done by then, and the fence that
+    // makes them visible to the tensor cores waits for nothing.
     regs_dec<L::kRegsDq>();
     const int wg = warp / 4 - 1;
     const int row = threadIdx.x & 127;
-    int g = 0;
+    int g = 0, owed = -1;  // chunks taken; the stage not handed over yet
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row;
       const uint8_t* zrow = zeros && n < N ? zeros + (int64_t)n * ld_z : nullptr;
-      for (int ch = cb; ch < ce && ok; ++ch, ++g) {
-        const int s = g % SQ;
-        uint32_t zp[4];
+      uint32_t zp[4], zn[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) zp[b] = zrow && ch * kChunk + b * 32 < K ? zrow[ch * kG + b * 32 / GROUP] & 127u : 8u;
+      for (int b = 0; b < 4; ++b) zn[b] = zero_at<GROUP>(zrow, cb * 4 + b, K);
+      for (int ch = cb; ch < ce; ++ch, ++g) {
+        const int s = g % SQ;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          zp[b] = zn[b];
+          if (ch + 1 < ce) zn[b] = zero_at<GROUP>(zrow, ch * 4 + 4 + b, K);
+        }
         if (!mbar_wait(q_full(s), (g / SQ) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
-        const uint4* src = reinterpret_cast<const uint4*>(gbase + L::kOffQ + s * L::kStageQ + row * 64);
+        // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
+        const unsigned char* src = gbase + L::kOffQ + s * L::kStageQ + row * 64;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (L::kDqGroups == 2 && half != wg) continue;
-          const uint4 q[2] = {src[2 * half], src[2 * half + 1]};
-          const int ks = 2 * g + half, sa = ks % SA;
-          if (ks >= SA && !mbar_wait(a_empty(sa), (ks / SA + 1) & 1, kWaitLimit)) {
-            ok = false;
-            break;
-          }
-          unsigned char* dst = gbase + L::kOffA + sa * L::kStageA + row * 128;
+          uint4 q[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            q[b] = *reinterpret_cast<const uint4*>(src + (((2 * half + b) ^ ((row >> 1) & 3)) << 4));
+          const int ks = 2 * g + half, sa = ks % S;
+          uint4 v[8];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const __nv_bfloat162 zc = zero_pair(zp[2 * half + b]);
-            const uint32_t w[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(dst + (((b * 4 + i) ^ (row & 7)) << 4)) = unpack8(w[i], zc);
+            v[4 * b] = unpack8(q[b].x, zc);
+            v[4 * b + 1] = unpack8(q[b].y, zc);
+            v[4 * b + 2] = unpack8(q[b].z, zc);
+            v[4 * b + 3] = unpack8(q[b].w, zc);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(a_full(sa));
+          if (owed >= 0) hand_over(full(owed), lane);  // before a wait that may need it
+          owed = -1;
+          if (ks >= S && !mbar_wait(empty(sa), (ks / S + 1) & 1, kWaitLimit)) {
+            ok = false;
+            break;
+          }
+          unsigned char* dst = gbase + sa * L::kStage + L::kStageB + row * 128;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (row & 7)) << 4)) = v[i];
+          owed = sa;
+          // the copy of the next weights goes through another proxy than the reads of
+          // these: it may start when they are done for certain, their results stored
+          if (L::kDqGroups == 2 || half == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty(s));
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty(s));
+        if (!ok) break;
       }
     }
+    if (owed >= 0) hand_over(full(owed), lane);
     if (!ok && lane == 0) fail_w4(abort_flag);
   } else {
     regs_inc<L::kRegsEpi>();
@@ -364,16 +433,17 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       float2 total[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) total[j] = make_float2(0.0f, 0.0f);
-      auto scale_of = [&](int gr) {
-        if (!n_in || (int64_t)gr * GROUP >= K) return 0.0f;
-        const int64_t i = (int64_t)n * ld_s + gr;
-        return s_bf16 ? to_f32(static_cast<const __nv_bfloat16*>(scales)[i]) : static_cast<const float*>(scales)[i];
-      };
-      float next = scale_of(cb * kG);
+      const int groups = n_in ? (K + GROUP - 1) / GROUP : 0;
+      const int64_t s_row = (int64_t)n * ld_s;
+      float next = scale_at(scales, s_bf16, s_row, cb * kG, groups);
       for (int gr = cb * kG; gr < ce * kG; ++gr, ++acc) {
         const float sc = next;
-        if (gr + 1 < ce * kG) next = scale_of(gr + 1);
-        if (!mbar_wait(acc_full(acc & 1), (acc / 2) & 1, kWaitLimit)) {
+        next = scale_at(scales, s_bf16, s_row, gr + 1, groups);
+        // the group is complete when its last stage is (or half of it): the products are
+        // at most two groups ahead of this, so that barrier's next phase is not over
+        const int ks = GROUP == 128 ? 2 * acc + 1 : (GROUP == 64 ? acc : acc / 2);
+        const bool half = GROUP == 32 && !(acc & 1);
+        if (!mbar_wait(half ? mid(ks & 1) : empty(ks % S), (half ? ks / 2 : ks / S) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
@@ -409,27 +479,10 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       } else if (n_in) {
         const int cols = M - m0 < kCols ? M - m0 : kCols;
         const float* rp = r ? r + (int64_t)m0 * ld_r + n : nullptr;
-        if (c_bf16) {
-          __nv_bfloat16* cp = static_cast<__nv_bfloat16*>(c) + (int64_t)m0 * ld_c + n;
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) {
-            float v = j & 1 ? total[j / 2].y : total[j / 2].x;
-            if (j < cols) {
-              if (rp) v += rp[(int64_t)j * ld_r];
-              cp[(int64_t)j * ld_c] = __float2bfloat16_rn(v);
-            }
-          }
-        } else {
-          float* cp = static_cast<float*>(c) + (int64_t)m0 * ld_c + n;
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) {
-            float v = j & 1 ? total[j / 2].y : total[j / 2].x;
-            if (j < cols) {
-              if (rp) v += rp[(int64_t)j * ld_r];
-              cp[(int64_t)j * ld_c] = v;
-            }
-          }
-        }
+        if (c_bf16)
+          store_totals(static_cast<__nv_bfloat16*>(c) + (int64_t)m0 * ld_c + n, ld_c, rp, ld_r, total, cols);
+        else
+          store_totals(static_cast<float*>(c) + (int64_t)m0 * ld_c + n, ld_c, rp, ld_r, total, cols);
       }
     }
     if (!ok && lane == 0) fail_w4(abort_flag);
@@ -468,25 +521,85 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols) : "memory");
 }
 
+constexpr int kMaxSplits = 8;
+constexpr int kMaxDevices = 64;
+
+// Shared memory, the check of the registers, and how many clusters of each size the
+// device holds at once (a GPC's SMs are no multiple of most sizes).
+struct Resident {
+  int configured;
+  int clusters[kMaxSplits + 1];
+};
+
 template <int BT, int GROUP, bool SPLIT>
-cudaError_t launch_one(const LinearW4Args& g, const CUtensorMap& ma, const CUtensorMap& mq, int sms, int splits,
-                       cudaStream_t stream) {
+cudaError_t configure(const Resident** out) {
   auto kern = gemm_w4_kernel<BT, GROUP, SPLIT>;
   using L = Cfg<BT>;
-  static int configured[64];
+  static Resident resident[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!__atomic_load_n(&configured[dev], __ATOMIC_RELAXED)) {
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  Resident& r = resident[dev];
+  if (!__atomic_load_n(&r.configured, __ATOMIC_ACQUIRE)) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
     // the roles' registers come out of what the CTA is launched with
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
     if (at.numRegs * (L::kThreads / 128) < L::kRegs) return cudaErrorInvalidConfiguration;
-    __atomic_store_n(&configured[dev], 1, __ATOMIC_RELAXED);
+    if (SPLIT) {
+      for (int size = 2; size <= kMaxSplits; ++size) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(L::kThreads);
+        cfg.dynamicSmemBytes = L::kAlloc;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+        __atomic_store_n(&r.clusters[size], n, __ATOMIC_RELAXED);
+      }
+    }
+    __atomic_store_n(&r.configured, 1, __ATOMIC_RELEASE);
   }
+  *out = &r;
+  return cudaSuccess;
+}
+
+// Chunks of K a CTA works through one after another, and the reduction's time in chunks
+template <int BT, int GROUP>
+cudaError_t choose_splits(const LinearW4Args& g, int sms, int* splits) {
+  const Resident* r = nullptr;
+  const cudaError_t e = configure<BT, GROUP, true>(&r);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((g.M + BT - 1) / BT) * ((g.N + kBN - 1) / kBN), chunks = (g.K + kChunk - 1) / kChunk;
+  int64_t best = (tiles + sms - 1) / sms * chunks;
+  *splits = 1;
+  for (int size = 2; size <= kMaxSplits && size <= chunks; ++size) {
+    const int64_t held = __atomic_load_n(&r->clusters[size], __ATOMIC_RELAXED);
+    if (held < 1) continue;
+    const int64_t cost = (tiles + held - 1) / held * ((chunks + size - 1) / size + kReduceChunks);
+    if (cost < best) {
+      best = cost;
+      *splits = size;
+    }
+  }
+  return cudaSuccess;
+}
+
+template <int BT, int GROUP, bool SPLIT>
+cudaError_t launch_one(const LinearW4Args& g, const CUtensorMap& ma, const CUtensorMap& mq, int sms, int splits,
+                       cudaStream_t stream) {
+  auto kern = gemm_w4_kernel<BT, GROUP, SPLIT>;
+  using L = Cfg<BT>;
+  const Resident* held = nullptr;
+  const cudaError_t e = configure<BT, GROUP, SPLIT>(&held);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.M + BT - 1) / BT) * ((g.N + kBN - 1) / kBN);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * splits : (tiles < sms ? tiles : sms)));
@@ -513,18 +626,18 @@ cudaError_t launch_bt(const LinearW4Args& g, int sms, cudaStream_t stream) {
   if (!tensor_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, g.M, g.K, (g.M > 1 ? g.ld_a : (g.K + 7) / 8 * 8) * 2,
                      BT, kBK, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tensor_map_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, g.N, row_bytes, g.N > 1 ? g.ld_q : row_bytes, kBN,
-                     kChunk / 2, CU_TENSOR_MAP_SWIZZLE_NONE))
+                     kChunk / 2, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  // a cluster per tile where the tiles leave SMs idle: up to 8 CTAs, a chunk each at least
-  const int64_t tiles = ((g.M + BT - 1) / BT) * ((g.N + kBN - 1) / kBN), chunks = (g.K + kChunk - 1) / kChunk;
-  int64_t splits = tiles <= sms ? sms / tiles : 1;
-  if (splits > 8) splits = 8;
-  if (splits > chunks) splits = chunks;
   if constexpr (BT <= 128) {
+    int splits = 1;
+    const cudaError_t e = g.group == 32   ? choose_splits<BT, 32>(g, sms, &splits)
+                          : g.group == 64 ? choose_splits<BT, 64>(g, sms, &splits)
+                                          : choose_splits<BT, 128>(g, sms, &splits);
+    if (e != cudaSuccess) return e;
     if (splits > 1) {
-      if (g.group == 32) return launch_one<BT, 32, true>(g, ma, mq, sms, (int)splits, stream);
-      if (g.group == 64) return launch_one<BT, 64, true>(g, ma, mq, sms, (int)splits, stream);
-      return launch_one<BT, 128, true>(g, ma, mq, sms, (int)splits, stream);
+      if (g.group == 32) return launch_one<BT, 32, true>(g, ma, mq, sms, splits, stream);
+      if (g.group == 64) return launch_one<BT, 64, true>(g, ma, mq, sms, splits, stream);
+      return launch_one<BT, 128, true>(g, ma, mq, sms, splits, stream);
     }
   }
   if (g.group == 32) return launch_one<BT, 32, false>(g, ma, mq, sms, 1, stream);
