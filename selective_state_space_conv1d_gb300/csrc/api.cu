@@ -460,14 +460,14 @@ int mamba_device_faults(int clear) {
   const int v2 = mamba::read_scan_faults(clear != 0);
   if (v2 < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the scan watchdog failed");
   const int vg = mamba::read_gemm_faults(clear != 0);
-  const int vq = mamba::read_gemm_w4_faults(clear != 0), vl = mamba::read_linear_w4_faults(clear != 0);
-  if (vg < 0 || vq < 0 || vl < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the GEMM watchdog failed");
+  const int vq = mamba::read_gemm_w4_faults(clear != 0);
+  if (vg < 0 || vq < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the GEMM watchdog failed");
   if (v3 < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the Mamba-3 watchdog failed");
   const int vs = mamba::read_selftest_faults(clear != 0);
   if (vs < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the self-test watchdog failed");
   const int vd = mamba::read_delta_faults(clear != 0);
   if (vd < 0) return fail(MAMBA_ERR_CUDA, "mamba_device_faults: reading the gated-delta watchdog failed");
-  return ok(), v | v2 | v3 | vs | vg | vq | vl | vd;
+  return ok(), v | v2 | v3 | vs | vg | vq | vd;
 }
 
 int mamba_selftest_bounded_wait(int64_t limit_cycles, int complete, void* stream) {

@@ -45,7 +45,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kBN = 128;    // weight rows per tile
-constexpr int kBK = 64;     // k per operand stage: one 128-byte swizzle row
+constexpr int kBK = 64;     // k per operand block: one 128-byte swizzle row
 constexpr int kChunk = 128; // k per copy of weights
 constexpr int kEpiWarps = 8;
 constexpr int kReduceChunks = 3;  // a cluster's reduction takes about as long as 3 chunks
@@ -54,33 +54,54 @@ constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
 __device__ int g_gemm_w4_faults = 0;
 
+// The totals of a wide tile take half of the registers, so stages are of 64 k and two
+// warpgroups make bf16 of nibbles; narrow ones have stages of 128 k (a stage costs its
+// waits and hand-overs, whatever it holds) and four such warpgroups.  Each takes 32 k of
+// every stage, which is ready after a quarter (or half) of the work.
 template <int BT>
 struct Cfg {
-  static constexpr int kDqGroups = BT > 128 ? 1 : 2;  // warpgroups that make bf16 of nibbles
+  static constexpr int kSub = BT > 128 ? 1 : 2;   // operand blocks per stage
+  static constexpr int kDqGroups = 2 * kSub;      // warpgroups that make bf16 of nibbles
   static constexpr int kThreads = 128 * (1 + kDqGroups + 2);
   static constexpr int kEpiWarp = 4 * (1 + kDqGroups);
   // registers per thread of the roles; their sum over the warpgroups is within what
-  // the CTA is launched with (128 x 4 and 96 x 5)
-  static constexpr int kRegsLoad = 40;
-  static constexpr int kRegsDq = 88;
-  static constexpr int kRegsEpi = kDqGroups == 1 ? 192 : 128;
+  // the CTA is launched with (96 x 5 and 72 x 7)
+  static constexpr int kRegsLoad = BT > 128 ? 32 : 40;
+  static constexpr int kRegsDq = BT > 128 ? 56 : 48;
+  static constexpr int kRegsEpi = BT > 128 ? 168 : (BT > 64 ? 128 : 104);
   static constexpr int kRegs = kRegsLoad + kDqGroups * kRegsDq + 2 * kRegsEpi;
   static_assert(kRegs <= (65536 / kThreads / 8 * 8) * (kThreads / 128), "more registers than a CTA has");
-  static constexpr int kStageB = BT * kBK * 2;
-  static constexpr int kStageA = kBN * kBK * 2;
+  static constexpr int kBlockB = BT * kBK * 2;
+  static constexpr int kBlockA = kBN * kBK * 2;
+  static constexpr int kStageB = kSub * kBlockB;
+  static constexpr int kStage = kStageB + kSub * kBlockA;
   static constexpr int kStageQ = kBN * kChunk / 2;
-  static constexpr int kStage = kStageB + kStageA;
-  static constexpr int kS = BT == 256 ? 4 : (BT == 128 ? 5 : 6);  // operand stages
+  static constexpr int kS = BT > 128 ? 4 : 3;                     // operand stages
   static constexpr int kOffQ = kS * kStage;
   static constexpr int kSQ0 = (kSmemLimit - 1024 - 512 - kOffQ) / kStageQ;
   static constexpr int kSQ = kSQ0 > 8 ? 8 : kSQ0;                 // weights as they are stored
   static constexpr int kOffBar = kOffQ + kSQ * kStageQ;
-  static constexpr int kBars = 2 * (kS + kSQ) + 5;
+  static constexpr int kBars = 2 * (kS + kSQ) + 3 * 8 + 1;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base
-  static constexpr int kTmemCols = 2 * BT;
   static constexpr int kPartPitch = kBN + 4;
-  static_assert(kAlloc <= kSmemLimit && kSQ >= 2 && kS >= 4, "shared memory");
+  static_assert(kAlloc <= kSmemLimit && kSQ >= 2 && kS >= 3, "shared memory");
+};
+
+// Accumulators: as many as tensor memory holds, up to 8, so that the way from a group's
+// products to its totals and back (about 800 cycles) is not waited for group by group.
+template <int BT, int GROUP>
+struct Acc {
+  static constexpr int kStageK = Cfg<BT>::kSub * kBK;
+  static constexpr int kMost = 512 / BT < 8 ? 512 / BT : 8;
+  // (a group inside a stage is told by a barrier of its own, one that ends a stage by the
+  // stage's: the products may be ahead of the totals by fewer stages than there are)
+  static constexpr int kAcc = GROUP == 64 && kMost > 4 ? 4 : kMost;
+  // a stage is a group: the groups' barriers tell both, and there are accumulators enough
+  // that none is a whole round behind
+  static constexpr bool kOne = GROUP == kStageK && kAcc >= Cfg<BT>::kS;
+  static constexpr int kCols = kAcc * BT;
+  static_assert(kOne || (kAcc * GROUP + kStageK - 1) / kStageK <= Cfg<BT>::kS, "a stage's barrier a round behind");
 };
 
 template <int BT>
@@ -146,11 +167,11 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {
   return *reinterpret_cast<const __nv_bfloat162*>(&v);
 }
 
-// a row's scale of group g, 0 past its groups
-__device__ __forceinline__ float scale_at(const void* scales, int s_bf16, int64_t row, int g, int groups) {
-  if (g >= groups) return 0.0f;
-  return s_bf16 ? to_f32(static_cast<const __nv_bfloat16*>(scales)[row + g])
-                : static_cast<const float*>(scales)[row + g];
+// the bits of a row's scale of group g, 0 past its groups (a value that is made of what a
+// load brings would be waited for where it is made)
+__device__ __forceinline__ uint32_t scale_bits(const void* scales, int s_bf16, int64_t row, int g, int groups) {
+  if (g >= groups) return 0;
+  return s_bf16 ? static_cast<const uint16_t*>(scales)[row + g] : static_cast<const uint32_t*>(scales)[row + g];
 }
 
 // a row's zero point for the b-th 32 k
@@ -192,13 +213,6 @@ __device__ __forceinline__ void store_totals(T* c, int64_t ld_c, const float* r,
   }
 }
 
-// the stage that was written is handed to the tensor cores
-__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-
 __device__ __forceinline__ void fail_w4(volatile int* abort_flag) {
   atomicOr(&g_gemm_w4_faults, MAMBA_FAULT_GEMM_WAIT);
   *abort_flag = 1;
@@ -214,6 +228,8 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   constexpr int S = L::kS, SQ = L::kSQ;
   constexpr int kG = kChunk / GROUP;          // groups per chunk
   constexpr int kStepsPerGroup = GROUP / 16;  // products per group
+  constexpr int kStages = 2 / L::kSub;        // operand stages per chunk
+  constexpr int kSteps = 4 * L::kSub;         // products per stage
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
@@ -223,9 +239,18 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   auto empty = [&](int s) { return bars + 8 * (S + s); };
   auto q_full = [&](int s) { return bars + 8 * (2 * S + s); };
   auto q_empty = [&](int s) { return bars + 8 * (2 * S + SQ + s); };
+  using A = Acc<BT, GROUP>;
+  constexpr int kAcc = A::kAcc;
   auto mid = [&](int a) { return bars + 8 * (2 * (S + SQ) + a); };
-  auto acc_empty = [&](int a) { return bars + 8 * (2 * (S + SQ) + 2 + a); };
-  const uint32_t drain = bars + 8 * (2 * (S + SQ) + 4);
+  auto acc_empty = [&](int a) { return bars + 8 * (2 * (S + SQ) + 8 + a); };
+  auto done = [&](int a) { return bars + 8 * (2 * (S + SQ) + 16 + a); };
+  const uint32_t drain = bars + 8 * (2 * (S + SQ) + 24);
+  // stage number st may be written again: the products that read what it held are done
+  auto stage_free = [&](int st) {
+    if (st < S) return true;
+    if (A::kOne) return mbar_wait(done((st - S) % kAcc), (uint32_t)((st - S) / kAcc) & 1, kWaitLimit);
+    return mbar_wait(empty(st % S), (uint32_t)(st / S + 1) & 1, kWaitLimit);
+  };
   auto stage_b = [&](int s) { return base + (uint32_t)(s * L::kStage); };
   auto stage_a = [&](int s) { return base + (uint32_t)(s * L::kStage + L::kStageB); };
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
@@ -246,15 +271,16 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 5);  // the copy of the activations and four warps' weights
+      mbar_init(full(s), 1 + 4 * L::kDqGroups);  // the copy of the activations, the weights' warps
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < SQ; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 4 * L::kDqGroups);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kAcc; ++a) {
       mbar_init(mid(a), 1);
+      mbar_init(done(a), 1);
       mbar_init(acc_empty(a), kEpiWarps);
     }
     mbar_init(drain, 1);
@@ -263,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_ptr)),
-                 "r"(L::kTmemCols)
+                 "r"(A::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -282,14 +308,16 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       int g = 0;
       for (int t = t_first; t < tiles && !*abort_flag; t += t_step) {
         const int m0 = t / n_tiles * BT;
-        for (int ks = 2 * cb; ks < 2 * ce; ++ks, ++g) {
+        for (int st = kStages * cb; st < kStages * ce; ++st, ++g) {
           const int s = g % S;
-          if (g >= S && !mbar_wait(empty(s), (g / S + 1) & 1, kWaitLimit)) {
+          if (!stage_free(g)) {
             fail_w4(abort_flag);
             break;
           }
           mbar_arrive_expect_tx(full(s), L::kStageB);
-          tma_load_2d(stage_b(s), &map_a, ks * kBK, m0, full(s));
+#pragma unroll
+          for (int sub = 0; sub < L::kSub; ++sub)
+            tma_load_2d(stage_b(s) + sub * L::kBlockB, &map_a, (st * L::kSub + sub) * kBK, m0, full(s));
         }
       }
       // the copies issued land: their stages complete, unless the weights' side gave up
@@ -315,12 +343,12 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
     } else if (warp == 1 && lane == 0) {
       // products
       constexpr uint32_t idesc = instr_desc<BT>();
-      int g = 0, acc = 0;
+      int g = 0, acc = 0, inner = 0;
       bool ok = true;
       for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
         for (int ch = cb; ch < ce && ok; ++ch) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half, ++g) {
+          for (int st = 0; st < kStages; ++st, ++g) {
             if (!ok) break;
             const int s = g % S;
             if (!mbar_wait(full(s), (g / S) & 1, kWaitLimit)) {
@@ -328,24 +356,27 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
               break;
             }
             tcgen05_fence_after();
-            const uint64_t da = smem_desc(stage_a(s)), db = smem_desc(stage_b(s));
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) {
-              const int step = half * 4 + k;
+            for (int k = 0; k < kSteps; ++k) {
+              const int step = st * kSteps + k;
               if (step % kStepsPerGroup == 0) {
-                if (acc >= 2 && !mbar_wait(acc_empty(acc & 1), (acc / 2 + 1) & 1, kWaitLimit)) {
+                if (acc >= kAcc && !mbar_wait(acc_empty(acc % kAcc), (uint32_t)(acc / kAcc + 1) & 1, kWaitLimit)) {
                   ok = false;
                   break;
                 }
                 tcgen05_fence_after();
               }
-              mma_bf16(tmem + (uint32_t)((acc & 1) * BT), da + 2 * k, db + 2 * k, idesc, step % kStepsPerGroup != 0);
-              if ((step + 1) % kStepsPerGroup == 0) ++acc;
-              // a commit takes the issuing thread about 180 cycles: a stage's own says
-              // too that the group which ends with it is complete
-              if (GROUP == 32 && k == 1) mma_commit(mid(g & 1));
+              const uint64_t da = smem_desc(stage_a(s) + (k / 4) * L::kBlockA) + 2 * (k % 4);
+              const uint64_t db = smem_desc(stage_b(s) + (k / 4) * L::kBlockB) + 2 * (k % 4);
+              mma_bf16(tmem + (uint32_t)(acc % kAcc * BT), da, db, idesc, step % kStepsPerGroup != 0);
+              if ((step + 1) % kStepsPerGroup == 0) {
+                ++acc;
+                // a commit takes the issuing thread about 180 cycles: the stage's own
+                // says too that the group which ends with it is complete
+                if (k + 1 < kSteps) mma_commit(mid(inner++ % kAcc));
+              }
             }
-            mma_commit(empty(s));
+            mma_commit(A::kOne ? done((acc - 1) % kAcc) : empty(s));
           }
         }
       }
@@ -354,78 +385,56 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       if (!mbar_wait(drain, 0, kWaitLimit)) fail_w4(abort_flag);
     }
   } else if (warp < L::kEpiWarp) {
-    // nibbles to bf16: thread = weight row of the tile.  A stage is handed over one
-    // turn after it was written: its stores are done by then, and the fence that
-    // makes them visible to the tensor cores waits for nothing.
+    // nibbles to bf16: thread = weight row of the tile
     regs_dec<L::kRegsDq>();
     const int wg = warp / 4 - 1;
     const int row = threadIdx.x & 127;
-    int g = 0, owed = -1;  // chunks taken; the stage not handed over yet
+    int g = 0;  // chunks so far
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row;
       const uint8_t* zrow = zeros && n < N ? zeros + (int64_t)n * ld_z : nullptr;
-      uint32_t zp[4], zn[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) zn[b] = zero_at<GROUP>(zrow, cb * 4 + b, K);
-      for (int ch = cb; ch < ce; ++ch, ++g) {
+      for (int ch = cb; ch < ce && ok; ++ch, ++g) {
         const int s = g % SQ;
+        uint32_t zp[kStages];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          zp[b] = zn[b];
-          if (ch + 1 < ce) zn[b] = zero_at<GROUP>(zrow, ch * 4 + 4 + b, K);
-        }
+        for (int st = 0; st < kStages; ++st) zp[st] = zero_at<GROUP>(zrow, ch * 4 + st * 2 + wg, K);
         if (!mbar_wait(q_full(s), (g / SQ) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
-        // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
         const unsigned char* src = gbase + L::kOffQ + s * L::kStageQ + row * 64;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (L::kDqGroups == 2 && half != wg) continue;
-          uint4 q[2];
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            q[b] = *reinterpret_cast<const uint4*>(src + (((2 * half + b) ^ ((row >> 1) & 3)) << 4));
-          const int ks = 2 * g + half, sa = ks % S;
-          uint4 v[8];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const __nv_bfloat162 zc = zero_pair(zp[2 * half + b]);
-            v[4 * b] = unpack8(q[b].x, zc);
-            v[4 * b + 1] = unpack8(q[b].y, zc);
-            v[4 * b + 2] = unpack8(q[b].z, zc);
-            v[4 * b + 3] = unpack8(q[b].w, zc);
-          }
-          if (owed >= 0) hand_over(full(owed), lane);  // before a wait that may need it
-          owed = -1;
-          if (ks >= S && !mbar_wait(empty(sa), (ks / S + 1) & 1, kWaitLimit)) {
+        for (int st = 0; st < kStages; ++st) {
+          // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
+          const uint4 q = *reinterpret_cast<const uint4*>(src + (((st * 2 + wg) ^ ((row >> 1) & 3)) << 4));
+          const __nv_bfloat162 zc = zero_pair(zp[st]);
+          const uint4 v[4] = {unpack8(q.x, zc), unpack8(q.y, zc), unpack8(q.z, zc), unpack8(q.w, zc)};
+          const int at = g * kStages + st, sa = at % S;
+          if (!stage_free(at)) {
             ok = false;
             break;
           }
-          unsigned char* dst = gbase + sa * L::kStage + L::kStageB + row * 128;
+          // 16-byte granule i of the row's 128 bytes at i ^ (r % 8)
+          unsigned char* dst = gbase + sa * L::kStage + L::kStageB + (wg / 2) * L::kBlockA + row * 128;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (row & 7)) << 4)) = v[i];
-          owed = sa;
-          // the copy of the next weights goes through another proxy than the reads of
-          // these: it may start when they are done for certain, their results stored
-          if (L::kDqGroups == 2 || half == 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_empty(s));
-          }
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + ((((wg & 1) * 4 + i) ^ (row & 7)) << 4)) = v[i];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(sa));
         }
-        if (!ok) break;
+        // the copy of the next weights goes through another proxy than the reads of
+        // these: it may start when they are done for certain, their results stored
+        if (lane == 0 && ok) mbar_arrive(q_empty(s));
       }
     }
-    if (owed >= 0) hand_over(full(owed), lane);
     if (!ok && lane == 0) fail_w4(abort_flag);
   } else {
     regs_inc<L::kRegsEpi>();
     constexpr int kCols = BT / 2;  // columns of a warp
     const int quad = warp & 3, h = (warp - L::kEpiWarp) / 4;
     const int row = quad * 32 + lane;
-    int acc = 0;
+    int acc = 0, inner = 0;
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row, m0 = t / n_tiles * BT + h * kCols;
@@ -435,37 +444,53 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       for (int j = 0; j < kCols / 2; ++j) total[j] = make_float2(0.0f, 0.0f);
       const int groups = n_in ? (K + GROUP - 1) / GROUP : 0;
       const int64_t s_row = (int64_t)n * ld_s;
-      float next = scale_at(scales, s_bf16, s_row, cb * kG, groups);
+      uint32_t ahead[2];  // the bits of the next two groups' scales
+      ahead[0] = scale_bits(scales, s_bf16, s_row, cb * kG, groups);
+      ahead[1] = scale_bits(scales, s_bf16, s_row, cb * kG + 1, groups);
+#pragma unroll 2
       for (int gr = cb * kG; gr < ce * kG; ++gr, ++acc) {
-        const float sc = next;
-        next = scale_at(scales, s_bf16, s_row, gr + 1, groups);
-        // the group is complete when its last stage is (or half of it): the products are
-        // at most two groups ahead of this, so that barrier's next phase is not over
-        const int ks = GROUP == 128 ? 2 * acc + 1 : (GROUP == 64 ? acc : acc / 2);
-        const bool half = GROUP == 32 && !(acc & 1);
-        if (!mbar_wait(half ? mid(ks & 1) : empty(ks % S), (half ? ks / 2 : ks / S) & 1, kWaitLimit)) {
+        const uint32_t bits = ahead[(gr - cb * kG) & 1];
+        const uint32_t fetched = scale_bits(scales, s_bf16, s_row, gr + 2, groups);
+        if ((gr - cb * kG) & 1) ahead[1] = fetched;
+        else ahead[0] = fetched;
+        const float sc = __uint_as_float(s_bf16 ? bits << 16 : bits);
+        // the group is complete when the stage that it ends with is, or at a barrier of its
+        // own inside a stage: the products are at most kAcc groups ahead of this, so the
+        // barrier's next phase is not over
+        const int last = (acc % kG + 1) * kStepsPerGroup - 1;  // its last product in the chunk
+        uint32_t bar, parity;
+        if (A::kOne) {
+          bar = done(acc % kAcc), parity = (uint32_t)(acc / kAcc) & 1;
+        } else if ((last + 1) % kSteps == 0) {
+          const int st = acc / kG * kStages + last / kSteps;
+          bar = empty(st % S), parity = (uint32_t)(st / S) & 1;
+        } else {
+          bar = mid(inner % kAcc), parity = (uint32_t)(inner / kAcc) & 1;
+          ++inner;
+        }
+        if (!mbar_wait(bar, parity, kWaitLimit)) {
           ok = false;
           break;
         }
         tcgen05_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((acc & 1) * BT + h * kCols);
+        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc % kAcc * BT + h * kCols);
         const float2 s2 = make_float2(sc, sc);
-        uint32_t v[2][16];
-        tmem_ld16(taddr, v[0]);
+        uint32_t v[2][8];
+        tmem_ld8(taddr, v[0]);
         tmem_wait(v[0]);
 #pragma unroll
-        for (int j = 0; j < kCols / 16; ++j) {
-          if (j + 1 < kCols / 16) tmem_ld16(taddr + (uint32_t)(16 * (j + 1)), v[(j + 1) & 1]);
+        for (int j = 0; j < kCols / 8; ++j) {
+          if (j + 1 < kCols / 8) tmem_ld8(taddr + (uint32_t)(8 * (j + 1)), v[(j + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            total[8 * j + i] = __ffma2_rn(
+          for (int i = 0; i < 4; ++i)
+            total[4 * j + i] = __ffma2_rn(
                 s2, make_float2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
-                total[8 * j + i]);
-          if (j + 1 < kCols / 16) tmem_wait(v[(j + 1) & 1]);
+                total[4 * j + i]);
+          if (j + 1 < kCols / 8) tmem_wait(v[(j + 1) & 1]);
         }
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(acc & 1));
+        if (lane == 0) mbar_arrive(acc_empty(acc % kAcc));
       }
       if (!ok) break;
       if constexpr (SPLIT) {
@@ -518,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   tcgen05_fence_before();
   __syncthreads();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(A::kCols) : "memory");
 }
 
 constexpr int kMaxSplits = 8;

@@ -374,7 +374,6 @@ cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaS
 // its many-row form (gemm_w4.cu)
 cudaError_t launch_gemm_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream);
 int read_gemm_w4_faults(bool clear);
-int read_linear_w4_faults(bool clear);
 
 // x' = x + scale gate . (y, normed if post), out = x' normed (block_norm.cu)
 struct BlockNormArgs {

@@ -13,34 +13,24 @@
 // takes 128 + z off.  The pairs (i, i + 4) are the product's k order; the
 // activations are put into the same order.
 //
-// Bound: the weights' way from HBM, and close behind it the integer pipe that takes
-// the nibbles apart.  A CTA takes 16 or 32 weight rows; bulk copies bring 1024 k
-// (512 bytes a row) at a time, several such slabs in flight, and each of its 8 warps
-// takes 128 k of a slab.  The warps' sums are added in warp order at the end.
+// Bound: the weights' way from HBM, and the warp-level product, which takes 32 cycles
+// of a quarter of an SM (50000 x 2560: 11.7 us to read, 13.8 to multiply).  A CTA takes 16
+// weight rows and its warps the rows' units of 128 k in turn.  Lane (g, t) reads 16 bytes
+// of rows g and g + 8, straight into registers and some units ahead (tensor copies of 16
+// x 64 bytes into shared memory took 33 us for those weights, bulk copies of 512 bytes
+// 40).  Activations come from the L1 cache.  The warps' sums are added in warp order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "../../include/mamba_ssm.h"
-#include "async_copy.cuh"
 #include "device_math.cuh"
 #include "launch.h"
-#include "tcgen05.cuh"
 
 namespace mamba {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 128;                // k of a warp's turn
-constexpr int kSlab = kWarps * kChunk;     // k per stage
-constexpr int kPitchW = kSlab / 2 + 16;    // bytes of a weight row in a stage: 8 rows' words meet 32 banks
-constexpr int kPitchX = kSlab * 2 + 64;    // and of an activation row: two rows' 64 bytes meet 32 banks
-constexpr int kSpan = 8 * kSlab;           // k whose scales are held at once
-constexpr int kMaxStages = 4;
-constexpr int kStageBudget = 72 * 1024;    // of a CTA's stages: three CTAs per SM
-constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
-
-__device__ int g_linear_w4_faults = 0;
+constexpr int kUnit = 128;   // k of a warp's turn: 64 bytes of a weight row
+constexpr int kSpan = 8192;  // k whose scales are held at once
+constexpr int kRows = 16;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -64,238 +54,207 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {
   return *reinterpret_cast<const __nv_bfloat162*>(&v);
 }
 
-struct RowsShape {
-  int stages;       // slabs in flight
-  int x_rows;       // activation rows of a stage
-  int scale_pitch;  // floats per weight row of the scales held (odd)
-};
+// 8 activations from k on, zeros past K (and past the rows: p null)
+__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* p, int k, int K) {
+  if (!p || k >= K) return make_uint4(0, 0, 0, 0);
+  if (k + 8 <= K) return *reinterpret_cast<const uint4*>(p + k);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int j = 0; k + j < K; ++j) {
+    const uint64_t v = reinterpret_cast<const uint16_t*>(p)[k + j];
+    if (j < 4) lo |= v << (16 * j);
+    else hi |= v << (16 * (j - 4));
+  }
+  return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
 
-// MT x 16 weight rows, NT x 8 activation rows
-template <int MT, int NT, int GROUP>
-__global__ void __launch_bounds__(kThreads, 3)
-    linear_w4_rows_kernel(const LinearW4Args a, const RowsShape sh) {
-  constexpr int kRows = 16 * MT, kCols = 8 * NT;
-  constexpr int kG = kChunk / GROUP;  // groups per chunk
+// word t of the four lanes' w[0 .. 3] in the place of this lane's words: w[b] becomes
+// word t of lane b's
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
+  const bool odd = t & 1, high = t & 2;
+  uint32_t s0 = odd ? w[0] : w[1], s1 = odd ? w[2] : w[3];
+  s0 = __shfl_xor_sync(0xffffffffu, s0, 1);
+  s1 = __shfl_xor_sync(0xffffffffu, s1, 1);
+  if (odd) w[0] = s0, w[2] = s1;
+  else w[1] = s0, w[3] = s1;
+  s0 = high ? w[0] : w[2], s1 = high ? w[1] : w[3];
+  s0 = __shfl_xor_sync(0xffffffffu, s0, 2);
+  s1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+  if (high) w[0] = s0, w[1] = s1;
+  else w[2] = s0, w[3] = s1;
+}
+
+// 16 weight rows, NT x 8 activation rows.  scale_pitch: floats per weight row of the
+// scales held (odd: 8 rows in 8 banks), whole units of them.
+//
+// The k of one product have to be of one group.  With groups of 128 lane t multiplies
+// word i of its own 16 bytes in product i (k = 32 t + 8 i ..); with smaller ones the four
+// lanes of a row exchange words first, and product b takes word t of piece b (k = 32 b +
+// 8 t ..).
+template <int WARPS, int NT, int GROUP, int AHEAD>
+__global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 768 / (32 * WARPS))
+    linear_w4_rows_kernel(const LinearW4Args a, const int scale_pitch) {
+  constexpr int kCols = 8 * NT;
+  constexpr int kG = kUnit / GROUP;  // groups per unit
+  constexpr bool kOwn = GROUP == kUnit;
+  static_assert(kSpan / kUnit / WARPS % AHEAD == 0, "a span ends with the last of the registers ahead");
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ uint64_t bar_mem[2 * kMaxStages];
-  __shared__ int abort_mem;
-  volatile int* abort_flag = &abort_mem;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
   const int N = (int)a.N, K = (int)a.K;
   const int n0 = blockIdx.x * kRows, m0 = blockIdx.y * kCols;
   const int rows_m = a.M - m0 < kCols ? (int)(a.M - m0) : kCols;
   const int rows_n = N - n0 < kRows ? N - n0 : kRows;
-  const int row_bytes = (K + 31) / 32 * 16;
-  const int slabs = (K + kSlab - 1) / kSlab;
+  const int pieces = (K + 31) / 32;  // 16 bytes of a weight row
+  const int units = (K + kUnit - 1) / kUnit;
   const int groups = (K + GROUP - 1) / GROUP;
-  const int stage_bytes = kRows * kPitchW + sh.x_rows * kPitchX;
-  const uint32_t base = smem_u32(smem);
-  float* scales = reinterpret_cast<float*>(smem + sh.stages * stage_bytes);
-  unsigned char* zeros = reinterpret_cast<unsigned char*>(scales + kRows * sh.scale_pitch);
-  auto full = [&](int s) { return smem_u32(bar_mem) + 8 * s; };
-  auto empty = [&](int s) { return smem_u32(bar_mem) + 8 * (kMaxStages + s); };
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < sh.stages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kWarps);
-    }
-    *abort_flag = 0;
-    mbar_fence_init();
-  }
-  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);
+  float* scales = part + WARPS * kCols * kRows;
+  unsigned char* zeros = reinterpret_cast<unsigned char*>(scales + kRows * scale_pitch);
   grid_dependency_begin();
 
-  const __nv_bfloat16* x0 = static_cast<const __nv_bfloat16*>(a.a) + (int64_t)m0 * a.ld_a;
-  auto fail = [&]() {
-    atomicOr(&g_linear_w4_faults, MAMBA_FAULT_GEMM_WAIT);
-    *abort_flag = 1;
+  const uint8_t* q0 = g < rows_n ? a.q + (int64_t)(n0 + g) * a.ld_q + t * 16 : nullptr;
+  const uint8_t* q1 = g + 8 < rows_n ? a.q + (int64_t)(n0 + g + 8) * a.ld_q + t * 16 : nullptr;
+  uint4 ahead[AHEAD][2];
+  auto fetch = [&](int u, uint4 (&w)[2]) {
+    w[0] = w[1] = make_uint4(0, 0, 0, 0);
+    if (u * 4 + t < pieces) {
+      if (q0) w[0] = __ldcs(reinterpret_cast<const uint4*>(q0 + (int64_t)u * 64));
+      if (q1) w[1] = __ldcs(reinterpret_cast<const uint4*>(q1 + (int64_t)u * 64));
+    }
   };
-  // slab i by warp 0, a row per lane: whole 16 bytes inside K; the rest of a stage
-  // keeps what it held (its nibbles meet activations that are made zero)
-  auto issue = [&](int i) {
-    const int s = i % sh.stages, off = i * (kSlab / 2), k0 = i * kSlab;
-    const int wb = row_bytes - off < kSlab / 2 ? row_bytes - off : kSlab / 2;
-    const int xb = (K - k0 < kSlab ? K - k0 : kSlab) / 8 * 16;
-    const uint32_t w = base + s * stage_bytes, x = w + kRows * kPitchW;
-    if (lane == 0) mbar_arrive_expect_tx(full(s), rows_n * wb + rows_m * xb);
-    __syncwarp();
-    if (lane < rows_n) bulk_g2s(w + lane * kPitchW, a.q + (int64_t)(n0 + lane) * a.ld_q + off, wb, full(s));
-    if (lane < rows_m && xb > 0) bulk_g2s(x + lane * kPitchX, x0 + (int64_t)lane * a.ld_a + k0, xb, full(s));
-  };
-  int issued = 0;
-  if (warp == 0)
-    for (; issued < sh.stages && issued < slabs; ++issued) issue(issued);
-
-  float total[MT][NT][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) total[i][j][0] = total[i][j][1] = total[i][j][2] = total[i][j][3] = 0.0f;
+  for (int d = 0; d < AHEAD; ++d) fetch(warp + d * WARPS, ahead[d]);
 
-  bool ok = true;
-  for (int i = 0; i < slabs && ok; ++i) {
-    if (i % (kSpan / kSlab) == 0) {
+  const __nv_bfloat16* xr[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    xr[j] = j * 8 + g < rows_m ? static_cast<const __nv_bfloat16*>(a.a) + (int64_t)(m0 + j * 8 + g) * a.ld_a : nullptr;
+
+  float total[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) total[j][0] = total[j][1] = total[j][2] = total[j][3] = 0.0f;
+
+  int u = warp;
+  for (int span = 0; span < K; span += kSpan) {
+    {
       // the scales and zero points of the next kSpan k, 0 outside the matrix
-      const int g0 = i * (kSlab / GROUP), left = groups - g0;
+      const int g0 = span / GROUP, left = groups - g0;
       const int held = left < kSpan / GROUP ? left : kSpan / GROUP;
-      if (i > 0) __syncthreads();
-      for (int e = threadIdx.x; e < kRows * sh.scale_pitch; e += kThreads) {
-        const int row = e / sh.scale_pitch, gr = e % sh.scale_pitch;
-        const bool in = row < rows_n && gr < held;
-        const int64_t at = (int64_t)(n0 + row) * a.ld_s + g0 + gr;
-        scales[e] = !in ? 0.0f
-                        : (a.s_bf16 ? to_f32(static_cast<const __nv_bfloat16*>(a.scales)[at])
-                                    : static_cast<const float*>(a.scales)[at]);
-        if (a.zeros) zeros[e] = in ? a.zeros[(int64_t)(n0 + row) * a.ld_z + g0 + gr] & 127 : 0;
+      if (span > 0) __syncthreads();
+#pragma unroll
+      for (int row = warp; row < kRows; row += WARPS) {
+        const int n = n0 + row;
+        const float* sf = static_cast<const float*>(a.scales) + (int64_t)n * a.ld_s + g0;
+        const __nv_bfloat16* sb = static_cast<const __nv_bfloat16*>(a.scales) + (int64_t)n * a.ld_s + g0;
+        const uint8_t* z = a.zeros + (int64_t)n * a.ld_z + g0;
+        for (int gr = lane; gr < scale_pitch; gr += 32) {
+          const bool in = row < rows_n && gr < held;
+          const float v = !in ? 0.0f : (a.s_bf16 ? to_f32(__ldg(sb + gr)) : __ldg(sf + gr));
+          const uint32_t zv = a.zeros && in ? __ldg(z + gr) & 127u : 0u;
+          scales[row * scale_pitch + gr] = v;
+          if (a.zeros) zeros[row * scale_pitch + gr] = (unsigned char)zv;
+        }
       }
       __syncthreads();
     }
-    const int s = i % sh.stages, ch = i * kWarps + warp;
-    if (!mbar_wait(full(s), (i / sh.stages) & 1, kWaitLimit)) {
-      ok = false;
-      break;
-    }
-    if (ch * kChunk < K) {
-      const unsigned char* w = smem + s * stage_bytes + warp * (kChunk / 2) + g * kPitchW + t * 4;
-      const unsigned char* x = smem + s * stage_bytes + kRows * kPitchW + warp * (kChunk * 2) + g * kPitchX + t * 16;
-      const float* sc = scales + g * sh.scale_pitch + ch % (kSpan / kChunk) * kG;
-      const unsigned char* zc = zeros + g * sh.scale_pitch + ch % (kSpan / kChunk) * kG;
-      const bool tail = K - ch * kChunk < kChunk;
-      float acc[MT][NT][4];
+    const int u_end = units < (span + kSpan) / kUnit ? units : (span + kSpan) / kUnit;
+    while (u < u_end) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b * 32 % GROUP == 0) {
+      for (int d = 0; d < AHEAD; ++d) {
+        if (u >= u_end) break;
+        uint4 xv[NT][4];
 #pragma unroll
-          for (int mi = 0; mi < MT; ++mi)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[mi][j][0] = acc[mi][j][1] = acc[mi][j][2] = acc[mi][j][3] = 0.0f;
+          for (int i = 0; i < 4; ++i)
+            xv[j][i] = load_x(xr[j], u * kUnit + (kOwn ? t * 32 + i * 8 : i * 32 + t * 8), K);
+        // (registers that stay where they are: a move would wait for the load)
+        uint32_t w0[4] = {ahead[d][0].x, ahead[d][0].y, ahead[d][0].z, ahead[d][0].w};
+        uint32_t w1[4] = {ahead[d][1].x, ahead[d][1].y, ahead[d][1].z, ahead[d][1].w};
+        fetch(u + AHEAD * WARPS, ahead[d]);
+        if (!kOwn) {
+          transpose4(w0, t);
+          transpose4(w1, t);
         }
-        uint32_t xp[NT][4];  // the activations' pairs (k, k + 4)
+        const float* sc = scales + g * scale_pitch + (u * kUnit - span) / GROUP;
+        const unsigned char* zc = zeros + g * scale_pitch + (u * kUnit - span) / GROUP;
+        float acc[NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          const int m = j * 8 + g, k = ch * kChunk + b * 32 + t * 8;
-          if (m < rows_m) {
-            if (!tail || k + 8 <= K) {
-              v = *reinterpret_cast<const uint4*>(x + j * 8 * kPitchX + b * 64);
-            } else if (k < K) {  // a piece across K, from where it lies
-              uint32_t h[8];
+        for (int i = 0; i < 4; ++i) {
+          if (i * 32 % GROUP == 0) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                h[e] = k + e < K ? reinterpret_cast<const uint16_t*>(x0)[(int64_t)m * a.ld_a + k + e] : 0u;
-              v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-            }
+            for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
           }
-          xp[j][0] = __byte_perm(v.x, v.z, 0x5410);
-          xp[j][1] = __byte_perm(v.x, v.z, 0x7632);
-          xp[j][2] = __byte_perm(v.y, v.w, 0x5410);
-          xp[j][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
-        const int e = b * 32 / GROUP;
-#pragma unroll
-        for (int mi = 0; mi < MT; ++mi) {
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(w + (mi * 16) * kPitchW + b * 16);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(w + (mi * 16 + 8) * kPitchW + b * 16);
-          const __nv_bfloat162 z0 = zero_pair(a.zeros ? zc[(mi * 16) * sh.scale_pitch + e] : 8u);
-          const __nv_bfloat162 z1 = zero_pair(a.zeros ? zc[(mi * 16 + 8) * sh.scale_pitch + e] : 8u);
-          const uint32_t p0[4] = {nibble_pair<0>(w0, z0), nibble_pair<1>(w0, z0), nibble_pair<2>(w0, z0),
-                                  nibble_pair<3>(w0, z0)};
-          const uint32_t p1[4] = {nibble_pair<0>(w1, z1), nibble_pair<1>(w1, z1), nibble_pair<2>(w1, z1),
-                                  nibble_pair<3>(w1, z1)};
+          const int e = i * 32 / GROUP;
+          const __nv_bfloat162 z0 = zero_pair(a.zeros ? zc[e] : 8u);
+          const __nv_bfloat162 z1 = zero_pair(a.zeros ? zc[8 * scale_pitch + e] : 8u);
+          const uint32_t p0[4] = {nibble_pair<0>(w0[i], z0), nibble_pair<1>(w0[i], z0), nibble_pair<2>(w0[i], z0),
+                                  nibble_pair<3>(w0[i], z0)};
+          const uint32_t p1[4] = {nibble_pair<0>(w1[i], z1), nibble_pair<1>(w1[i], z1), nibble_pair<2>(w1[i], z1),
+                                  nibble_pair<3>(w1[i], z1)};
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            mma16816(acc[mi][j], p0[0], p1[0], p0[1], p1[1], xp[j][0], xp[j][1]);
-            mma16816(acc[mi][j], p0[2], p1[2], p0[3], p1[3], xp[j][2], xp[j][3]);
+            // the activations' pairs (k, k + 4)
+            mma16816(acc[j], p0[0], p1[0], p0[1], p1[1], __byte_perm(xv[j][i].x, xv[j][i].z, 0x5410),
+                     __byte_perm(xv[j][i].x, xv[j][i].z, 0x7632));
+            mma16816(acc[j], p0[2], p1[2], p0[3], p1[3], __byte_perm(xv[j][i].y, xv[j][i].w, 0x5410),
+                     __byte_perm(xv[j][i].y, xv[j][i].w, 0x7632));
           }
-          if ((b + 1) * 32 % GROUP == 0) {
-            const float s0 = sc[(mi * 16) * sh.scale_pitch + e], s1 = sc[(mi * 16 + 8) * sh.scale_pitch + e];
+          if ((i + 1) * 32 % GROUP == 0) {
+            const float s0 = sc[e], s1 = sc[8 * scale_pitch + e];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              total[mi][j][0] = fmaf(s0, acc[mi][j][0], total[mi][j][0]);
-              total[mi][j][1] = fmaf(s0, acc[mi][j][1], total[mi][j][1]);
-              total[mi][j][2] = fmaf(s1, acc[mi][j][2], total[mi][j][2]);
-              total[mi][j][3] = fmaf(s1, acc[mi][j][3], total[mi][j][3]);
+              total[j][0] = fmaf(s0, acc[j][0], total[j][0]);
+              total[j][1] = fmaf(s0, acc[j][1], total[j][1]);
+              total[j][2] = fmaf(s1, acc[j][2], total[j][2]);
+              total[j][3] = fmaf(s1, acc[j][3], total[j][3]);
             }
           }
         }
-      }
-    }
-    if (i + sh.stages < slabs) {
-      fence_proxy_async_smem();  // this warp's reads of the stage, before the next copy into it
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-      if (warp == 0) {  // the stage again, once every warp has read it
-        if (!mbar_wait(empty(s), (i / sh.stages) & 1, kWaitLimit)) {
-          ok = false;
-          break;
-        }
-        issue(issued++);
+        u += WARPS;
       }
     }
   }
-  if (!ok && lane == 0) fail();
-  if (warp == 0)  // every copy has landed
-    for (int i = issued > sh.stages ? issued - sh.stages : 0; i < issued; ++i)
-      if (!mbar_wait(full(i % sh.stages), (i / sh.stages) & 1, kWaitLimit)) fail();
-  __syncthreads();
-  if (*abort_flag) return;
   // the warps' sums, [warp][m][row]
-  float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int mi = 0; mi < MT; ++mi)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float* p = part + (warp * kCols + j * 8 + 2 * t) * kRows + mi * 16 + g;
-      p[0] = total[mi][j][0];
-      p[kRows] = total[mi][j][1];
-      p[8] = total[mi][j][2];
-      p[kRows + 8] = total[mi][j][3];
-    }
+  for (int j = 0; j < NT; ++j) {
+    float* p = part + (warp * kCols + j * 8 + 2 * t) * kRows + g;
+    p[0] = total[j][0];
+    p[kRows] = total[j][1];
+    p[8] = total[j][2];
+    p[kRows + 8] = total[j][3];
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < rows_m * kRows; e += kThreads) {
+  for (int e = threadIdx.x; e < rows_m * kRows; e += 32 * WARPS) {
     const int n = n0 + e % kRows, m = m0 + e / kRows;
     if (n >= N) continue;
     float v = part[e];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += part[w * (kCols * kRows) + e];
+    for (int w = 1; w < WARPS; ++w) v += part[w * (kCols * kRows) + e];
     if (a.r) v += a.r[(int64_t)m * a.ld_r + n];
     store_out(a.c, (int64_t)m * a.ld_c + n, a.c_bf16, v);
   }
 }
 
-template <int MT, int NT, int GROUP>
+template <int WARPS, int NT, int GROUP, int AHEAD>
 cudaError_t launch_rows(const LinearW4Args& g, cudaStream_t stream) {
-  auto kern = linear_w4_rows_kernel<MT, NT, GROUP>;
-  constexpr int kRows = 16 * MT, kCols = 8 * NT;
-  RowsShape sh;
-  sh.x_rows = (int)(g.M < kCols ? g.M : kCols);
-  const int stage = kRows * kPitchW + sh.x_rows * kPitchX;
-  const int64_t slabs = (g.K + kSlab - 1) / kSlab;
-  sh.stages = kStageBudget / stage;
-  sh.stages = sh.stages < 2 ? 2 : (sh.stages > kMaxStages ? kMaxStages : sh.stages);
-  if (sh.stages > slabs) sh.stages = (int)slabs;
-  // the groups of whole chunks: a chunk across K reads (and ignores) those past the last
-  const int64_t groups = (g.K + kChunk - 1) / kChunk * (kChunk / GROUP);
-  sh.scale_pitch = (int)(groups < kSpan / GROUP ? groups : kSpan / GROUP) | 1;
-  int smem = sh.stages * stage + kRows * sh.scale_pitch * (g.zeros ? 5 : 4);
-  const int parts = kWarps * kCols * kRows * 4;  // the warps' sums, over the stages
-  if (smem < parts) smem = parts;
-  constexpr int kMost = 2 * (kRows * kPitchW + kCols * kPitchX) > kStageBudget ? 2 * (kRows * kPitchW + kCols * kPitchX)
-                                                                               : kStageBudget;
-  static_assert(kMost + kRows * (kSpan / GROUP + 1) * 5 + 1024 <= 232448, "shared memory over the opt-in limit");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMost + kRows * (kSpan / GROUP + 1) * 5);
-  if (e != cudaSuccess) return e;
+  constexpr int kCols = 8 * NT;
+  // the groups of whole units: a unit across K reads (and ignores) those past the last
+  const int64_t groups = (g.K + kUnit - 1) / kUnit * (kUnit / GROUP);
+  const int scale_pitch = (int)(groups < kSpan / GROUP ? groups : kSpan / GROUP) | 1;
+  static_assert(WARPS * kCols * kRows * 4 + kRows * (kSpan / GROUP + 1) * 5 <= 48 * 1024, "static limit of shared memory");
+  const int smem = WARPS * kCols * kRows * 4 + kRows * scale_pitch * (g.zeros ? 5 : 4);
   const dim3 grid((unsigned)((g.N + kRows - 1) / kRows), (unsigned)((g.M + kCols - 1) / kCols));
-  return launch_pdl(true, kern, grid, dim3(kThreads), smem, stream, g, sh);
+  return launch_pdl(true, linear_w4_rows_kernel<WARPS, NT, GROUP, AHEAD>, grid, dim3(32 * WARPS), smem, stream, g,
+                    scale_pitch);
 }
 
-template <int MT, int NT>
+template <int WARPS, int NT, int AHEAD>
 cudaError_t launch_group(const LinearW4Args& g, cudaStream_t stream) {
-  if (g.group == 32) return launch_rows<MT, NT, 32>(g, stream);
-  if (g.group == 64) return launch_rows<MT, NT, 64>(g, stream);
-  return launch_rows<MT, NT, 128>(g, stream);
+  if (g.group == 32) return launch_rows<WARPS, NT, 32, AHEAD>(g, stream);
+  if (g.group == 64) return launch_rows<WARPS, NT, 64, AHEAD>(g, stream);
+  return launch_rows<WARPS, NT, 128, AHEAD>(g, stream);
 }
 
 }  // namespace
@@ -303,19 +262,10 @@ cudaError_t launch_group(const LinearW4Args& g, cudaStream_t stream) {
 cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream) {
   if (g.M <= 0 || g.N <= 0) return cudaSuccess;
   if (g.M > 16) return launch_gemm_w4(g, dev, stream);
-  const bool wide = g.N >= 64 * (int64_t)dev.sm_count;  // 32 rows a CTA, two CTAs per SM and more
-  if (g.M > 8) return wide ? launch_group<2, 2>(g, stream) : launch_group<1, 2>(g, stream);
-  return wide ? launch_group<2, 1>(g, stream) : launch_group<1, 1>(g, stream);
-}
-
-int read_linear_w4_faults(bool clear) {
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_linear_w4_faults, sizeof(int)) != cudaSuccess) return -1;
-  if (clear && v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_linear_w4_faults, &zero, sizeof(int)) != cudaSuccess) return -1;
-  }
-  return v;
+  // two CTAs per SM or fewer: more warps to a row, so that all of it is on its way at once
+  const bool few = (g.N + kRows - 1) / kRows <= 2 * (int64_t)dev.sm_count && g.K > 8 * kUnit;
+  if (g.M > 8) return few ? launch_group<16, 2, 2>(g, stream) : launch_group<8, 2, 2>(g, stream);
+  return few ? launch_group<16, 1, 2>(g, stream) : launch_group<8, 1, 2>(g, stream);
 }
 
 }  // namespace mamba
