@@ -11,15 +11,17 @@
 // every weight to 8 bits, and save only the epilogue's reads.)
 //
 // Roles of a CTA (persistent, one per SM):
-//  * warp 0 brings activation tiles, BT x 64 bf16 with the 128-byte swizzle (TMA);
+//  * warp 0 brings activations, BT x 64 bf16 with the 128-byte swizzle a copy (TMA);
 //  * warp 2 brings weights as they are stored, 128 rows x 64 bytes (128 k) a copy;
-//  * a warpgroup (two for narrow tiles), a thread per weight row, makes bf16 of the
-//    nibbles: two operations a pair (nibbles i and i + 4 of a word in the halves of
-//    a register, 0x4300 above them: 128 + q; a packed subtraction of 128 + z), a
-//    byte permutation that puts neighbours side by side, 16-byte stores into the
-//    product's swizzled operand;
-//  * warp 1 issues the products, one group of k into one of two accumulators;
-//  * two warpgroups take the other accumulator meanwhile, each half of the columns:
+//  * four warpgroups, a thread per weight row, make bf16 of the nibbles, 32 k of each
+//    chunk of 128 a warpgroup: two operations a pair (nibbles i and i + 4 of a word in
+//    the halves of a register, 0x4300 above them: 128 + q; a packed subtraction of
+//    128 + z), a byte permutation that puts neighbours side by side, and a store into
+//    tensor memory, where the product reads its weights (through shared memory they
+//    cost it 32 KB written and 32 read per chunk, beside the activations' own: 343 us
+//    for 8192 x 10240 x 2560);
+//  * warp 1 issues the products, a group of k into one of a few accumulators;
+//  * two warpgroups take the finished accumulators meanwhile, each half of the columns:
 //    total += scale * group's sum, BT / 2 totals a thread in registers, and store
 //    the totals at the end of a tile (a warp stores 32 neighbours of a row of C).
 // Few tiles: K is split over a cluster whose CTAs add their totals through
@@ -54,54 +56,43 @@ constexpr long long kWaitLimit = 1ll << 31;  // SM cycles (about a second)
 
 __device__ int g_gemm_w4_faults = 0;
 
-// The totals of a wide tile take half of the registers, so stages are of 64 k and two
-// warpgroups make bf16 of nibbles; narrow ones have stages of 128 k (a stage costs its
-// waits and hand-overs, whatever it holds) and four such warpgroups.  Each takes 32 k of
-// every stage, which is ready after a quarter (or half) of the work.
+constexpr int kDqGroups = 4;   // warpgroups that make bf16 of nibbles
+constexpr int kThreads = 128 * (1 + kDqGroups + 2);
+constexpr int kEpiWarp = 4 * (1 + kDqGroups);
+// registers per thread of the roles; their sum over the warpgroups is what the CTA is
+// launched with (72 x 7)
+constexpr int kRegsLoad = 40, kRegsDq = 48, kRegsEpi = 136;
+constexpr int kRegs = kRegsLoad + kDqGroups * kRegsDq + 2 * kRegsEpi;
+static_assert(kRegs <= (65536 / kThreads / 8 * 8) * (kThreads / 128), "more registers than a CTA has");
+constexpr int kSA = 4;         // stages of weights in tensor memory
+constexpr int kDone = 8;       // barriers of finished stages
+constexpr int kTmemCols = 512;
+
+// Stages are of 128 k (a stage costs its waits and hand-overs, whatever it holds), of 64
+// where tensor memory has no room for four such beside the accumulators.
 template <int BT>
 struct Cfg {
-  static constexpr int kSub = BT > 128 ? 1 : 2;   // operand blocks per stage
-  static constexpr int kDqGroups = 2 * kSub;      // warpgroups that make bf16 of nibbles
-  static constexpr int kThreads = 128 * (1 + kDqGroups + 2);
-  static constexpr int kEpiWarp = 4 * (1 + kDqGroups);
-  // registers per thread of the roles; their sum over the warpgroups is within what
-  // the CTA is launched with (96 x 5 and 72 x 7)
-  static constexpr int kRegsLoad = BT > 128 ? 32 : 40;
-  static constexpr int kRegsDq = BT > 128 ? 56 : 48;
-  static constexpr int kRegsEpi = BT > 128 ? 168 : (BT > 64 ? 128 : 104);
-  static constexpr int kRegs = kRegsLoad + kDqGroups * kRegsDq + 2 * kRegsEpi;
-  static_assert(kRegs <= (65536 / kThreads / 8 * 8) * (kThreads / 128), "more registers than a CTA has");
+  static constexpr int kSub = BT > 128 ? 1 : 2;  // blocks of 64 k per stage
+  static constexpr int kStageCols = 32 * kSub;   // of weights in tensor memory
+  static constexpr int kOffA = kTmemCols - kSA * kStageCols;
+  static constexpr int kAcc0 = kOffA / BT;       // accumulators
+  static constexpr int kAcc = kAcc0 > 4 ? 4 : kAcc0;
   static constexpr int kBlockB = BT * kBK * 2;
-  static constexpr int kBlockA = kBN * kBK * 2;
   static constexpr int kStageB = kSub * kBlockB;
-  static constexpr int kStage = kStageB + kSub * kBlockA;
+  static constexpr int kSB = BT == 128 ? 4 : 8;                   // stages of activations
   static constexpr int kStageQ = kBN * kChunk / 2;
-  static constexpr int kS = BT > 128 ? 4 : 3;                     // operand stages
-  static constexpr int kOffQ = kS * kStage;
+  static constexpr int kOffQ = kSB * kStageB;
   static constexpr int kSQ0 = (kSmemLimit - 1024 - 512 - kOffQ) / kStageQ;
-  static constexpr int kSQ = kSQ0 > 8 ? 8 : kSQ0;                 // weights as they are stored
+  static constexpr int kSQ = kSQ0 > 8 ? 8 : kSQ0;                 // chunks of weights as they are stored
   static constexpr int kOffBar = kOffQ + kSQ * kStageQ;
-  static constexpr int kBars = 2 * (kS + kSQ) + 3 * 8 + 1;
+  static constexpr int kBars = kSA + kSB + 2 * kSQ + kDone + 3 * 4 + 1;
   static constexpr int kBytes = kOffBar + 8 * kBars + 16;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base
   static constexpr int kPartPitch = kBN + 4;
-  static_assert(kAlloc <= kSmemLimit && kSQ >= 2 && kS >= 3, "shared memory");
-};
-
-// Accumulators: as many as tensor memory holds, up to 8, so that the way from a group's
-// products to its totals and back (about 800 cycles) is not waited for group by group.
-template <int BT, int GROUP>
-struct Acc {
-  static constexpr int kStageK = Cfg<BT>::kSub * kBK;
-  static constexpr int kMost = 512 / BT < 8 ? 512 / BT : 8;
-  // (a group inside a stage is told by a barrier of its own, one that ends a stage by the
-  // stage's: the products may be ahead of the totals by fewer stages than there are)
-  static constexpr int kAcc = GROUP == 64 && kMost > 4 ? 4 : kMost;
-  // a stage is a group: the groups' barriers tell both, and there are accumulators enough
-  // that none is a whole round behind
-  static constexpr bool kOne = GROUP == kStageK && kAcc >= Cfg<BT>::kS;
-  static constexpr int kCols = kAcc * BT;
-  static_assert(kOne || (kAcc * GROUP + kStageK - 1) / kStageK <= Cfg<BT>::kS, "a stage's barrier a round behind");
+  static_assert(kAlloc <= kSmemLimit && kSQ >= 4 && kAcc >= 2, "shared or tensor memory");
+  // a stage's barrier is waited for by the copies (kSB stages later), the weights (kSA
+  // later) and the totals (of up to kAcc groups of 128 k): none is a round behind
+  static_assert(kSB <= kDone && kAcc * 2 / kSub < kDone, "a stage's barrier a round behind");
 };
 
 template <int BT>
@@ -118,15 +109,26 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A from tensor memory: lane = row, a 32-bit column = two values of K
+__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint32_t a, uint32_t b_hi, uint32_t b_lo, uint32_t idesc,
+                                         uint32_t acc) {
   asm volatile(
       "{\n"
       "  .reg .pred p;\n"
-      "  setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "  .reg .b64 b;\n"
+      "  mov.b64 b, {%3, %2};\n"
+      "  setp.ne.b32 p, %5, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
       "}\n" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "r"(a), "r"(b_hi), "r"(b_lo), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// one thread of a whole warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n  .reg .pred p;\n  elect.sync _|p, 0xffffffff;\n  selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 template <int N>
@@ -219,40 +221,36 @@ __device__ __forceinline__ void fail_w4(volatile int* abort_flag) {
 }
 
 template <int BT, int GROUP, bool SPLIT>
-__global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_w4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_q, void* c,
                    int64_t ld_c, int c_bf16, const void* __restrict__ scales, int64_t ld_s, int s_bf16,
                    const uint8_t* __restrict__ zeros, int64_t ld_z, const float* r, int64_t ld_r, int M, int N, int K,
                    int splits) {
   using L = Cfg<BT>;
-  constexpr int S = L::kS, SQ = L::kSQ;
+  constexpr int SB = L::kSB, SQ = L::kSQ, kAcc = L::kAcc;
   constexpr int kG = kChunk / GROUP;          // groups per chunk
   constexpr int kStepsPerGroup = GROUP / 16;  // products per group
-  constexpr int kStages = 2 / L::kSub;        // operand stages per chunk
+  constexpr int kStages = 2 / L::kSub;        // stages per chunk
   constexpr int kSteps = 4 * L::kSub;         // products per stage
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
   unsigned char* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::kOffBar;
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (S + s); };
-  auto q_full = [&](int s) { return bars + 8 * (2 * S + s); };
-  auto q_empty = [&](int s) { return bars + 8 * (2 * S + SQ + s); };
-  using A = Acc<BT, GROUP>;
-  constexpr int kAcc = A::kAcc;
-  auto mid = [&](int a) { return bars + 8 * (2 * (S + SQ) + a); };
-  auto acc_empty = [&](int a) { return bars + 8 * (2 * (S + SQ) + 8 + a); };
-  auto done = [&](int a) { return bars + 8 * (2 * (S + SQ) + 16 + a); };
-  const uint32_t drain = bars + 8 * (2 * (S + SQ) + 24);
-  // stage number st may be written again: the products that read what it held are done
-  auto stage_free = [&](int st) {
-    if (st < S) return true;
-    if (A::kOne) return mbar_wait(done((st - S) % kAcc), (uint32_t)((st - S) / kAcc) & 1, kWaitLimit);
-    return mbar_wait(empty(st % S), (uint32_t)(st / S + 1) & 1, kWaitLimit);
+  auto a_full = [&](int s) { return bars + 8 * s; };
+  auto b_full = [&](int s) { return bars + 8 * (kSA + s); };
+  auto q_full = [&](int s) { return bars + 8 * (kSA + SB + s); };
+  auto q_empty = [&](int s) { return bars + 8 * (kSA + SB + SQ + s); };
+  const uint32_t bars1 = bars + 8 * (kSA + SB + 2 * SQ);
+  auto done = [&](int s) { return bars1 + 8 * s; };
+  auto mid = [&](int a) { return bars1 + 8 * (kDone + a); };
+  auto acc_empty = [&](int a) { return bars1 + 8 * (kDone + 4 + a); };
+  const uint32_t drain = bars1 + 8 * (kDone + 8);
+  auto stage_b = [&](int s) { return base + (uint32_t)(s * L::kStageB); };
+  // the products of stage number st (and all before it) are complete
+  auto stage_done = [&](int st) {
+    return st < 0 || mbar_wait(done(st % kDone), (uint32_t)(st / kDone) & 1, kWaitLimit);
   };
-  auto stage_b = [&](int s) { return base + (uint32_t)(s * L::kStage); };
-  auto stage_a = [&](int s) { return base + (uint32_t)(s * L::kStage + L::kStageB); };
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * L::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
 
@@ -270,17 +268,15 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1 + 4 * L::kDqGroups);  // the copy of the activations, the weights' warps
-      mbar_init(empty(s), 1);
-    }
+    for (int s = 0; s < kSA; ++s) mbar_init(a_full(s), 4 * kDqGroups / kStages);
+    for (int s = 0; s < SB; ++s) mbar_init(b_full(s), 1);
     for (int s = 0; s < SQ; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 4 * L::kDqGroups);
+      mbar_init(q_empty(s), 4 * kDqGroups);
     }
+    for (int s = 0; s < kDone; ++s) mbar_init(done(s), 1);
     for (int a = 0; a < kAcc; ++a) {
       mbar_init(mid(a), 1);
-      mbar_init(done(a), 1);
       mbar_init(acc_empty(a), kEpiWarps);
     }
     mbar_init(drain, 1);
@@ -289,7 +285,7 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_ptr)),
-                 "r"(A::kCols)
+                 "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -302,27 +298,27 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   grid_dependency_wait();
 
   if (warp < 4) {
-    regs_dec<L::kRegsLoad>();
+    regs_dec<kRegsLoad>();
     if (warp == 0 && lane == 0) {
       // activations
       int g = 0;
       for (int t = t_first; t < tiles && !*abort_flag; t += t_step) {
         const int m0 = t / n_tiles * BT;
         for (int st = kStages * cb; st < kStages * ce; ++st, ++g) {
-          const int s = g % S;
-          if (!stage_free(g)) {
+          const int s = g % SB;
+          if (!stage_done(g - SB)) {
             fail_w4(abort_flag);
             break;
           }
-          mbar_arrive_expect_tx(full(s), L::kStageB);
+          mbar_arrive_expect_tx(b_full(s), L::kStageB);
 #pragma unroll
           for (int sub = 0; sub < L::kSub; ++sub)
-            tma_load_2d(stage_b(s) + sub * L::kBlockB, &map_a, (st * L::kSub + sub) * kBK, m0, full(s));
+            tma_load_2d(stage_b(s) + sub * L::kBlockB, &map_a, (st * L::kSub + sub) * kBK, m0, b_full(s));
         }
       }
-      // the copies issued land: their stages complete, unless the weights' side gave up
-      for (int i = g > S ? g - S : 0; i < g; ++i)
-        if (!mbar_wait(full(i % S), (i / S) & 1, kWaitLimit)) fail_w4(abort_flag);
+      // every copy issued lands before this thread moves on
+      for (int i = g > SB ? g - SB : 0; i < g; ++i)
+        if (!mbar_wait(b_full(i % SB), (i / SB) & 1, kWaitLimit)) fail_w4(abort_flag);
     } else if (warp == 2 && lane == 0) {
       // weights
       int g = 0;
@@ -340,99 +336,105 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
       }
       for (int i = g > SQ ? g - SQ : 0; i < g; ++i)
         if (!mbar_wait(q_full(i % SQ), (i / SQ) & 1, kWaitLimit)) fail_w4(abort_flag);
-    } else if (warp == 1 && lane == 0) {
-      // products
+    } else if (warp == 1) {
+      // products.  The whole warp goes through the loop and one thread of it issues: what
+      // the instructions take from uniform registers (descriptors, addresses) stays there.
+      // Counters wrap by masks: this warp's own instructions are what a stage takes least.
       constexpr uint32_t idesc = instr_desc<BT>();
+      const uint64_t desc0 = smem_desc(base);
+      const uint32_t desc_hi = (uint32_t)(desc0 >> 32), desc_lo = (uint32_t)desc0;
+      const bool issuer = elect_one();
       int g = 0, acc = 0, inner = 0;
       bool ok = true;
       for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
         for (int ch = cb; ch < ce && ok; ++ch) {
 #pragma unroll
           for (int st = 0; st < kStages; ++st, ++g) {
-            if (!ok) break;
-            const int s = g % S;
-            if (!mbar_wait(full(s), (g / S) & 1, kWaitLimit)) {
-              ok = false;
-              break;
-            }
-            tcgen05_fence_after();
+            const int sa = g % kSA, sb = g % SB;
+            ok = mbar_wait(a_full(sa), (g / kSA) & 1, kWaitLimit) && mbar_wait(b_full(sb), (g / SB) & 1, kWaitLimit);
+            const uint32_t da = tmem + (uint32_t)(L::kOffA + sa * L::kStageCols);
+            const uint32_t db = desc_lo + (uint32_t)(sb * (L::kStageB >> 4));
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               const int step = st * kSteps + k;
-              if (step % kStepsPerGroup == 0) {
-                if (acc >= kAcc && !mbar_wait(acc_empty(acc % kAcc), (uint32_t)(acc / kAcc + 1) & 1, kWaitLimit)) {
-                  ok = false;
-                  break;
-                }
-                tcgen05_fence_after();
-              }
-              const uint64_t da = smem_desc(stage_a(s) + (k / 4) * L::kBlockA) + 2 * (k % 4);
-              const uint64_t db = smem_desc(stage_b(s) + (k / 4) * L::kBlockB) + 2 * (k % 4);
-              mma_bf16(tmem + (uint32_t)(acc % kAcc * BT), da, db, idesc, step % kStepsPerGroup != 0);
+              if (step % kStepsPerGroup == 0 && acc >= kAcc)
+                ok = ok && mbar_wait(acc_empty(acc % kAcc), (uint32_t)(acc / kAcc + 1) & 1, kWaitLimit);
+              if (!ok) break;
+              if (k == 0 || step % kStepsPerGroup == 0) tcgen05_fence_after();
+              const uint32_t d = tmem + (uint32_t)(acc % kAcc * BT);
+              if (issuer)
+                mma_bf16(d, da + 8 * k, desc_hi, db + (k / 4) * (L::kBlockB >> 4) + 2 * (k % 4), idesc,
+                         step % kStepsPerGroup != 0);
               if ((step + 1) % kStepsPerGroup == 0) {
                 ++acc;
                 // a commit takes the issuing thread about 180 cycles: the stage's own
                 // says too that the group which ends with it is complete
-                if (k + 1 < kSteps) mma_commit(mid(inner++ % kAcc));
+                if (k + 1 < kSteps) {
+                  if (issuer) mma_commit(mid(inner % kAcc));
+                  ++inner;
+                }
               }
             }
-            mma_commit(A::kOne ? done((acc - 1) % kAcc) : empty(s));
+            if (!ok) break;
+            if (issuer) mma_commit(done(g % kDone));
           }
         }
       }
-      if (!ok) fail_w4(abort_flag);
-      mma_commit(drain);
-      if (!mbar_wait(drain, 0, kWaitLimit)) fail_w4(abort_flag);
+      if (!ok && issuer) fail_w4(abort_flag);
+      if (issuer) mma_commit(drain);
+      if (!mbar_wait(drain, 0, kWaitLimit) && issuer) fail_w4(abort_flag);
     }
-  } else if (warp < L::kEpiWarp) {
-    // nibbles to bf16: thread = weight row of the tile
-    regs_dec<L::kRegsDq>();
+  } else if (warp < kEpiWarp) {
+    // nibbles to bf16: thread = weight row of the tile, warpgroup = 32 k of each chunk
+    regs_dec<kRegsDq>();
     const int wg = warp / 4 - 1;
     const int row = threadIdx.x & 127;
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) +
+                               (uint32_t)(L::kOffA + wg % (2 * L::kSub) * 16);
     int g = 0;  // chunks so far
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row;
       const uint8_t* zrow = zeros && n < N ? zeros + (int64_t)n * ld_z : nullptr;
-      for (int ch = cb; ch < ce && ok; ++ch, ++g) {
+      for (int ch = cb; ch < ce; ++ch, ++g) {
         const int s = g % SQ;
-        uint32_t zp[kStages];
-#pragma unroll
-        for (int st = 0; st < kStages; ++st) zp[st] = zero_at<GROUP>(zrow, ch * 4 + st * 2 + wg, K);
+        const uint32_t zp = zero_at<GROUP>(zrow, ch * 4 + wg, K);
         if (!mbar_wait(q_full(s), (g / SQ) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
-        const unsigned char* src = gbase + L::kOffQ + s * L::kStageQ + row * 64;
-#pragma unroll
-        for (int st = 0; st < kStages; ++st) {
-          // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
-          const uint4 q = *reinterpret_cast<const uint4*>(src + (((st * 2 + wg) ^ ((row >> 1) & 3)) << 4));
-          const __nv_bfloat162 zc = zero_pair(zp[st]);
-          const uint4 v[4] = {unpack8(q.x, zc), unpack8(q.y, zc), unpack8(q.z, zc), unpack8(q.w, zc)};
-          const int at = g * kStages + st, sa = at % S;
-          if (!stage_free(at)) {
-            ok = false;
-            break;
-          }
-          // 16-byte granule i of the row's 128 bytes at i ^ (r % 8)
-          unsigned char* dst = gbase + sa * L::kStage + L::kStageB + (wg / 2) * L::kBlockA + row * 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + ((((wg & 1) * 4 + i) ^ (row & 7)) << 4)) = v[i];
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full(sa));
+        // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
+        const uint4 q = *reinterpret_cast<const uint4*>(gbase + L::kOffQ + s * L::kStageQ + row * 64 +
+                                                        ((wg ^ ((row >> 1) & 3)) << 4));
+        const __nv_bfloat162 zc = zero_pair(zp);
+        const uint4 v[4] = {unpack8(q.x, zc), unpack8(q.y, zc), unpack8(q.z, zc), unpack8(q.w, zc)};
+        const int st = g * kStages + wg / (2 * L::kSub);
+        if (!stage_done(st - kSA)) {
+          ok = false;
+          break;
         }
-        // the copy of the next weights goes through another proxy than the reads of
-        // these: it may start when they are done for certain, their results stored
-        if (lane == 0 && ok) mbar_arrive(q_empty(s));
+        tcgen05_fence_after();
+        const uint32_t at = lane_addr + (uint32_t)(st % kSA * L::kStageCols);
+        const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        const uint32_t hi[8] = {v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+        tmem_st8(at, lo);
+        tmem_st8(at + 8, hi);
+        tmem_wait_st();
+        tcgen05_fence_before();
+        // the copy of the next weights goes through another proxy than the read of these:
+        // it may start when that is done for certain, its result stored
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(a_full(st % kSA));
+          mbar_arrive(q_empty(s));
+        }
       }
     }
     if (!ok && lane == 0) fail_w4(abort_flag);
   } else {
-    regs_inc<L::kRegsEpi>();
+    regs_inc<kRegsEpi>();
     constexpr int kCols = BT / 2;  // columns of a warp
-    const int quad = warp & 3, h = (warp - L::kEpiWarp) / 4;
+    const int quad = warp & 3, h = (warp - kEpiWarp) / 4;
     const int row = quad * 32 + lane;
     int acc = 0, inner = 0;
     bool ok = true;
@@ -459,11 +461,9 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
         // barrier's next phase is not over
         const int last = (acc % kG + 1) * kStepsPerGroup - 1;  // its last product in the chunk
         uint32_t bar, parity;
-        if (A::kOne) {
-          bar = done(acc % kAcc), parity = (uint32_t)(acc / kAcc) & 1;
-        } else if ((last + 1) % kSteps == 0) {
+        if ((last + 1) % kSteps == 0) {
           const int st = acc / kG * kStages + last / kSteps;
-          bar = empty(st % S), parity = (uint32_t)(st / S) & 1;
+          bar = done(st % kDone), parity = (uint32_t)(st / kDone) & 1;
         } else {
           bar = mid(inner % kAcc), parity = (uint32_t)(inner / kAcc) & 1;
           ++inner;
@@ -516,11 +516,11 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   if constexpr (SPLIT) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();  // the totals of every rank are in place
-    if (warp >= L::kEpiWarp && !*abort_flag) {
+    if (warp >= kEpiWarp && !*abort_flag) {
       // rank q finishes columns [q BT / splits, (q + 1) BT / splits): each element the
       // ranks' totals in rank order, 4 weight rows a thread
       const int n0 = t_first % n_tiles * kBN, m0 = t_first / n_tiles * BT;
-      const int e = threadIdx.x - 32 * L::kEpiWarp, n = n0 + (e & 31) * 4;
+      const int e = threadIdx.x - 32 * kEpiWarp, n = n0 + (e & 31) * 4;
       for (int j = rank * BT / splits + e / 32; j < (rank + 1) * BT / splits; j += kEpiWarps) {
         if (m0 + j >= M) break;
         const uint32_t at = base + (uint32_t)((j * L::kPartPitch + (e & 31) * 4) * 4);
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<BT>::kThreads, 1)
   tcgen05_fence_before();
   __syncthreads();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(A::kCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
 constexpr int kMaxSplits = 8;
@@ -572,12 +572,12 @@ cudaError_t configure(const Resident** out) {
     // the roles' registers come out of what the CTA is launched with
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-    if (at.numRegs * (L::kThreads / 128) < L::kRegs) return cudaErrorInvalidConfiguration;
+    if (at.numRegs * (kThreads / 128) < kRegs) return cudaErrorInvalidConfiguration;
     if (SPLIT) {
       for (int size = 2; size <= kMaxSplits; ++size) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(size);
-        cfg.blockDim = dim3(L::kThreads);
+        cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = L::kAlloc;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -628,7 +628,7 @@ cudaError_t launch_one(const LinearW4Args& g, const CUtensorMap& ma, const CUten
   const int64_t tiles = ((g.M + BT - 1) / BT) * ((g.N + kBN - 1) / kBN);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * splits : (tiles < sms ? tiles : sms)));
-  cfg.blockDim = dim3(L::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -675,8 +675,13 @@ cudaError_t launch_bt(const LinearW4Args& g, int sms, cudaStream_t stream) {
 cudaError_t launch_gemm_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream) {
   if (g.M <= 32) return launch_bt<32>(g, dev.sm_count, stream);
   if (g.M <= 64) return launch_bt<64>(g, dev.sm_count, stream);
-  if (g.M <= 128) return launch_bt<128>(g, dev.sm_count, stream);
-  return launch_bt<256>(g, dev.sm_count, stream);
+  // rounds of tiles times a tile's width and fixed share
+  auto cost = [&](int64_t bt) {
+    const int64_t tiles = ((g.M + bt - 1) / bt) * ((g.N + kBN - 1) / kBN);
+    return (tiles + dev.sm_count - 1) / dev.sm_count * (bt + 32);
+  };
+  return g.M <= 128 || cost(128) <= cost(192) ? launch_bt<128>(g, dev.sm_count, stream)
+                                              : launch_bt<192>(g, dev.sm_count, stream);
 }
 
 int read_gemm_w4_faults(bool clear) {
