@@ -61,7 +61,7 @@ constexpr int kThreads = 128 * (1 + kDqGroups + 2);
 constexpr int kEpiWarp = 4 * (1 + kDqGroups);
 // registers per thread of the roles; their sum over the warpgroups is what the CTA is
 // launched with (72 x 7)
-constexpr int kRegsLoad = 40, kRegsDq = 48, kRegsEpi = 136;
+constexpr int kRegsLoad = 40, kRegsDq = 40, kRegsEpi = 152;
 constexpr int kRegs = kRegsLoad + kDqGroups * kRegsDq + 2 * kRegsEpi;
 static_assert(kRegs <= (65536 / kThreads / 8 * 8) * (kThreads / 128), "more registers than a CTA has");
 constexpr int kSA = 4;         // stages of weights in tensor memory
@@ -169,18 +169,52 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {
   return *reinterpret_cast<const __nv_bfloat162*>(&v);
 }
 
-// the bits of a row's scale of group g, 0 past its groups (a value that is made of what a
-// load brings would be waited for where it is made)
-__device__ __forceinline__ uint32_t scale_bits(const void* scales, int s_bf16, int64_t row, int g, int groups) {
-  if (g >= groups) return 0;
-  return s_bf16 ? static_cast<const uint16_t*>(scales)[row + g] : static_cast<const uint32_t*>(scales)[row + g];
-}
+// The scales of a row's G groups in a chunk, as the bits that the loads bring (a value
+// made of them would be waited for where it is made): mode 0 f32, 1 bf16 in a word each,
+// 2 bf16 in pairs (aligned: a warp's rows are 32 lines of the cache, whatever it takes of
+// them).  0 past the row's groups.
+template <int G>
+struct ChunkScales {
+  uint32_t r[G];
+  __device__ __forceinline__ void fetch(const void* scales, int mode, int64_t row, int g, int groups) {
+    if (mode == 2 && G > 1) {
+#pragma unroll
+      for (int e = 0; e < G / 2; ++e) r[e] = 0;
+      const uint16_t* p = static_cast<const uint16_t*>(scales) + row + g;
+      if (g + G <= groups) {
+        if constexpr (G == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          r[0] = v.x, r[1] = v.y;
+        } else {
+          r[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e + 1 < G; ++e)
+          if (g + e < groups) r[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < G; ++e)
+        r[e] = g + e >= groups ? 0u
+                               : (mode ? (uint32_t)static_cast<const uint16_t*>(scales)[row + g + e]
+                                       : static_cast<const uint32_t*>(scales)[row + g + e]);
+    }
+  }
+  __device__ __forceinline__ float get(int mode, int e) const {
+    if (mode == 2 && G > 1) return __uint_as_float(e & 1 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
+    return __uint_as_float(mode ? r[e] << 16 : r[e]);
+  }
+};
 
 // a row's zero point for the b-th 32 k
 template <int GROUP>
 __device__ __forceinline__ uint32_t zero_at(const uint8_t* row, int b, int K) {
   return row && b * 32 < K ? row[b * 32 / GROUP] & 127u : 8u;
 }
+
+__device__ __forceinline__ void tmem_take(uint32_t taddr, uint32_t (&v)[8]) { tmem_ld8(taddr, v); }
+__device__ __forceinline__ void tmem_take(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
 
 // one weight row's totals down a column of C, the residual (or null) added: 16 at a
 // time, a batch's residuals read together
@@ -223,7 +257,7 @@ __device__ __forceinline__ void fail_w4(volatile int* abort_flag) {
 template <int BT, int GROUP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_w4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_q, void* c,
-                   int64_t ld_c, int c_bf16, const void* __restrict__ scales, int64_t ld_s, int s_bf16,
+                   int64_t ld_c, int c_bf16, const void* __restrict__ scales, int64_t ld_s, int s_mode,
                    const uint8_t* __restrict__ zeros, int64_t ld_z, const float* r, int64_t ld_r, int M, int N, int K,
                    int splits) {
   using L = Cfg<BT>;
@@ -268,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSA; ++s) mbar_init(a_full(s), 4 * kDqGroups / kStages);
+    for (int s = 0; s < kSA; ++s) mbar_init(a_full(s), 4 * L::kSub);
     for (int s = 0; s < SB; ++s) mbar_init(b_full(s), 1);
     for (int s = 0; s < SQ; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 4 * kDqGroups);
+      mbar_init(q_empty(s), 8);
     }
     for (int s = 0; s < kDone; ++s) mbar_init(done(s), 1);
     for (int a = 0; a < kAcc; ++a) {
@@ -385,44 +419,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(drain, 0, kWaitLimit) && issuer) fail_w4(abort_flag);
     }
   } else if (warp < kEpiWarp) {
-    // nibbles to bf16: thread = weight row of the tile, warpgroup = 32 k of each chunk
+    // nibbles to bf16: thread = weight row of the tile; warpgroups 0 and 1 take the halves
+    // of one chunk, 2 and 3 those of the next
     regs_dec<kRegsDq>();
-    const int wg = warp / 4 - 1;
+    const int wg = warp / 4 - 1, half = wg & 1;
     const int row = threadIdx.x & 127;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) +
-                               (uint32_t)(L::kOffA + wg % (2 * L::kSub) * 16);
+                               (uint32_t)(L::kOffA + (L::kSub == 2 ? half * 32 : 0));
     int g = 0;  // chunks so far
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row;
       const uint8_t* zrow = zeros && n < N ? zeros + (int64_t)n * ld_z : nullptr;
       for (int ch = cb; ch < ce; ++ch, ++g) {
+        if ((g & 1) != wg / 2) continue;
         const int s = g % SQ;
-        const uint32_t zp = zero_at<GROUP>(zrow, ch * 4 + wg, K);
+        uint32_t zp[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) zp[b] = zero_at<GROUP>(zrow, ch * 4 + half * 2 + b, K);
         if (!mbar_wait(q_full(s), (g / SQ) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
-        // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
-        const uint4 q = *reinterpret_cast<const uint4*>(gbase + L::kOffQ + s * L::kStageQ + row * 64 +
-                                                        ((wg ^ ((row >> 1) & 3)) << 4));
-        const __nv_bfloat162 zc = zero_pair(zp);
-        const uint4 v[4] = {unpack8(q.x, zc), unpack8(q.y, zc), unpack8(q.z, zc), unpack8(q.w, zc)};
-        const int st = g * kStages + wg / (2 * L::kSub);
-        if (!stage_done(st - kSA)) {
-          ok = false;
-          break;
-        }
-        tcgen05_fence_after();
+        const unsigned char* src = gbase + L::kOffQ + s * L::kStageQ + row * 64;
+        const int st = g * kStages + (L::kSub == 2 ? 0 : half);
         const uint32_t at = lane_addr + (uint32_t)(st % kSA * L::kStageCols);
-        const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-        const uint32_t hi[8] = {v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-        tmem_st8(at, lo);
-        tmem_st8(at + 8, hi);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          // the copy's 64-byte swizzle: piece b of row r at b ^ (r / 2 % 4)
+          const uint4 q = *reinterpret_cast<const uint4*>(src + (((half * 2 + b) ^ ((row >> 1) & 3)) << 4));
+          const __nv_bfloat162 zc = zero_pair(zp[b]);
+          const uint4 v[4] = {unpack8(q.x, zc), unpack8(q.y, zc), unpack8(q.z, zc), unpack8(q.w, zc)};
+          if (b == 0) {
+            if (!stage_done(st - kSA)) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after();
+          }
+          const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+          const uint32_t hi[8] = {v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+          tmem_st8(at + 16 * b, lo);
+          tmem_st8(at + 16 * b + 8, hi);
+        }
+        if (!ok) break;
         tmem_wait_st();
         tcgen05_fence_before();
-        // the copy of the next weights goes through another proxy than the read of these:
-        // it may start when that is done for certain, its result stored
+        // the copy of the next weights goes through another proxy than the reads of these:
+        // it may start when they are done for certain, their results stored
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(a_full(st % kSA));
@@ -436,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = BT / 2;  // columns of a warp
     const int quad = warp & 3, h = (warp - kEpiWarp) / 4;
     const int row = quad * 32 + lane;
-    int acc = 0, inner = 0;
+    constexpr int kTake = BT > 128 ? 8 : 16;  // columns at a time
+    int g = 0;  // chunks so far
     bool ok = true;
     for (int t = t_first; t < tiles && ok && !*abort_flag; t += t_step) {
       const int n = t % n_tiles * kBN + row, m0 = t / n_tiles * BT + h * kCols;
@@ -446,51 +491,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kCols / 2; ++j) total[j] = make_float2(0.0f, 0.0f);
       const int groups = n_in ? (K + GROUP - 1) / GROUP : 0;
       const int64_t s_row = (int64_t)n * ld_s;
-      uint32_t ahead[2];  // the bits of the next two groups' scales
-      ahead[0] = scale_bits(scales, s_bf16, s_row, cb * kG, groups);
-      ahead[1] = scale_bits(scales, s_bf16, s_row, cb * kG + 1, groups);
-#pragma unroll 2
-      for (int gr = cb * kG; gr < ce * kG; ++gr, ++acc) {
-        const uint32_t bits = ahead[(gr - cb * kG) & 1];
-        const uint32_t fetched = scale_bits(scales, s_bf16, s_row, gr + 2, groups);
-        if ((gr - cb * kG) & 1) ahead[1] = fetched;
-        else ahead[0] = fetched;
-        const float sc = __uint_as_float(s_bf16 ? bits << 16 : bits);
-        // the group is complete when the stage that it ends with is, or at a barrier of its
-        // own inside a stage: the products are at most kAcc groups ahead of this, so the
-        // barrier's next phase is not over
-        const int last = (acc % kG + 1) * kStepsPerGroup - 1;  // its last product in the chunk
-        uint32_t bar, parity;
-        if ((last + 1) % kSteps == 0) {
-          const int st = acc / kG * kStages + last / kSteps;
-          bar = done(st % kDone), parity = (uint32_t)(st / kDone) & 1;
-        } else {
-          bar = mid(inner % kAcc), parity = (uint32_t)(inner / kAcc) & 1;
-          ++inner;
-        }
-        if (!mbar_wait(bar, parity, kWaitLimit)) {
-          ok = false;
-          break;
-        }
-        tcgen05_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc % kAcc * BT + h * kCols);
-        const float2 s2 = make_float2(sc, sc);
-        uint32_t v[2][8];
-        tmem_ld8(taddr, v[0]);
-        tmem_wait(v[0]);
+      ChunkScales<kG> next;
+      next.fetch(scales, s_mode, s_row, cb * kG, groups);
+      for (int ch = cb; ch < ce && ok; ++ch, ++g) {
+        const ChunkScales<kG> now = next;
+        if (ch + 1 < ce) next.fetch(scales, s_mode, s_row, (ch + 1) * kG, groups);
 #pragma unroll
-        for (int j = 0; j < kCols / 8; ++j) {
-          if (j + 1 < kCols / 8) tmem_ld8(taddr + (uint32_t)(8 * (j + 1)), v[(j + 1) & 1]);
+        for (int e = 0; e < kG; ++e) {
+          // the group is complete when the stage that it ends with is, or at a barrier of its
+          // own inside a stage: the products are at most kAcc groups ahead of this, so the
+          // barrier's next phase is not over
+          constexpr int kInner = kG > kStages ? kG - kStages : 0;  // such groups in a chunk
+          const int last = (e + 1) * kStepsPerGroup - 1;           // its last product in the chunk
+          uint32_t bar, parity;
+          if ((last + 1) % kSteps == 0) {
+            const int st = g * kStages + last / kSteps;
+            bar = done(st % kDone), parity = (uint32_t)(st / kDone) & 1;
+          } else {
+            const int i = g * kInner + e - last / kSteps;
+            bar = mid(i % kAcc), parity = (uint32_t)(i / kAcc) & 1;
+          }
+          if (!mbar_wait(bar, parity, kWaitLimit)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          const int acc = (g * kG + e) % kAcc;
+          const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * BT + h * kCols);
+          const float sc = now.get(s_mode, e);
+          const float2 s2 = make_float2(sc, sc);
+          uint32_t v[2][kTake];
+          tmem_take(taddr, v[0]);
+          tmem_wait(v[0]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            total[4 * j + i] = __ffma2_rn(
-                s2, make_float2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
-                total[4 * j + i]);
-          if (j + 1 < kCols / 8) tmem_wait(v[(j + 1) & 1]);
+          for (int j = 0; j < kCols / kTake; ++j) {
+            if (j + 1 < kCols / kTake) tmem_take(taddr + (uint32_t)(kTake * (j + 1)), v[(j + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < kTake / 2; ++i)
+              total[kTake / 2 * j + i] = __ffma2_rn(
+                  s2, make_float2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
+                  total[kTake / 2 * j + i]);
+            if (j + 1 < kCols / kTake) tmem_wait(v[(j + 1) & 1]);
+          }
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty(acc));
         }
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(acc % kAcc));
       }
       if (!ok) break;
       if constexpr (SPLIT) {
@@ -640,7 +686,10 @@ cudaError_t launch_one(const LinearW4Args& g, const CUtensorMap& ma, const CUten
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mq, g.c, g.ld_c, g.c_bf16, g.scales, g.ld_s, g.s_bf16, g.zeros, g.ld_z,
+  constexpr int kG = kChunk / GROUP;  // a chunk's scales in one load, where they are aligned
+  const bool pairs = g.ld_s % kG == 0 && reinterpret_cast<uintptr_t>(g.scales) % (2 * kG) == 0;
+  const int s_mode = !g.s_bf16 ? 0 : (pairs ? 2 : 1);
+  return cudaLaunchKernelEx(&cfg, kern, ma, mq, g.c, g.ld_c, g.c_bf16, g.scales, g.ld_s, s_mode, g.zeros, g.ld_z,
                             g.r, g.ld_r, (int)g.M, (int)g.N, (int)g.K, SPLIT ? splits : 1);
 }
 

@@ -2,23 +2,17 @@
 //
 //   C[m][n] = sum_g s[n][g] sum_{k in g} (q[n][k] - z[n][g]) a[m][k]  (+ R[m][n])
 //
-// One warp-level tensor product (16 weight rows x 8 activation rows) per 16 k:
-// the difference q - z, an integer of at most 4 bits and a sign, is exact in
-// bf16, so the products are exact, the sums are f32, and the scale meets the
-// sum of a group in f32: no weight is rounded.
+// The difference q - z, an integer of few bits, is exact in bf16 and in f32, so the
+// products are exact, the sums are f32, and the scale meets the sum of a group in f32:
+// no weight is rounded.  Three kernels:
 //
-// A nibble becomes a bf16 by two operations per pair: (w >> 4 i) & 0x000f000f
-// puts nibbles i and i + 4 of a word into the low bits of the halves of a
-// register, 0x4300 above them makes them 128 + q, and a packed subtraction
-// takes 128 + z off.  The pairs (i, i + 4) are the product's k order; the
-// activations are put into the same order.
+//   one row         f32 units (one_kernel)
+//   up to 8 rows    warp-level products of 16 weight rows x 8 activation rows (rows_kernel)
+//   more            tensor memory and tcgen05 (gemm_w4.cu)
 //
-// Bound: the weights' way from HBM, and the warp-level product, which takes 32 cycles
-// of a quarter of an SM (50000 x 2560: 11.7 us to read, 13.8 to multiply).  A CTA takes 16
-// weight rows and its warps the rows' units of 128 k in turn.  Lane (g, t) reads 16 bytes
-// of rows g and g + 8, straight into registers and some units ahead (tensor copies of 16
-// x 64 bytes into shared memory took 33 us for those weights, bulk copies of 512 bytes
-// 40).  Activations come from the L1 cache.  The warps' sums are added in warp order.
+// All read a weight row's bytes once.  A warp-level product of 16 x 8 x 16 takes about 64
+// cycles of a quarter of an SM, whatever part of its 8 columns is filled; two rows on the
+// f32 units take as long (50000 x 2560, us: one row 30 against 35, two 42 against 35).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +24,8 @@ namespace {
 
 constexpr int kUnit = 128;   // k of a warp's turn: 64 bytes of a weight row
 constexpr int kSpan = 8192;  // k whose scales are held at once
-constexpr int kRows = 16;
+constexpr int kRows = 16, kCols = 8;
+constexpr int kAhead = 2;    // units on their way to a warp's registers
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -68,6 +63,144 @@ __device__ __forceinline__ uint4 load_x(const __nv_bfloat16* p, int k, int K) {
   return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
 
+constexpr int kOneWarps = 8;
+constexpr int kOneRows = 4;  // weight rows of a warp
+constexpr int kOneK = 512;   // k of a warp's turn, 16 a lane
+
+// two nibbles' bytes of w as f32, by a byte permutation each
+template <uint32_t SEL0, uint32_t SEL1>
+__device__ __forceinline__ float2 nibbles_f32(uint32_t w, uint32_t magic, float2 zero) {
+  const float2 v = make_float2(__uint_as_float(__byte_perm(w, magic, SEL0)), __uint_as_float(__byte_perm(w, magic, SEL1)));
+  return __fadd2_rn(v, zero);
+}
+
+// One activation row.  A warp takes four weight rows, lane l k = 512 i + 16 l .. of
+// them (256 neighbouring bytes a row); 2^kw_shift warps of a CTA share their rows and take
+// the turns i in turn.  A nibble becomes f32 by one byte permutation: its byte moved to bits
+// 8 .. 15 below 0x47 (even nibbles: 2^15 + q) or 0x45 (odd nibbles, left in the byte's high
+// half: 2^11 + q), less 2^15 + z or 2^11 + z, all exact.  A lane's 16 products, of one
+// group, are summed and meet their scale; the lanes' totals are added by a butterfly, the
+// warps' in order.  Lanes and rows outside the matrix read inside it and multiply zeros, or
+// are not stored: the loop has no branches (it is bound by its instructions).
+template <bool ZEROS>
+__global__ void __launch_bounds__(32 * kOneWarps, 3) linear_w4_one_kernel(const LinearW4Args a, int group_shift, int kw_shift) {
+  constexpr int R = kOneRows;
+  __shared__ float part[kOneWarps][R];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int kw_n = 1 << kw_shift, kw = warp & (kw_n - 1), rw = warp >> kw_shift;
+  const int rows_cta = (kOneWarps >> kw_shift) * R;
+  const int N = (int)a.N, K = (int)a.K;
+  const int n0 = blockIdx.x * rows_cta + rw * R;
+  const int k_last = (K + 31) / 32 * 32 - 16, g_last = (K - 1) >> group_shift;
+  const int turns = (K + kOneK - 1) / kOneK;
+  grid_dependency_begin();
+
+  // rows past N: the last one's bytes
+  const int n_first = n0 < N ? n0 : N - 1;
+  const int last = N - 1 - n_first < R - 1 ? N - 1 - n_first : R - 1;
+  const uint8_t* qp = a.q + (int64_t)n_first * a.ld_q;
+  const uint16_t* sh = static_cast<const uint16_t*>(a.scales) + (int64_t)n_first * a.ld_s;
+  const uint32_t* sw = static_cast<const uint32_t*>(a.scales) + (int64_t)n_first * a.ld_s;
+  const uint8_t* zp = ZEROS ? a.zeros + (int64_t)n_first * a.ld_z : nullptr;
+  int64_t dq[R], ds[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    dq[r] = (r < last ? r : last) * a.ld_q;
+    ds[r] = (r < last ? r : last) * a.ld_s;
+  }
+  uint2 w_next[R];
+  uint32_t s_next[R], z_next[R];
+  auto fetch = [&](int i) {
+    const int k0 = i * kOneK + lane * 16;
+    const int k = k0 < k_last ? k0 : k_last, g0 = k0 >> group_shift, g = g0 < g_last ? g0 : g_last;
+    const uint8_t* qk = qp + (k >> 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w_next[r] = __ldcs(reinterpret_cast<const uint2*>(qk + dq[r]));
+      s_next[r] = a.s_bf16 ? (uint32_t)__ldg(sh + ds[r] + g) : __ldg(sw + ds[r] + g);
+      if (ZEROS) z_next[r] = __ldg(zp + (r < last ? r : last) * a.ld_z + g);
+    }
+  };
+  float total[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) total[r] = 0.0f;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.a);
+  if (kw < turns) fetch(kw);
+#pragma unroll 1
+  for (int i = kw; i < turns; i += kw_n) {
+    const int k = i * kOneK + lane * 16;
+    const uint4 xv[2] = {load_x(x, k, K), load_x(x, k + 8, K)};
+    uint2 w[R];
+    float sc[R];
+    uint32_t z[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[r] = w_next[r];
+      sc[r] = k < K ? __uint_as_float(a.s_bf16 ? s_next[r] << 16 : s_next[r]) : 0.0f;
+      z[r] = ZEROS ? z_next[r] & 127u : 8u;
+    }
+    if (i + kw_n < turns) fetch(i + kw_n);
+    float2 acc[R];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the activations in pairs (k, k + 2), even and odd
+      float2 xe[2], xo[2];
+      const uint32_t u[4] = {xv[h].x, xv[h].y, xv[h].z, xv[h].w};
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        xe[p] = make_float2(__uint_as_float(u[2 * p] << 16), __uint_as_float(u[2 * p + 1] << 16));
+        xo[p] = make_float2(__uint_as_float(u[2 * p] & 0xffff0000u), __uint_as_float(u[2 * p + 1] & 0xffff0000u));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float e = __uint_as_float(0xc7000000u | z[r] << 8), o = __uint_as_float(0xc5000000u | z[r] << 12);
+        const float2 ze = make_float2(e, e), zo = make_float2(o, o);
+        const uint32_t word = h ? w[r].y : w[r].x;
+        const uint32_t even = word & 0x0f0f0f0fu, odd = word & 0xf0f0f0f0u;
+        const float2 e0 = nibbles_f32<0x7404, 0x7414>(even, 0x47000000u, ze);
+        const float2 e1 = nibbles_f32<0x7424, 0x7434>(even, 0x47000000u, ze);
+        const float2 o0 = nibbles_f32<0x7404, 0x7414>(odd, 0x45000000u, zo);
+        const float2 o1 = nibbles_f32<0x7424, 0x7434>(odd, 0x45000000u, zo);
+        acc[r] = h ? __ffma2_rn(e0, xe[0], acc[r]) : __fmul2_rn(e0, xe[0]);
+        acc[r] = __ffma2_rn(e1, xe[1], acc[r]);
+        acc[r] = __ffma2_rn(o0, xo[0], acc[r]);
+        acc[r] = __ffma2_rn(o1, xo[1], acc[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) total[r] = fmaf(sc[r], acc[r].x + acc[r].y, total[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v = total[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) part[warp][r] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < rows_cta) {
+    const int row = threadIdx.x, n = blockIdx.x * rows_cta + row;
+    if (n >= N) return;
+    const int first = (row / R) << kw_shift;
+    float v = part[first][row % R];
+    for (int j = 1; j < kw_n; ++j) v += part[first + j][row % R];
+    if (a.r) v += a.r[n];
+    store_out(a.c, n, a.c_bf16, v);
+  }
+}
+
+// as many warps to a row as it takes to give every SM 24 warps
+cudaError_t launch_one(const LinearW4Args& g, int sms, cudaStream_t stream) {
+  const int64_t warps = (g.N + kOneRows - 1) / kOneRows, want = 24 * (int64_t)sms, turns = (g.K + kOneK - 1) / kOneK;
+  int kw_shift = 0;
+  while (kw_shift < 3 && (warps << kw_shift) < want && (1 << kw_shift) < turns) ++kw_shift;
+  const int rows_cta = (kOneWarps >> kw_shift) * kOneRows;
+  const int shift = g.group == 32 ? 5 : (g.group == 64 ? 6 : 7);
+  const dim3 grid((unsigned)((g.N + rows_cta - 1) / rows_cta)), block(32 * kOneWarps);
+  return g.zeros ? launch_pdl(true, linear_w4_one_kernel<true>, grid, block, 0, stream, g, shift, kw_shift)
+                 : launch_pdl(true, linear_w4_one_kernel<false>, grid, block, 0, stream, g, shift, kw_shift);
+}
+
 // word t of the four lanes' w[0 .. 3] in the place of this lane's words: w[b] becomes
 // word t of lane b's
 __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
@@ -84,26 +217,24 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
   else w[2] = s0, w[3] = s1;
 }
 
-// 16 weight rows, NT x 8 activation rows.  scale_pitch: floats per weight row of the
+// 16 weight rows, 8 activation rows.  scale_pitch: floats per weight row of the
 // scales held (odd: 8 rows in 8 banks), whole units of them.
 //
 // The k of one product have to be of one group.  With groups of 128 lane t multiplies
 // word i of its own 16 bytes in product i (k = 32 t + 8 i ..); with smaller ones the four
 // lanes of a row exchange words first, and product b takes word t of piece b (k = 32 b +
 // 8 t ..).
-template <int WARPS, int NT, int GROUP, int AHEAD>
-__global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 768 / (32 * WARPS))
+template <int WARPS, int GROUP>
+__global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
     linear_w4_rows_kernel(const LinearW4Args a, const int scale_pitch) {
-  constexpr int kCols = 8 * NT;
   constexpr int kG = kUnit / GROUP;  // groups per unit
   constexpr bool kOwn = GROUP == kUnit;
-  static_assert(kSpan / kUnit / WARPS % AHEAD == 0, "a span ends with the last of the registers ahead");
+  static_assert(kSpan / kUnit / WARPS % kAhead == 0, "a span ends with the last of the registers ahead");
   extern __shared__ __align__(16) unsigned char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
   const int N = (int)a.N, K = (int)a.K;
-  const int n0 = blockIdx.x * kRows, m0 = blockIdx.y * kCols;
-  const int rows_m = a.M - m0 < kCols ? (int)(a.M - m0) : kCols;
+  const int n0 = blockIdx.x * kRows, rows_m = (int)a.M;
   const int rows_n = N - n0 < kRows ? N - n0 : kRows;
   const int pieces = (K + 31) / 32;  // 16 bytes of a weight row
   const int units = (K + kUnit - 1) / kUnit;
@@ -115,7 +246,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
 
   const uint8_t* q0 = g < rows_n ? a.q + (int64_t)(n0 + g) * a.ld_q + t * 16 : nullptr;
   const uint8_t* q1 = g + 8 < rows_n ? a.q + (int64_t)(n0 + g + 8) * a.ld_q + t * 16 : nullptr;
-  uint4 ahead[AHEAD][2];
+  uint4 ahead[kAhead][2];
   auto fetch = [&](int u, uint4 (&w)[2]) {
     w[0] = w[1] = make_uint4(0, 0, 0, 0);
     if (u * 4 + t < pieces) {
@@ -124,16 +255,10 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
     }
   };
 #pragma unroll
-  for (int d = 0; d < AHEAD; ++d) fetch(warp + d * WARPS, ahead[d]);
+  for (int d = 0; d < kAhead; ++d) fetch(warp + d * WARPS, ahead[d]);
 
-  const __nv_bfloat16* xr[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    xr[j] = j * 8 + g < rows_m ? static_cast<const __nv_bfloat16*>(a.a) + (int64_t)(m0 + j * 8 + g) * a.ld_a : nullptr;
-
-  float total[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) total[j][0] = total[j][1] = total[j][2] = total[j][3] = 0.0f;
+  const __nv_bfloat16* x = g < rows_m ? static_cast<const __nv_bfloat16*>(a.a) + g * a.ld_a : nullptr;
+  float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
   int u = warp;
   for (int span = 0; span < K; span += kSpan) {
@@ -161,31 +286,25 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
     const int u_end = units < (span + kSpan) / kUnit ? units : (span + kSpan) / kUnit;
     while (u < u_end) {
 #pragma unroll
-      for (int d = 0; d < AHEAD; ++d) {
+      for (int d = 0; d < kAhead; ++d) {
         if (u >= u_end) break;
-        uint4 xv[NT][4];
+        uint4 xv[4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            xv[j][i] = load_x(xr[j], u * kUnit + (kOwn ? t * 32 + i * 8 : i * 32 + t * 8), K);
+        for (int i = 0; i < 4; ++i) xv[i] = load_x(x, u * kUnit + (kOwn ? t * 32 + i * 8 : i * 32 + t * 8), K);
         // (registers that stay where they are: a move would wait for the load)
         uint32_t w0[4] = {ahead[d][0].x, ahead[d][0].y, ahead[d][0].z, ahead[d][0].w};
         uint32_t w1[4] = {ahead[d][1].x, ahead[d][1].y, ahead[d][1].z, ahead[d][1].w};
-        fetch(u + AHEAD * WARPS, ahead[d]);
+        fetch(u + kAhead * WARPS, ahead[d]);
         if (!kOwn) {
           transpose4(w0, t);
           transpose4(w1, t);
         }
         const float* sc = scales + g * scale_pitch + (u * kUnit - span) / GROUP;
         const unsigned char* zc = zeros + g * scale_pitch + (u * kUnit - span) / GROUP;
-        float acc[NT][4];
+        float acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (i * 32 % GROUP == 0) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-          }
+          if (i * 32 % GROUP == 0) acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
           const int e = i * 32 / GROUP;
           const __nv_bfloat162 z0 = zero_pair(a.zeros ? zc[e] : 8u);
           const __nv_bfloat162 z1 = zero_pair(a.zeros ? zc[8 * scale_pitch + e] : 8u);
@@ -193,23 +312,17 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
                                   nibble_pair<3>(w0[i], z0)};
           const uint32_t p1[4] = {nibble_pair<0>(w1[i], z1), nibble_pair<1>(w1[i], z1), nibble_pair<2>(w1[i], z1),
                                   nibble_pair<3>(w1[i], z1)};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            // the activations' pairs (k, k + 4)
-            mma16816(acc[j], p0[0], p1[0], p0[1], p1[1], __byte_perm(xv[j][i].x, xv[j][i].z, 0x5410),
-                     __byte_perm(xv[j][i].x, xv[j][i].z, 0x7632));
-            mma16816(acc[j], p0[2], p1[2], p0[3], p1[3], __byte_perm(xv[j][i].y, xv[j][i].w, 0x5410),
-                     __byte_perm(xv[j][i].y, xv[j][i].w, 0x7632));
-          }
+          // the activations' pairs (k, k + 4)
+          mma16816(acc, p0[0], p1[0], p0[1], p1[1], __byte_perm(xv[i].x, xv[i].z, 0x5410),
+                   __byte_perm(xv[i].x, xv[i].z, 0x7632));
+          mma16816(acc, p0[2], p1[2], p0[3], p1[3], __byte_perm(xv[i].y, xv[i].w, 0x5410),
+                   __byte_perm(xv[i].y, xv[i].w, 0x7632));
           if ((i + 1) * 32 % GROUP == 0) {
             const float s0 = sc[e], s1 = sc[8 * scale_pitch + e];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              total[j][0] = fmaf(s0, acc[j][0], total[j][0]);
-              total[j][1] = fmaf(s0, acc[j][1], total[j][1]);
-              total[j][2] = fmaf(s1, acc[j][2], total[j][2]);
-              total[j][3] = fmaf(s1, acc[j][3], total[j][3]);
-            }
+            total[0] = fmaf(s0, acc[0], total[0]);
+            total[1] = fmaf(s0, acc[1], total[1]);
+            total[2] = fmaf(s1, acc[2], total[2]);
+            total[3] = fmaf(s1, acc[3], total[3]);
           }
         }
         u += WARPS;
@@ -217,17 +330,14 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
     }
   }
   // the warps' sums, [warp][m][row]
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    float* p = part + (warp * kCols + j * 8 + 2 * t) * kRows + g;
-    p[0] = total[j][0];
-    p[kRows] = total[j][1];
-    p[8] = total[j][2];
-    p[kRows + 8] = total[j][3];
-  }
+  float* p = part + (warp * kCols + 2 * t) * kRows + g;
+  p[0] = total[0];
+  p[kRows] = total[1];
+  p[8] = total[2];
+  p[kRows + 8] = total[3];
   __syncthreads();
   for (int e = threadIdx.x; e < rows_m * kRows; e += 32 * WARPS) {
-    const int n = n0 + e % kRows, m = m0 + e / kRows;
+    const int n = n0 + e % kRows, m = e / kRows;
     if (n >= N) continue;
     float v = part[e];
 #pragma unroll
@@ -237,35 +347,33 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 1024 / (32 * WARPS) : 76
   }
 }
 
-template <int WARPS, int NT, int GROUP, int AHEAD>
+template <int WARPS, int GROUP>
 cudaError_t launch_rows(const LinearW4Args& g, cudaStream_t stream) {
-  constexpr int kCols = 8 * NT;
   // the groups of whole units: a unit across K reads (and ignores) those past the last
   const int64_t groups = (g.K + kUnit - 1) / kUnit * (kUnit / GROUP);
   const int scale_pitch = (int)(groups < kSpan / GROUP ? groups : kSpan / GROUP) | 1;
-  static_assert(WARPS * kCols * kRows * 4 + kRows * (kSpan / GROUP + 1) * 5 <= 48 * 1024, "static limit of shared memory");
+  static_assert(WARPS * kCols * kRows * 4 + kRows * (kSpan / GROUP + 1) * 5 <= 48 * 1024, "shared memory without opt-in");
   const int smem = WARPS * kCols * kRows * 4 + kRows * scale_pitch * (g.zeros ? 5 : 4);
-  const dim3 grid((unsigned)((g.N + kRows - 1) / kRows), (unsigned)((g.M + kCols - 1) / kCols));
-  return launch_pdl(true, linear_w4_rows_kernel<WARPS, NT, GROUP, AHEAD>, grid, dim3(32 * WARPS), smem, stream, g,
-                    scale_pitch);
+  const dim3 grid((unsigned)((g.N + kRows - 1) / kRows));
+  return launch_pdl(true, linear_w4_rows_kernel<WARPS, GROUP>, grid, dim3(32 * WARPS), smem, stream, g, scale_pitch);
 }
 
-template <int WARPS, int NT, int AHEAD>
+template <int WARPS>
 cudaError_t launch_group(const LinearW4Args& g, cudaStream_t stream) {
-  if (g.group == 32) return launch_rows<WARPS, NT, 32, AHEAD>(g, stream);
-  if (g.group == 64) return launch_rows<WARPS, NT, 64, AHEAD>(g, stream);
-  return launch_rows<WARPS, NT, 128, AHEAD>(g, stream);
+  if (g.group == 32) return launch_rows<WARPS, 32>(g, stream);
+  if (g.group == 64) return launch_rows<WARPS, 64>(g, stream);
+  return launch_rows<WARPS, 128>(g, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream) {
   if (g.M <= 0 || g.N <= 0) return cudaSuccess;
-  if (g.M > 16) return launch_gemm_w4(g, dev, stream);
+  if (g.M > kCols) return launch_gemm_w4(g, dev, stream);
+  if (g.M == 1) return launch_one(g, dev.sm_count, stream);
   // two CTAs per SM or fewer: more warps to a row, so that all of it is on its way at once
   const bool few = (g.N + kRows - 1) / kRows <= 2 * (int64_t)dev.sm_count && g.K > 8 * kUnit;
-  if (g.M > 8) return few ? launch_group<16, 2, 2>(g, stream) : launch_group<8, 2, 2>(g, stream);
-  return few ? launch_group<16, 1, 2>(g, stream) : launch_group<8, 1, 2>(g, stream);
+  return few ? launch_group<16>(g, stream) : launch_group<8>(g, stream);
 }
 
 }  // namespace mamba

@@ -8,7 +8,12 @@
 // Bound: HBM, one pass over the logits.  A row is cut over the CTAs of a cluster
 // (one CTA if there are rows enough), a CTA's slice over its threads in vectors of
 // 16 bytes, vector v to thread v % 256.  A thread keeps a running maximum (with
-// the first vector that holds it) and the two sums below it.
+// the first vector that holds it) and the two sums below it, in units of log2: e^d is
+// 2^(l L - r) with L = log2 e and r = L max l rounded once, one multiply-add and one
+// exponential an element.  (Rounding r moves every term alike, and the same r is in the
+// logarithm's other side.)  Elements below -2^100, -inf among them, are taken as -2^100, so
+// that no product is 0 times infinity; a row whose maximum is 2^24 from 0 or further gets
+// its sums again, from differences l - m.
 //
 // Alternatives cost no second pass: an element of the row's first n is at least as
 // large as the n-th largest thread maximum, so it lies in the subset of a thread
@@ -34,6 +39,8 @@ constexpr int kMaxTop = MAMBA_MAX_TOP;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 2048;
 constexpr float kLowest = -3.402823466e38f;
+constexpr float kLeast = -0x1p100f;  // its product with log2 e is exact
+constexpr float kNear = 0x1p24f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -67,28 +74,42 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
 template <typename T>
 struct Row {
   static constexpr int VEC = 16 / sizeof(T);
+  static constexpr uint32_t kNothing = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
   const T* base;  // 16-byte aligned
-  int skew;
-  int64_t V;
+  int skew, V;
+  int full_lo, full_hi;  // the vectors that lie inside the row
   __device__ Row(const void* p, int64_t v) {
     const uintptr_t u = reinterpret_cast<uintptr_t>(p);
     base = reinterpret_cast<const T*>(u & ~(uintptr_t)15);
     skew = (int)((u & 15) / sizeof(T));
-    V = v;
+    V = (int)v;
+    full_lo = skew ? 1 : 0;
+    full_hi = (int)(((int64_t)skew + V) / VEC);
   }
-  __device__ int64_t vectors() const { return (skew + V + VEC - 1) / VEC; }
-  // the values of vector v, -inf outside the row (whose memory is not read)
-  __device__ void load(int64_t v, float (&x)[VEC]) const {
-    const int64_t e0 = v * VEC - skew;
-    if (e0 >= 0 && e0 + VEC <= V) {
-      const uint4 u = *reinterpret_cast<const uint4*>(base + v * VEC);
-      unpack(u, x);
-    } else {
+  __device__ int vectors() const { return (int)(((int64_t)skew + V + VEC - 1) / VEC); }
+  // the words of vector v, -inf outside the row (whose memory is not read)
+  __device__ uint4 load(int v) const {
+    if (v >= full_lo && v < full_hi) return reinterpret_cast<const uint4*>(base)[v];
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        x[j] = e0 + j >= 0 && e0 + j < V ? to_f32(base[v * VEC + j]) : -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t lo = inside(element(v, 2 * i)) ? bits(v, 2 * i) : 0xff80u;
+        const uint32_t hi = inside(element(v, 2 * i + 1)) ? bits(v, 2 * i + 1) : 0xff80u;
+        w[i] = lo | hi << 16;
+      } else {
+        w[i] = inside(element(v, i)) ? bits(v, i) : 0xff800000u;
+      }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __device__ uint32_t bits(int v, int j) const {
+    const int64_t at = (int64_t)v * VEC + j;
+    if constexpr (sizeof(T) == 2) return reinterpret_cast<const uint16_t*>(base)[at];
+    else return reinterpret_cast<const uint32_t*>(base)[at];
+  }
+  __device__ int64_t element(int v, int j) const { return (int64_t)v * VEC - skew + j; }
+  __device__ bool inside(int64_t e) const { return e >= 0 && e < V; }
   static __device__ void unpack(const uint4& u, float (&x)[VEC]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     if constexpr (sizeof(T) == 2) {
@@ -102,21 +123,60 @@ struct Row {
       for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
     }
   }
-  __device__ bool inside(int64_t e) const { return e >= 0 && e < V; }
+  // the largest value (NaN if there is one), and the values, none below kLeast
+  static __device__ float largest(const uint4& u) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+      return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    } else {
+      return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                     max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+  }
+  static __device__ void bounded(const uint4& u, float (&x)[VEC]) {
+    if constexpr (sizeof(T) == 2) {
+      constexpr uint32_t kLow = 0xf180f180u;  // kLeast in bf16, twice
+      unpack(make_uint4(max2(u.x, kLow), max2(u.y, kLow), max2(u.z, kLow), max2(u.w, kLow)), x);
+    } else {
+      unpack(u, x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[i] = max_nan(x[i], kLeast);
+    }
+  }
+  static __device__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 
-// running maximum and sums of one thread; ref is max(m, lowest finite), so a
-// row of -inf has sums of nothing and no inf - inf
+// Running maximum m and sums of one thread; ref is L times the largest bounded value, s1
+// and s2 the sums of 2^d and d 2^d, d = l L - ref.
 struct Stats {
   float m, ref, s1, s2;
 };
 
 __device__ __forceinline__ void rescale(Stats& s, float ref) {
-  const float d = fmaxf(s.ref - ref, -1e30f);  // <= 0; NaN only when ref is NaN, and then s1 becomes NaN below
-  const float c = ex2_approx(d * kLog2e);
-  s.s2 = c * fmaf(d, s.s1, s.s2);
-  s.s1 *= c;
+  const float d = s.ref - ref;  // <= 0; NaN with a NaN, and so are the sums then
+  const float c = ex2_approx(d);
+  s.s2 = c == 0.0f ? 0.0f : c * fmaf(d, s.s1, s.s2);  // (sums below a far reference may be infinite)
+  s.s1 = c == 0.0f ? 0.0f : s.s1 * c;
   s.ref = ref;
+}
+
+template <int VEC>
+__device__ __forceinline__ void add_terms(Stats& s, const float (&x)[VEC]) {
+  const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-s.ref, -s.ref);
+  float2 a1 = make_float2(0.0f, 0.0f), a2 = a1;
+#pragma unroll
+  for (int j = 0; j < VEC; j += 2) {
+    const float2 d = __ffma2_rn(make_float2(x[j], x[j + 1]), l2, r2);
+    const float2 e = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+    a1 = __fadd2_rn(a1, e);
+    a2 = __ffma2_rn(e, d, a2);
+  }
+  s.s1 += a1.x + a1.y;
+  s.s2 += a2.x + a2.y;
 }
 
 struct SharedState {
@@ -125,14 +185,15 @@ struct SharedState {
   uint64_t all[kMaxCluster * kMaxTop];    // the cluster's
   uint64_t bound[kWarps];
   int subset[kThreads];
-  float stat[kWarps][3];
-  float mine[3];                          // this CTA's reference, S1, S2
+  float stat[kWarps][4];
+  float mine[4];                          // this CTA's maximum, reference, sums
   int n_subset, n_keys;
   uint64_t best;
+  uint64_t reach;                         // a bound that n of this CTA's elements reach
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLogprobsArgs a, int cluster) {
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const TokenLogprobsArgs a, int cluster) {
   using R = Row<T>;
   constexpr int VEC = R::VEC;
   __shared__ SharedState sh;
@@ -141,74 +202,88 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
   const int rank = (int)(blockIdx.x % cluster);
   grid_dependency_begin();
   const R r(static_cast<const T*>(a.logits) + row * a.ld, a.V);
-  const int64_t nv = r.vectors();
-  const int64_t v_lo = nv * rank / cluster, v_hi = nv * (rank + 1) / cluster;
+  const int nv = r.vectors();
+  const int v_lo = (int)((int64_t)nv * rank / cluster), v_hi = (int)((int64_t)nv * (rank + 1) / cluster);
 
-  Stats st{-INFINITY, kLowest, 0.0f, 0.0f};
-  int64_t first = -1;  // the first vector that holds m
-  for (int64_t v = v_lo + threadIdx.x; v < v_hi; v += kThreads) {
-    float x[VEC];
-    r.load(v, x);
-    float vm = x[0];
-#pragma unroll
-    for (int j = 1; j < VEC; ++j) vm = max_nan(vm, x[j]);
-    if (first < 0 || (!(vm <= st.m) && st.m == st.m)) {
-      st.m = vm;
-      first = v;
-    }
-    const float ref = max_nan(st.ref, vm);
+  Stats st{-INFINITY, kLeast * kLog2e, 0.0f, 0.0f};
+  int first = -1;  // the first vector that holds m
+  auto take = [&](const uint4& u0, const uint4& u1, int v) {
+    const float m0 = R::largest(u0), m1 = R::largest(u1);
+    // NaN stands above all; the first of equal ones stays
+    if (first < 0 || (!(m0 <= st.m) && st.m == st.m)) st.m = m0, first = v;
+    if (!(m1 <= st.m) && st.m == st.m) st.m = m1, first = v + kThreads;
+    const float ref = max_nan(st.ref, st.m * kLog2e);
     if (ref != st.ref) rescale(st, ref);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float d = max_nan(x[j] - ref, -1e30f);
-      const float e = ex2_approx(d * kLog2e);
-      st.s1 += e;
-      st.s2 = fmaf(e, d, st.s2);
+    float x[VEC];
+    R::bounded(u0, x);
+    add_terms(st, x);
+    R::bounded(u1, x);
+    add_terms(st, x);
+  };
+  const uint4 nothing = make_uint4(R::kNothing, R::kNothing, R::kNothing, R::kNothing);
+  // vectors that lie inside the row, two at a time and four on their way; the row's ends
+  // are their threads' first and last
+  const int hi = v_hi < r.full_hi ? v_hi : r.full_hi;
+  auto full = [&](int v) { return v >= r.full_lo && v < hi ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : nothing; };
+  int v = v_lo + (int)threadIdx.x;
+  if (v == 0 && r.full_lo > 0) take(r.load(0), nothing, 0);
+  if (v < hi) {
+    uint4 a0 = full(v), a1 = full(v + kThreads), b0 = full(v + 2 * kThreads), b1 = full(v + 3 * kThreads);
+    while (true) {
+      take(a0, a1, v);
+      a0 = full(v + 4 * kThreads), a1 = full(v + 5 * kThreads);
+      if ((v += 2 * kThreads) >= hi) break;
+      take(b0, b1, v);
+      b0 = full(v + 4 * kThreads), b1 = full(v + 5 * kThreads);
+      if ((v += 2 * kThreads) >= hi) break;
     }
   }
+  if (r.full_hi < nv && v_hi == nv && nv - 1 >= r.full_lo && (nv - 1 - v_lo) % kThreads == (int)threadIdx.x)
+    take(r.load(nv - 1), nothing, nv - 1);
 
-  // the CTA's sums
-  float ref = st.ref;
+  // sums over the CTA
+  auto join = [&](Stats s) {
+    float m = s.m, ref = s.ref;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ref = max_nan(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-  if (lane == 0) sh.stat[warp][0] = ref;
-  if (threadIdx.x == 0) sh.n_subset = sh.n_keys = 0;
-  __syncthreads();
-  ref = sh.stat[0][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) ref = max_nan(ref, sh.stat[w][0]);
-  rescale(st, ref);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    st.s1 += __shfl_xor_sync(0xffffffffu, st.s1, o);
-    st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, o);
-  }
-  if (lane == 0) {
-    sh.stat[warp][1] = st.s1;
-    sh.stat[warp][2] = st.s2;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-      s1 += sh.stat[w][1];
-      s2 += sh.stat[w][2];
+    for (int o = 16; o > 0; o >>= 1) {
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      ref = max_nan(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     }
-    sh.mine[0] = ref;
-    sh.mine[1] = s1;
-    sh.mine[2] = s2;
-  }
+    rescale(s, ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.s1 += __shfl_xor_sync(0xffffffffu, s.s1, o);
+      s.s2 += __shfl_xor_sync(0xffffffffu, s.s2, o);
+    }
+    if (lane == 0) {
+      sh.stat[warp][0] = m, sh.stat[warp][1] = ref;
+      sh.stat[warp][2] = s.s1, sh.stat[warp][3] = s.s2;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      Stats t{sh.stat[0][0], sh.stat[0][1], 0.0f, 0.0f};
+      for (int w = 1; w < kWarps; ++w) t.m = max_nan(t.m, sh.stat[w][0]), t.ref = max_nan(t.ref, sh.stat[w][1]);
+      for (int w = 0; w < kWarps; ++w) {
+        Stats q{0.0f, sh.stat[w][1], sh.stat[w][2], sh.stat[w][3]};
+        rescale(q, t.ref);
+        t.s1 += q.s1, t.s2 += q.s2;
+      }
+      sh.mine[0] = t.m, sh.mine[1] = t.ref, sh.mine[2] = t.s1, sh.mine[3] = t.s2;
+    }
+  };
+  if (threadIdx.x == 0) sh.n_subset = sh.n_keys = 0;
+  join(st);
 
   const int n = a.n_top;
+  uint64_t key = 0, bound = 0;
   if (n > 0) {
     // the thread's largest key
-    uint64_t key = 0;
     if (first >= 0) {
       float x[VEC];
-      r.load(first, x);
+      R::unpack(r.load(first), x);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const int64_t e = first * VEC - r.skew + j;
+        const int64_t e = r.element(first, j);
         if (r.inside(e)) {
           const uint64_t k = key_of(x[j], (uint32_t)e);
           key = k > key ? k : key;
@@ -226,7 +301,6 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
     if (lane == 0) sh.bound[warp] = best;
     __syncthreads();
     const int need = (n + per_warp - 1) / per_warp;
-    uint64_t bound = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       int above = 0;
@@ -244,24 +318,93 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
       __syncthreads();
       bound = sh.best;
     }
+    if (threadIdx.x == 0) sh.reach = bound;
+  }
+  // the row's sums, from the CTAs', and the best of their bounds: the CTA it comes from has n
+  // elements that reach it
+  Stats row_st;
+  auto gather = [&]() {
+    if (cluster > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      cl.sync();
+      row_st = Stats{-INFINITY, kLeast * kLog2e, 0.0f, 0.0f};
+      for (int c = 0; c < cluster; ++c) {
+        const float* p = cl.map_shared_rank(sh.mine, c);
+        row_st.m = max_nan(row_st.m, p[0]);
+        row_st.ref = max_nan(row_st.ref, p[1]);
+        if (n > 0) {
+          const uint64_t o = *cl.map_shared_rank(&sh.reach, c);
+          bound = o > bound ? o : bound;
+        }
+      }
+      for (int c = 0; c < cluster; ++c) {
+        const float* p = cl.map_shared_rank(sh.mine, c);
+        Stats o{0.0f, p[1], p[2], p[3]};
+        rescale(o, row_st.ref);
+        row_st.s1 += o.s1, row_st.s2 += o.s2;
+      }
+    } else {
+      __syncthreads();
+      row_st = Stats{sh.mine[0], sh.mine[1], sh.mine[2], sh.mine[3]};
+    }
+  };
+  gather();
+  // a maximum whose product with L is off by a part of 1 or more (a row of nothing but -inf
+  // among them): the sums from differences, their reference 0
+  const bool far = fabsf(row_st.m) >= kNear;
+  const float top_l = max_nan(row_st.m, kLowest);
+  if (far) {
+    Stats f{row_st.m, 0.0f, 0.0f, 0.0f};
+    for (int v = v_lo + (int)threadIdx.x; v < v_hi; v += kThreads) {
+      float x[VEC];
+      R::unpack(r.load(v), x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float d = max_nan(x[j] - top_l, kLeast) * kLog2e, e = ex2_approx(d);
+        f.s1 += e;
+        f.s2 = fmaf(e, d, f.s2);
+      }
+    }
+    if (cluster > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    join(f);
+    gather();
+  }
+
+  // the elements that reach the bound, and the first n of them
+  if (n > 0) {
     if (key >= bound && key != 0) sh.subset[atomicAdd(&sh.n_subset, 1)] = threadIdx.x;
     if (threadIdx.x < kMaxTop) sh.top[threadIdx.x] = 0;
     __syncthreads();
-    // the elements of those subsets that reach the bound
-    for (int s = warp; s < sh.n_subset; s += kWarps) {
-      for (int64_t v = v_lo + sh.subset[s] + (int64_t)lane * kThreads; v < v_hi; v += 32 * kThreads) {
-        float x[VEC];
-        r.load(v, x);
+    // the elements of those subsets that reach the bound, a thread's reads together
+    const int per = (v_hi - v_lo + kThreads - 1) / kThreads, items = sh.n_subset * per;
+    for (int i0 = threadIdx.x; i0 < items; i0 += 4 * kThreads) {
+      uint4 u[4];
+      int at[4];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int64_t e = v * VEC - r.skew + j;
-          if (!r.inside(e)) continue;
-          const uint64_t k = key_of(x[j], (uint32_t)e);
-          if (k >= bound) {
-            const int i = atomicAdd(&sh.n_keys, 1);
-            if (i < kCandidates) sh.keys[i] = k;
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q * kThreads;
+        at[q] = i < items ? v_lo + sh.subset[i / per] + i % per * kThreads : v_hi;
+        u[q] = at[q] < v_hi ? r.load(at[q]) : nothing;
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        if (order_of(R::largest(u[0])) >= (uint32_t)(bound >> 32) && at[0] < v_hi) {
+          float x[VEC];
+          R::unpack(u[0], x);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const int64_t e = r.element(at[0], j);
+            if (!r.inside(e)) continue;
+            const uint64_t k = key_of(x[j], (uint32_t)e);
+            if (k >= bound) {
+              const int i = atomicAdd(&sh.n_keys, 1);
+              if (i < kCandidates) sh.keys[i] = k;
+            }
           }
         }
+        u[0] = u[1], u[1] = u[2], u[2] = u[3];
+        at[0] = at[1], at[1] = at[2], at[2] = at[3];
       }
     }
     __syncthreads();
@@ -279,12 +422,12 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
       uint64_t last = ~0ull;
       for (int i = 0; i < n; ++i) {
         uint64_t k_best = 0;
-        for (int64_t v = v_lo + threadIdx.x; v < v_hi; v += kThreads) {
+        for (int v = v_lo + (int)threadIdx.x; v < v_hi; v += kThreads) {
           float x[VEC];
-          r.load(v, x);
+          R::unpack(r.load(v), x);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int64_t e = v * VEC - r.skew + j;
+            const int64_t e = r.element(v, j);
             if (!r.inside(e)) continue;
             const uint64_t k = key_of(x[j], (uint32_t)e);
             if (k < last && k > k_best) k_best = k;
@@ -300,34 +443,17 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
       }
     }
   }
-  __syncthreads();
-
-  // the row's sums and first n, from the CTAs'
-  float s1, s2;
-  if (cluster > 1) {
+  if (n > 0 && cluster > 1) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    ref = kLowest;
-    for (int c = 0; c < cluster; ++c) ref = max_nan(ref, *cl.map_shared_rank(&sh.mine[0], c));
-    s1 = s2 = 0.0f;
-    for (int c = 0; c < cluster; ++c) {
-      const float* p = cl.map_shared_rank(sh.mine, c);
-      Stats o{0.0f, p[0], p[1], p[2]};
-      rescale(o, ref);
-      s1 += o.s1;
-      s2 += o.s2;
-    }
-    if (n > 0) {
-      for (int i = threadIdx.x; i < cluster * n; i += kThreads) sh.all[i] = cl.map_shared_rank(sh.top, i / n)[i % n];
-    }
-    cl.sync();  // nobody's shared memory is read past here
-  } else {
-    ref = sh.mine[0];
-    s1 = sh.mine[1];
-    s2 = sh.mine[2];
+    for (int i = threadIdx.x; i < cluster * n; i += kThreads) sh.all[i] = cl.map_shared_rank(sh.top, i / n)[i % n];
   }
-  const float log_s1 = logf(s1);  // -inf for a row of -inf
-  auto logprob_of = [&](float l) { return l == -INFINITY && s1 == s1 ? -INFINITY : (l - ref) - log_s1; };
+  __syncthreads();
+  const float s1 = row_st.s1, s2 = row_st.s2;
+  const float log_s1 = log2f(s1);  // -inf for a row of -inf
+  // ln of the row's sum of e^(l - top_l): the reference is not quite L top_l
+  const float log_sum = (log_s1 - (far ? 0.0f : fmaf(top_l, kLog2e, -row_st.ref))) * kLn2;
+  auto logprob_of = [&](float l) { return l == -INFINITY && s1 == s1 ? -INFINITY : (l - top_l) - log_sum; };
   if (n > 0) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t k = sh.top[i];
@@ -343,20 +469,22 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
     }
   }
   if (rank == 0 && threadIdx.x == 0) {
-    if (a.entropy) a.entropy[row] = s1 == 0.0f ? 0.0f : log_s1 - s2 / s1;
+    if (a.entropy) a.entropy[row] = s1 == 0.0f ? 0.0f : (log_s1 - s2 / s1) * kLn2;
     if (a.logprob) {
       const int64_t t = a.tokens[row];
       a.logprob[row] = t < 0 ? 0.0f
                              : (t < a.V ? logprob_of(to_f32(static_cast<const T*>(a.logits)[row * a.ld + t])) : NAN);
     }
   }
+  if (cluster > 1) cg::this_cluster().sync();  // nobody's shared memory is read past here
 }
 
 template <typename T>
 cudaError_t launch_typed(const TokenLogprobsArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  // few rows: a row over a cluster, until every SM has a CTA or a slice falls under 4096 elements
+  // few rows: a row over a cluster, up to two CTAs per SM and no slice under 4096 elements
+  // (128 x 128000 bf16, 20 alternatives, us: one CTA a row 34, two 24, four 33, eight 49)
   int cluster = 1;
-  while (cluster < kMaxCluster && a.M * cluster * 2 <= dev.sm_count * 2 && a.V / (cluster * 2) >= 4096) cluster *= 2;
+  while (cluster < kMaxCluster && a.M * cluster * 2 <= dev.sm_count * (int64_t)2 && a.V / (cluster * 2) >= 4096) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.M * cluster));
   cfg.blockDim = dim3(kThreads);

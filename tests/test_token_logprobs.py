@@ -254,3 +254,25 @@ def test_on_another_stream_and_in_a_graph(cuda_lib, M):
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [700, 30011])
+@pytest.mark.parametrize("offset", [1e5, -1e5, 1e8, -1e9, -1e20, 1e30, -3e38])
+def test_rows_far_from_zero_and_masks_of_any_size(cuda_lib, V, dtype, offset):
+    """Rows of one far value, and rows of ordinary ones among far ones."""
+    l, t = rows(6, 4, V, dtype)
+    l[0] = offset
+    l[1, ::3] = offset
+    l[2] = torch.where(torch.arange(V, device="cuda") % 5 == 0, l[2].float(), -abs(offset)).to(DT[dtype])
+    l[3, V // 2:] = offset
+    # ln p of a token is as exact as its difference from the maximum, which the reference takes from the same logits
+    check(l, t, 6)
+
+
+@pytest.mark.gpu
+def test_steep_rows(cuda_lib):
+    """Differences of hundreds: every part but the largest underflows."""
+    l, t = rows(7, 5, 50000, "f32", spread=300.0)
+    check(l, t, 12)
