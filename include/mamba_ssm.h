@@ -462,8 +462,8 @@ MAMBA_API int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* 
  *     C[m][n] = sum_k a[m][k] s[n][k / group] (q[n][k] - z[n][k / group])  (+ R[m][n])
  * (No counterpart in the mamba-rs pages: an addition of this library.)  Differences
  * q - z are exact and a group's sum meets its scale in f32, so the result is that of
- * the weights as they are, to f32 rounding.  A row of the result does not depend on
- * how many rows the call has only up to that rounding.
+ * the weights as they are, to f32 rounding.  A row's result depends on how many rows the
+ * call has only by that rounding.
  *
  *   c         [M] rows of N at ld_c, dtype c_dtype                           (out)
  *   a         [M] rows of K bf16 at ld_a                                     (in)
@@ -475,7 +475,7 @@ MAMBA_API int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* 
  *   group     32, 64 or 128
  *   residual  [M] rows of N f32 at ld_r, or NULL; may be c itself (f32, same stride)
  * a and q must be 16-byte aligned, ld_a a multiple of 8 and ld_q of 16.  M, N, K
- * below 2^31.  Deterministic: the order of the sums depends on the sizes only.
+ * up to 2^30.  Deterministic: the order of the sums depends on the sizes only.
  * Errors: MAMBA_ERR_INVALID_ARG for NULL pointers, strides smaller than a row,
  * misaligned a / q, overlap of c with an input (other than the residual as above),
  * extent overflow; MAMBA_ERR_UNSUPPORTED for another group.
@@ -758,6 +758,41 @@ MAMBA_API int mamba_layer_step(float* hidden, const MambaLayer* layer, float* co
 MAMBA_API int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const MambaLayer* layers, int64_t n_layers,
                                               float* hidden, float* conv_state, float* ssm_state, int64_t B,
                                               void* workspace, int64_t workspace_bytes);
+
+/*
+ * The block with 4-bit projections: a projection whose q is not NULL is the
+ * mamba_linear_w4 call on it, in the place of mamba_linear_bf16 on the layer's bf16
+ * weight (which may then be NULL).  in_proj [2 d_inner][d_model], x_proj [dt_rank +
+ * 2 d_state][d_inner], dt_proj [d_inner][dt_rank], out_proj [d_model][d_inner].  Each
+ * call is its namesake's above with that one change: the same states, workspace
+ * (mamba_layer_workspace_bytes of the layer), checks and errors, and mamba_linear_w4's.
+ */
+typedef struct MambaW4 {
+  const uint8_t* q;     /* [out] rows of ceil(in / 32) * 16 bytes at ld_q, or NULL */
+  int64_t ld_q;
+  const void* scales;   /* [out] rows of ceil(in / group) at ld_s, scale_dtype */
+  int64_t ld_s;
+  int scale_dtype;
+  const uint8_t* zeros; /* [out] rows of ceil(in / group) at ld_z, or NULL (8) */
+  int64_t ld_z;
+  int64_t group;        /* 32, 64 or 128 */
+} MambaW4;
+
+typedef struct MambaLayerW4 {
+  MambaLayer layer;
+  MambaW4 in_proj, x_proj, dt_proj, out_proj;
+} MambaLayerW4;
+
+MAMBA_API int mamba_layer_w4_prefill(float* hidden, const MambaLayerW4* layer, const float* conv_state_in,
+                                     float* conv_state_out, const float* ssm_state_in, float* ssm_state_out,
+                                     int64_t B, int64_t T, void* workspace, int64_t workspace_bytes, void* stream);
+MAMBA_API int mamba_layer_w4_step(float* hidden, const MambaLayerW4* layer, float* conv_state, float* ssm_state,
+                                  int64_t layer_index, int64_t n_layers, int64_t B, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+MAMBA_API int mamba_layer_w4_decode_graph_create(MambaDecodeGraph** out, const MambaLayerW4* layers,
+                                                 int64_t n_layers, float* hidden, float* conv_state,
+                                                 float* ssm_state, int64_t B, void* workspace,
+                                                 int64_t workspace_bytes);
 
 /*
  * mamba_selective_scan_prefill_noalloc - the selective-scan prefill for callers

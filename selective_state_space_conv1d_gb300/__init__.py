@@ -21,7 +21,8 @@ C-ABI entry points (include/mamba_ssm.h), each backed by hand-written CUDA kerne
   mamba_gated_delta_step_batched  its T=1 step on a [n_layers][B][Hv][dv][dk] state
   mamba_qk_norm_rotary          per-head norms of queries and keys with the position rotation
   mamba_head_norm_gated         per-head RMSNorm of a layer's output with its SiLU(z) gate
-  mamba_layer_prefill / _step   the whole Mamba-1 block (norm, projections, mixer, residual)
+  mamba_layer_prefill / _step   the whole Mamba-1 block (norm, projections, mixer, residual), its
+                                projections in bf16 or 4 bits (mamba_layer_w4_*; weights from `w4`)
   mamba_layer_decode_graph_create  one decode token through n_layers blocks as one CUDA graph
   mamba_selective_scan_prefill_noalloc  the scan prefill with a static scratch
   mamba_selective_scan_workspace_bytes  scratch size of the prefill's balanced routes
@@ -82,5 +83,15 @@ from ._binding import (  # noqa: F401
     mamba_ssm_step_batched,
     mamba_version,
 )
+
+
+def __getattr__(name):
+    """The 4-bit weights' helpers (module w4), which need torch when they are asked for."""
+    if name in ("W4", "dequantize_w4", "pack_w4", "quantize_w4", "unpack_w4"):
+        from . import w4
+
+        return getattr(w4, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __version__ = "0.1.0"

@@ -57,6 +57,9 @@ ABI_SYMBOLS = (
     "mamba_layer_prefill",
     "mamba_layer_step",
     "mamba_layer_decode_graph_create",
+    "mamba_layer_w4_prefill",
+    "mamba_layer_w4_step",
+    "mamba_layer_w4_decode_graph_create",
     "mamba_decode_graph_create",
     "mamba_decode_graph_launch",
     "mamba_decode_graph_kernels",
@@ -85,6 +88,19 @@ class _MambaLayer(ctypes.Structure):
                 ("conv_b", ctypes.c_void_p), ("x_proj_w", ctypes.c_void_p), ("dt_proj_w", ctypes.c_void_p),
                 ("dt_proj_b", ctypes.c_void_p), ("A_log", ctypes.c_void_p), ("D", ctypes.c_void_p),
                 ("out_proj_w", ctypes.c_void_p)]
+
+
+class _MambaW4(ctypes.Structure):
+    """struct MambaW4 of the C ABI (a projection in 4 bits; q NULL: none)."""
+    _fields_ = [("q", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("scales", ctypes.c_void_p), ("ld_s", ctypes.c_int64),
+                ("scale_dtype", ctypes.c_int), ("zeros", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
+                ("group", ctypes.c_int64)]
+
+
+class _MambaLayerW4(ctypes.Structure):
+    """struct MambaLayerW4 of the C ABI."""
+    _fields_ = [("layer", _MambaLayer), ("in_proj", _MambaW4), ("x_proj", _MambaW4), ("dt_proj", _MambaW4),
+                ("out_proj", _MambaW4)]
 
 
 def load(path: str | None = None):
@@ -163,6 +179,13 @@ def load(path: str | None = None):
         lib.mamba_layer_step.restype = ctypes.c_int
         lib.mamba_layer_decode_graph_create.argtypes = [ctypes.POINTER(vp), lp, i64, vp, vp, vp, i64, vp, i64]
         lib.mamba_layer_decode_graph_create.restype = ctypes.c_int
+        wp = ctypes.POINTER(_MambaLayerW4)
+        lib.mamba_layer_w4_prefill.argtypes = [vp, wp, vp, vp, vp, vp, i64, i64, vp, i64, vp]
+        lib.mamba_layer_w4_prefill.restype = ctypes.c_int
+        lib.mamba_layer_w4_step.argtypes = [vp, wp, vp, vp, i64, i64, i64, vp, i64, vp]
+        lib.mamba_layer_w4_step.restype = ctypes.c_int
+        lib.mamba_layer_w4_decode_graph_create.argtypes = [ctypes.POINTER(vp), wp, i64, vp, vp, vp, i64, vp, i64]
+        lib.mamba_layer_w4_decode_graph_create.restype = ctypes.c_int
         lib.mamba_decode_graph_create.argtypes = [ctypes.POINTER(vp), vp, vp, i64, i64, i32, i32, vp, vp,
                                                   i64, i64, i64, i64]
         lib.mamba_decode_graph_create.restype = ctypes.c_int
@@ -859,7 +882,7 @@ def _rows_of(t, name, shape, dtype):
     """Pointer and row stride of a [rows, cols] tensor of `shape` and dtype (None:
     float32 or bfloat16), columns dense."""
     if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous():
@@ -895,6 +918,8 @@ def mamba_linear_w4(c, a, q, scales, zeros=None, residual=None, *, group=128, st
 
 def _token_rows(t, name, shape, dtype):
     """Pointer and row stride of a [B, T, D] or [M, D] tensor."""
+    if t.is_contiguous() and t.shape == shape and (dtype is None or t.dtype is dtype):
+        return t.data_ptr(), shape[-1]
     if len(shape) == 2:
         return _rows_of(t, name, shape, dtype)
     return t.data_ptr(), _heads_ld(t, name, shape, 2, shape[2], t.dtype if dtype is None else dtype)
@@ -910,9 +935,9 @@ def mamba_block_norm(x_out, out, x, y, pre_weight=None, post_weight=None, gate=N
     f32; gate: f32 or bf16 [D], [B, D] (one per sequence) or of x's shape, or None."""
     import torch
 
-    s = tuple(x.shape)
+    s, f32 = x.shape, torch.float32
     if len(s) not in (2, 3):
-        raise ValueError(f"x must be [B, T, D] or [M, D], got {s}")
+        raise ValueError(f"x must be [B, T, D] or [M, D], got {tuple(s)}")
     D = s[-1]
     M = s[0] if len(s) == 2 else s[0] * s[1]
     po, ld_o, code_o = None, 0, 0
@@ -920,16 +945,20 @@ def mamba_block_norm(x_out, out, x, y, pre_weight=None, post_weight=None, gate=N
         (po, ld_o), code_o = _token_rows(out, "out", s, None), _dtype_code(out)
     pg, ld_g, code_g, g_rows = None, 0, 0, 0
     if gate is not None:
-        code_g = _dtype_code(gate)
-        if gate.dim() == 1:
-            pg, ld_g = _rows_of(gate.unsqueeze(0), "gate", (1, D), None)
-        elif gate.dim() == len(s):
+        code_g, n = _dtype_code(gate), gate.dim()
+        if n == 1:
+            if gate.shape[0] != D or not gate.is_contiguous():
+                raise ValueError(f"gate must be dense, of {D}, or have a row per sequence or token")
+            pg, ld_g = gate.data_ptr(), D
+        elif n == len(s):
             (pg, ld_g), g_rows = _token_rows(gate, "gate", s, None), 1
         else:
             (pg, ld_g), g_rows = _rows_of(gate, "gate", (s[0], D), None), s[1]
+    px, ld_x = _token_rows(x, "x", s, f32)
+    py, ld_y = _token_rows(y, "y", s, None)
+    pxo, ld_xo = _token_rows(x_out, "x_out", s, f32)
     _check(load().mamba_block_norm(
-        *_token_rows(x_out, "x_out", s, torch.float32), po, ld_o, code_o, *_token_rows(x, "x", s, torch.float32),
-        *_token_rows(y, "y", s, None), _dtype_code(y), _f32_dense(pre_weight, "pre_weight", (D,)),
+        pxo, ld_xo, po, ld_o, code_o, px, ld_x, py, ld_y, _dtype_code(y), _f32_dense(pre_weight, "pre_weight", (D,)),
         _f32_dense(post_weight, "post_weight", (D,)), pg, ld_g, code_g, g_rows, scale, eps, M, D,
         _current_stream(stream, x)))
 
@@ -969,14 +998,43 @@ LAYER_WEIGHTS = ("norm_w", "in_proj_w", "conv_w", "conv_b", "x_proj_w", "dt_proj
                  "out_proj_w")
 
 
+def _w4_struct(t, name, shape):
+    """(struct MambaW4, the shape) of a 4-bit weight, checked against [out, in] = shape."""
+    import torch
+
+    n, k = shape
+    sg = (n, -(-k // t.group) if t.group > 0 else 0)
+    pq, ld_q = _rows_of(t.q, f"{name}.q", (n, (k + 31) // 32 * 16), torch.uint8)
+    ps, ld_s = _rows_of(t.scales, f"{name}.scales", sg, None)
+    pz, ld_z = (None, 0) if t.zeros is None else _rows_of(t.zeros, f"{name}.zeros", sg, torch.uint8)
+    return _MambaW4(pq, ld_q, ps, ld_s, _dtype_code(t.scales), pz, ld_z, t.group)
+
+
+def _layer_dims(s):
+    return s.layer if isinstance(s, _MambaLayerW4) else s
+
+
+def _layer_structs(weights, eps):
+    """The structs of some layers as one C array, of the form with 4-bit projections if any
+    layer has them: (array, whether it is that form)."""
+    structs = [layer_struct(w, eps) for w in weights]
+    if not any(isinstance(s, _MambaLayerW4) for s in structs):
+        return (_MambaLayer * len(structs))(*structs), False
+    return (_MambaLayerW4 * len(structs))(
+        *[s if isinstance(s, _MambaLayerW4) else _MambaLayerW4(s) for s in structs]), True
+
+
 def layer_struct(w, eps=1e-5):
     """The C struct MambaLayer for a dict of block weights: norm_w [dm],
     in_proj_w [2 Di, dm] bf16, conv_w [Di, K], conv_b [Di] or None, x_proj_w
     [R + 2N, Di] bf16, dt_proj_w [Di, R] bf16, dt_bias (dt_proj's bias) [Di] or
-    None, A_log [Di, N], D [Di] or None, out_proj_w [dm, Di] bf16.  Shapes and
+    None, A_log [Di, N], D [Di] or None, out_proj_w [dm, Di] bf16.  Each of the four
+    projections may be a W4 instead (the struct is then MambaLayerW4).  Shapes and
     dtypes are checked here; the tensors must outlive every call that uses
     the struct."""
     import torch
+
+    from .w4 import W4
 
     for k in ("norm_w", "in_proj_w", "conv_w", "x_proj_w", "dt_proj_w", "A_log", "out_proj_w"):
         if w.get(k) is None:
@@ -984,25 +1042,32 @@ def layer_struct(w, eps=1e-5):
     Di, K = w["conv_w"].shape
     N = w["A_log"].shape[1]
     dm = w["norm_w"].shape[0]
-    R = w["dt_proj_w"].shape[1]
+    # dt_rank: a 4-bit dt_proj's rows are padded, x_proj has dt_rank + 2 N rows
+    t, x = w["dt_proj_w"], w["x_proj_w"]
+    R = (x.q if isinstance(x, W4) else x).shape[0] - 2 * N if isinstance(t, W4) else t.shape[1]
+    w4 = {}
     for k, shp in (("in_proj_w", (2 * Di, dm)), ("x_proj_w", (R + 2 * N, Di)), ("dt_proj_w", (Di, R)),
                    ("out_proj_w", (dm, Di))):
         t = w[k]
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != shp or not t.is_contiguous():
+        if isinstance(t, W4):
+            w4[k[:-2]] = _w4_struct(t, k, shp)
+        elif t.dtype != torch.bfloat16 or tuple(t.shape) != shp or not t.is_contiguous():
             raise ValueError(f"{k} must be a contiguous bfloat16 {shp} tensor")
     _f32_param(w["norm_w"], "norm_w", (dm,))
     _f32_param(w["conv_w"], "conv_w", (Di, K))
     _f32_param(w["A_log"], "A_log", (Di, N))
     for k in ("conv_b", "dt_bias", "D"):
         _f32_param(w.get(k), k, (Di,))
-    return _MambaLayer(dm, Di, N, K, R, float(eps), _ptr(w["norm_w"]), _ptr(w["in_proj_w"]), _ptr(w["conv_w"]),
-                       _ptr(w.get("conv_b")), _ptr(w["x_proj_w"]), _ptr(w["dt_proj_w"]), _ptr(w.get("dt_bias")),
-                       _ptr(w["A_log"]), _ptr(w.get("D")), _ptr(w["out_proj_w"]))
+    p = lambda k: None if isinstance(w[k], W4) else _ptr(w[k])  # noqa: E731
+    s = _MambaLayer(dm, Di, N, K, R, float(eps), _ptr(w["norm_w"]), p("in_proj_w"), _ptr(w["conv_w"]),
+                    _ptr(w.get("conv_b")), p("x_proj_w"), p("dt_proj_w"), _ptr(w.get("dt_bias")),
+                    _ptr(w["A_log"]), _ptr(w.get("D")), p("out_proj_w"))
+    return _MambaLayerW4(layer=s, **w4) if w4 else s
 
 
 def mamba_layer_workspace_bytes(w, Bsz, T, eps=1e-5) -> int:
     """Workspace bytes of a block over Bsz x T tokens (activations + the scan's share)."""
-    v = load().mamba_layer_workspace_bytes(ctypes.byref(layer_struct(w, eps)), Bsz, T)
+    v = load().mamba_layer_workspace_bytes(ctypes.byref(_layer_dims(layer_struct(w, eps))), Bsz, T)
     if v < 0:
         raise MambaError(int(v), mamba_last_error())
     return int(v)
@@ -1025,7 +1090,8 @@ def mamba_layer_prefill(hidden, w, conv_state_in=None, conv_state_out=None, ssm_
     if hidden.dtype != torch.float32 or hidden.dim() != 3 or not hidden.is_contiguous():
         raise ValueError("hidden must be a contiguous float32 [B, T, d_model] tensor")
     Bsz, T, dm = hidden.shape
-    S = layer_struct(w, eps)
+    layer = layer_struct(w, eps)
+    S = _layer_dims(layer)
     if dm != S.d_model:
         raise ValueError(f"hidden has d_model {dm}, the weights {S.d_model}")
     for t, nm, last in ((conv_state_in, "conv_state_in", S.d_conv), (conv_state_out, "conv_state_out", S.d_conv),
@@ -1033,8 +1099,9 @@ def mamba_layer_prefill(hidden, w, conv_state_in=None, conv_state_out=None, ssm_
         _f32_param(t, nm, (Bsz, S.d_inner, last))
     st = _stream(stream, hidden)
     with _layer_scratch(workspace, w, Bsz, T, eps, hidden.device, st) as ws:
-        _check(load().mamba_layer_prefill(_ptr(hidden), ctypes.byref(S), _ptr(conv_state_in), _ptr(conv_state_out),
-                                          _ptr(ssm_state_in), _ptr(ssm_state_out), Bsz, T, *_ptr_bytes(ws), st))
+        call = load().mamba_layer_prefill if layer is S else load().mamba_layer_w4_prefill
+        _check(call(_ptr(hidden), ctypes.byref(layer), _ptr(conv_state_in), _ptr(conv_state_out), _ptr(ssm_state_in),
+                    _ptr(ssm_state_out), Bsz, T, *_ptr_bytes(ws), st))
 
 
 def mamba_layer_step(hidden, w, conv_state, ssm_state, layer, *, eps=1e-5, workspace=None, stream=None):
@@ -1045,7 +1112,8 @@ def mamba_layer_step(hidden, w, conv_state, ssm_state, layer, *, eps=1e-5, works
     if hidden.dtype != torch.float32 or hidden.dim() != 2 or not hidden.is_contiguous():
         raise ValueError("hidden must be a contiguous float32 [B, d_model] tensor")
     Bsz, dm = hidden.shape
-    S = layer_struct(w, eps)
+    layer_s = layer_struct(w, eps)
+    S = _layer_dims(layer_s)
     if dm != S.d_model:
         raise ValueError(f"hidden has d_model {dm}, the weights {S.d_model}")
     for t, nm, last in ((conv_state, "conv_state", S.d_conv), (ssm_state, "ssm_state", S.d_state)):
@@ -1056,8 +1124,9 @@ def mamba_layer_step(hidden, w, conv_state, ssm_state, layer, *, eps=1e-5, works
         raise ValueError("conv_state and ssm_state must have the same number of layers")
     st = _stream(stream, hidden)
     with _layer_scratch(workspace, w, Bsz, 1, eps, hidden.device, st) as ws:
-        _check(load().mamba_layer_step(_ptr(hidden), ctypes.byref(S), _ptr(conv_state), _ptr(ssm_state), int(layer),
-                                       conv_state.shape[0], Bsz, *_ptr_bytes(ws), st))
+        call = load().mamba_layer_step if layer_s is S else load().mamba_layer_w4_step
+        _check(call(_ptr(hidden), ctypes.byref(layer_s), _ptr(conv_state), _ptr(ssm_state), int(layer),
+                    conv_state.shape[0], Bsz, *_ptr_bytes(ws), st))
 
 
 def mamba_selective_scan_prefill_noalloc(y, u, dt, Bm, Cm, A_log, D=None, dt_bias=None, z=None,
@@ -1126,8 +1195,8 @@ class LayerDecodeGraph:
         if hidden.dtype != torch.float32 or hidden.dim() != 2 or not hidden.is_contiguous():
             raise ValueError("hidden must be a contiguous float32 [B, d_model] tensor")
         Bsz, dm = hidden.shape
-        structs = (_MambaLayer * L)(*[layer_struct(w, eps) for w in weights])
-        S0 = structs[0]
+        structs, w4 = _layer_structs(weights, eps)
+        S0 = _layer_dims(structs[0])
         if dm != S0.d_model:
             raise ValueError(f"hidden has d_model {dm}, the weights {S0.d_model}")
         for t, nm, last in ((conv_state, "conv_state", S0.d_conv), (ssm_state, "ssm_state", S0.d_state)):
@@ -1142,9 +1211,9 @@ class LayerDecodeGraph:
             workspace = torch.empty(max(int(v), 16), dtype=torch.uint8, device=hidden.device)
         self._ws = workspace
         h = ctypes.c_void_p()
-        _check(lib.mamba_layer_decode_graph_create(ctypes.byref(h), structs, L, _ptr(hidden), _ptr(conv_state),
-                                                   _ptr(ssm_state), Bsz, _ptr(workspace),
-                                                   workspace.numel() * workspace.element_size()))
+        create = lib.mamba_layer_w4_decode_graph_create if w4 else lib.mamba_layer_decode_graph_create
+        _check(create(ctypes.byref(h), structs, L, _ptr(hidden), _ptr(conv_state), _ptr(ssm_state), Bsz,
+                      _ptr(workspace), workspace.numel() * workspace.element_size()))
         self._h = h
         self._device = hidden.device
         self.n_layers = L

@@ -324,13 +324,33 @@ int layer_plan(const MambaLayer* L, int64_t B, int64_t T, LayerPlan* p) {
   return MAMBA_OK;
 }
 
+// what mamba_linear_w4 asks of a weight of N x K, before anything of the block is launched
+int check_w4(const char* name, const MambaW4& w, int64_t N, int64_t K) {
+  if (w.group != 32 && w.group != 64 && w.group != 128)
+    return fail(MAMBA_ERR_UNSUPPORTED, "%s: group=%lld not in {32, 64, 128}", name, (long long)w.group);
+  if (w.scale_dtype != MAMBA_F32 && w.scale_dtype != MAMBA_BF16)
+    return fail(MAMBA_ERR_INVALID_ARG, "%s: unknown scale_dtype %d", name, w.scale_dtype);
+  if (!w.scales) return fail(MAMBA_ERR_INVALID_ARG, "%s: scales must not be NULL", name);
+  const int64_t groups = (K + w.group - 1) / w.group;
+  View views[] = {{"q", w.q, N, (K + 31) / 32 * 16, w.ld_q, 1, 0},
+                  {"scales", w.scales, N, groups, w.ld_s, es_of(w.scale_dtype), 0},
+                  {"zeros", w.zeros, N, groups, w.ld_z, 1, 0}};
+  for (View& v : views) {
+    const int rc = view_of(&v);
+    if (rc) return rc;
+  }
+  if (reinterpret_cast<uintptr_t>(w.q) % 16 || (N > 1 && w.ld_q % 16))
+    return fail(MAMBA_ERR_INVALID_ARG, "%s: q must be 16-byte aligned and ld_q a multiple of 16", name);
+  return MAMBA_OK;
+}
+
 // the block over B x T tokens.  A prefill gives the scan the workspace past
 // the activations; a step (T = 1, states updated in place on their slab) runs
 // the conv and SSM step kernels on the same strided views instead of the
 // prefill kernels -- the same arithmetic, bit for bit
 int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* conv_out, const float* ssm_in,
               float* ssm_out, int64_t B, int64_t T, void* workspace, int64_t workspace_bytes, bool step,
-              void* stream) {
+              void* stream, const MambaLayerW4* W = nullptr) {
   int rc;
   LayerPlan p;
   if ((rc = layer_plan(L, B, T, &p))) return rc;
@@ -345,22 +365,47 @@ int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* c
                                         Di, N, nullptr, 0, stream);
   }
   if (!hidden || !workspace) return fail(MAMBA_ERR_INVALID_ARG, "hidden and workspace must not be NULL");
-  if (!L->norm_w || !L->in_proj_w || !L->conv_w || !L->x_proj_w || !L->dt_proj_w || !L->A_log || !L->out_proj_w)
-    return fail(MAMBA_ERR_INVALID_ARG, "a required weight of the layer is NULL");
+  // the projections: out x in features, in 4 bits where W has them so
+  const int64_t xdim = R + 2 * N;
+  struct Proj {
+    const char* name;
+    const void* w;
+    MambaW4 w4;
+    int64_t out, in;
+  } proj[4] = {{"in_proj_w", L->in_proj_w, {}, 2 * Di, dm},
+               {"x_proj_w", L->x_proj_w, {}, xdim, Di},
+               {"dt_proj_w", L->dt_proj_w, {}, Di, R},
+               {"out_proj_w", L->out_proj_w, {}, dm, Di}};
+  if (W) proj[0].w4 = W->in_proj, proj[1].w4 = W->x_proj, proj[2].w4 = W->dt_proj, proj[3].w4 = W->out_proj;
+  if (!L->norm_w || !L->conv_w || !L->A_log) return fail(MAMBA_ERR_INVALID_ARG, "a required weight of the layer is NULL");
+  for (Proj& q : proj) {
+    if (!q.w4.q && !q.w) return fail(MAMBA_ERR_INVALID_ARG, "a required weight of the layer is NULL");
+    if (q.w4.q && (rc = check_w4(q.name, q.w4, q.out, q.in))) return rc;
+  }
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(MAMBA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (workspace_bytes < p.act_bytes)
     return fail(MAMBA_ERR_INVALID_ARG, "workspace_bytes=%lld below the %lld bytes of the block's activations",
                 (long long)workspace_bytes, (long long)p.act_bytes);
-  for (const void* w : {L->in_proj_w, L->x_proj_w, L->dt_proj_w, L->out_proj_w})
-    if (reinterpret_cast<uintptr_t>(w) & 15) return fail(MAMBA_ERR_INVALID_ARG, "the bf16 weights must be 16-byte aligned");
-  // every range the sequence touches, checked together before the first launch
-  const int64_t xdim = R + 2 * N;
-  Range ins[] = {range_of("norm_w", L->norm_w, dm * 4), range_of("in_proj_w", L->in_proj_w, 2 * Di * dm * 2),
-                 range_of("conv_w", L->conv_w, Di * K * 4), range_of("conv_b", L->conv_b, Di * 4),
-                 range_of("x_proj_w", L->x_proj_w, xdim * Di * 2), range_of("dt_proj_w", L->dt_proj_w, Di * R * 2),
-                 range_of("dt_proj_b", L->dt_proj_b, Di * 4), range_of("A_log", L->A_log, Di * N * 4),
-                 range_of("D", L->D, Di * 4), range_of("out_proj_w", L->out_proj_w, dm * Di * 2),
-                 range_of("conv_state_in", conv_in, B * Di * K * 4), range_of("ssm_state_in", ssm_in, B * Di * N * 4)};
+  for (const Proj& q : proj)
+    if (!q.w4.q && (reinterpret_cast<uintptr_t>(q.w) & 15))
+      return fail(MAMBA_ERR_INVALID_ARG, "the bf16 weights must be 16-byte aligned");
+  // every range the sequence touches, checked together before the first launch; the
+  // states first: they may be updated in place
+  Range ins[20] = {range_of("conv_state_in", conv_in, B * Di * K * 4), range_of("ssm_state_in", ssm_in, B * Di * N * 4),
+                   range_of("norm_w", L->norm_w, dm * 4), range_of("conv_w", L->conv_w, Di * K * 4),
+                   range_of("conv_b", L->conv_b, Di * 4), range_of("dt_proj_b", L->dt_proj_b, Di * 4),
+                   range_of("A_log", L->A_log, Di * N * 4), range_of("D", L->D, Di * 4)};
+  int n_ins = 8;
+  for (const Proj& q : proj) {
+    if (!q.w4.q) {
+      ins[n_ins++] = range_of(q.name, q.w, q.out * q.in * 2);
+      continue;
+    }
+    const int64_t groups = (q.in + q.w4.group - 1) / q.w4.group;
+    ins[n_ins++] = range_of(q.name, q.w4.q, (q.out - 1) * q.w4.ld_q + (q.in + 31) / 32 * 16);
+    ins[n_ins++] = range_of("scales", q.w4.scales, ((q.out - 1) * q.w4.ld_s + groups) * es_of(q.w4.scale_dtype));
+    ins[n_ins++] = range_of("zeros", q.w4.zeros, (q.out - 1) * q.w4.ld_z + groups);
+  }
   Range outs[] = {range_of("hidden", hidden, p.rows * dm * 4), range_of("workspace", workspace, workspace_bytes),
                   range_of("conv_state_out", conv_out, B * Di * K * 4),
                   range_of("ssm_state_out", ssm_out, B * Di * N * 4)};
@@ -368,15 +413,11 @@ int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* c
   if ((rc = current_device(&dev))) return rc;
   int dev_id = 0;
   cudaGetDevice(&dev_id);
-  if ((rc = check_pointers(ins, 12, dev_id)) || (rc = check_pointers(outs, 4, dev_id))) return rc;
-  // a state may be updated in place: then its input range is its output range
-  Range ins_x[12];
-  int n_in = 0;
-  for (int i = 0; i < 12; ++i) {
-    if ((i == 10 && conv_in && conv_in == conv_out) || (i == 11 && ssm_in && ssm_in == ssm_out)) continue;
-    ins_x[n_in++] = ins[i];
-  }
-  if ((rc = check_overlaps(outs, 4, ins_x, n_in))) return rc;
+  if ((rc = check_pointers(ins, n_ins, dev_id)) || (rc = check_pointers(outs, 4, dev_id))) return rc;
+  // a state updated in place: its input range is its output range
+  if (conv_in && conv_in == conv_out) ins[0] = range_of("", nullptr, 0);
+  if (ssm_in && ssm_in == ssm_out) ins[1] = range_of("", nullptr, 0);
+  if ((rc = check_overlaps(outs, 4, ins, n_ins))) return rc;
 
   char* ws = static_cast<char*>(workspace);
   auto* h = ws + p.off_h;
@@ -388,10 +429,16 @@ int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* c
   void* scan_ws = !step && workspace_bytes > p.act_bytes ? ws + p.act_bytes : nullptr;
   const int64_t scan_bytes = scan_ws ? workspace_bytes - p.act_bytes : 0;
   const int64_t rows = p.rows, ldx = p.ldx;
+  auto project = [&](const Proj& q, void* c, int64_t ld_c, int c_dtype, const void* a, int64_t ld_a,
+                     const float* r) -> int {
+    if (q.w4.q)
+      return mamba_linear_w4(c, ld_c, c_dtype, a, ld_a, q.w4.q, q.w4.ld_q, q.w4.scales, q.w4.ld_s, q.w4.scale_dtype,
+                             q.w4.zeros, q.w4.ld_z, q.w4.group, r, r ? ld_c : 0, rows, q.out, q.in, stream);
+    return mamba_linear_bf16(c, ld_c, c_dtype, a, ld_a, q.w, q.in, r, r ? ld_c : 0, rows, q.out, q.in, stream);
+  };
   // F1 RMSNorm (f32 residual in, bf16 out); F2 in_proj
   if ((rc = mamba_rmsnorm(h, dm, MAMBA_BF16, hidden, dm, L->norm_w, L->eps, rows, dm, stream))) return rc;
-  if ((rc = mamba_linear_bf16(xz, 2 * Di, MAMBA_BF16, h, dm, L->in_proj_w, dm, nullptr, 0, rows, 2 * Di, dm, stream)))
-    return rc;
+  if ((rc = project(proj[0], xz, 2 * Di, MAMBA_BF16, h, dm, nullptr))) return rc;
   // F3-F4: the conv reads the x half of xz in place (row stride 2 d_inner)
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (step) {
@@ -404,10 +451,8 @@ int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* c
     return rc;
   }
   // F5 x_proj -> [dt_rank | B | C]; F6 dt_proj on the first dt_rank columns
-  if ((rc = mamba_linear_bf16(xd, ldx, MAMBA_BF16, u, Di, L->x_proj_w, Di, nullptr, 0, rows, xdim, Di, stream)))
-    return rc;
-  if ((rc = mamba_linear_bf16(dt, Di, MAMBA_BF16, xd, ldx, L->dt_proj_w, R, nullptr, 0, rows, Di, R, stream)))
-    return rc;
+  if ((rc = project(proj[1], xd, ldx, MAMBA_BF16, u, Di, nullptr))) return rc;
+  if ((rc = project(proj[2], dt, Di, MAMBA_BF16, xd, ldx, nullptr))) return rc;
   // F7-F10: softplus(dt + dt_proj_b), the scan and the SiLU(z) gate in one call
   char* xz_z = xz + Di * 2;
   char* xd_b = xd + R * 2;
@@ -427,7 +472,7 @@ int run_layer(float* hidden, const MambaLayer* L, const float* conv_in, float* c
     return rc;
   }
   // F11-F12: out_proj with the residual added in its epilogue, in place
-  return mamba_linear_bf16(hidden, dm, MAMBA_F32, y, Di, L->out_proj_w, Di, hidden, dm, rows, dm, Di, stream);
+  return project(proj[3], hidden, dm, MAMBA_F32, y, Di, hidden);
 }
 
 }  // namespace
@@ -887,6 +932,8 @@ int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t
   return ok();
 }
 
+static constexpr int64_t kMaxW4 = int64_t(1) << 30;  // the kernels' indexes of rows and k are ints
+
 int mamba_linear_w4(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t ld_a, const uint8_t* q, int64_t ld_q,
                     const void* scales, int64_t ld_s, int scale_dtype, const uint8_t* zeros, int64_t ld_z,
                     int64_t group, const float* residual, int64_t ld_r, int64_t M, int64_t N, int64_t K,
@@ -896,7 +943,7 @@ int mamba_linear_w4(void* c, int64_t ld_c, int c_dtype, const void* a, int64_t l
   if (M < 0 || N < 0 || K < 1) return fail(MAMBA_ERR_INVALID_ARG, "sizes (M=%lld N=%lld K=%lld)", (long long)M, (long long)N, (long long)K);
   if (group != 32 && group != 64 && group != 128)
     return fail(MAMBA_ERR_UNSUPPORTED, "group=%lld not in {32, 64, 128}", (long long)group);
-  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || !sizes_ok(M, K) || !sizes_ok(N, K) || !sizes_ok(M, N))
+  if (M > kMaxW4 || N > kMaxW4 || K > kMaxW4 || !sizes_ok(M, K) || !sizes_ok(N, K) || !sizes_ok(M, N))
     return fail(MAMBA_ERR_INVALID_ARG, "extent overflow");
   if (M == 0 || N == 0) return ok();
   if (!c || !a || !q || !scales) return fail(MAMBA_ERR_INVALID_ARG, "c, a, q and scales must not be NULL");
@@ -1286,9 +1333,9 @@ int mamba_layer_prefill(float* hidden, const MambaLayer* layer, const float* con
                    workspace_bytes, false, stream);
 }
 
-int mamba_layer_step(float* hidden, const MambaLayer* layer, float* conv_state, float* ssm_state,
-                     int64_t layer_index, int64_t n_layers, int64_t B, void* workspace, int64_t workspace_bytes,
-                     void* stream) {
+static int layer_step(float* hidden, const MambaLayer* layer, float* conv_state, float* ssm_state,
+                      int64_t layer_index, int64_t n_layers, int64_t B, void* workspace, int64_t workspace_bytes,
+                      void* stream, const MambaLayerW4* w4) {
   if (workspace_bytes < 0) return fail(MAMBA_ERR_INVALID_ARG, "negative workspace_bytes");
   if (!layer) return fail(MAMBA_ERR_INVALID_ARG, "layer is NULL");
   if (n_layers < 1 || layer_index < 0 || layer_index >= n_layers)
@@ -1302,7 +1349,31 @@ int mamba_layer_step(float* hidden, const MambaLayer* layer, float* conv_state, 
     return fail(MAMBA_ERR_INVALID_ARG, "extent overflow or invalid dims");
   float* cslab = conv_state + layer_index * B * Di * K;
   float* sslab = ssm_state + layer_index * B * Di * N;
-  return run_layer(hidden, layer, cslab, cslab, sslab, sslab, B, 1, workspace, workspace_bytes, true, stream);
+  return run_layer(hidden, layer, cslab, cslab, sslab, sslab, B, 1, workspace, workspace_bytes, true, stream, w4);
+}
+
+int mamba_layer_step(float* hidden, const MambaLayer* layer, float* conv_state, float* ssm_state,
+                     int64_t layer_index, int64_t n_layers, int64_t B, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  return layer_step(hidden, layer, conv_state, ssm_state, layer_index, n_layers, B, workspace, workspace_bytes, stream,
+                    nullptr);
+}
+
+int mamba_layer_w4_prefill(float* hidden, const MambaLayerW4* layer, const float* conv_state_in,
+                           float* conv_state_out, const float* ssm_state_in, float* ssm_state_out, int64_t B,
+                           int64_t T, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (workspace_bytes < 0) return fail(MAMBA_ERR_INVALID_ARG, "negative workspace_bytes");
+  if (!layer) return fail(MAMBA_ERR_INVALID_ARG, "layer is NULL");
+  return run_layer(hidden, &layer->layer, conv_state_in, conv_state_out, ssm_state_in, ssm_state_out, B, T, workspace,
+                   workspace_bytes, false, stream, layer);
+}
+
+int mamba_layer_w4_step(float* hidden, const MambaLayerW4* layer, float* conv_state, float* ssm_state,
+                        int64_t layer_index, int64_t n_layers, int64_t B, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  if (!layer) return fail(MAMBA_ERR_INVALID_ARG, "layer is NULL");
+  return layer_step(hidden, &layer->layer, conv_state, ssm_state, layer_index, n_layers, B, workspace, workspace_bytes,
+                    stream, layer);
 }
 
 }  // extern "C"

@@ -184,23 +184,36 @@ extern "C" int mamba3_decode_graph_create(MambaDecodeGraph** out, const Mamba3To
 }
 
 // The whole-block form: one token through n_layers Mamba-1 blocks, each the
-// public mamba_layer_step call on slab l of the states, recorded once.
-extern "C" int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const MambaLayer* layers, int64_t n_layers,
-                                               float* hidden, float* conv_state, float* ssm_state, int64_t B,
-                                               void* workspace, int64_t workspace_bytes) {
-  if (!out) return mamba::set_last_error(MAMBA_ERR_INVALID_ARG, "mamba_layer_decode_graph_create: out is NULL");
+// public mamba_layer_step (or mamba_layer_w4_step) call on slab l of the states,
+// recorded once.
+namespace {
+
+const MambaLayer& dims_of(const MambaLayer& l) { return l; }
+const MambaLayer& dims_of(const MambaLayerW4& l) { return l.layer; }
+
+int graph_error(int code, const char* name, const char* what) {
+  char text[256];
+  snprintf(text, sizeof(text), "%s: %s", name, what);
+  return mamba::set_last_error(code, text);
+}
+
+template <typename Layer, typename Step>
+int create_layer_graph(const char* name, Step step, MambaDecodeGraph** out, const Layer* layers, int64_t n_layers,
+                       float* hidden, float* conv_state, float* ssm_state, int64_t B, void* workspace,
+                       int64_t workspace_bytes) {
+  if (!out) return graph_error(MAMBA_ERR_INVALID_ARG, name, "out is NULL");
   *out = nullptr;
-  if (!layers) return mamba::set_last_error(MAMBA_ERR_INVALID_ARG, "mamba_layer_decode_graph_create: layers is NULL");
+  if (!layers) return graph_error(MAMBA_ERR_INVALID_ARG, name, "layers is NULL");
   if (n_layers < 1 || n_layers > (int64_t(1) << 16))
-    return mamba::set_last_error(MAMBA_ERR_INVALID_ARG, "mamba_layer_decode_graph_create: n_layers not in 1..2^16");
+    return graph_error(MAMBA_ERR_INVALID_ARG, name, "n_layers not in 1..2^16");
   for (int64_t l = 1; l < n_layers; ++l) {
-    const MambaLayer& a = layers[0];
-    const MambaLayer& b = layers[l];
+    const MambaLayer& a = dims_of(layers[0]);
+    const MambaLayer& b = dims_of(layers[l]);
     if (a.d_model != b.d_model || a.d_inner != b.d_inner || a.d_state != b.d_state || a.d_conv != b.d_conv ||
         a.dt_rank != b.dt_rank)
-      return mamba::set_last_error(MAMBA_ERR_INVALID_ARG,
-                                   "mamba_layer_decode_graph_create: every layer must have the dims of layer 0 "
-                                   "(the states are one [n_layers][B][d_inner][.] slab array)");
+      return graph_error(MAMBA_ERR_INVALID_ARG, name,
+                         "every layer must have the dims of layer 0 (the states are one [n_layers][B][d_inner][.] "
+                         "slab array)");
   }
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -215,10 +228,10 @@ extern "C" int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const Mam
   int rc = MAMBA_OK;
   std::string msg;
   for (int64_t l = 0; l < n_layers; ++l) {
-    rc = mamba_layer_step(hidden, &layers[l], conv_state, ssm_state, l, n_layers, B, workspace, workspace_bytes, s);
+    rc = step(hidden, &layers[l], conv_state, ssm_state, l, n_layers, B, workspace, workspace_bytes, s);
     if (rc != MAMBA_OK) {
       char head[80];
-      snprintf(head, sizeof(head), "mamba_layer_decode_graph_create: layer %lld: ", (long long)l);
+      snprintf(head, sizeof(head), "%s: layer %lld: ", name, (long long)l);
       msg = std::string(head) + mamba_last_error();
       break;
     }
@@ -245,7 +258,7 @@ extern "C" int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const Mam
   if (!g) {
     cudaGraphExecDestroy(exec);
     cudaGraphDestroy(graph);
-    return mamba::set_last_error(MAMBA_ERR_CUDA, "mamba_layer_decode_graph_create: out of host memory");
+    return graph_error(MAMBA_ERR_CUDA, name, "out of host memory");
   }
   g->graph = graph;
   g->exec = exec;
@@ -253,6 +266,23 @@ extern "C" int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const Mam
   g->kernels = (int64_t)nodes;
   *out = g;
   return mamba::set_last_error(MAMBA_OK, "");
+}
+
+}  // namespace
+
+extern "C" int mamba_layer_decode_graph_create(MambaDecodeGraph** out, const MambaLayer* layers, int64_t n_layers,
+                                               float* hidden, float* conv_state, float* ssm_state, int64_t B,
+                                               void* workspace, int64_t workspace_bytes) {
+  return create_layer_graph("mamba_layer_decode_graph_create", mamba_layer_step, out, layers, n_layers, hidden,
+                            conv_state, ssm_state, B, workspace, workspace_bytes);
+}
+
+extern "C" int mamba_layer_w4_decode_graph_create(MambaDecodeGraph** out, const MambaLayerW4* layers,
+                                                  int64_t n_layers, float* hidden, float* conv_state,
+                                                  float* ssm_state, int64_t B, void* workspace,
+                                                  int64_t workspace_bytes) {
+  return create_layer_graph("mamba_layer_w4_decode_graph_create", mamba_layer_w4_step, out, layers, n_layers, hidden,
+                            conv_state, ssm_state, B, workspace, workspace_bytes);
 }
 
 extern "C" int mamba_decode_graph_launch(MambaDecodeGraph* g, void* stream) {

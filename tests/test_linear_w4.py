@@ -70,7 +70,7 @@ def _call(**kw):
     (dict(c=None), -1), (dict(a=None), -1), (dict(q=None), -1), (dict(s=None), -1), (dict(c_dt=2), -1),
     (dict(s_dt=-1), -1), (dict(ld_c=63), -1), (dict(ld_a=95), -1), (dict(ld_q=47), -1), (dict(ld_q=56), -1),
     (dict(ld_a=100), -1), (dict(K=97), -1), (dict(group=32), -1), (dict(group=32, ld_s=3), -1), (dict(group=16), -2),
-    (dict(group=0), -2), (dict(group=-128), -2), (dict(M=-1), -1), (dict(N=-1), -1), (dict(K=0), -1), (dict(M=1 << 31), -1),
+    (dict(group=0), -2), (dict(group=-128), -2), (dict(M=-1), -1), (dict(N=-1), -1), (dict(K=0), -1), (dict(M=1 << 31), -1), (dict(K=(1 << 30) + 1), -1), (dict(N=(1 << 30) + 1), -1),
     (dict(a=ctypes.c_void_p(0x20000008)), -1), (dict(q=ctypes.c_void_p(0x30000008)), -1), (dict(c=FAKE, a=FAKE), -1),
     (dict(c=FAKE, q=FAKE), -1), (dict(c=FAKE, s=FAKE), -1), (dict(c=FAKE, z=FAKE), -1), (dict(r=FAKE, ld_r=63), -1),
     (dict(c=FAKE, r=FAKE, ld_r=64, c_dt=1), -1), (dict(c=FAKE, r=FAKE, ld_r=65), -1),
