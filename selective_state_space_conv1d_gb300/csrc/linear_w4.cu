@@ -10,9 +10,9 @@
 //   up to 8 rows    warp-level products of 16 weight rows x 8 activation rows (rows_kernel)
 //   more            tensor memory and tcgen05 (gemm_w4.cu)
 //
-// All read a weight row's bytes once.  A warp-level product of 16 x 8 x 16 takes about 64
-// cycles of a quarter of an SM, whatever part of its 8 columns is filled; two rows on the
-// f32 units take as long (50000 x 2560, us: one row 30 against 35, two 42 against 35).
+// All read a weight row's bytes once; the first two are bound by the instructions that make
+// numbers of nibbles and by their loads' latency (50000 x 2560, whose bytes take 10 us of
+// HBM: one row 31 us; four rows in products 28, without the weights' loads 22).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,9 +49,9 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {
   return *reinterpret_cast<const __nv_bfloat162*>(&v);
 }
 
-// 8 activations from k on, zeros past K (and past the rows: p null)
+// 8 activations from k on, zeros past K
 __device__ __forceinline__ uint4 load_x(const __nv_bfloat16* p, int k, int K) {
-  if (!p || k >= K) return make_uint4(0, 0, 0, 0);
+  if (k >= K) return make_uint4(0, 0, 0, 0);
   if (k + 8 <= K) return *reinterpret_cast<const uint4*>(p + k);
   uint64_t lo = 0, hi = 0;
 #pragma unroll 1
@@ -129,7 +129,14 @@ __global__ void __launch_bounds__(32 * kOneWarps, 3) linear_w4_one_kernel(const 
 #pragma unroll 1
   for (int i = kw; i < turns; i += kw_n) {
     const int k = i * kOneK + lane * 16;
-    const uint4 xv[2] = {load_x(x, k, K), load_x(x, k + 8, K)};
+    uint4 xv[2];
+    if ((i + 1) * kOneK <= K) {
+      xv[0] = reinterpret_cast<const uint4*>(x + k)[0];
+      xv[1] = reinterpret_cast<const uint4*>(x + k)[1];
+    } else {
+      xv[0] = load_x(x, k, K);
+      xv[1] = load_x(x, k + 8, K);
+    }
     uint2 w[R];
     float sc[R];
     uint32_t z[R];
@@ -224,8 +231,8 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
 // word i of its own 16 bytes in product i (k = 32 t + 8 i ..); with smaller ones the four
 // lanes of a row exchange words first, and product b takes word t of piece b (k = 32 b +
 // 8 t ..).
-template <int WARPS, int GROUP>
-__global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
+template <int WARPS, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 16 ? 2 : 768 / (32 * WARPS))
     linear_w4_rows_kernel(const LinearW4Args a, const int scale_pitch) {
   constexpr int kG = kUnit / GROUP;  // groups per unit
   constexpr bool kOwn = GROUP == kUnit;
@@ -244,20 +251,21 @@ __global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
   unsigned char* zeros = reinterpret_cast<unsigned char*>(scales + kRows * scale_pitch);
   grid_dependency_begin();
 
-  const uint8_t* q0 = g < rows_n ? a.q + (int64_t)(n0 + g) * a.ld_q + t * 16 : nullptr;
-  const uint8_t* q1 = g + 8 < rows_n ? a.q + (int64_t)(n0 + g + 8) * a.ld_q + t * 16 : nullptr;
+  // what lies outside the matrix is read inside it: rows past the last are not stored (and
+  // their scales are 0), pieces past the last meet activations of 0
+  const uint8_t* q0 = a.q + (int64_t)(n0 + (g < rows_n ? g : rows_n - 1)) * a.ld_q;
+  const uint8_t* q1 = a.q + (int64_t)(n0 + (g + 8 < rows_n ? g + 8 : rows_n - 1)) * a.ld_q;
+  const uint32_t q_last = (uint32_t)(pieces - 1) * 16;
   uint4 ahead[kAhead][2];
   auto fetch = [&](int u, uint4 (&w)[2]) {
-    w[0] = w[1] = make_uint4(0, 0, 0, 0);
-    if (u * 4 + t < pieces) {
-      if (q0) w[0] = __ldcs(reinterpret_cast<const uint4*>(q0 + (int64_t)u * 64));
-      if (q1) w[1] = __ldcs(reinterpret_cast<const uint4*>(q1 + (int64_t)u * 64));
-    }
+    const uint32_t at = (uint32_t)(u * 4 + t) * 16, off = at < q_last ? at : q_last;
+    w[0] = __ldcs(reinterpret_cast<const uint4*>(q0 + off));
+    w[1] = __ldcs(reinterpret_cast<const uint4*>(q1 + off));
   };
 #pragma unroll
   for (int d = 0; d < kAhead; ++d) fetch(warp + d * WARPS, ahead[d]);
 
-  const __nv_bfloat16* x = g < rows_m ? static_cast<const __nv_bfloat16*>(a.a) + g * a.ld_a : nullptr;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.a) + (g < rows_m ? g : rows_m - 1) * a.ld_a;
   float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
   int u = warp;
@@ -276,9 +284,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
         for (int gr = lane; gr < scale_pitch; gr += 32) {
           const bool in = row < rows_n && gr < held;
           const float v = !in ? 0.0f : (a.s_bf16 ? to_f32(__ldg(sb + gr)) : __ldg(sf + gr));
-          const uint32_t zv = a.zeros && in ? __ldg(z + gr) & 127u : 0u;
+          const uint32_t zv = ZEROS && in ? __ldg(z + gr) & 127u : 0u;
           scales[row * scale_pitch + gr] = v;
-          if (a.zeros) zeros[row * scale_pitch + gr] = (unsigned char)zv;
+          if (ZEROS) zeros[row * scale_pitch + gr] = (unsigned char)zv;
         }
       }
       __syncthreads();
@@ -289,8 +297,14 @@ __global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
       for (int d = 0; d < kAhead; ++d) {
         if (u >= u_end) break;
         uint4 xv[4];
+        const int k = u * kUnit + (kOwn ? t * 32 : t * 8);  // and 8 or 32 further for the next
+        if ((u + 1) * kUnit <= K) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = load_x(x, u * kUnit + (kOwn ? t * 32 + i * 8 : i * 32 + t * 8), K);
+          for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const uint4*>(x + k + i * (kOwn ? 8 : 32));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xv[i] = load_x(x, k + i * (kOwn ? 8 : 32), K);
+        }
         // (registers that stay where they are: a move would wait for the load)
         uint32_t w0[4] = {ahead[d][0].x, ahead[d][0].y, ahead[d][0].z, ahead[d][0].w};
         uint32_t w1[4] = {ahead[d][1].x, ahead[d][1].y, ahead[d][1].z, ahead[d][1].w};
@@ -306,8 +320,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1024 / (32 * WARPS))
         for (int i = 0; i < 4; ++i) {
           if (i * 32 % GROUP == 0) acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
           const int e = i * 32 / GROUP;
-          const __nv_bfloat162 z0 = zero_pair(a.zeros ? zc[e] : 8u);
-          const __nv_bfloat162 z1 = zero_pair(a.zeros ? zc[8 * scale_pitch + e] : 8u);
+          const __nv_bfloat162 z0 = zero_pair(ZEROS ? zc[e] : 8u), z1 = zero_pair(ZEROS ? zc[8 * scale_pitch + e] : 8u);
           const uint32_t p0[4] = {nibble_pair<0>(w0[i], z0), nibble_pair<1>(w0[i], z0), nibble_pair<2>(w0[i], z0),
                                   nibble_pair<3>(w0[i], z0)};
           const uint32_t p1[4] = {nibble_pair<0>(w1[i], z1), nibble_pair<1>(w1[i], z1), nibble_pair<2>(w1[i], z1),
@@ -355,7 +368,10 @@ cudaError_t launch_rows(const LinearW4Args& g, cudaStream_t stream) {
   static_assert(WARPS * kCols * kRows * 4 + kRows * (kSpan / GROUP + 1) * 5 <= 48 * 1024, "shared memory without opt-in");
   const int smem = WARPS * kCols * kRows * 4 + kRows * scale_pitch * (g.zeros ? 5 : 4);
   const dim3 grid((unsigned)((g.N + kRows - 1) / kRows));
-  return launch_pdl(true, linear_w4_rows_kernel<WARPS, GROUP>, grid, dim3(32 * WARPS), smem, stream, g, scale_pitch);
+  return g.zeros ? launch_pdl(true, linear_w4_rows_kernel<WARPS, GROUP, true>, grid, dim3(32 * WARPS), smem, stream, g,
+                              scale_pitch)
+                 : launch_pdl(true, linear_w4_rows_kernel<WARPS, GROUP, false>, grid, dim3(32 * WARPS), smem, stream, g,
+                              scale_pitch);
 }
 
 template <int WARPS>
@@ -371,9 +387,14 @@ cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaS
   if (g.M <= 0 || g.N <= 0) return cudaSuccess;
   if (g.M > kCols) return launch_gemm_w4(g, dev, stream);
   if (g.M == 1) return launch_one(g, dev.sm_count, stream);
-  // two CTAs per SM or fewer: more warps to a row, so that all of it is on its way at once
-  const bool few = (g.N + kRows - 1) / kRows <= 2 * (int64_t)dev.sm_count && g.K > 8 * kUnit;
-  return few ? launch_group<16>(g, stream) : launch_group<8>(g, stream);
+  // as many warps to 16 weight rows as give every SM 32: a warp's start and end cost it what
+  // three units do (50000 x 2560, 4 rows, us: eight warps 36, two 33, two
+  // with 80 registers a thread instead of 64 28)
+  const int64_t ctas = (g.N + kRows - 1) / kRows, want = 32 * (int64_t)dev.sm_count, units = (g.K + kUnit - 1) / kUnit;
+  if (ctas * 2 >= want || units <= 2) return launch_group<2>(g, stream);
+  if (ctas * 4 >= want || units <= 4) return launch_group<4>(g, stream);
+  if (ctas * 8 >= want || units <= 8) return launch_group<8>(g, stream);
+  return launch_group<16>(g, stream);
 }
 
 }  // namespace mamba
