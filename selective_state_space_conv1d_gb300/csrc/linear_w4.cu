@@ -11,8 +11,9 @@
 //   more            tensor memory and tcgen05 (gemm_w4.cu)
 //
 // All read a weight row's bytes once; the first two are bound by the instructions that make
-// numbers of nibbles and by their loads' latency (50000 x 2560, whose bytes take 10 us of
-// HBM: one row 31 us; four rows in products 28, without the weights' loads 22).
+// numbers of nibbles, and then by the wait for loads (50000 x 2560, whose bytes take 10 us of
+// HBM: one row 31 us; four rows in products 28, with neither the weights' nor the activations'
+// loads in the loop 21).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -390,7 +391,7 @@ cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaS
   if (g.M == 1) return launch_one(g, dev.sm_count, stream);
   // as many warps to 16 weight rows as give every SM 32: a warp's start and end cost it what
   // three units do (50000 x 2560, 4 rows, us: eight warps 36, two 33, two
-  // with 80 registers a thread instead of 64, 28)
+  // with 80 registers a thread instead of 64, 28, and one 30; 20480 x 2560: two 14, one 25)
   const int64_t ctas = (g.N + kRows - 1) / kRows, want = 32 * (int64_t)dev.sm_count, units = (g.K + kUnit - 1) / kUnit;
   if (ctas * 2 >= want || units <= 2) return launch_group<2>(g, stream);
   if (ctas * 4 >= want || units <= 4) return launch_group<4>(g, stream);
