@@ -17,7 +17,7 @@
 //
 // Alternatives cost no second pass: an element of the row's first n is at least as
 // large as the n-th largest thread maximum, so it lies in the subset of a thread
-// whose maximum reaches that bound, and only those subsets (n of 256, and a few
+// whose maximum reaches that bound, and only those subsets (n of 256, rarely
 // more) are read again, out of the caches.  (128 rows of 128000 bf16: 13 us without
 // alternatives, 23 with 20; 8192 rows of 50000 with one token each: 154, 5.3 TB/s, the
 // rest latency and the 60 % of issue slots the exponentials and sums take.)  Elements are compared as 64-bit keys,
@@ -190,7 +190,6 @@ struct SharedState {
   float stat[kWarps][4];
   float mine[4];                          // this CTA's maximum, reference, sums
   int n_subset, n_keys;
-  uint64_t best;
   uint64_t reach;                         // a bound that n of this CTA's elements reach
 };
 
@@ -292,35 +291,25 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const Token
         }
       }
     }
-    // a bound that at least n thread maxima reach: the j-th largest of each warp,
-    // j = ceil(n / 8), and of those the ceil(n / j)-th
-    const int per_warp = (n + kWarps - 1) / kWarps;
-    uint64_t left = key, best = 0;
+    // a bound that n thread maxima reach: the n-th of the warps' first 2 ceil(n / 8) (of all
+    // thread maxima, unless one warp holds more than twice its share of the first n).  Where
+    // there is none, fewer than half of the threads have an element, and every one is taken.
+    const int per_warp = (n + kWarps - 1) / kWarps * 2;
+    uint64_t left = key;
     for (int i = 0; i < per_warp; ++i) {
-      best = warp_max(left);
+      const uint64_t best = warp_max(left);
       if (left == best) left = 0;
+      if (lane == 0) sh.keys[i * kWarps + warp] = best;
     }
-    if (lane == 0) sh.bound[warp] = best;
+    if (threadIdx.x == 0) sh.reach = 0;
     __syncthreads();
-    const int need = (n + per_warp - 1) / per_warp;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    if ((int)threadIdx.x < per_warp * kWarps) {
+      const uint64_t k = sh.keys[threadIdx.x];
       int above = 0;
-#pragma unroll
-      for (int u = 0; u < kWarps; ++u) above += sh.bound[u] > sh.bound[w] || (sh.bound[u] == sh.bound[w] && u < w);
-      if (above == need - 1) bound = sh.bound[w];
+#pragma unroll 8
+      for (int j = 0; j < per_warp * kWarps; ++j) above += sh.keys[j] > k;
+      if (above == n - 1 && k != 0) sh.reach = k;
     }
-    if (bound == 0) {  // fewer vectors than threads: the n-th largest of all thread maxima
-      sh.keys[threadIdx.x] = key;
-      if (threadIdx.x == 0) sh.best = 0;
-      __syncthreads();
-      int above = 0;
-      for (int j = 0; j < kThreads; ++j) above += sh.keys[j] > key;
-      if (above == n - 1 && key != 0) sh.best = key;
-      __syncthreads();
-      bound = sh.best;
-    }
-    if (threadIdx.x == 0) sh.reach = bound;
   }
   // the row's sums, from the CTAs', and the best of their bounds: the CTA it comes from has n
   // elements that reach it
@@ -348,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const Token
     } else {
       __syncthreads();
       row_st = Stats{sh.mine[0], sh.mine[1], sh.mine[2], sh.mine[3]};
+      if (n > 0) bound = sh.reach;
     }
   };
   gather();
