@@ -193,8 +193,10 @@ struct SharedState {
   uint64_t reach;                         // a bound that n of this CTA's elements reach
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const TokenLogprobsArgs a, int cluster) {
+// BLOCKS: CTAs an SM holds, and with them a thread's registers and its reads ahead
+template <typename T, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const TokenLogprobsArgs a, int cluster) {
+  constexpr int kAhead = BLOCKS > 2 ? 4 : 6;
   using R = Row<T>;
   constexpr int VEC = R::VEC;
   __shared__ SharedState sh;
@@ -222,21 +224,24 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const Token
     add_terms(st, x);
   };
   const uint4 nothing = make_uint4(R::kNothing, R::kNothing, R::kNothing, R::kNothing);
-  // vectors that lie inside the row, two at a time and four on their way; the row's ends
+  // vectors that lie inside the row, two at a time and kAhead on their way; the row's ends
   // are their threads' first and last
   const int hi = v_hi < r.full_hi ? v_hi : r.full_hi;
   auto full = [&](int v) { return v >= r.full_lo && v < hi ? __ldg(reinterpret_cast<const uint4*>(r.base) + v) : nothing; };
   int v = v_lo + (int)threadIdx.x;
   if (v == 0 && r.full_lo > 0) take(r.load(0), nothing, 0);
   if (v < hi) {
-    uint4 a0 = full(v), a1 = full(v + kThreads), b0 = full(v + 2 * kThreads), b1 = full(v + 3 * kThreads);
-    while (true) {
-      take(a0, a1, v);
-      a0 = full(v + 4 * kThreads), a1 = full(v + 5 * kThreads);
-      if ((v += 2 * kThreads) >= hi) break;
-      take(b0, b1, v);
-      b0 = full(v + 4 * kThreads), b1 = full(v + 5 * kThreads);
-      if ((v += 2 * kThreads) >= hi) break;
+    uint4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = full(v + i * kThreads);
+    while (v < hi) {
+#pragma unroll
+      for (int i = 0; i < kAhead; i += 2) {
+        take(ahead[i], ahead[i + 1], v);
+        ahead[i] = full(v + kAhead * kThreads);
+        ahead[i + 1] = full(v + (kAhead + 1) * kThreads);
+        if ((v += 2 * kThreads) >= hi) break;
+      }
     }
   }
   if (r.full_hi < nv && v_hi == nv && nv - 1 >= r.full_lo && (nv - 1 - v_lo) % kThreads == (int)threadIdx.x)
@@ -490,7 +495,10 @@ cudaError_t launch_typed(const TokenLogprobsArgs& a, const DeviceInfo& dev, cuda
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a, cluster);
+  // no more CTAs than two an SM: the registers of both (128 x 128000 bf16, 20 alternatives, us:
+  // 16.5 with two an SM, 19.7 with three, 22.7 with four; 4096 x 50000: 94, 77 and 71)
+  return a.M * cluster <= dev.sm_count * (int64_t)2 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 2>, a, cluster)
+                                                     : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 4>, a, cluster);
 }
 
 }  // namespace
