@@ -6,13 +6,13 @@
 // products are exact, the sums are f32, and the scale meets the sum of a group in f32:
 // no weight is rounded.  Three kernels:
 //
-//   one row         f32 units (one_kernel)
+//   one row         f32 units (one_kernel), where the weights are not many
 //   up to 8 rows    warp-level products of 16 weight rows x 8 activation rows (rows_kernel)
 //   more            tensor memory and tcgen05 (gemm_w4.cu)
 //
 // All read a weight row's bytes once; the first two are bound by the instructions that make
 // numbers of nibbles, and then by the wait for loads (50000 x 2560, whose bytes take 10 us of
-// HBM: one row 31 us; four rows in products 28, with neither the weights' nor the activations'
+// HBM: one row 31 us on the f32 units and 26 in products; four rows 28, with neither the weights' nor the activations'
 // loads in the loop 21).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -388,7 +388,12 @@ cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaS
   if (g.M <= 0 || g.N <= 0) return cudaSuccess;
   // (10240 x 2560, us: 8 rows 11.4, 9 rows on the tensor memory path 13.3)
   if (g.M > kCols) return launch_gemm_w4(g, dev, stream);
-  if (g.M == 1) return launch_one(g, dev.sm_count, stream);
+  // one row: on the f32 units, but for many long weight rows in groups of 128, where a unit of
+  // products takes fewer instructions (us, products against f32 units: 20480 x 2560 13.2 and
+  // 15.1, 50000 x 2560 26 and 31; 10240 x 2560 9.4 and 9.2, 2560 x 5120 7.4 and 6.2; groups of
+  // 32, whose words change lanes first, 50000 x 2560 43 and 36)
+  const bool much = g.N / kOneRows * ((g.K + kUnit - 1) / kUnit) >= 16 * 24 * (int64_t)dev.sm_count;
+  if (g.M == 1 && !(much && g.group == kUnit)) return launch_one(g, dev.sm_count, stream);
   // as many warps to 16 weight rows as give every SM 32: a warp's start and end cost it what
   // three units do (50000 x 2560, 4 rows, us: eight warps 36, two 33, two
   // with 80 registers a thread instead of 64, 28, and one 30; 20480 x 2560: two 14, one 25)

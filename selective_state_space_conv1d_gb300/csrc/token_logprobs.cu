@@ -18,9 +18,9 @@
 // Alternatives cost no second pass: an element of the row's first n is at least as
 // large as the n-th largest thread maximum, so it lies in the subset of a thread
 // whose maximum reaches that bound, and only those subsets (n of 256, rarely
-// more) are read again, out of the caches.  (128 rows of 128000 bf16: 13 us without
-// alternatives, 23 with 20; 8192 rows of 50000 with one token each: 154, 5.3 TB/s, the
-// rest latency and the 60 % of issue slots the exponentials and sums take.)  Elements are compared as 64-bit keys,
+// more) are read again, out of the caches.  (128 rows of 128000 bf16: 11 us without
+// alternatives, 16.6 with 20; 8192 rows of 50000 with one token each: 137 us, 6.0 TB/s, the
+// rest the issue slots that exponentials and sums take.)  Elements are compared as 64-bit keys,
 // value above inverted index, so all keys differ and ties go to the lowest index.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const 
 template <typename T>
 cudaError_t launch_typed(const TokenLogprobsArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   // few rows: a row over a cluster, up to two CTAs per SM and no slice under 4096 elements
-  // (128 x 128000 bf16, 20 alternatives, us: one CTA a row 34, two 24, four 33, eight 49)
+  // (128 x 128000 bf16, 20 alternatives, us, all with three CTAs an SM: one CTA a row 34, two
+  // 24, four 33, eight 49)
   int cluster = 1;
   while (cluster < kMaxCluster && a.M * cluster * 2 <= dev.sm_count * (int64_t)2 && a.V / (cluster * 2) >= 4096) cluster *= 2;
   cudaLaunchConfig_t cfg = {};

@@ -235,6 +235,21 @@ def test_large(cuda_lib, M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,scales,zeros,out", [(20480, 2560, "bf16", True, "f32"), (20003, 2603, "f32", False, "bf16"),
+                                                  (60001, 1000, "bf16", False, "f32"), (1300, 32768 + 40, "f32", True, "f32"),
+                                                  (10001, 9000, "bf16", True, "bf16")])
+def test_one_row_of_many_weights(cuda_lib, N, K, scales, zeros, out):
+    q, s, z = weights(9, N, K, 128, scales, zeros)
+    a = activations(9, 1, K)
+    r = torch.randn(1, N, generator=torch.Generator().manual_seed(5)).cuda()
+    got = run(a, q, s, z, 128, out, r)
+    rows = torch.cat((torch.arange(0, N, max(1, N // 97)), torch.arange(N - 17, N)))
+    pick = lambda t: None if t is None else t[rows]  # noqa: E731
+    check(got[:, rows], *reference(a, q[rows], s[rows], pick(z), 128, r[:, rows]), K)
+    assert bool(got.isfinite().all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 6, 50, 300])
 def test_repeats_on_other_streams_and_in_a_graph(cuda_lib, M):
     N, K, group = 1040, 1536, 128
