@@ -415,8 +415,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const 
       }
     } else {
       // more than the list holds (values that repeat in the threads' pattern): one
-      // pass over the slice per alternative
-      uint64_t last = ~0ull;
+      // pass over the slice per alternative, the first of them without a key to stay below: a NaN
+      // at index 0 has the largest there is
+      uint64_t last = 0;
       for (int i = 0; i < n; ++i) {
         uint64_t k_best = 0;
         for (int v = v_lo + (int)threadIdx.x; v < v_hi; v += kThreads) {
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const 
             const int64_t e = r.element(v, j);
             if (!r.inside(e)) continue;
             const uint64_t k = key_of(x[j], (uint32_t)e);
-            if (k < last && k > k_best) k_best = k;
+            if ((i == 0 || k < last) && k > k_best) k_best = k;
           }
         }
         k_best = warp_max(k_best);
