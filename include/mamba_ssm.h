@@ -541,6 +541,7 @@ MAMBA_API int mamba_block_norm(float* x_out, int64_t ld_xo, void* out, int64_t l
  *   tokens       [M] int64; a negative one asks for none (logprob 0: padding), one
  *                from V on gives NaN                                         (in)
  *   n_top        0..MAMBA_MAX_TOP, at most V; equal logits go by the lowest index
+ * ln p is at most 0 and an entropy at least 0, after rounding too.
  * Logits of -inf have probability 0 (ln p = -inf); a row of nothing else has entropy 0
  * and ln p = -inf everywhere.  A NaN or +inf in a row makes its entropy and every ln p
  * NaN, as the formula does; in the order of tokens NaN stands above +inf.

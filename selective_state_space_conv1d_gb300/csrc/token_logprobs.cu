@@ -451,7 +451,13 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const 
   const float log_s1 = log2f(s1);  // -inf for a row of -inf
   // ln of the row's sum of e^(l - top_l): the reference is not quite L top_l
   const float log_sum = (log_s1 - (far ? 0.0f : fmaf(top_l, kLog2e, -row_st.ref))) * kLn2;
-  auto logprob_of = [&](float l) { return l == -INFINITY && s1 == s1 ? -INFINITY : (l - top_l) - log_sum; };
+  // The row's largest element adds 2^(L top_l - r) to S1, which is 1 only before rounding, so the
+  // logarithm of a certain token may come out 2^-24 above 0 and the entropy as much below: both
+  // are cut at 0 (a NaN compares false and stays).
+  auto logprob_of = [&](float l) {
+    const float v = (l - top_l) - log_sum;
+    return l == -INFINITY && s1 == s1 ? -INFINITY : (v > 0.0f ? 0.0f : v);
+  };
   if (n > 0) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t k = sh.top[i];
@@ -467,7 +473,10 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) token_logprobs_kernel(const 
     }
   }
   if (rank == 0 && threadIdx.x == 0) {
-    if (a.entropy) a.entropy[row] = s1 == 0.0f ? 0.0f : (log_s1 - s2 / s1) * kLn2;
+    if (a.entropy) {
+      const float h = (log_s1 - s2 / s1) * kLn2;
+      a.entropy[row] = s1 == 0.0f || h < 0.0f ? 0.0f : h;
+    }
     if (a.logprob) {
       const int64_t t = a.tokens[row];
       a.logprob[row] = t < 0 ? 0.0f
