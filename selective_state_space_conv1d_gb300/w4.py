@@ -42,7 +42,8 @@ def unpack_w4(q, K):
 def quantize_w4(weight, group=128, *, zeros=False, scale_dtype=torch.bfloat16):
     """A floating-point weight [N, K] to the nearest 4-bit one, group by group: values -7..7
     of a scale max|w| / 7, or, with zeros, 0..15 of a scale (max - min) / 15 with a zero
-    point (max and min of the group and 0)."""
+    point (max and min of the group and 0).  Weights have to be finite, and so has a
+    group's max - min in f32."""
     if weight.dim() != 2 or not weight.is_floating_point():
         raise ValueError("weight must be a floating-point [N, K] tensor")
     if group not in GROUPS:
@@ -59,6 +60,8 @@ def quantize_w4(weight, group=128, *, zeros=False, scale_dtype=torch.bfloat16):
     else:
         s = (p.abs().amax(-1) / 7).clamp(min=tiny).to(scale_dtype)
         z = torch.full_like(s, 8, dtype=torch.float32)
+    if not bool(s.isfinite().all()):
+        raise ValueError("weight must be finite, and so must each group's range in float32")
     v = (torch.round(p / s.float()[..., None]) + z[..., None]).clamp(0, 15).to(torch.uint8)
     return W4(pack_w4(v.flatten(1)[:, :K]), s, z.to(torch.uint8) if zeros else None, group)
 
