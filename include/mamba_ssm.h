@@ -475,7 +475,9 @@ MAMBA_API int mamba_linear_bf16(void* c, int64_t ld_c, int c_dtype, const void* 
  *   group     32, 64 or 128
  *   residual  [M] rows of N f32 at ld_r, or NULL; may be c itself (f32, same stride)
  * a and q must be 16-byte aligned, ld_a a multiple of 8 and ld_q of 16.  M, N, K
- * up to 2^30.  Deterministic: the order of the sums depends on the sizes only.
+ * up to 2^30.  Deterministic on a device: the order of the sums depends on the sizes
+ * and on the device (its SMs, and the clusters of them that it holds at once), on nothing
+ * else.
  * Errors: MAMBA_ERR_INVALID_ARG for NULL pointers, strides smaller than a row,
  * misaligned a / q, overlap of c with an input (other than the residual as above),
  * extent overflow; MAMBA_ERR_UNSUPPORTED for another group.

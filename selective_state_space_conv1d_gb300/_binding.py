@@ -898,8 +898,8 @@ def mamba_linear_w4(c, a, q, scales, zeros=None, residual=None, *, group=128, st
 
     a: bf16; q: uint8 [N, ceil(K / 32) * 16], byte j of a row holding q of k = 2j in
     its low half and of 2j + 1 in its high half (pack_w4, quantize_w4); scales: f32
-    or bf16 [N, ceil(K / group)]; zeros: uint8 of that shape, or None (8); group: 32,
-    64 or 128; c: f32 or bf16; residual: f32 [M, N], may be c itself.  Row-strided
+    or bf16 [N, ceil(K / group)]; zeros: uint8 of that shape, 0..127, or None (8); group:
+    32, 64 or 128; c: f32 or bf16; residual: f32 [M, N], may be c itself.  Row-strided
     views allowed, the rows of a and q 16-byte aligned."""
     import torch
 

@@ -13,13 +13,14 @@
 // Roles of a CTA (persistent, one per SM):
 //  * warp 0 brings activations, BT x 64 bf16 with the 128-byte swizzle a copy (TMA);
 //  * warp 2 brings weights as they are stored, 128 rows x 64 bytes (128 k) a copy;
-//  * four warpgroups, a thread per weight row, make bf16 of the nibbles, 32 k of each
-//    chunk of 128 a warpgroup: two operations a pair (nibbles i and i + 4 of a word in
-//    the halves of a register, 0x4300 above them: 128 + q; a packed subtraction of
-//    128 + z), a byte permutation that puts neighbours side by side, and a store into
-//    tensor memory, where the product reads its weights (through shared memory they
-//    cost it 32 KB written and 32 read per chunk, beside the activations' own: 343 us
-//    for 8192 x 10240 x 2560);
+//  * four warpgroups, a thread per weight row, make bf16 of the nibbles, 64 k of every
+//    second chunk of 128 a warpgroup (two take the even chunks' halves, two the odd
+//    ones'): two operations a pair (nibbles i and i + 4 of a word in the halves of a
+//    register, 0x4300 above them: 128 + q; a packed subtraction of 128 + z), a byte
+//    permutation that puts neighbours side by side, and a store into tensor memory,
+//    where the product reads its weights (through shared memory they cost it 32 KB
+//    written and 32 read per chunk, beside the activations' own: 343 us for 8192 x
+//    10240 x 2560);
 //  * warp 1 issues the products, a group of k into one of a few accumulators;
 //  * two warpgroups take the finished accumulators meanwhile, each half of the columns:
 //    total += scale * group's sum, BT / 2 totals a thread in registers, and store
@@ -27,11 +28,16 @@
 // Few tiles: K is split over a cluster whose CTAs add their totals through
 // distributed shared memory in rank order.
 //
-// Bound by issue slots, which the nibbles, the totals and the products' own warp share:
-// 8192 x 10240 x 2560 in groups of 128 takes 330 us (1.30 PFLOP/s; the tensor pipe busy 55 %
-// of the cycles, issue slots 71 %), in groups of 64 421 and of 32 627 (a group costs its
-// commit and a pass of the totals, whatever it holds).  128 rows: 18.7 us, 8 of them
-// the start up to the first product and the end; 0.36 us a chunk.
+// 8192 x 10240 x 2560 in groups of 128 takes 330 us in a graph of four calls (1.30 PFLOP/s)
+// and 349 call by call (long runs come under the power limit); in groups of 64 421 and of 32
+// 629 in such a graph: a group costs its commit and a pass of the totals, whatever it holds.
+// No unit is full (2048 rows: issue slots 65 %, the waiting roles' polls among them, tensor
+// pipe 50, L2 29): the roles wait for one another, which for which is not measured.
+// 128 rows in groups of 64: 18.7 us in a graph, 8 of them the start up to the first product
+// and the end; 0.36 us a chunk.
+// Against mamba_linear_bf16 (gemm.cu), us in a graph, groups of 128 here: 10240 x 2560, 16
+// rows 13.4 and 22.3, 128 rows 15.6 and 15.3, 256 rows 27.3 and 18.0, 8192 rows 343 and 276;
+// 2560 x 5120, 128 rows 11.2 and 16.3, 8192 rows 168 and 161.
 //
 // Every wait is bounded (about a second); one that runs out sets
 // MAMBA_FAULT_GEMM_WAIT and an abort flag that ends every role's loop, and the CTA

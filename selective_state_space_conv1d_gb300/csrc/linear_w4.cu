@@ -10,10 +10,12 @@
 //   up to 8 rows    warp-level products of 16 weight rows x 8 activation rows (rows_kernel)
 //   more            tensor memory and tcgen05 (gemm_w4.cu)
 //
-// All read a weight row's bytes once; the first two are bound by the instructions that make
-// numbers of nibbles, and then by the wait for loads (50000 x 2560, whose bytes take 10 us of
-// HBM: one row 31 us on the f32 units and 26 in products; four rows 28, with neither the weights' nor the activations'
-// loads in the loop 21).
+// The first two read a weight row's bytes once, gemm_w4.cu once for every tile of activation
+// rows.  50000 x 2560, whose bytes take 10 us of HBM: one row 31 us on the f32 units and 26 in
+// products; four rows 28, with neither the weights' nor the activations' loads in the loop
+// 21.  No unit is full there (issue slots 39 %, ALU pipe 41, tensor pipe 10; 20 warps an
+// SM): a warp waits for its loads in half of its time, and beside them stand the scales that
+// start every CTA and the last of 1.7 waves.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -394,9 +396,10 @@ cudaError_t launch_linear_w4(const LinearW4Args& g, const DeviceInfo& dev, cudaS
   // 32, whose words change lanes first, 50000 x 2560 43 and 36)
   const bool much = g.N / kOneRows * ((g.K + kUnit - 1) / kUnit) >= 16 * 24 * (int64_t)dev.sm_count;
   if (g.M == 1 && !(much && g.group == kUnit)) return launch_one(g, dev.sm_count, stream);
-  // as many warps to 16 weight rows as give every SM 32: a warp's start and end cost it what
-  // three units do (50000 x 2560, 4 rows, us: eight warps 36, two 33, two
-  // with 80 registers a thread instead of 64, 28, and one 30; 20480 x 2560: two 14, one 25)
+  // as many warps to 16 weight rows as make 32 for every SM (24 of them resident at once, by
+  // their registers): a warp's start and end cost it what three units do (50000 x 2560, 4
+  // rows, us: eight warps 36, two 33, two with 80 registers a thread instead of 64, 28, and
+  // one 30; 20480 x 2560: two 14, one 25)
   const int64_t ctas = (g.N + kRows - 1) / kRows, want = 32 * (int64_t)dev.sm_count, units = (g.K + kUnit - 1) / kUnit;
   if (ctas * 2 >= want || units <= 2) return launch_group<2>(g, stream);
   if (ctas * 4 >= want || units <= 4) return launch_group<4>(g, stream);

@@ -7,7 +7,7 @@
 //
 // Bound: HBM, one pass over the logits.  A row is cut over the CTAs of a cluster
 // (one CTA if there are rows enough), a CTA's slice over its threads in vectors of
-// 16 bytes, vector v to thread v % 256.  A thread keeps a running maximum (with
+// 16 bytes, in turn: a slice's vector i to thread i % 256.  A thread keeps a running maximum (with
 // the first vector that holds it) and the two sums below it, in units of log2: e^d is
 // 2^(l L - r) with L = log2 e and r = L max l rounded once, one multiply-add and one
 // exponential an element.  (Rounding r moves every term alike, and the same r is in the
@@ -19,8 +19,9 @@
 // large as the n-th largest thread maximum, so it lies in the subset of a thread
 // whose maximum reaches that bound, and only those subsets (n of 256, rarely
 // more) are read again, out of the caches.  (128 rows of 128000 bf16: 11 us without
-// alternatives, 16.6 with 20; 8192 rows of 50000 with one token each: 137 us, 6.0 TB/s, the
-// rest the issue slots that exponentials and sums take.)  Elements are compared as 64-bit keys,
+// alternatives, 16.6 with 20; 8192 rows of 50000 with one token each: 137 us, 6.0 TB/s;
+// 2048 such rows keep 60 % of the issue slots busy, with the warps' longest wait the one for
+// loads.)  Elements are compared as 64-bit keys,
 // value above inverted index, so all keys differ and ties go to the lowest index.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

@@ -16,7 +16,7 @@ GROUPS = (32, 64, 128)
 
 class W4(NamedTuple):
     """A weight [N, K]: q uint8 [N, ceil(K / 32) * 16], scales f32 or bf16 [N, ceil(K /
-    group)], zeros uint8 of that shape (None: 8)."""
+    group)], zeros uint8 of that shape, 0..127 (None: 8)."""
     q: torch.Tensor
     scales: torch.Tensor
     zeros: Optional[torch.Tensor] = None
