@@ -511,6 +511,8 @@ MAMBA_API int mamba_rmsnorm(void* out, int64_t ld_out, int out_dtype, const floa
  *     out = x' / sqrt(mean_j x'_j^2 + eps) * pre_weight
  * (No counterpart in the mamba-rs pages, whose residual add sits in out_proj's epilogue
  *  and whose RMSNorm in the next block's start: an addition of this library.)
+ * Sums of squares are f32: a row of y or x' whose squares pass its largest value has the
+ * norm 0, one whose squares all underflow with eps 0 a norm that is not finite.
  *
  *   x_out   [M] rows of D f32 at ld_xo; may be x itself (same stride)        (out)
  *   out     [M] rows of D at ld_out, out_dtype, or NULL (no norm: the last block) (out)
